@@ -59,6 +59,7 @@ typedef enum {
 } medusa_status;
 
 enum { MEDUSA_F32 = 0, MEDUSA_BF16 = 1 };
+enum { MEDUSA_KV4 = 2 };   /* a cache's format only: 4-bit blocks, see medusa_cache_dims */
 enum { MEDUSA_GREEDY = 0, MEDUSA_TYPICAL = 1, MEDUSA_REJECT = 2 };
 
 /* device status word bits */
@@ -67,6 +68,8 @@ enum { MEDUSA_GREEDY = 0, MEDUSA_TYPICAL = 1, MEDUSA_REJECT = 2 };
 #define MEDUSA_FLAG_PAGE_RANGE  0x4u  /* a page-table entry fell outside [0, num_pages) */
 #define MEDUSA_FLAG_NONFINITE   0x8u  /* a logit or softmax statistic was NaN or Inf */
 #define MEDUSA_FLAG_TIMEOUT     0x10u /* a bounded wait in a pipelined kernel expired */
+#define MEDUSA_FLAG_POS_RANGE   0x20u /* a position fell outside a rotary table */
+#define MEDUSA_FLAG_ROW_RANGE   0x40u /* a row index, offset or count was out of range */
 
 typedef struct medusa_plan medusa_plan;   /* opaque */
 
@@ -398,6 +401,182 @@ medusa_status medusa_tree_greedy_device(int K, const int* s, int smax, const dou
  * [max_n + 1] as from medusa_tree_greedy_device.  Returns the index or a negative status. */
 int medusa_tree_size_choose(const double* expected, int max_n, const int* sizes,
                             const double* step_ms, int n);
+
+/* ------------------------------------------------------------------ rotary positions */
+/* Rotation of query and key rows by their positions ([MEDUSA] §3.4 Step 4 uses the depth
+ * positions medusa_tree_build writes), for callers whose checkpoints rotate differently from
+ * medusa_layer_qkv's synthetic layer or whose rows come from another projection.
+ *
+ * Pair i < rot/2 of a head turns by the angle p * f_i at position p, with the plain
+ * frequencies theta_i = base^(-2i/rot) and
+ *   MEDUSA_ROPE_PLAIN   f_i = theta_i
+ *   MEDUSA_ROPE_LINEAR  f_i = theta_i / factor
+ *   MEDUSA_ROPE_BANDED  f_i = w_i theta_i + (1 - w_i) theta_i / factor with
+ *                       w_i = clamp((turns_i - low) / (high - low), 0, 1), turns_i =
+ *                       orig_pos theta_i / (2 pi): full turns over the original context
+ *   MEDUSA_ROPE_RAMP    the same mixture, w_i falling linearly over the pair index, from 1
+ *                       at a = max(0, floor(c(high))) to 0 at b = min(rot - 1, ceil(c(low)))
+ *                       (clamped to [0, 1]; b - a taken as at least 0.001), where c(r) =
+ *                       rot ln(orig_pos / (2 pi r)) / (2 ln base) is the index that makes r turns
+ * Cosine and sine are multiplied by attn (0 means 1).  Layout MEDUSA_ROPE_HALF pairs element
+ * i with i + rot/2, MEDUSA_ROPE_INTERLEAVED 2i with 2i + 1; elements past rot pass through:
+ *   y1 = x1 cos - x2 sin,  y2 = x2 cos + x1 sin      (inverse: sin negated)
+ * The table of cosines and sines is computed in double on the GPU when the handle is created,
+ * rounded once to float; products and sums are single IEEE float operations, and the result
+ * is rounded once to the rows' dtype. */
+enum { MEDUSA_ROPE_HALF = 0, MEDUSA_ROPE_INTERLEAVED = 1 };
+enum { MEDUSA_ROPE_PLAIN = 0, MEDUSA_ROPE_LINEAR = 1, MEDUSA_ROPE_BANDED = 2, MEDUSA_ROPE_RAMP = 3 };
+typedef struct {
+  int rot;         /* rotated elements of a head: even, >= 2 */
+  int layout;      /* MEDUSA_ROPE_HALF or MEDUSA_ROPE_INTERLEAVED */
+  int max_pos;     /* positions 0..max_pos-1; the table takes max_pos * rot floats */
+  int scaling;     /* MEDUSA_ROPE_PLAIN .. MEDUSA_ROPE_RAMP */
+  double base;     /* > 1 */
+  double factor;   /* > 0; read unless PLAIN */
+  double orig_pos; /* > 0; BANDED and RAMP */
+  double low, high;/* turns, 0 < low < high; BANDED and RAMP */
+  double attn;     /* multiplier of cosine and sine, 0 means 1 */
+} medusa_rope_desc;
+typedef struct medusa_rope medusa_rope;   /* opaque: the table and a status word, on one GPU */
+/* Creates the handle on the current device (allocates, and waits for the table). */
+medusa_status medusa_rope_create(const medusa_rope_desc* desc, medusa_rope** out);
+void medusa_rope_destroy(medusa_rope* rope);
+/* As medusa_get_status, for the handle's own status word. */
+medusa_status medusa_rope_get_status(const medusa_rope* rope, void* stream, uint32_t* flags);
+/* One set of rows: element e of head h of row r is x[r * x_row + h * x_head + e] (strides in
+ * elements), its result y[r * y_row + h * y_head + e].  y == x with equal strides turns the
+ * rows in place; otherwise x and y must not overlap. */
+typedef struct {
+  const void* x;
+  void* y;
+  int heads;
+  long long x_row, x_head, y_row, y_head;
+} medusa_rope_rows;
+/* Turns up to 4 sets of rows (queries, keys) in one launch.  dtype: MEDUSA_F32 or
+ * MEDUSA_BF16 elements; dh >= rot elements per head; pos: device [rows].  A row whose position
+ * is outside the table is passed through unturned and sets MEDUSA_FLAG_POS_RANGE.  rows = 0
+ * does nothing.  Any alignment of whole elements works; rows whose pointers and strides are
+ * multiples of 16 bytes (and rot/2 of 16 bytes for HALF, rot for INTERLEAVED) move in 16-byte
+ * units. */
+medusa_status medusa_rope_apply(const medusa_rope* rope, int dtype, int dh, int rows,
+                                const int32_t* pos, const medusa_rope_rows* parts, int n_parts,
+                                int inverse, void* stream);
+
+/* ------------------------------------------------------------------ KV caches */
+/* A cache of B sequences, contiguous or paged (the layouts medusa_kv describes), that these
+ * calls fill, read back and attend over.  In the formats MEDUSA_F32 and MEDUSA_BF16 it is the
+ * cache medusa_step works on.  MEDUSA_KV4 holds 4.5 bits an element: 16 consecutive slots of
+ * one head are a block of 9 dh bytes,
+ *   16 rows of dh/2 bytes: element 2i in the low, 2i + 1 in the high four bits of byte i
+ *                          (e2m1: sign, and one of 0 .5 1 1.5 2 3 4 6),
+ *   16 rows of dh/16 bytes: one e4m3 scale for each 16 elements,
+ * and an element stands for e2m1 * e4m3 * g, g = k_scale for keys and v_scale for values (any
+ * positive numbers the caller keeps to; powers of two make every element exact in bf16).  The
+ * blocks lie [B][Hkv][capacity/16] (contiguous) or [num_pages][Hkv][page_size/16] (paged), so
+ * a head's blocks follow each other.  Writing takes, over each 16 elements, s = max|x| / (6 g)
+ * rounded to e4m3 and each x / (g s) rounded to e2m1 (both to nearest, ties to even, the
+ * largest where beyond); 16 elements that hold an infinity or a NaN read back as NaN and set
+ * MEDUSA_FLAG_NONFINITE. */
+typedef struct {
+  int B;             /* sequences */
+  int Hq, Hkv, dh;   /* query heads (a multiple of Hkv), key/value heads, head size 32, 64 or 128 */
+  int format;        /* MEDUSA_F32, MEDUSA_BF16 or MEDUSA_KV4 */
+  int capacity;      /* slots per sequence (paged: a multiple of page_size) */
+  int page_size;     /* 0: contiguous; KV4: page_size, or the contiguous capacity, is a multiple of 16 */
+  int num_pages;     /* paged: pages in the pool */
+  int max_nodes;     /* query rows (tree nodes) per sequence and attention call, 1..MEDUSA_MAX_NODES */
+} medusa_cache_dims;
+typedef struct medusa_cache medusa_cache;   /* opaque: sizes and a status word, on one GPU */
+medusa_status medusa_cache_create(const medusa_cache_dims* dims, medusa_cache** out);
+void medusa_cache_destroy(medusa_cache* cache);
+/* Bytes of the key pool, and of the value pool. */
+size_t medusa_cache_pool_bytes(const medusa_cache* cache);
+/* Bytes of device workspace medusa_kv4_attention needs (256-byte aligned; 0 for other formats). */
+size_t medusa_cache_workspace_size(const medusa_cache* cache);
+/* As medusa_get_status, for the cache's own status word. */
+medusa_status medusa_cache_get_status(const medusa_cache* cache, void* stream, uint32_t* flags);
+
+/* Rows for the cache.  k, v: element e of head h of row r at [r * row + h * head + e] (strides
+ * in elements).  Items are the rows as they are appended; `rows` is how many item places there
+ * are, and they belong to the sequences in one of two ways:
+ *   packed  start: device [B+1], items start[b] .. start[b+1]-1 are sequence b's; places
+ *           before start[0] and from start[B] on belong to none and are skipped
+ *   padded  start NULL: rows = B * per_seq, sequence b has the first count[b] (device [B],
+ *           NULL: all) of the per_seq places from b * per_seq
+ * index (device [rows], NULL: item i is row i): item i of sequence b is row
+ * b * index_rows + index[i], 0 <= index[i] < index_rows; items outside are skipped and set
+ * MEDUSA_FLAG_ROW_RANGE.  With per_seq = K+1, count = n_acc, index = path_nodes, index_rows =
+ * N+1 and k, v the tree's keys/values this is medusa_kv_compact for any format. */
+typedef struct {
+  const void* k;
+  const void* v;
+  int dtype;                            /* MEDUSA_F32 or MEDUSA_BF16 */
+  long long k_row, k_head, v_row, v_head;
+  int rows;
+  const int32_t* start;
+  int per_seq;
+  const int32_t* count;
+  const int32_t* index;
+  int index_rows;
+  const int32_t* pos;                   /* device [rows]: rotate item i as position pos[i] (NULL: its slot) */
+} medusa_kv_rows;
+/* Item j of sequence b goes to slot len[b] + j; its key is first turned by `rope` (NULL: as it
+ * is).  len_out[b] = min(len[b] + items, capacity); it may alias len, and both lie apart from
+ * everything else.  Slots past the capacity are not written and set MEDUSA_FLAG_KV_CAPACITY (as
+ * a len outside 0..capacity does, which is then taken as the nearer end), a page outside the
+ * pool MEDUSA_FLAG_PAGE_RANGE; an item with a position outside the table is stored unturned and
+ * sets MEDUSA_FLAG_POS_RANGE.  No two sequences may share a page that is written.  The scales
+ * are read for KV4 only. */
+medusa_status medusa_kv_append(const medusa_cache* cache, const medusa_kv* kv,
+                               const medusa_kv_rows* rows, const medusa_rope* rope, float k_scale,
+                               float v_scale, void* stream);
+/* Places that receive cached rows: item j of sequence b is slot first[b] + j (first NULL: j),
+ * b and j from start or per_seq / count as in medusa_kv_rows.  Element strides as there. */
+typedef struct {
+  void* k;
+  void* v;
+  int dtype;                            /* MEDUSA_F32 or MEDUSA_BF16 */
+  long long k_row, k_head, v_row, v_head;
+  int rows;
+  const int32_t* start;
+  int per_seq;
+  const int32_t* count;
+  const int32_t* first;                 /* device [B] or NULL */
+} medusa_kv_places;
+/* Reads slots back (kv->k, v, page_table, len): what the cache holds, rounded once to dtype.
+ * Only slots in [0, len[b]) are read; places of other slots are left as they were and set
+ * MEDUSA_FLAG_KV_CAPACITY. */
+medusa_status medusa_kv_read(const medusa_cache* cache, const medusa_kv* kv,
+                             const medusa_kv_places* places, float k_scale, float v_scale,
+                             void* stream);
+/* Attention over a 4-bit cache: row n of sequence b, query head h attends to the slots
+ * [0, len[b]) of key/value head h / (Hq/Hkv) and, where tree_k is given, to the call's own
+ * rows j that n sees: bit j of mask row n (medusa_tree_build's mask), or j <= n without a mask.
+ *   o = sum_j p_j v_j,  p = softmax(scale q . k_j)
+ * One row (n1 = 1) is plain decoding: tree_k, tree_v are that token's keys/values, or NULL when
+ * it has been appended already.  A row that sees nothing gives zeros.  Slots from len[b] on
+ * may hold anything.
+ *   q: [B * n1] rows of Hq heads, element strides q_row, q_head; o: as q, strides o_row, o_head
+ *   tree_k, tree_v: [B][n1][Hkv][dh]; q, o, tree_k, tree_v all of dtype (MEDUSA_F32 or
+ *   MEDUSA_BF16), 16-byte aligned with strides of whole 16 bytes
+ * Scores, softmax statistics and sums are 32 bits wide.  With MEDUSA_F32 the products keep
+ * 22 bits of queries and probabilities, with MEDUSA_BF16 the queries are exact and the
+ * probabilities keep 11 bits. */
+typedef struct {
+  const void* q;
+  void* o;
+  int dtype;
+  int n1;                               /* 1..max_nodes */
+  long long q_row, q_head, o_row, o_head;
+  const void* tree_k;
+  const void* tree_v;
+  const uint32_t* mask;                 /* device [n1][8] or NULL */
+  float scale;                          /* 0: 1/sqrt(dh) */
+  float k_scale, v_scale;
+} medusa_kv4_query;
+medusa_status medusa_kv4_attention(const medusa_cache* cache, const medusa_kv* kv,
+                                   const medusa_kv4_query* query, void* workspace,
+                                   size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -16,10 +16,13 @@ LIB_PATH = os.path.join(_HERE, "libmedusa.so")
 
 MEDUSA_OK, MEDUSA_ERR_INVALID, MEDUSA_ERR_UNSUPPORTED = 0, -1, -2
 MEDUSA_ERR_CUDA, MEDUSA_ERR_DEVICE, MEDUSA_ERR_WORKSPACE = -3, -4, -6
-F32, BF16 = 0, 1
+F32, BF16, KV4 = 0, 1, 2
 GREEDY, TYPICAL, REJECT = 0, 1, 2
 MAX_HEADS, MAX_TOPS, MAX_NODES = 8, 16, 256
 FLAG_TOKEN_RANGE, FLAG_KV_CAPACITY, FLAG_PAGE_RANGE, FLAG_NONFINITE, FLAG_TIMEOUT = 1, 2, 4, 8, 16
+FLAG_POS_RANGE, FLAG_ROW_RANGE = 32, 64
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "banded": 2, "ramp": 3}
 STATUS_NAMES = {0: "OK", -1: "INVALID", -2: "UNSUPPORTED", -3: "CUDA", -4: "DEVICE", -6: "WORKSPACE"}
 
 
@@ -65,6 +68,44 @@ class KernelTime(C.Structure):
 class Outputs(C.Structure):
     _fields_ = [("out_tok", C.c_void_p), ("n_acc", C.c_void_p), ("path_nodes", C.c_void_p),
                 ("h_next", C.c_void_p), ("root_next", C.c_void_p)]
+
+
+class RopeDesc(C.Structure):
+    _fields_ = [("rot", C.c_int), ("layout", C.c_int), ("max_pos", C.c_int), ("scaling", C.c_int),
+                ("base", C.c_double), ("factor", C.c_double), ("orig_pos", C.c_double),
+                ("low", C.c_double), ("high", C.c_double), ("attn", C.c_double)]
+
+
+class RopeRows(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("y", C.c_void_p), ("heads", C.c_int), ("x_row", C.c_longlong),
+                ("x_head", C.c_longlong), ("y_row", C.c_longlong), ("y_head", C.c_longlong)]
+
+
+class CacheDims(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("B", "Hq", "Hkv", "dh", "format", "capacity", "page_size",
+                                       "num_pages", "max_nodes")]
+
+
+class KVRows(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("dtype", C.c_int), ("k_row", C.c_longlong),
+                ("k_head", C.c_longlong), ("v_row", C.c_longlong), ("v_head", C.c_longlong),
+                ("rows", C.c_int), ("start", C.c_void_p), ("per_seq", C.c_int), ("count", C.c_void_p),
+                ("index", C.c_void_p), ("index_rows", C.c_int), ("pos", C.c_void_p)]
+
+
+class KVPlaces(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("dtype", C.c_int), ("k_row", C.c_longlong),
+                ("k_head", C.c_longlong), ("v_row", C.c_longlong), ("v_head", C.c_longlong),
+                ("rows", C.c_int), ("start", C.c_void_p), ("per_seq", C.c_int), ("count", C.c_void_p),
+                ("first", C.c_void_p)]
+
+
+class KV4Query(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("o", C.c_void_p), ("dtype", C.c_int), ("n1", C.c_int),
+                ("q_row", C.c_longlong), ("q_head", C.c_longlong), ("o_row", C.c_longlong),
+                ("o_head", C.c_longlong), ("tree_k", C.c_void_p), ("tree_v", C.c_void_p),
+                ("mask", C.c_void_p), ("scale", C.c_float), ("k_scale", C.c_float),
+                ("v_scale", C.c_float)]
 
 
 _lib = None
@@ -116,6 +157,18 @@ def lib():
         "medusa_loop_steps": (I, [P, P, C.POINTER(C.c_longlong)]),
         "medusa_loop_destroy": (None, [P]),
         "medusa_plan_expire_wait_once": (I, [P, C.c_ulonglong]),
+        "medusa_rope_create": (I, [C.POINTER(RopeDesc), C.POINTER(P)]),
+        "medusa_rope_destroy": (None, [P]),
+        "medusa_rope_get_status": (I, [P, P, C.POINTER(C.c_uint32)]),
+        "medusa_rope_apply": (I, [P, I, I, I, P, C.POINTER(RopeRows), I, I, P]),
+        "medusa_cache_create": (I, [C.POINTER(CacheDims), C.POINTER(P)]),
+        "medusa_cache_destroy": (None, [P]),
+        "medusa_cache_pool_bytes": (SZ, [P]),
+        "medusa_cache_workspace_size": (SZ, [P]),
+        "medusa_cache_get_status": (I, [P, P, C.POINTER(C.c_uint32)]),
+        "medusa_kv_append": (I, [P, C.POINTER(KV), C.POINTER(KVRows), P, C.c_float, C.c_float, P]),
+        "medusa_kv_read": (I, [P, C.POINTER(KV), C.POINTER(KVPlaces), C.c_float, C.c_float, P]),
+        "medusa_kv4_attention": (I, [P, C.POINTER(KV), C.POINTER(KV4Query), P, SZ, P]),
     }
     for name, (res, args) in sigs.items():
         f = getattr(L, name)
@@ -392,3 +445,175 @@ class Loop:
         except Exception:
             pass
 
+
+
+# ------------------------------------------------------------------ rotary positions, KV caches
+def _status(fn, handle, stream):
+    flags = C.c_uint32(0)
+    code = getattr(lib(), fn)(handle, _stream(stream), C.byref(flags))
+    if code not in (MEDUSA_OK, MEDUSA_ERR_DEVICE):
+        raise MedusaError(fn, code)
+    return flags.value
+
+
+_DTYPES = {}
+
+
+def _dtype(*tensors):
+    """F32 or BF16, the same for every tensor given (None: none)."""
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: F32, torch.bfloat16: BF16})
+    t = _DTYPES.get(tensors[0].dtype)
+    if t is None or any(x is not None and x.dtype != tensors[0].dtype for x in tensors[1:]):
+        raise TypeError("float32 or bfloat16 tensors of one dtype are needed: "
+                        + ", ".join(str(x.dtype) for x in tensors if x is not None))
+    return t
+
+
+def _ints(what, t, n):
+    """Address of an int32 tensor of at least n entries in order, or None."""
+    if t is None:
+        return None
+    if t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{what}: a contiguous int32 tensor of at least {n} entries is needed")
+    return t.data_ptr()
+
+
+def _rows(what, x, rows, heads, dh):
+    """(row, head) strides of [rows][heads][dh] whose elements lie together."""
+    if x.dim() != 3 or x.shape[0] < rows or x.shape[1] != heads or x.shape[2] != dh or \
+            (x.stride(2) != 1 and dh > 1):
+        raise ValueError(f"{what}: [{rows}][{heads}][{dh}] with elements in order is needed, got "
+                         f"shape {tuple(x.shape)}, strides {x.stride()}")
+    return x.stride(0), x.stride(1)
+
+
+class Rope:
+    """Owns a medusa_rope: the cosine/sine table of one rotation, on the current device."""
+
+    def __init__(self, rot, max_pos, layout="half", base=10000.0, scaling="plain", factor=1.0,
+                 orig_pos=0, low=1.0, high=32.0, attn=1.0):
+        self.desc = RopeDesc(rot, ROPE_LAYOUTS[layout], max_pos, ROPE_SCALINGS[scaling], base, factor,
+                             orig_pos, low, high, attn)
+        out = P()
+        _check("medusa_rope_create", lib().medusa_rope_create(C.byref(self.desc), C.byref(out)))
+        self.handle = out
+
+    def status(self, stream=None):
+        return _status("medusa_rope_get_status", self.handle, stream)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            lib().medusa_rope_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def rope_apply(rope, pos, parts, inverse=False, stream=None):
+    """medusa_rope_apply: `parts` holds (x, y) pairs of [rows][heads][dh] tensors (any strides
+    between rows and heads); y may be x."""
+    rows, dh = pos.numel(), parts[0][0].shape[2]
+    dtype = _dtype(*(t for p in parts for t in p))
+    arr = (RopeRows * len(parts))()
+    for a, (x, y) in zip(arr, parts):
+        a.heads = x.shape[1]
+        a.x_row, a.x_head = _rows("x", x, rows, a.heads, dh)
+        a.y_row, a.y_head = _rows("y", y, rows, a.heads, dh)
+        a.x, a.y = x.data_ptr(), y.data_ptr()
+    _check("medusa_rope_apply",
+           lib().medusa_rope_apply(rope.handle, dtype, dh, rows, _ints("pos", pos, rows), arr,
+                                   len(parts), int(inverse), _stream(stream)))
+
+
+class Cache:
+    """Owns a medusa_cache: the sizes and format of a KV cache whose pools the caller holds."""
+
+    def __init__(self, B, Hq, Hkv, dh, format, capacity, page_size=0, num_pages=0, max_nodes=1):
+        self.dims = CacheDims(B, Hq, Hkv, dh, format, capacity, page_size, num_pages, max_nodes)
+        out = P()
+        _check("medusa_cache_create", lib().medusa_cache_create(C.byref(self.dims), C.byref(out)))
+        self.handle = out
+        self.B, self.Hq, self.Hkv, self.dh, self.format = B, Hq, Hkv, dh, format
+        self.pool_bytes = lib().medusa_cache_pool_bytes(out)
+        self.workspace_size = lib().medusa_cache_workspace_size(out)
+
+    def status(self, stream=None):
+        return _status("medusa_cache_get_status", self.handle, stream)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            lib().medusa_cache_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _items(cache, k, v, start, rows, per_seq, count):
+    """rows, start, per_seq and count of medusa_kv_rows / medusa_kv_places."""
+    if start is not None:
+        return k.shape[0] if rows is None else rows, _ints("start", start, cache.B + 1), 0, None
+    per_seq = (k.shape[0] if rows is None else rows) // cache.B if per_seq is None else per_seq
+    return cache.B * per_seq, None, per_seq, _ints("count", count, cache.B)
+
+
+def kv_append(cache, kv, k, v, start=None, per_seq=None, count=None, index=None, index_rows=0,
+              pos=None, rope=None, k_scale=1.0, v_scale=1.0, rows=None, stream=None):
+    """medusa_kv_append: k, v [rows][Hkv][dh] (any strides between rows and heads).  Packed
+    batches give `start`, padded ones `per_seq` (default: an equal share of the rows) and
+    `count`; with `index` the item places are index's and k, v the rows they name."""
+    n, start, per_seq, count = _items(cache, k if index is None else index, v, start, rows, per_seq, count)
+    need = n if index is None else cache.B * index_rows
+    kr, kh = _rows("k", k, need, cache.Hkv, cache.dh)
+    vr, vh = _rows("v", v, need, cache.Hkv, cache.dh)
+    r = KVRows(k.data_ptr(), v.data_ptr(), _dtype(k, v), kr, kh, vr, vh, n, start, per_seq, count,
+               _ints("index", index, n), index_rows, _ints("pos", pos, n))
+    _check("medusa_kv_append",
+           lib().medusa_kv_append(cache.handle, kv, r, rope.handle if rope is not None else None,
+                                  k_scale, v_scale, _stream(stream)))
+
+
+def kv_read(cache, kv, k, v, start=None, per_seq=None, count=None, first=None, k_scale=1.0,
+            v_scale=1.0, rows=None, stream=None):
+    """medusa_kv_read into k, v [rows][Hkv][dh]; batches as in kv_append."""
+    n, start, per_seq, count = _items(cache, k, v, start, rows, per_seq, count)
+    kr, kh = _rows("k", k, n, cache.Hkv, cache.dh)
+    vr, vh = _rows("v", v, n, cache.Hkv, cache.dh)
+    r = KVPlaces(k.data_ptr(), v.data_ptr(), _dtype(k, v), kr, kh, vr, vh, n, start, per_seq, count,
+                 _ints("first", first, cache.B))
+    _check("medusa_kv_read",
+           lib().medusa_kv_read(cache.handle, kv, r, k_scale, v_scale, _stream(stream)))
+
+
+def kv4_attention(cache, kv, q, o, ws, tree_k=None, tree_v=None, mask=None, scale=0.0, k_scale=1.0,
+                  v_scale=1.0, stream=None):
+    """medusa_kv4_attention: q, o [B][n1][Hq][dh] (rows evenly spaced), tree_k, tree_v
+    [B][n1][Hkv][dh] contiguous or None, mask int32 [n1][8] or None."""
+    B, n1 = q.shape[0], q.shape[1]
+    if B != cache.B or o.shape != q.shape:
+        raise ValueError(f"q, o: [{cache.B}][n1][Hq][dh] is needed, got {tuple(q.shape)}, {tuple(o.shape)}")
+    if (B > 1 and n1 > 1) and (q.stride(0) != n1 * q.stride(1) or o.stride(0) != n1 * o.stride(1)):
+        raise ValueError("q, o: the B * n1 rows have to be evenly spaced")
+    at = 0 if n1 == 1 else 1
+    for x in (q, o):
+        if x.shape[2] != cache.Hq or x.shape[3] != cache.dh or x.stride(3) != 1:
+            raise ValueError(f"q, o: [{cache.B}][n1][{cache.Hq}][{cache.dh}] with elements in order is needed")
+    dtype = _dtype(q, o, tree_k, tree_v)
+    for t in (tree_k, tree_v):
+        if t is not None and (tuple(t.shape) != (B, n1, cache.Hkv, cache.dh) or not t.is_contiguous()):
+            raise ValueError(f"tree_k, tree_v: contiguous [{B}][{n1}][{cache.Hkv}][{cache.dh}] is needed")
+    a = KV4Query(q.data_ptr(), o.data_ptr(), dtype, n1, q.stride(at), q.stride(2), o.stride(at),
+                 o.stride(2), ptr(tree_k), ptr(tree_v), _ints("mask", mask, 8 * n1), scale, k_scale,
+                 v_scale)
+    _check("medusa_kv4_attention",
+           lib().medusa_kv4_attention(cache.handle, kv, a, ptr(ws), ws.numel() * ws.element_size(),
+                                      _stream(stream)))

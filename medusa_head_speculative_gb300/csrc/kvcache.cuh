@@ -1,0 +1,167 @@
+// Device helpers of the KV-cache kernels: which sequence an item belongs to, where a slot of
+// a cache lies, groups of 16 elements, and the 4-bit format (described in include/medusa.h).
+#pragma once
+#include <cuda_fp16.h>
+#include <cuda_fp4.h>
+#include <cuda_fp8.h>
+
+#include "cache.h"
+#include "common.cuh"
+
+namespace medusa {
+
+constexpr int KV4_SLOTS = 16;                           // slots of a block
+__host__ __device__ constexpr int kv4_block(int dh) { return 9 * dh; }   // its bytes
+
+// Sequence (< 0: none) and place within it of item i.
+__device__ __forceinline__ int2 item_of(const ItemMap& m, int B, int i) {
+  if (!m.start) {
+    const int b = i / m.per_seq, j = i - b * m.per_seq;
+    return make_int2(!m.count || j < m.count[b] ? b : -1, j);
+  }
+  int lo = 0, hi = B;                                   // the last b with start[b] <= i
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (m.start[mid] <= i) lo = mid;
+    else hi = mid;
+  }
+  const int s0 = m.start[lo];
+  return make_int2(i >= s0 && i < m.start[lo + 1] ? lo : -1, i - s0);
+}
+__device__ __forceinline__ int item_count(const ItemMap& m, int b) {
+  const int n = m.start ? m.start[b + 1] - m.start[b] : (m.count ? min(m.count[b], m.per_seq) : m.per_seq);
+  return max(n, 0);
+}
+
+// A length as the calls take it: outside 0..capacity the nearer end.
+__device__ __forceinline__ int clamp_len(const CacheView& c, int len) { return min(max(len, 0), c.capacity); }
+
+// Unit (page, or the sequence's whole stretch of a contiguous cache) and slot within it of
+// slot t of sequence b; false when the page is outside the pool.
+__device__ __forceinline__ bool unit_of(const CacheView& c, int b, int t, long& unit, int& in) {
+  if (!c.page_table) {
+    unit = b;
+    in = t;
+    return true;
+  }
+  const int p = t / c.page_size;
+  const int page = c.page_table[(long)b * c.pages_per_seq + p];
+  unit = page;
+  in = t - p * c.page_size;
+  return page >= 0 && page < c.num_pages;
+}
+// First element of head h in a plain cache, first byte of its block in a 4-bit one.
+__device__ __forceinline__ long plain_offset(const CacheView& c, long unit, int in, int h) {
+  const int per = c.page_table ? c.page_size : c.capacity;
+  return ((unit * per + in) * c.Hkv + h) * c.dh;
+}
+__device__ __forceinline__ long kv4_offset(const CacheView& c, long unit, int in, int h) {
+  const int per = (c.page_table ? c.page_size : c.capacity) / KV4_SLOTS;
+  return ((unit * c.Hkv + h) * per + in / KV4_SLOTS) * kv4_block(c.dh);
+}
+
+// 16 consecutive elements, in 16-byte units when vec.
+__device__ __forceinline__ void load16(const bf16* p, bool vec, float (&f)[16]) {
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float t[8];
+      unpack16(reinterpret_cast<const uint4*>(p)[i], t);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[8 * i + e] = t[e];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) f[e] = to_f32(p[e]);
+  }
+}
+__device__ __forceinline__ void load16(const float* p, bool vec, float (&f)[16]) {
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 t = reinterpret_cast<const float4*>(p)[i];
+      f[4 * i] = t.x; f[4 * i + 1] = t.y; f[4 * i + 2] = t.z; f[4 * i + 3] = t.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) f[e] = p[e];
+  }
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+__device__ __forceinline__ void store16(bf16* p, bool vec, const float (&f)[16]) {
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      reinterpret_cast<uint4*>(p)[i] = make_uint4(pack2(f[8 * i], f[8 * i + 1]), pack2(f[8 * i + 2], f[8 * i + 3]),
+                                                  pack2(f[8 * i + 4], f[8 * i + 5]), pack2(f[8 * i + 6], f[8 * i + 7]));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) p[e] = from_f32<bf16>(f[e]);
+  }
+}
+__device__ __forceinline__ void store16(float* p, bool vec, const float (&f)[16]) {
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      reinterpret_cast<float4*>(p)[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) p[e] = f[e];
+  }
+}
+
+// 16 elements -> 8 bytes of e2m1 pairs and one e4m3 scale.  The scale is the nearest e4m3 to
+// max|x| / (6 g), each code the nearest to x / (g s): true (IEEE) quotients, because a bf16
+// element divided by a 4-bit scale is often exactly half way between two codes, and a
+// quotient off by one unit in the last place would send it the wrong way.
+__device__ __forceinline__ bool kv4_encode(const float (&x)[16], float g, uint2& codes, uint8_t& scale) {
+  float top = 0.f;
+  bool finite = true;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const float a = fabsf(x[e]);
+    finite = finite && a < INFINITY;
+    top = fmaxf(top, a);
+  }
+  if (!finite) {                            // the whole group reads back as NaN
+    codes = make_uint2(0x22222222u, 0x22222222u);
+    scale = 0x7f;
+    return false;
+  }
+  scale = __nv_cvt_float_to_fp8(__fdiv_rn(top, 6.f * g), __NV_SATFINITE, __NV_E4M3);
+  const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(scale, __NV_E4M3))) * g;
+  uint32_t w[2] = {0u, 0u};
+  if (s > 0.f) {
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      const float2 y = make_float2(__fdiv_rn(x[e], s), __fdiv_rn(x[e + 1], s));
+      w[e >> 3] |= (uint32_t)__nv_cvt_float2_to_fp4x2(y, __NV_E2M1, cudaRoundNearest) << (4 * (e & 7));
+    }
+  }
+  codes = make_uint2(w[0], w[1]);
+  return true;
+}
+
+// Two e2m1 codes (one byte) as halves, exactly.
+__device__ __forceinline__ __half2 kv4_pair(uint32_t byte) {
+  return __half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)byte, __NV_E2M1));
+}
+// An e4m3 scale as a half, exactly (NaN for a group that held none of the numbers).
+__device__ __forceinline__ __half kv4_scale(uint8_t s) { return __half(__nv_cvt_fp8_to_halfraw(s, __NV_E4M3)); }
+
+// What 16 elements of a block stand for: e2m1 * e4m3 is exact in a half (6 bits, 2^-10..2688).
+__device__ __forceinline__ void kv4_decode(uint2 codes, uint8_t scale, float g, float (&f)[16]) {
+  const __half2 s2 = __half2half2(kv4_scale(scale));
+  const uint32_t w[2] = {codes.x, codes.y};
+#pragma unroll
+  for (int e = 0; e < 16; e += 2) {
+    const float2 v = __half22float2(__hmul2(kv4_pair((w[e >> 3] >> (4 * (e & 7))) & 0xffu), s2));
+    f[e] = v.x * g;
+    f[e + 1] = v.y * g;
+  }
+}
+
+}  // namespace medusa

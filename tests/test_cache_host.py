@@ -1,0 +1,85 @@
+"""Rotary and cache handles: what creation refuses, and the 4-bit reference's own pins (CPU)."""
+import ctypes as C
+
+import numpy as np
+import pytest
+
+import kv4_ref as R
+from harness import ensure_built
+from medusa_head_speculative_gb300 import binding as Bnd
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    ensure_built()
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(rot=0), -1), (dict(rot=7), -1), (dict(max_pos=0), -1), (dict(base=1.0), -1),
+    (dict(base=float("nan")), -1), (dict(scaling="linear", factor=0.0), -1),
+    (dict(scaling="banded", orig_pos=0, factor=2.0), -1),
+    (dict(scaling="ramp", orig_pos=64, factor=2.0, low=4.0, high=4.0), -1),
+    (dict(attn=-1.0), -1), (dict(attn=float("inf")), -1), (dict(rot=2048), -2),
+])
+def test_rope_creation_refuses(bad, code):
+    kw = dict(rot=64, max_pos=16)
+    kw.update(bad)
+    with pytest.raises(Bnd.MedusaError) as e:
+        Bnd.Rope(**kw)
+    assert e.value.code == code
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(B=0), -1), (dict(Hq=3), -1), (dict(Hkv=0), -1), (dict(format=3), -1), (dict(format=-1), -1),
+    (dict(capacity=0), -1), (dict(page_size=-1), -1), (dict(page_size=16, num_pages=0), -1),
+    (dict(page_size=16, num_pages=4, capacity=40), -1), (dict(max_nodes=0), -1),
+    (dict(max_nodes=257), -2), (dict(dh=48), -2), (dict(dh=256), -2), (dict(capacity=40), -2),
+    (dict(page_size=8, num_pages=8, capacity=64), -2),
+])
+def test_cache_creation_refuses(bad, code):
+    kw = dict(B=2, Hq=4, Hkv=2, dh=64, format=Bnd.KV4, capacity=64)
+    kw.update(bad)
+    with pytest.raises(Bnd.MedusaError) as e:
+        Bnd.Cache(**kw)
+    assert e.value.code == code
+
+
+def test_calls_without_a_handle_are_refused():
+    L = Bnd.lib()
+    kv, rows, places, q = Bnd.KV(), Bnd.KVRows(), Bnd.KVPlaces(), Bnd.KV4Query()
+    part = (Bnd.RopeRows * 1)()
+    assert L.medusa_rope_apply(None, 0, 64, 1, None, part, 1, 0, None) == -1
+    assert L.medusa_kv_append(None, kv, rows, None, 1.0, 1.0, None) == -1
+    assert L.medusa_kv_read(None, kv, places, 1.0, 1.0, None) == -1
+    assert L.medusa_kv4_attention(None, kv, q, None, 0, None) == -1
+    assert L.medusa_rope_create(None, None) == -1 and L.medusa_cache_create(None, None) == -1
+    out = C.c_void_p()
+    assert L.medusa_rope_create(None, C.byref(out)) == -1 and not out
+    assert L.medusa_cache_create(None, C.byref(out)) == -1 and not out
+    assert L.medusa_cache_pool_bytes(None) == 0 and L.medusa_cache_workspace_size(None) == 0
+    L.medusa_rope_destroy(None)
+    L.medusa_cache_destroy(None)
+
+
+def test_reference_formats():
+    assert R.E4M3[0x7e] == 448 and R.E4M3[1] == 2.0 ** -9 and np.isnan(R.E4M3[0x7f])
+    for i in range(126):                      # every e4m3 and every midpoint
+        assert R.e4m3_nearest(R.E4M3[i]) == i
+        assert R.e4m3_nearest((R.E4M3[i] + R.E4M3[i + 1]) / 2) % 2 == 0
+    assert list(R.e2m1_nearest(np.array([.25, .75, 1.25, 1.75, 2.5, 3.5, 5, 9]))) == [0, 2, 2, 4, 4, 6, 6, 7]
+    x = np.random.default_rng(0).standard_normal((5, 3, 64))
+    codes, scales = R.encode(x, 0.5)
+    y = R.decode(codes, scales, 0.5)
+    # the widest gap between codes is 2, and a scale rounded down clips less than that
+    assert (np.abs(y - x) <= np.repeat(R.E4M3[scales], 16, -1) * 0.5).all()
+
+
+def test_reference_rotation_depends_on_distance_only():
+    r = np.random.default_rng(1)
+    q, k = r.standard_normal((1, 1, 32)), r.standard_normal((1, 1, 32))
+    for layout in ("half", "interleaved"):
+        a = (R.rope(q, [9], 32, layout) * R.rope(k, [4], 32, layout)).sum()
+        b = (R.rope(q, [105], 32, layout) * R.rope(k, [100], 32, layout)).sum()
+        assert abs(a - b) < 1e-12
+        back = R.rope(R.rope(q, [77], 24, layout), [77], 24, layout, inverse=True)
+        assert np.abs(back - q).max() < 1e-14
