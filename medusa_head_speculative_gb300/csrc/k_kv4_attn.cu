@@ -3,7 +3,7 @@
 // include/medusa.h), for few query rows a key/value head: single tokens and small trees.
 //
 // Rows: the n1 nodes x G query heads that share a key/value head, 16 at a time (a "row
-// block").  Work: every (sequence, head, row block) has ceil(len / 64) chunks of 64 cached
+// block").  Work: every (sequence, head, row block) has ceil(len / 128) chunks of 128 cached
 // slots; all chunks of the call in that order are dealt out evenly, CTA i of n taking the
 // chunks [W i / n, W (i + 1) / n), n at most W, whatever sequences they belong to (the lengths are read on
 // the GPU).  A CTA that leaves a (sequence, head, row block) writes its unnormalised partial
@@ -11,8 +11,8 @@
 // are never shared, and one triple's slots lie together.  kv4_combine_kernel joins them, adds
 // the call's own tree rows and rounds once.
 //
-// In a CTA each of four warps takes 16 slots of a chunk: one block of the format, which lies
-// in one piece, so each warp keeps its own ring of blocks filled by the copy engine.  With
+// In a CTA each of four warps takes 32 slots of a chunk: two blocks of the format, each in one
+// piece, so each warp keeps its own ring of blocks filled by the copy engine.  With
 // few rows a 128-row tcgen05 tile would be mostly padding; the products here go through
 // warp-wide 16 x 8 x 16 MMAs whose operands are decoded straight into registers, never
 // written to shared memory: S = Q K^T with K as the column operand (a lane's 16 bytes are 32
@@ -30,7 +30,9 @@
 
 namespace medusa {
 
-constexpr int KD_WARPS = 4, KD_ROWS = 16, KD_CHUNK = KD_WARPS * KV4_SLOTS, KD_STAGES = 4, KD_CTAS = 3;
+constexpr int KD_WARPS = 4, KD_ROWS = 16, KD_STAGES = 3, KD_CTAS = 3;
+constexpr int KD_KEYS = 2 * KV4_SLOTS;              // slots a warp takes at a time: two blocks
+constexpr int KD_CHUNK = KD_WARPS * KD_KEYS;
 // P is taken against a reference 2^KD_TOP below a half's range: a row's reference starts KD_BACK
 // (log2) below its running maximum and is raised, O rescaled, only once a score passes it by
 // KD_TOP.  Small probabilities then stay normal halves down to 2^(-14 - back) of the largest; with
@@ -161,14 +163,14 @@ __global__ void __launch_bounds__(KD_WARPS * 32, KD_CTAS) kv4_rows_kernel(const 
   constexpr int QW = STEPS * 128 * (SPLIT ? 2 : 1);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t bars[KD_WARPS][KD_STAGES];
-  __shared__ uint32_t qf[QW];
+  __shared__ __align__(16) uint32_t qf[QW];
   __shared__ float rs[KD_ROWS];
   __shared__ float2 ml[KD_WARPS][KD_ROWS];
   const CacheView& c = w.a.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
   const int per = c.Hkv * w.nrb;
-  uint8_t* ring = smem + warp * KD_STAGES * 2 * BLK;
-  float* merge = reinterpret_cast<float*>(smem + KD_WARPS * KD_STAGES * 2 * BLK);   // [warps][rb][DH + 4]
+  uint8_t* ring = smem + warp * KD_STAGES * 4 * BLK;
+  float* merge = reinterpret_cast<float*>(smem + KD_WARPS * KD_STAGES * 4 * BLK);   // [warps][rb][DH + 4]
   constexpr int ML = DH + 4;
   const long W = kd_total(c, per);
   // every CTA that takes part has at least one chunk, so a triple's slots have no gaps
@@ -182,50 +184,52 @@ __global__ void __launch_bounds__(KD_WARPS * 32, KD_CTAS) kv4_rows_kernel(const 
   __syncwarp();
   const uint64_t pol = policy_evict_first();
 
-  // ---- this warp's blocks, in order: the copies run up to KD_STAGES ahead
+  // ---- this warp's blocks, in order: the copies run up to KD_STAGES ahead.  Lane 2 i + x knows
+  // where block x of the warp's chunk win0 + i lies (head 0's) and issues its copies.
   KdCursor pc = kd_seek(c, per, w0), k = pc;
-  long pw = w0;                            // next chunk to copy
+  int left = (int)(w1 - w0);               // chunks to copy
   int issued = 0, taken = 0, drain = 0;
-  int win_b = -1, win0 = 0, my_page = 0;   // page ids of 32 of the warp's blocks from win0 on
+  int win_b = -1, win0 = 0, plen = 0, head = pc.q / w.nrb;
+  long my_blk = 0;
+  const int upp = (c.page_table ? c.page_size : c.capacity) / KV4_SLOTS;
   bool dead = false;
   auto copy_next = [&]() {
-    // skips chunks whose part of 16 slots lies past the length
-    while (pw < w1) {
-      const int t0 = pc.j * KD_CHUNK + warp * KV4_SLOTS;
-      const bool any = t0 < clamp_len(c, c.len[pc.b]);
-      if (any) {
-        long blk;
-        const int g = pc.q / w.nrb;
-        if (c.page_table) {
-          if (win_b != pc.b || pc.j < win0 || pc.j >= win0 + 32) {
-            win_b = pc.b;
-            win0 = pc.j;
-            const int t = t0 + lane * KD_CHUNK;
-            my_page = 0;
-            if (t < clamp_len(c, c.len[pc.b])) {
-              my_page = c.page_table[(long)pc.b * c.pages_per_seq + t / c.page_size];
-              if (my_page < 0 || my_page >= c.num_pages) {
-                set_flag(c.status, MEDUSA_FLAG_PAGE_RANGE);
-                my_page = 0;
-              }
-            }
+    // skips chunks whose part of 32 slots lies past the length
+    while (left > 0) {
+      if (win_b != pc.b || pc.j < win0 || pc.j >= win0 + 16) {
+        plen = clamp_len(c, c.len[pc.b]);
+        win_b = pc.b;
+        win0 = pc.j;
+        const int t = (win0 + (lane >> 1)) * KD_CHUNK + warp * KD_KEYS + (lane & 1) * KV4_SLOTS;
+        if (t < plen) {
+          long unit;
+          int in;
+          if (!unit_of(c, pc.b, t, unit, in)) {
+            set_flag(c.status, MEDUSA_FLAG_PAGE_RANGE);
+            unit = 0;
           }
-          const long page = __shfl_sync(0xffffffffu, my_page, pc.j - win0);
-          blk = (page * c.Hkv + g) * (c.page_size / KV4_SLOTS) + t0 % c.page_size / KV4_SLOTS;
-        } else {
-          blk = ((long)pc.b * c.Hkv + g) * (c.capacity / KV4_SLOTS) + t0 / KV4_SLOTS;
+          my_blk = unit * c.Hkv * upp + in / KV4_SLOTS;
         }
-        if (lane == 0) {
-          const int s = issued % KD_STAGES;
-          const uint32_t bar = smem_u32(&bars[warp][s]), dst = smem_u32(ring + s * 2 * BLK);
-          mbar_expect_tx(bar, 2 * BLK);
-          bulk_load(dst, static_cast<const uint8_t*>(c.k) + blk * BLK, BLK, bar, pol);
-          bulk_load(dst + BLK, static_cast<const uint8_t*>(c.v) + blk * BLK, BLK, bar, pol);
+      }
+      const int t0 = pc.j * KD_CHUNK + warp * KD_KEYS;
+      const bool any = t0 < plen;
+      if (any) {
+        const bool both = t0 + KV4_SLOTS < plen;
+        if ((lane >> 1) == pc.j - win0 && (both || !(lane & 1))) {
+          const int st = issued % KD_STAGES;
+          const uint32_t bar = smem_u32(&bars[warp][st]), dst = smem_u32(ring + st * 4 * BLK) + (lane & 1) * BLK;
+          const long off = (my_blk + (long)head * upp) * BLK;
+          if (!(lane & 1)) mbar_expect_tx(bar, both ? 4 * BLK : 2 * BLK);
+          bulk_load(dst, static_cast<const uint8_t*>(c.k) + off, BLK, bar, pol);
+          bulk_load(dst + 2 * BLK, static_cast<const uint8_t*>(c.v) + off, BLK, bar, pol);
         }
         ++issued;
       }
-      ++pw;
-      if (pw < w1) kd_next(c, per, pc);
+      if (--left > 0) {
+        const int q0 = pc.q, b0 = pc.b;
+        kd_next(c, per, pc);
+        if (pc.q != q0 || pc.b != b0) head = pc.q / w.nrb;
+      }
       if (any) return;
     }
   };
@@ -240,17 +244,13 @@ __global__ void __launch_bounds__(KD_WARPS * 32, KD_CTAS) kv4_rows_kernel(const 
     const int j0 = k.j;
     kd_load_q<T, DH, SPLIT>(w, b, g, rb, qf, rs);
     __syncthreads();
-    uint32_t qa[STEPS][4];
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s)
-      *reinterpret_cast<uint4*>(qa[s]) = *reinterpret_cast<const uint4*>(qf + (s * 32 + lane) * 4);
     const float rs0 = rs[g8], rs1 = rs[g8 + 8];
     float o[NT][4];
 #pragma unroll
     for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     for (int j = j0; j < j0 + (int)n; ++j) {
-      const int t0 = j * KD_CHUNK + warp * KV4_SLOTS;
+      const int t0 = j * KD_CHUNK + warp * KD_KEYS;
       if (t0 >= len) break;
       const int st = taken % KD_STAGES;
       if (!dead && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars[warp][st]), (taken / KD_STAGES) & 1, TC_TIMEOUT_NS))) {
@@ -259,50 +259,66 @@ __global__ void __launch_bounds__(KD_WARPS * 32, KD_CTAS) kv4_rows_kernel(const 
       }
       ++taken;
       if (dead) continue;
-      const uint8_t* kb = ring + st * 2 * BLK;
-      const uint8_t* vb = kb + BLK;
-      // ---- S = Q K^T for 16 keys
-      float s[2][4];
+      const uint8_t* kb = ring + st * 4 * BLK;
+      const uint8_t* vb = kb + 2 * BLK;
+      // ---- S = Q K^T for 32 keys, 8 a tile: four independent sums, each operand of Q read once
+      float s[4][4];
+      uint32_t kw[4][DH / 32];
+      __half2 s2[4];                       // the lane's dh/4 elements have one scale (dh 128: two)
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
+      for (int nt = 0; nt < 4; ++nt) {
         s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-        const int key = nt * 8 + g8;
-        uint32_t kw[DH / 32];
-        const uint8_t* src = kb + key * (DH / 2) + t4 * (DH / 8);
-        if (DH == 128) *reinterpret_cast<uint4*>(kw) = *reinterpret_cast<const uint4*>(src);
-        else if (DH == 64) *reinterpret_cast<uint2*>(kw) = *reinterpret_cast<const uint2*>(src);
-        else kw[0] = *reinterpret_cast<const uint32_t*>(src);
-        const uint8_t* sc = kb + 8 * DH + key * (DH / 16);
+        const uint8_t* blk = kb + (nt >> 1) * BLK;
+        const int key = (nt & 1) * 8 + g8;
+        const uint8_t* src = blk + key * (DH / 2) + t4 * (DH / 8);
+        if (DH == 128) *reinterpret_cast<uint4*>(kw[nt]) = *reinterpret_cast<const uint4*>(src);
+        else if (DH == 64) *reinterpret_cast<uint2*>(kw[nt]) = *reinterpret_cast<const uint2*>(src);
+        else kw[nt][0] = *reinterpret_cast<const uint32_t*>(src);
+        const uint8_t* sc = blk + 8 * DH + key * (DH / 16) + t4 * DH / 64;
+        if (DH == 128) s2[nt] = kv4_scales(*reinterpret_cast<const uint16_t*>(sc));
+        else s2[nt] = __half2half2(kv4_scale(*sc));
+      }
 #pragma unroll
-        for (int x = 0; x < DH / 32; ++x) {
-          const __half2 s2 = __half2half2(kv4_scale(sc[(t4 * (DH / 4) + 8 * x) / 16]));
+      for (int x = 0; x < DH / 32; ++x) {
+        __half2 y[4][4];
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const uint32_t b0 = h2u(__hmul2(kv4_pair((kw[x] >> (16 * y)) & 0xffu), s2));
-            const uint32_t b1 = h2u(__hmul2(kv4_pair((kw[x] >> (16 * y + 8)) & 0xffu), s2));
-            mma16816(s[nt], qa[2 * x + y], b0, b1);
-            if (SPLIT) {
-              uint32_t ql[4];
-              *reinterpret_cast<uint4*>(ql) =
-                  *reinterpret_cast<const uint4*>(qf + STEPS * 128 + ((2 * x + y) * 32 + lane) * 4);
-              mma16816(s[nt], ql, b0, b1);
-            }
+        for (int nt = 0; nt < 4; ++nt) {
+          kv4_pairs(kw[nt][x], y[nt]);
+          const __half2 sc = x < 2 ? __low2half2(s2[nt]) : __high2half2(s2[nt]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[nt][e] = __hmul2(y[nt][e], sc);
+        }
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const uint32_t* qp = qf + ((2 * x + z) * 32 + lane) * 4;
+          uint32_t qa[4];
+          *reinterpret_cast<uint4*>(qa) = *reinterpret_cast<const uint4*>(qp);
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt) mma16816(s[nt], qa, h2u(y[nt][2 * z]), h2u(y[nt][2 * z + 1]));
+          if (SPLIT) {
+            *reinterpret_cast<uint4*>(qa) = *reinterpret_cast<const uint4*>(qp + STEPS * 128);
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt) mma16816(s[nt], qa, h2u(y[nt][2 * z]), h2u(y[nt][2 * z + 1]));
           }
         }
       }
       // ---- softmax: a lane has rows g8 (0, 1) and g8 + 8 (2, 3), keys 2 t4 + {0, 1} of each tile
-      const bool tail = t0 + KV4_SLOTS > len;
+      const bool tail = t0 + KD_KEYS > len;
+      if (tail) {
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
+        for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const bool in = !tail || t0 + nt * 8 + 2 * t4 + e < len;
-          s[nt][e] = in ? s[nt][e] * rs0 : -INFINITY;
-          s[nt][2 + e] = in ? s[nt][2 + e] * rs1 : -INFINITY;
-        }
+          for (int e = 0; e < 4; ++e)
+            if (t0 + nt * 8 + 2 * t4 + (e & 1) >= len) s[nt][e] = -INFINITY;
       }
-      float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-      float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+      float x0 = fmaxf(s[0][0], s[0][1]), x1 = fmaxf(s[0][2], s[0][3]);
+#pragma unroll
+      for (int nt = 1; nt < 4; ++nt) {
+        x0 = fmaxf(x0, fmaxf(s[nt][0], s[nt][1]));
+        x1 = fmaxf(x1, fmaxf(s[nt][2], s[nt][3]));
+      }
+      x0 *= rs0;                             // the rows' factors are positive
+      x1 *= rs1;
       if (__any_sync(0xffffffffu, x0 > m0 + KD_TOP || x1 > m1 + KD_TOP)) {
 #pragma unroll
         for (int d = 1; d < 4; d <<= 1) {
@@ -321,50 +337,59 @@ __global__ void __launch_bounds__(KD_WARPS * 32, KD_CTAS) kv4_rows_kernel(const 
           o[i][2] *= f1; o[i][3] *= f1;
         }
       }
-      uint32_t pa[4], pl[4];
+      uint32_t pa[2][4], pl[2][4];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        const float p0 = ex2_approx(s[nt][0] - m0), p1 = ex2_approx(s[nt][1] - m0);
-        const float p2 = ex2_approx(s[nt][2] - m1), p3 = ex2_approx(s[nt][3] - m1);
+      for (int nt = 0; nt < 4; ++nt) {
+        const float p0 = ex2_approx(fmaf(s[nt][0], rs0, -m0)), p1 = ex2_approx(fmaf(s[nt][1], rs0, -m0));
+        const float p2 = ex2_approx(fmaf(s[nt][2], rs1, -m1)), p3 = ex2_approx(fmaf(s[nt][3], rs1, -m1));
         l0 += p0 + p1;
         l1 += p2 + p3;
         const __half2 h0 = __floats2half2_rn(p0, p1), h1 = __floats2half2_rn(p2, p3);
-        pa[2 * nt] = h2u(h0);
-        pa[2 * nt + 1] = h2u(h1);
+        pa[nt >> 1][2 * (nt & 1)] = h2u(h0);
+        pa[nt >> 1][2 * (nt & 1) + 1] = h2u(h1);
         if (SPLIT) {
           const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
-          pl[2 * nt] = half_pair(p0 - f0.x, p1 - f0.y);
-          pl[2 * nt + 1] = half_pair(p2 - f1.x, p3 - f1.y);
+          pl[nt >> 1][2 * (nt & 1)] = half_pair(p0 - f0.x, p1 - f0.y);
+          pl[nt >> 1][2 * (nt & 1) + 1] = half_pair(p2 - f1.x, p3 - f1.y);
         }
       }
-      // ---- O += P V: lane's keys 2 t4, + 1, + 8, + 9, elements g8 DH/8 + i
-      uint32_t vw[4][DH > 64 ? 2 : 1];
-      __half2 vs[2];
-      __half vh[4];
+      // ---- O += P V: lane's keys 2 t4, + 1, + 8, + 9 of each block, elements g8 DH/8 + i
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int key = 2 * t4 + (x & 1) + 8 * (x >> 1);
-        const uint8_t* src = vb + key * (DH / 2) + g8 * (DH / 16);
-        if (DH == 128) *reinterpret_cast<uint2*>(vw[x]) = *reinterpret_cast<const uint2*>(src);
-        else if (DH == 64) vw[x][0] = *reinterpret_cast<const uint32_t*>(src);
-        else vw[x][0] = *reinterpret_cast<const uint16_t*>(src);
-        vh[x] = kv4_scale(vb[8 * DH + key * (DH / 16) + g8 * DH / 128]);
-        if (tail && t0 + key >= len) vh[x] = __float2half(0.f);     // p is 0 there: keep 0 * NaN out
-      }
-      vs[0] = __halves2half2(vh[0], vh[1]);
-      vs[1] = __halves2half2(vh[2], vh[3]);
+      for (int hb = 0; hb < 2; ++hb) {
+        const uint8_t* blk = vb + hb * BLK;
+        uint32_t vw[4][DH > 64 ? 2 : 1];
+        __half vh[4];
 #pragma unroll
-      for (int i = 0; i < NT; i += 2) {
-        __half2 y[4];
+        for (int x = 0; x < 4; ++x) {
+          const int key = 2 * t4 + (x & 1) + 8 * (x >> 1);
+          const uint8_t* src = blk + key * (DH / 2) + g8 * (DH / 16);
+          if (DH == 128) *reinterpret_cast<uint2*>(vw[x]) = *reinterpret_cast<const uint2*>(src);
+          else if (DH == 64) vw[x][0] = *reinterpret_cast<const uint32_t*>(src);
+          else vw[x][0] = *reinterpret_cast<const uint16_t*>(src);
+          vh[x] = kv4_scale(blk[8 * DH + key * (DH / 16) + g8 * DH / 128]);
+          if (tail && t0 + hb * KV4_SLOTS + key >= len) vh[x] = __float2half(0.f);   // p is 0 there: keep 0 * NaN out
+        }
+        const __half2 v0 = __halves2half2(vh[0], vh[1]), v1 = __halves2half2(vh[2], vh[3]);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) y[x] = kv4_pair((vw[x][i / 8] >> (4 * (i & 7))) & 0xffu);
-        const uint32_t a0 = h2u(__hmul2(__lows2half2(y[0], y[1]), vs[0])), a1 = h2u(__hmul2(__lows2half2(y[2], y[3]), vs[1]));
-        const uint32_t c0 = h2u(__hmul2(__highs2half2(y[0], y[1]), vs[0])), c1 = h2u(__hmul2(__highs2half2(y[2], y[3]), vs[1]));
-        mma16816(o[i], pa, a0, a1);
-        mma16816(o[i + 1], pa, c0, c1);
-        if (SPLIT) {
-          mma16816(o[i], pl, a0, a1);
-          mma16816(o[i + 1], pl, c0, c1);
+        for (int x = 0; x < (DH > 64 ? 2 : 1); ++x) {
+          // nibbles of two keys side by side: bytes of the even elements, then of the odd ones
+          constexpr uint32_t LO = 0x0f0f0f0fu;
+          __half2 e0[4], e1[4], o0[4], o1[4];
+          kv4_pairs((vw[0][x] & LO) | ((vw[1][x] << 4) & ~LO), e0);
+          kv4_pairs((vw[2][x] & LO) | ((vw[3][x] << 4) & ~LO), e1);
+          kv4_pairs(((vw[0][x] >> 4) & LO) | (vw[1][x] & ~LO), o0);
+          kv4_pairs(((vw[2][x] >> 4) & LO) | (vw[3][x] & ~LO), o1);
+#pragma unroll
+          for (int i = 0; i < 4 && 8 * x + 2 * i < NT; ++i) {
+            const uint32_t a0 = h2u(__hmul2(e0[i], v0)), a1 = h2u(__hmul2(e1[i], v1));
+            const uint32_t c0 = h2u(__hmul2(o0[i], v0)), c1 = h2u(__hmul2(o1[i], v1));
+            mma16816(o[8 * x + 2 * i], pa[hb], a0, a1);
+            mma16816(o[8 * x + 2 * i + 1], pa[hb], c0, c1);
+            if (SPLIT) {
+              mma16816(o[8 * x + 2 * i], pl[hb], a0, a1);
+              mma16816(o[8 * x + 2 * i + 1], pl[hb], c0, c1);
+            }
+          }
         }
       }
       __syncwarp();                          // every lane has read the stage
@@ -429,6 +454,37 @@ __global__ void __launch_bounds__(KD_WARPS * 32, KD_CTAS) kv4_rows_kernel(const 
   }
 }
 
+// N = 1, 2 or 4 consecutive elements of a lane.
+template <int N> __device__ __forceinline__ void load_f(const float* p, float (&f)[N]) {
+  if constexpr (N == 4) *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(p);
+  else if constexpr (N == 2) *reinterpret_cast<float2*>(f) = *reinterpret_cast<const float2*>(p);
+  else f[0] = p[0];
+}
+template <int N> __device__ __forceinline__ void load_f(const bf16* p, float (&f)[N]) {
+  if constexpr (N == 1) {
+    f[0] = to_f32(p[0]);
+  } else {
+    uint32_t u[N / 2];
+    if constexpr (N == 4) *reinterpret_cast<uint2*>(u) = *reinterpret_cast<const uint2*>(p);
+    else u[0] = *reinterpret_cast<const uint32_t*>(p);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      f[2 * i] = __uint_as_float(u[i] << 16);
+      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+}
+template <int N> __device__ __forceinline__ void store_f(float* p, const float (&f)[N]) {
+  if constexpr (N == 4) *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  else if constexpr (N == 2) *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
+  else p[0] = f[0];
+}
+template <int N> __device__ __forceinline__ void store_f(bf16* p, const float (&f)[N]) {
+  if constexpr (N == 4) *reinterpret_cast<uint2*>(p) = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
+  else if constexpr (N == 2) *reinterpret_cast<uint32_t*>(p) = pack2(f[0], f[1]);
+  else p[0] = from_f32<bf16>(f[0]);
+}
+
 // One warp a query row: joins the prefix's partials (o, max, sum), adds the call's own rows the
 // row sees, one at a time in float, and rounds the quotient once.  A tree row sees its
 // ancestors only (at most 9), so going through the set bits beats a masked product with all n1.
@@ -450,20 +506,35 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant_
 #pragma unroll
   for (int i = 0; i < C; ++i) o[i] = 0.f;
   if (clamp_len(c, c.len[b]) > 0) {
+    // eight slots in one round trip; the reference moves once for them
     const int2 sp = w.span[((long)b * c.Hkv + g) * w.nrb + rb];
-    for (int s = sp.x; s < sp.y; ++s) {
-      const long at = (long)s * w.rb + in;
-      const float2 y = w.part_ml[at];
-      float v[C];
+    for (int s0 = sp.x; s0 < sp.y; s0 += 8) {
+      float2 y[8];
+      float v[8][C];
 #pragma unroll
-      for (int i = 0; i < C; ++i) v[i] = w.part_o[at * DH + lane * C + i];
-      const float mn = fmaxf(m, y.x);
+      for (int u = 0; u < 8; ++u) {
+        const long at = (long)(s0 + u) * w.rb + in;
+        y[u] = s0 + u < sp.y ? w.part_ml[at] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int i = 0; i < C; ++i) v[u][i] = 0.f;
+        if (s0 + u < sp.y) load_f<C>(w.part_o + at * DH + lane * C, v[u]);
+      }
+      float mn = m;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) mn = fmaxf(mn, y[u].x);
       if (mn == -INFINITY) continue;
-      const float f = ex2_approx(m - mn), h = ex2_approx(y.x - mn);
+      const float f = ex2_approx(m - mn);
       m = mn;
-      l = l * f + y.y * h;
+      l *= f;
 #pragma unroll
-      for (int i = 0; i < C; ++i) o[i] = o[i] * f + v[i] * h;
+      for (int i = 0; i < C; ++i) o[i] *= f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float h = ex2_approx(y[u].x - mn);
+        l += y[u].y * h;
+#pragma unroll
+        for (int i = 0; i < C; ++i) o[i] = fmaf(v[u][i], h, o[i]);
+      }
     }
   }
 #pragma unroll
@@ -471,36 +542,54 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant_
   if (a.tk) {
     const T* q = static_cast<const T*>(a.q) + bn * a.q_row + hq * a.q_head + lane * C;
     float x[C];
+    load_f<C>(q, x);
 #pragma unroll
-    for (int i = 0; i < C; ++i) x[i] = to_f32(q[i]) * (a.scale * 1.4426950408889634f);
+    for (int i = 0; i < C; ++i) x[i] *= a.scale * 1.4426950408889634f;
     for (int wd = 0; wd < (a.n1 + 31) / 32; ++wd) {
       uint32_t bits = a.mask ? a.mask[(long)node * 8 + wd]
                              : (node >= 32 * wd + 31 ? 0xffffffffu : node < 32 * wd ? 0u : (2u << (node - 32 * wd)) - 1u);
       if (a.n1 < 32 * wd + 32) bits &= (1u << (a.n1 - 32 * wd)) - 1u;
       while (bits) {
-        const int j = 32 * wd + __ffs(bits) - 1;
-        bits &= bits - 1;
-        const long off = (((long)b * a.n1 + j) * c.Hkv + g) * DH + lane * C;
-        const T* kp = static_cast<const T*>(a.tk) + off;
-        const T* vp = static_cast<const T*>(a.tv) + off;
-        float s = 0.f, v[C];
+        // four visible rows in one round trip
+        float sc[4], v[4][C];
 #pragma unroll
-        for (int i = 0; i < C; ++i) {
-          s = fmaf(x[i], to_f32(kp[i]), s);
-          v[i] = to_f32(vp[i]);
+        for (int u = 0; u < 4; ++u) {
+          sc[u] = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < C; ++i) v[u][i] = 0.f;
+          if (bits) {
+            const int j = 32 * wd + __ffs(bits) - 1;
+            bits &= bits - 1;
+            const long off = (((long)b * a.n1 + j) * c.Hkv + g) * DH + lane * C;
+            float kx[C];
+            load_f<C>(static_cast<const T*>(a.tk) + off, kx);
+            load_f<C>(static_cast<const T*>(a.tv) + off, v[u]);
+            sc[u] = 0.f;
+#pragma unroll
+            for (int i = 0; i < C; ++i) sc[u] = fmaf(x[i], kx[i], sc[u]);
+          }
         }
-        s = warp_sum(s);
-        const float mn = fmaxf(m, s), f = ex2_approx(m - mn), p = ex2_approx(s - mn);
-        m = mn;
-        l = l * f + p;
 #pragma unroll
-        for (int i = 0; i < C; ++i) o[i] = fmaf(p, v[i], o[i] * f);
+        for (int u = 0; u < 4; ++u) sc[u] = warp_sum(sc[u]);
+        const float mn = fmaxf(fmaxf(m, fmaxf(sc[0], sc[1])), fmaxf(sc[2], sc[3])), f = ex2_approx(m - mn);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < C; ++i) o[i] *= f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float p = ex2_approx(sc[u] - mn);
+          l += p;
+#pragma unroll
+          for (int i = 0; i < C; ++i) o[i] = fmaf(p, v[u][i], o[i]);
+        }
       }
     }
   }
   T* y = static_cast<T*>(a.o) + bn * a.o_row + hq * a.o_head + lane * C;
 #pragma unroll
-  for (int i = 0; i < C; ++i) y[i] = from_f32<T>(l > 0.f ? o[i] / l : 0.f);
+  for (int i = 0; i < C; ++i) o[i] = l > 0.f ? o[i] / l : 0.f;
+  store_f<C>(y, o);
 }
 
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -520,11 +609,13 @@ size_t kv4_workspace(int B, int Hq, int Hkv, int dh, int max_nodes, int num_sms)
 
 template <typename T, int DH, bool SPLIT>
 static cudaError_t rows_go(const Kv4Work& w, int num_sms, cudaStream_t st) {
-  const size_t smem = (size_t)KD_WARPS * KD_STAGES * 2 * kv4_block(DH) + (size_t)KD_WARPS * w.rb * (DH + 4) * 4;
+  const size_t smem = (size_t)KD_WARPS * KD_STAGES * 4 * kv4_block(DH) + (size_t)KD_WARPS * w.rb * (DH + 4) * 4;
   auto kern = kv4_rows_kernel<T, DH, SPLIT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  if ((e = launch_kernel(kern, dim3(num_sms * KD_CTAS), dim3(KD_WARPS * 32), smem, st, 1, w)) != cudaSuccess) return e;
+  // with 16 rows the partials take the room of a third CTA
+  const int ctas = smem + 10 * 1024 <= (size_t)(227 * 1024) / KD_CTAS ? KD_CTAS : KD_CTAS - 1;
+  if ((e = launch_kernel(kern, dim3(num_sms * ctas), dim3(KD_WARPS * 32), smem, st, 1, w)) != cudaSuccess) return e;
   const long rows = (long)w.a.c.B * w.a.n1 * w.a.Hq;
   return launch_kernel(kv4_combine_kernel<T, DH>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, 1, w);
 }

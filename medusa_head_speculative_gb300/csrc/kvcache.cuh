@@ -149,6 +149,22 @@ __device__ __forceinline__ bool kv4_encode(const float (&x)[16], float g, uint2&
 __device__ __forceinline__ __half2 kv4_pair(uint32_t byte) {
   return __half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)byte, __NV_E2M1));
 }
+// The four bytes of a word, two codes each.
+__device__ __forceinline__ void kv4_pairs(uint32_t w, __half2 (&y)[4]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(y);
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+}
+// Two e4m3 scales as halves.
+__device__ __forceinline__ __half2 kv4_scales(uint16_t s) {
+  return __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)s, __NV_E4M3));
+}
 // An e4m3 scale as a half, exactly (NaN for a group that held none of the numbers).
 __device__ __forceinline__ __half kv4_scale(uint8_t s) { return __half(__nv_cvt_fp8_to_halfraw(s, __NV_E4M3)); }
 
