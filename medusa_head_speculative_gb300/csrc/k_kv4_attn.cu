@@ -2,8 +2,8 @@
 // Multiple Decoding Heads" §3.4 Tree Attention, Steps 3 and 5, over the format of
 // include/medusa.h), for few query rows a key/value head: single tokens and small trees.
 //
-// Rows: the n1 nodes x G query heads that share a key/value head, 16 at a time (a "row
-// block").  Work: every (sequence, head, row block) has ceil(len / 128) chunks of 128 cached
+// Rows: the n1 nodes x G query heads that share a key/value head, up to 8 or 16 at a time (a
+// "row block").  Work: every (sequence, head, row block) has ceil(len / 128) chunks of 128 cached
 // slots; all chunks of the call in that order are dealt out evenly, CTA i of n taking the
 // chunks [W i / n, W (i + 1) / n), n at most W, whatever sequences they belong to (the lengths are read on
 // the GPU).  A CTA that leaves a (sequence, head, row block) writes its unnormalised partial
@@ -12,16 +12,17 @@
 // the call's own tree rows and rounds once.
 //
 // In a CTA each of four warps takes 32 slots of a chunk: two blocks of the format, each in one
-// piece, so each warp keeps its own ring of blocks filled by the copy engine.  With
-// few rows a 128-row tcgen05 tile would be mostly padding; the products here go through
-// warp-wide 16 x 8 x 16 MMAs whose operands are decoded straight into registers, never
-// written to shared memory: S = Q K^T with K as the column operand (a lane's 16 bytes are 32
-// elements of one key; the order of the head's elements is free as long as Q has the same),
-// then O += P V with S's own register layout as the row operand and pairs of keys packed per
-// element as the column operand.  e2m1 * e4m3 is exact in a half, so K and V lose nothing;
-// P is rounded to a half (11 bits), queries are scaled row by row by a power of two into a
-// half's range, which is exact for bf16 but for elements 2^-17 below the row's largest.  Float
-// queries and their P go as two halves (22 bits) in two MMAs.
+// piece, so each warp keeps its own ring of blocks filled by the copy engine.  With few rows a
+// 128-row tcgen05 tile would be mostly padding; the products here go through warp-wide
+// 16 x 8 x 16 MMAs whose operands are decoded straight into registers, never written to shared
+// memory.  The cache is the 16-row operand and the queries the 8-column one, so 8 rows waste
+// nothing and cost half the registers: S^T = K Q^T (a lane's 16 bytes are 32 elements of one
+// key; the order of the head's elements is free as long as Q has the same), then O^T += V^T P^T
+// with P^T turned into a column operand by one 8 x 8 register transpose a key tile, and the
+// codes of two keys put side by side before they are decoded.  e2m1 * e4m3 is exact in a half,
+// so K and V lose nothing; P is rounded to a half (11 bits), queries are scaled row by row by
+// a power of two into a half's range, which is exact for bf16 but for elements 2^-17 below the
+// row's largest.  Float queries and their P go as two halves (22 bits) in two MMAs.
 #include "cache.h"
 #include "common.cuh"
 #include "kvcache.cuh"
@@ -30,7 +31,9 @@
 
 namespace medusa {
 
-constexpr int KD_WARPS = 4, KD_ROWS = 16, KD_STAGES = 3, KD_CTAS = 3;
+constexpr int KD_WARPS = 4, KD_ROWS = 16, KD_STAGES = 2;
+template <int NR> constexpr int KD_CTAS = NR == 1 ? 4 : 3;     // resident CTAs per SM (registers, shared memory)
+constexpr int KD_CTAS_MOST = 4;
 constexpr int KD_KEYS = 2 * KV4_SLOTS;              // slots a warp takes at a time: two blocks
 constexpr int KD_CHUNK = KD_WARPS * KD_KEYS;
 // P is taken against a reference 2^KD_TOP below a half's range: a row's reference starts KD_BACK
@@ -117,14 +120,14 @@ __device__ __forceinline__ void kd_next(const CacheView& c, int per, KdCursor& k
   } while (k.nb == 0);
 }
 
-// Q as row operands: a[s] holds, for MMA step s, rows g and g + 8 and elements e, e + 1 and
-// e + 2, e + 3 with e = t dh/4 + 4 s; kept in shared memory as the lanes read it.
-template <typename T, int DH, bool SPLIT>
+// Q as column operands: for MMA step s and 8-row tile n, lane (g, t) holds row 8 n + g, elements
+// e, e + 1 and e + 2, e + 3 with e = t dh/4 + 4 s; kept in shared memory as the lanes read it.
+template <typename T, int DH, int NR, bool SPLIT>
 __device__ __forceinline__ void kd_load_q(const Kv4Work& w, int b, int g, int rb, uint32_t* qf, float* rs) {
   // one warp two rows at a time: 16 lanes a row, DH / 16 elements a lane
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = lane >> 4, li = lane & 15;
   constexpr int N = DH / 16;
-  for (int r0 = warp * 2; r0 < KD_ROWS; r0 += 2 * KD_WARPS) {
+  for (int r0 = warp * 2; r0 < 8 * NR; r0 += 2 * KD_WARPS) {
     const int r = r0 + half, gr = rb * w.rb + r;
     float x[N];
     float top = 0.f;
@@ -147,30 +150,35 @@ __device__ __forceinline__ void kd_load_q(const Kv4Work& w, int b, int g, int rb
       const int e = li * N + i, t = e / (DH / 4), in = e % (DH / 4), s = in >> 2, hi = (in >> 1) & 1;
       const float x0 = x[i] * down, x1 = x[i + 1] * down;
       const __half2 p = __floats2half2_rn(x0, x1);
-      const int at = ((s * 32 + (r & 7) * 4 + t) << 2) + (hi << 1) + (r >> 3);
+      const int at = (((s * NR + (r >> 3)) * 32 + (r & 7) * 4 + t) << 1) + hi;
       qf[at] = h2u(p);
       if (SPLIT) {
         const float2 f = __half22float2(p);
-        qf[DH / 16 * 128 + at] = half_pair(x0 - f.x, x1 - f.y);
+        qf[DH / 16 * NR * 64 + at] = half_pair(x0 - f.x, x1 - f.y);
       }
     }
   }
 }
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 
-template <typename T, int DH, bool SPLIT>
-__global__ void __launch_bounds__(KD_WARPS * 32, KD_CTAS) kv4_rows_kernel(const __grid_constant__ Kv4Work w) {
-  constexpr int BLK = kv4_block(DH), STEPS = DH / 16, NT = DH / 8;
-  constexpr int QW = STEPS * 128 * (SPLIT ? 2 : 1);
+template <typename T, int DH, int NR, bool SPLIT>
+__global__ void __launch_bounds__(KD_WARPS * 32, KD_CTAS<NR>) kv4_rows_kernel(const __grid_constant__ Kv4Work w) {
+  constexpr int BLK = kv4_block(DH), STEPS = DH / 16, MT = DH / 16;   // MT: 16-element tiles of O^T
+  constexpr int QW = STEPS * NR * 64 * (SPLIT ? 2 : 1);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t bars[KD_WARPS][KD_STAGES];
   __shared__ __align__(16) uint32_t qf[QW];
-  __shared__ float rs[KD_ROWS];
-  __shared__ float2 ml[KD_WARPS][KD_ROWS];
+  __shared__ float rs[8 * NR];
+  __shared__ float2 ml[KD_WARPS][8 * NR];
   const CacheView& c = w.a.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
   const int per = c.Hkv * w.nrb;
   uint8_t* ring = smem + warp * KD_STAGES * 4 * BLK;
-  float* merge = reinterpret_cast<float*>(smem + KD_WARPS * KD_STAGES * 4 * BLK);   // [warps][rb][DH + 4]
+  float* merge = reinterpret_cast<float*>(smem + KD_WARPS * KD_STAGES * 4 * BLK);   // [2 warps][rb][DH + 4]
   constexpr int ML = DH + 4;
   const long W = kd_total(c, per);
   // every CTA that takes part has at least one chunk, so a triple's slots have no gaps
@@ -242,13 +250,22 @@ __global__ void __launch_bounds__(KD_WARPS * 32, KD_CTAS) kv4_rows_kernel(const 
     const int len = clamp_len(c, c.len[b]);
     const long n = min((long)(k.nb - k.j), w1 - wi);
     const int j0 = k.j;
-    kd_load_q<T, DH, SPLIT>(w, b, g, rb, qf, rs);
+    kd_load_q<T, DH, NR, SPLIT>(w, b, g, rb, qf, rs);
     __syncthreads();
-    const float rs0 = rs[g8], rs1 = rs[g8 + 8];
-    float o[NT][4];
+    // a lane has the rows 8 x + 2 t4 + {0, 1} of each row tile x
+    float f[NR][2], m[NR][2], l[NR][2], o[MT][NR][4];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    for (int x = 0; x < NR; ++x)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        f[x][e] = rs[8 * x + 2 * t4 + e];
+        m[x][e] = -INFINITY;
+        l[x][e] = 0.f;
+      }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int x = 0; x < NR; ++x) o[i][x][0] = o[i][x][1] = o[i][x][2] = o[i][x][3] = 0.f;
     for (int j = j0; j < j0 + (int)n; ++j) {
       const int t0 = j * KD_CHUNK + warp * KD_KEYS;
       if (t0 >= len) break;
@@ -261,99 +278,109 @@ __global__ void __launch_bounds__(KD_WARPS * 32, KD_CTAS) kv4_rows_kernel(const 
       if (dead) continue;
       const uint8_t* kb = ring + st * 4 * BLK;
       const uint8_t* vb = kb + 2 * BLK;
-      // ---- S = Q K^T for 32 keys, 8 a tile: four independent sums, each operand of Q read once
-      float s[4][4];
+      // ---- S^T = K Q^T for two blocks of 16 keys: a lane has keys g8, g8 + 8 of each
+      float s[2][NR][4];
       uint32_t kw[4][DH / 32];
       __half2 s2[4];                       // the lane's dh/4 elements have one scale (dh 128: two)
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
-        s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-        const uint8_t* blk = kb + (nt >> 1) * BLK;
-        const int key = (nt & 1) * 8 + g8;
+      for (int y = 0; y < 4; ++y) {
+        const uint8_t* blk = kb + (y >> 1) * BLK;
+        const int key = (y & 1) * 8 + g8;
         const uint8_t* src = blk + key * (DH / 2) + t4 * (DH / 8);
-        if (DH == 128) *reinterpret_cast<uint4*>(kw[nt]) = *reinterpret_cast<const uint4*>(src);
-        else if (DH == 64) *reinterpret_cast<uint2*>(kw[nt]) = *reinterpret_cast<const uint2*>(src);
-        else kw[nt][0] = *reinterpret_cast<const uint32_t*>(src);
+        if (DH == 128) *reinterpret_cast<uint4*>(kw[y]) = *reinterpret_cast<const uint4*>(src);
+        else if (DH == 64) *reinterpret_cast<uint2*>(kw[y]) = *reinterpret_cast<const uint2*>(src);
+        else kw[y][0] = *reinterpret_cast<const uint32_t*>(src);
         const uint8_t* sc = blk + 8 * DH + key * (DH / 16) + t4 * DH / 64;
-        if (DH == 128) s2[nt] = kv4_scales(*reinterpret_cast<const uint16_t*>(sc));
-        else s2[nt] = __half2half2(kv4_scale(*sc));
+        if (DH == 128) s2[y] = kv4_scales(*reinterpret_cast<const uint16_t*>(sc));
+        else s2[y] = __half2half2(kv4_scale(*sc));
       }
+#pragma unroll
+      for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+        for (int x = 0; x < NR; ++x) s[hb][x][0] = s[hb][x][1] = s[hb][x][2] = s[hb][x][3] = 0.f;
 #pragma unroll
       for (int x = 0; x < DH / 32; ++x) {
         __half2 y[4][4];
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-          kv4_pairs(kw[nt][x], y[nt]);
-          const __half2 sc = x < 2 ? __low2half2(s2[nt]) : __high2half2(s2[nt]);
+        for (int k4 = 0; k4 < 4; ++k4) {
+          kv4_pairs(kw[k4][x], y[k4]);
+          const __half2 sc = x < 2 ? __low2half2(s2[k4]) : __high2half2(s2[k4]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) y[nt][e] = __hmul2(y[nt][e], sc);
+          for (int e = 0; e < 4; ++e) y[k4][e] = __hmul2(y[k4][e], sc);
         }
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-          const uint32_t* qp = qf + ((2 * x + z) * 32 + lane) * 4;
-          uint32_t qa[4];
-          *reinterpret_cast<uint4*>(qa) = *reinterpret_cast<const uint4*>(qp);
+          const uint32_t ka[2][4] = {{h2u(y[0][2 * z]), h2u(y[1][2 * z]), h2u(y[0][2 * z + 1]), h2u(y[1][2 * z + 1])},
+                                     {h2u(y[2][2 * z]), h2u(y[3][2 * z]), h2u(y[2][2 * z + 1]), h2u(y[3][2 * z + 1])}};
 #pragma unroll
-          for (int nt = 0; nt < 4; ++nt) mma16816(s[nt], qa, h2u(y[nt][2 * z]), h2u(y[nt][2 * z + 1]));
-          if (SPLIT) {
-            *reinterpret_cast<uint4*>(qa) = *reinterpret_cast<const uint4*>(qp + STEPS * 128);
+          for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) mma16816(s[nt], qa, h2u(y[nt][2 * z]), h2u(y[nt][2 * z + 1]));
-          }
+            for (int n = 0; n < NR; ++n) {
+              const uint2 q2 = *reinterpret_cast<const uint2*>(
+                  qf + part * STEPS * NR * 64 + (((2 * x + z) * NR + n) * 32 + lane) * 2);
+              mma16816(s[0][n], ka[0], q2.x, q2.y);
+              mma16816(s[1][n], ka[1], q2.x, q2.y);
+            }
         }
       }
-      // ---- softmax: a lane has rows g8 (0, 1) and g8 + 8 (2, 3), keys 2 t4 + {0, 1} of each tile
+      // ---- softmax
       const bool tail = t0 + KD_KEYS > len;
       if (tail) {
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
+        for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (t0 + nt * 8 + 2 * t4 + (e & 1) >= len) s[nt][e] = -INFINITY;
+          for (int x = 0; x < NR; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (t0 + hb * KV4_SLOTS + g8 + 8 * (e >> 1) >= len) s[hb][x][e] = -INFINITY;
       }
-      float x0 = fmaxf(s[0][0], s[0][1]), x1 = fmaxf(s[0][2], s[0][3]);
+      float top[NR][2];
+      bool raise = false;
 #pragma unroll
-      for (int nt = 1; nt < 4; ++nt) {
-        x0 = fmaxf(x0, fmaxf(s[nt][0], s[nt][1]));
-        x1 = fmaxf(x1, fmaxf(s[nt][2], s[nt][3]));
-      }
-      x0 *= rs0;                             // the rows' factors are positive
-      x1 *= rs1;
-      if (__any_sync(0xffffffffu, x0 > m0 + KD_TOP || x1 > m1 + KD_TOP)) {
+      for (int x = 0; x < NR; ++x)
 #pragma unroll
-        for (int d = 1; d < 4; d <<= 1) {
-          x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, d));
-          x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, d));
+        for (int e = 0; e < 2; ++e) {       // the rows' factors are positive
+          top[x][e] = fmaxf(fmaxf(s[0][x][e], s[0][x][e + 2]), fmaxf(s[1][x][e], s[1][x][e + 2])) * f[x][e];
+          raise = raise || top[x][e] > m[x][e] + KD_TOP;
         }
-        const float n0 = fmaxf(m0, x0 - KD_BACK<SPLIT>), n1 = fmaxf(m1, x1 - KD_BACK<SPLIT>);
-        const float f0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - n0), f1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - n1);
-        m0 = n0;
-        m1 = n1;
-        l0 *= f0;
-        l1 *= f1;
+      if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          o[i][0] *= f0; o[i][1] *= f0;
-          o[i][2] *= f1; o[i][3] *= f1;
-        }
-      }
-      uint32_t pa[2][4], pl[2][4];
+        for (int x = 0; x < NR; ++x)
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
-        const float p0 = ex2_approx(fmaf(s[nt][0], rs0, -m0)), p1 = ex2_approx(fmaf(s[nt][1], rs0, -m0));
-        const float p2 = ex2_approx(fmaf(s[nt][2], rs1, -m1)), p3 = ex2_approx(fmaf(s[nt][3], rs1, -m1));
-        l0 += p0 + p1;
-        l1 += p2 + p3;
-        const __half2 h0 = __floats2half2_rn(p0, p1), h1 = __floats2half2_rn(p2, p3);
-        pa[nt >> 1][2 * (nt & 1)] = h2u(h0);
-        pa[nt >> 1][2 * (nt & 1) + 1] = h2u(h1);
-        if (SPLIT) {
-          const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
-          pl[nt >> 1][2 * (nt & 1)] = half_pair(p0 - f0.x, p1 - f0.y);
-          pl[nt >> 1][2 * (nt & 1) + 1] = half_pair(p2 - f1.x, p3 - f1.y);
-        }
+          for (int e = 0; e < 2; ++e) {
+            float v = top[x][e];
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+            const float mn = fmaxf(m[x][e], v - KD_BACK<SPLIT>);
+            const float fall = m[x][e] == -INFINITY ? 0.f : ex2_approx(m[x][e] - mn);
+            m[x][e] = mn;
+            l[x][e] *= fall;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+              o[i][x][e] *= fall;
+              o[i][x][e + 2] *= fall;
+            }
+          }
       }
-      // ---- O += P V: lane's keys 2 t4, + 1, + 8, + 9 of each block, elements g8 DH/8 + i
+      uint32_t pb[2][NR][2], pl[2][NR][2];  // P^T as column operands, and what the halves left
+#pragma unroll
+      for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+        for (int x = 0; x < NR; ++x)
+#pragma unroll
+          for (int k8 = 0; k8 < 2; ++k8) {
+            const float p0 = ex2_approx(fmaf(s[hb][x][2 * k8], f[x][0], -m[x][0]));
+            const float p1 = ex2_approx(fmaf(s[hb][x][2 * k8 + 1], f[x][1], -m[x][1]));
+            l[x][0] += p0;
+            l[x][1] += p1;
+            const __half2 h = __floats2half2_rn(p0, p1);
+            pb[hb][x][k8] = transpose8(h2u(h));
+            if (SPLIT) {
+              const float2 hf = __half22float2(h);
+              pl[hb][x][k8] = transpose8(half_pair(p0 - hf.x, p1 - hf.y));
+            }
+          }
+      // ---- O^T += V^T P^T: lane's keys 2 t4, + 1, + 8, + 9 of each block, elements from g8 DH/8 on
 #pragma unroll
       for (int hb = 0; hb < 2; ++hb) {
         const uint8_t* blk = vb + hb * BLK;
@@ -380,14 +407,13 @@ __global__ void __launch_bounds__(KD_WARPS * 32, KD_CTAS) kv4_rows_kernel(const 
           kv4_pairs(((vw[0][x] >> 4) & LO) | (vw[1][x] & ~LO), o0);
           kv4_pairs(((vw[2][x] >> 4) & LO) | (vw[3][x] & ~LO), o1);
 #pragma unroll
-          for (int i = 0; i < 4 && 8 * x + 2 * i < NT; ++i) {
-            const uint32_t a0 = h2u(__hmul2(e0[i], v0)), a1 = h2u(__hmul2(e1[i], v1));
-            const uint32_t c0 = h2u(__hmul2(o0[i], v0)), c1 = h2u(__hmul2(o1[i], v1));
-            mma16816(o[8 * x + 2 * i], pa[hb], a0, a1);
-            mma16816(o[8 * x + 2 * i + 1], pa[hb], c0, c1);
-            if (SPLIT) {
-              mma16816(o[8 * x + 2 * i], pl[hb], a0, a1);
-              mma16816(o[8 * x + 2 * i + 1], pl[hb], c0, c1);
+          for (int i = 0; i < 4 && 4 * x + i < MT; ++i) {
+            const uint32_t va[4] = {h2u(__hmul2(e0[i], v0)), h2u(__hmul2(o0[i], v0)), h2u(__hmul2(e1[i], v1)),
+                                    h2u(__hmul2(o1[i], v1))};
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+              mma16816(o[4 * x + i][n], va, pb[hb][n][0], pb[hb][n][1]);
+              if (SPLIT) mma16816(o[4 * x + i][n], va, pl[hb][n][0], pl[hb][n][1]);
             }
           }
         }
@@ -395,48 +421,63 @@ __global__ void __launch_bounds__(KD_WARPS * 32, KD_CTAS) kv4_rows_kernel(const 
       __syncwarp();                          // every lane has read the stage
       copy_next();
     }
-    // ---- join the warps' partials and write the CTA's
+    // ---- join the warps' partials and write the CTA's: everybody on one reference, then the
+    // upper two warps' sums onto the lower two's
 #pragma unroll
-    for (int d = 1; d < 4; d <<= 1) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, d);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, d);
-    }
-    if (t4 == 0) {
-      ml[warp][g8] = make_float2(m0, l0);
-      ml[warp][g8 + 8] = make_float2(m1, l1);
-    }
-    float* mine = merge + warp * w.rb * ML;
+    for (int x = 0; x < NR; ++x)
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      // columns 2 t4, 2 t4 + 1 of tile i are elements (2 t4) DH/8 + i and (2 t4 + 1) DH/8 + i
-      if (g8 < w.rb) {
-        mine[g8 * ML + 2 * t4 * (DH / 8) + i] = o[i][0];
-        mine[g8 * ML + (2 * t4 + 1) * (DH / 8) + i] = o[i][1];
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], d);
+        if (g8 == 0) ml[warp][8 * x + 2 * t4 + e] = make_float2(m[x][e], l[x][e]);
       }
-      if (g8 + 8 < w.rb) {
-        mine[(g8 + 8) * ML + 2 * t4 * (DH / 8) + i] = o[i][2];
-        mine[(g8 + 8) * ML + (2 * t4 + 1) * (DH / 8) + i] = o[i][3];
-      }
-    }
     __syncthreads();
+    auto joined = [&](int r) {               // (reference, sum) of row r over the warps
+      float mn = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int y = 0; y < KD_WARPS; ++y) mn = fmaxf(mn, ml[y][r].x);
+#pragma unroll
+      for (int y = 0; y < KD_WARPS; ++y) sum += ml[y][r].x == -INFINITY ? 0.f : ex2_approx(ml[y][r].x - mn) * ml[y][r].y;
+      return make_float2(mn, sum);
+    };
+    float fall[NR][2];
+#pragma unroll
+    for (int x = 0; x < NR; ++x)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        fall[x][e] = m[x][e] == -INFINITY ? 0.f : ex2_approx(m[x][e] - joined(8 * x + 2 * t4 + e).x);
+    float* mine = merge + (warp & 1) * w.rb * ML;
+#pragma unroll
+    for (int step = 0; step < 2; ++step) {
+      if ((warp >> 1) == 1 - step) {
+#pragma unroll
+        for (int x = 0; x < NR; ++x)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 8 * x + 2 * t4 + e;
+            if (r >= w.rb) continue;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+              float2* at = reinterpret_cast<float2*>(mine + r * ML + g8 * (DH / 8) + 2 * i);
+              float2 v = make_float2(o[i][x][e] * fall[x][e], o[i][x][e + 2] * fall[x][e]);
+              if (step) {
+                v.x += at->x;
+                v.y += at->y;
+              }
+              *at = v;
+            }
+          }
+      }
+      __syncthreads();
+    }
     const long pair = (long)b * per + q, slot = pair + blockIdx.x;
     for (int e = tid; e < w.rb * (DH / 4); e += KD_WARPS * 32) {
       const int r = e / (DH / 4), col = (e - r * (DH / 4)) * 4;
-      float m = -INFINITY, l = 0.f;
-#pragma unroll
-      for (int x = 0; x < KD_WARPS; ++x) m = fmaxf(m, ml[x][r].x);
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int x = 0; x < KD_WARPS; ++x) {
-        const float2 y = ml[x][r];
-        if (y.x == -INFINITY) continue;
-        const float f = ex2_approx(y.x - m);
-        l += f * y.y;
-        const float4 v = *reinterpret_cast<const float4*>(merge + (x * w.rb + r) * ML + col);
-        acc.x += f * v.x; acc.y += f * v.y; acc.z += f * v.z; acc.w += f * v.w;
-      }
-      *reinterpret_cast<float4*>(w.part_o + (slot * w.rb + r) * DH + col) = acc;
-      if (col == 0) w.part_ml[slot * w.rb + r] = make_float2(m, l);
+      const float4 v0 = *reinterpret_cast<const float4*>(merge + r * ML + col);
+      const float4 v1 = *reinterpret_cast<const float4*>(merge + (w.rb + r) * ML + col);
+      *reinterpret_cast<float4*>(w.part_o + (slot * w.rb + r) * DH + col) =
+          make_float4(v0.x + v1.x, v0.y + v1.y, v0.z + v1.z, v0.w + v1.w);
+      if (col == 0) w.part_ml[slot * w.rb + r] = joined(r);
     }
     if (tid == 0) {
       if (j0 == 0) w.span[pair].x = (int)slot;
@@ -593,7 +634,7 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant_
 }
 
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-static size_t kd_slots(int B, int Hkv, int nrb, int num_sms) { return (size_t)num_sms * KD_CTAS + (size_t)B * Hkv * nrb; }
+static size_t kd_slots(int B, int Hkv, int nrb, int num_sms) { return (size_t)num_sms * KD_CTAS_MOST + (size_t)B * Hkv * nrb; }
 
 size_t kv4_workspace(int B, int Hq, int Hkv, int dh, int max_nodes, int num_sms) {
   size_t most = 0;
@@ -607,24 +648,23 @@ size_t kv4_workspace(int B, int Hq, int Hkv, int dh, int max_nodes, int num_sms)
   return most;
 }
 
-template <typename T, int DH, bool SPLIT>
+template <typename T, int DH, int NR, bool SPLIT>
 static cudaError_t rows_go(const Kv4Work& w, int num_sms, cudaStream_t st) {
-  const size_t smem = (size_t)KD_WARPS * KD_STAGES * 4 * kv4_block(DH) + (size_t)KD_WARPS * w.rb * (DH + 4) * 4;
-  auto kern = kv4_rows_kernel<T, DH, SPLIT>;
+  const size_t smem = (size_t)KD_WARPS * KD_STAGES * 4 * kv4_block(DH) + (size_t)2 * w.rb * (DH + 4) * 4;
+  auto kern = kv4_rows_kernel<T, DH, NR, SPLIT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  // with 16 rows the partials take the room of a third CTA
-  const int ctas = smem + 10 * 1024 <= (size_t)(227 * 1024) / KD_CTAS ? KD_CTAS : KD_CTAS - 1;
-  if ((e = launch_kernel(kern, dim3(num_sms * ctas), dim3(KD_WARPS * 32), smem, st, 1, w)) != cudaSuccess) return e;
+  if ((e = launch_kernel(kern, dim3(num_sms * KD_CTAS<NR>), dim3(KD_WARPS * 32), smem, st, 1, w)) != cudaSuccess) return e;
   const long rows = (long)w.a.c.B * w.a.n1 * w.a.Hq;
   return launch_kernel(kv4_combine_kernel<T, DH>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, 1, w);
 }
 template <typename T, bool SPLIT>
 static cudaError_t rows_dh(const Kv4Work& w, int num_sms, cudaStream_t st) {
+  const bool one = w.rb <= 8;
   switch (w.a.c.dh) {
-    case 32: return rows_go<T, 32, SPLIT>(w, num_sms, st);
-    case 64: return rows_go<T, 64, SPLIT>(w, num_sms, st);
-    default: return rows_go<T, 128, SPLIT>(w, num_sms, st);
+    case 32: return one ? rows_go<T, 32, 1, SPLIT>(w, num_sms, st) : rows_go<T, 32, 2, SPLIT>(w, num_sms, st);
+    case 64: return one ? rows_go<T, 64, 1, SPLIT>(w, num_sms, st) : rows_go<T, 64, 2, SPLIT>(w, num_sms, st);
+    default: return one ? rows_go<T, 128, 1, SPLIT>(w, num_sms, st) : rows_go<T, 128, 2, SPLIT>(w, num_sms, st);
   }
 }
 
