@@ -30,7 +30,105 @@ cudaError_t launch_rope_fill(float* cs, const double* freq, int rot, int max_pos
   return launch_kernel(rope_fill_kernel, dim3(blocks), dim3(256), 0, st, 1, cs, freq, rot, max_pos, attn);
 }
 
-// One thread per (row, head, pair) and per passed-through element pair.
+__device__ __forceinline__ void turn(float c, float s, float x1, float x2, float& y1, float& y2) {
+  y1 = __fsub_rn(__fmul_rn(x1, c), __fmul_rn(x2, s));
+  y2 = __fadd_rn(__fmul_rn(x2, c), __fmul_rn(x1, s));
+}
+template <typename T> struct Vec { static constexpr int N = 16 / sizeof(T); };   // elements of 16 bytes
+__device__ __forceinline__ uint4 pack16(const float (&f)[8]) {
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    r[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+__device__ __forceinline__ uint4 pack16(const float (&f)[4]) {
+  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+
+// Rows in 16-byte units (grid y: the part).  A thread takes one unit (HALF: 16 bytes and their
+// partners rot/2 further on; INTERLEAVED: 16 bytes; past rot: 16 bytes to copy) of HPT heads of
+// one row, which share its cosines and sines, all loads before the first use.  Neighbouring
+// threads take neighbouring units, then neighbouring heads.
+template <typename T, int LAYOUT, int HPT>
+__global__ void __launch_bounds__(256) rope_vec_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int N = Vec<T>::N;
+  const medusa_rope_rows& p = a.part[blockIdx.y];
+  const int h = a.t.rot / 2, turned = LAYOUT == MEDUSA_ROPE_HALF ? h / N : a.t.rot / N;
+  const bool place = p.x == p.y;
+  const int units = turned + (place ? 0 : (a.dh - a.t.rot) / N);
+  const int groups = (p.heads + HPT - 1) / HPT;
+  const unsigned long long e = (unsigned long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const int u = (int)(e % units);
+  const int hg = (int)(e / units % groups);
+  const long r = (long)(e / units / groups);
+  if (r >= a.rows) return;
+  const T* x = static_cast<const T*>(p.x) + r * p.x_row;
+  T* y = static_cast<T*>(p.y) + r * p.y_row;
+  const int at = u < turned ? u * N : a.t.rot + (u - turned) * N;
+  uint4 v[HPT][2];
+#pragma unroll
+  for (int i = 0; i < HPT; ++i) {
+    const int hd = hg + i * groups;
+    if (hd >= p.heads) break;
+    v[i][0] = *reinterpret_cast<const uint4*>(x + hd * p.x_head + at);
+    if (LAYOUT == MEDUSA_ROPE_HALF && u < turned) v[i][1] = *reinterpret_cast<const uint4*>(x + hd * p.x_head + at + h);
+  }
+  if (u < turned) {
+    const int pos = a.pos[r];
+    const bool ok = pos >= 0 && pos < a.t.max_pos;
+    if (!ok && u == 0 && hg == 0) set_flag(a.t.status, MEDUSA_FLAG_POS_RANGE);
+    constexpr int M = LAYOUT == MEDUSA_ROPE_HALF ? N : N / 2;   // angles of a unit
+    float c[M], s[M];
+    if (ok) {
+      const float* cs = a.t.cs + (long)pos * a.t.rot + u * M;
+#pragma unroll
+      for (int i = 0; i < M; i += 2) {
+        const float2 c2 = *reinterpret_cast<const float2*>(cs + i), s2 = *reinterpret_cast<const float2*>(cs + h + i);
+        c[i] = c2.x;
+        c[i + 1] = c2.y;
+        s[i] = a.inverse ? -s2.x : s2.x;
+        s[i + 1] = a.inverse ? -s2.y : s2.y;
+      }
+#pragma unroll
+      for (int i = 0; i < HPT; ++i) {
+        float f[N], g[N];
+        unpack16(v[i][0], f);
+        if (LAYOUT == MEDUSA_ROPE_HALF) {
+          unpack16(v[i][1], g);
+#pragma unroll
+          for (int k = 0; k < N; ++k) {
+            float y1, y2;
+            turn(c[k], s[k], f[k], g[k], y1, y2);
+            f[k] = y1;
+            g[k] = y2;
+          }
+          v[i][1] = pack16(g);
+        } else {
+#pragma unroll
+          for (int k = 0; k < N; k += 2) {
+            float y1, y2;
+            turn(c[k / 2], s[k / 2], f[k], f[k + 1], y1, y2);
+            f[k] = y1;
+            f[k + 1] = y2;
+          }
+        }
+        v[i][0] = pack16(f);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < HPT; ++i) {
+    const int hd = hg + i * groups;
+    if (hd >= p.heads) break;
+    *reinterpret_cast<uint4*>(y + hd * p.y_head + at) = v[i][0];
+    if (LAYOUT == MEDUSA_ROPE_HALF && u < turned) *reinterpret_cast<uint4*>(y + hd * p.y_head + at + h) = v[i][1];
+  }
+}
+
+// Any alignment and any even rot: one thread per (row, head, pair) and passed-through element.
 template <typename T>
 __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeArgs a) {
   const int h = a.t.rot / 2, units = h + (a.dh - a.t.rot);
@@ -57,21 +155,49 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeA
     const float x1 = to_f32(x[i1]), x2 = to_f32(x[i2]);
     float y1 = x1, y2 = x2;
     if (ok) {
-      const float c = a.t.cs[(long)pos * a.t.rot + u];
-      const float s0 = a.t.cs[(long)pos * a.t.rot + h + u], s = a.inverse ? -s0 : s0;
-      y1 = __fsub_rn(__fmul_rn(x1, c), __fmul_rn(x2, s));
-      y2 = __fadd_rn(__fmul_rn(x2, c), __fmul_rn(x1, s));
+      const float c = a.t.cs[(long)pos * a.t.rot + u], s = a.t.cs[(long)pos * a.t.rot + h + u];
+      turn(c, a.inverse ? -s : s, x1, x2, y1, y2);
     }
     y[i1] = from_f32<T>(y1);
     y[i2] = from_f32<T>(y2);
   }
 }
 
-cudaError_t launch_rope(const RopeArgs& a, int dtype, cudaStream_t st) {
+template <typename T, int HPT>
+static cudaError_t rope_vec(const RopeArgs& a, cudaStream_t st) {
+  constexpr int N = Vec<T>::N;
+  long most = 0;
+  for (int i = 0; i < a.n_parts; ++i) {
+    const medusa_rope_rows& p = a.part[i];
+    const int turned = a.t.layout == MEDUSA_ROPE_HALF ? a.t.rot / 2 / N : a.t.rot / N;
+    const int units = turned + (p.x == p.y ? 0 : (a.dh - a.t.rot) / N);
+    const long n = (long)a.rows * units * ((p.heads + HPT - 1) / HPT);
+    most = n > most ? n : most;
+  }
+  const dim3 grid((unsigned)((most + 255) / 256), (unsigned)a.n_parts);
+  return launch_kernel(a.t.layout == MEDUSA_ROPE_HALF ? rope_vec_kernel<T, MEDUSA_ROPE_HALF, HPT>
+                                                      : rope_vec_kernel<T, MEDUSA_ROPE_INTERLEAVED, HPT>,
+                       grid, dim3(256), 0, st, 1, a);
+}
+
+template <typename T>
+static cudaError_t rope_go(const RopeArgs& a, cudaStream_t st) {
+  constexpr int N = Vec<T>::N;
+  bool vec = a.dh % N == 0 && a.t.rot % N == 0 && (a.t.layout != MEDUSA_ROPE_HALF || a.t.rot / 2 % N == 0);
+  for (int i = 0; i < a.n_parts; ++i) {
+    const medusa_rope_rows& p = a.part[i];
+    vec = vec && reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && reinterpret_cast<uintptr_t>(p.y) % 16 == 0 &&
+          p.x_row % N == 0 && p.x_head % N == 0 && p.y_row % N == 0 && p.y_head % N == 0;
+  }
+  // four heads a thread share the angles' loads; too few rows for that leave the GPU idle
+  if (vec) return (long)a.rows * a.heads * a.dh >= 4l << 20 ? rope_vec<T, 4>(a, st) : rope_vec<T, 1>(a, st);
   const long n = (long)a.rows * a.heads * (a.dh - a.t.rot / 2);
   const int blocks = (int)((n + 255) / 256 < 1 << 20 ? (n + 255) / 256 : 1 << 20);
-  return launch_kernel(dtype == MEDUSA_F32 ? rope_kernel<float> : rope_kernel<bf16>, dim3(blocks), dim3(256), 0, st,
-                       1, a);
+  return launch_kernel(rope_kernel<T>, dim3(blocks), dim3(256), 0, st, 1, a);
+}
+
+cudaError_t launch_rope(const RopeArgs& a, int dtype, cudaStream_t st) {
+  return dtype == MEDUSA_F32 ? rope_go<float>(a, st) : rope_go<bf16>(a, st);
 }
 
 }  // namespace medusa

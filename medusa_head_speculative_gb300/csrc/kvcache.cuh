@@ -28,6 +28,21 @@ __device__ __forceinline__ int2 item_of(const ItemMap& m, int B, int i) {
   const int s0 = m.start[lo];
   return make_int2(i >= s0 && i < m.start[lo + 1] ? lo : -1, i - s0);
 }
+// The same with the whole warp on one item: 32 sequences' offsets at a time.
+__device__ __forceinline__ int2 item_of_warp(const ItemMap& m, int B, int i) {
+  if (!m.start) return item_of(m, B, i);
+  const int lane = threadIdx.x & 31;
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    const int b = b0 + lane;
+    const int s0 = b < B ? m.start[b] : 0, s1 = b < B ? m.start[b + 1] : 0;
+    const uint32_t hit = __ballot_sync(0xffffffffu, b < B && i >= s0 && i < s1);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      return make_int2(b0 + l, i - __shfl_sync(0xffffffffu, s0, l));
+    }
+  }
+  return make_int2(-1, 0);
+}
 __device__ __forceinline__ int item_count(const ItemMap& m, int b) {
   const int n = m.start ? m.start[b + 1] - m.start[b] : (m.count ? min(m.count[b], m.per_seq) : m.per_seq);
   return max(n, 0);
@@ -113,35 +128,49 @@ __device__ __forceinline__ void store16(float* p, bool vec, const float (&f)[16]
   }
 }
 
+// Eight floats to a word of e2m1 codes (nearest, ties to even, 6 at most).
+__device__ __forceinline__ uint32_t e2m1x8(const float* y) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(w)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+  return w;
+}
 // 16 elements -> 8 bytes of e2m1 pairs and one e4m3 scale.  The scale is the nearest e4m3 to
-// max|x| / (6 g), each code the nearest to x / (g s): true (IEEE) quotients, because a bf16
-// element divided by a 4-bit scale is often exactly half way between two codes, and a
-// quotient off by one unit in the last place would send it the wrong way.
-__device__ __forceinline__ bool kv4_encode(const float (&x)[16], float g, uint2& codes, uint8_t& scale) {
-  float top = 0.f;
-  bool finite = true;
+// max|x| / (6 g), each code the nearest to x / (g s): the correctly rounded quotients, because a
+// bf16 element divided by a 4-bit scale is often exactly half way between two codes, and a
+// quotient off by one unit in the last place would send it the wrong way.  16 divisions took
+// longer than the group's memory traffic, so the quotients come from one correctly rounded
+// reciprocal r and Markstein's correction (IBM J. Res. Dev. 34, 1990): q = x r, then
+// q + r (x - q s) with the residual exact in one fused multiply-add is the rounded quotient.
+__device__ __forceinline__ bool kv4_encode(float (&x)[16], float g, uint2& codes, uint8_t& scale) {
+  uint32_t bits = 0;                        // of the largest magnitude; NaN above all
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const float a = fabsf(x[e]);
-    finite = finite && a < INFINITY;
-    top = fmaxf(top, a);
-  }
-  if (!finite) {                            // the whole group reads back as NaN
+  for (int e = 0; e < 16; ++e) bits = max(bits, __float_as_uint(x[e]) & 0x7fffffffu);
+  if (bits >= 0x7f800000u) {                // the whole group reads back as NaN
     codes = make_uint2(0x22222222u, 0x22222222u);
     scale = 0x7f;
     return false;
   }
-  scale = __nv_cvt_float_to_fp8(__fdiv_rn(top, 6.f * g), __NV_SATFINITE, __NV_E4M3);
+  scale = __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(bits), 6.f * g), __NV_SATFINITE, __NV_E4M3);
   const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(scale, __NV_E4M3))) * g;
-  uint32_t w[2] = {0u, 0u};
-  if (s > 0.f) {
+  if (s > 1e-25f && s < 1e25f) {            // residuals neither vanish nor overflow
+    const float r = __frcp_rn(s);
 #pragma unroll
-    for (int e = 0; e < 16; e += 2) {
-      const float2 y = make_float2(__fdiv_rn(x[e], s), __fdiv_rn(x[e + 1], s));
-      w[e >> 3] |= (uint32_t)__nv_cvt_float2_to_fp4x2(y, __NV_E2M1, cudaRoundNearest) << (4 * (e & 7));
+    for (int e = 0; e < 16; ++e) {
+      const float q = x[e] * r;
+      x[e] = fmaf(fmaf(-q, s, x[e]), r, q);
     }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = s > 0.f ? __fdiv_rn(x[e], s) : 0.f;
   }
-  codes = make_uint2(w[0], w[1]);
+  codes = make_uint2(e2m1x8(x), e2m1x8(x + 8));
   return true;
 }
 
