@@ -48,6 +48,7 @@ extern "C" {
 #define MEDUSA_MAX_TOPS 16     /* s_k <= 16 candidates per head */
 #define MEDUSA_MAX_NODES 256   /* N + 1 <= 256 packed tree nodes (root included) */
 #define MEDUSA_MAX_LAYERS 1024 /* backbone layers of medusa_step_layers */
+#define MEDUSA_MAX_CAPACITY (1 << 24) /* slots per sequence of a medusa_cache */
 
 typedef enum {
   MEDUSA_OK = 0,
@@ -471,7 +472,7 @@ medusa_status medusa_rope_apply(const medusa_rope* rope, int dtype, int dh, int 
  *                          (e2m1: sign, and one of 0 .5 1 1.5 2 3 4 6),
  *   16 rows of dh/16 bytes: one e4m3 scale for each 16 elements,
  * and an element stands for e2m1 * e4m3 * g, g = k_scale for keys and v_scale for values (any
- * positive numbers the caller keeps to; powers of two make every element exact in bf16).  The
+ * numbers from 1e-20 to 1e20 the caller keeps to; powers of two make every element exact in bf16).  The
  * blocks lie [B][Hkv][capacity/16] (contiguous) or [num_pages][Hkv][page_size/16] (paged), so
  * a head's blocks follow each other.  Writing takes, over each 16 elements, s = max|x| / (6 g)
  * rounded to e4m3 and each x / (g s) rounded to e2m1 (both to nearest, ties to even, the
@@ -481,7 +482,7 @@ typedef struct {
   int B;             /* sequences */
   int Hq, Hkv, dh;   /* query heads (a multiple of Hkv), key/value heads, head size 32, 64 or 128 */
   int format;        /* MEDUSA_F32, MEDUSA_BF16 or MEDUSA_KV4 */
-  int capacity;      /* slots per sequence (paged: a multiple of page_size) */
+  int capacity;      /* slots per sequence, at most MEDUSA_MAX_CAPACITY (paged: a multiple of page_size) */
   int page_size;     /* 0: contiguous; KV4: page_size, or the contiguous capacity, is a multiple of 16 */
   int num_pages;     /* paged: pages in the pool */
   int max_nodes;     /* query rows (tree nodes) per sequence and attention call, 1..MEDUSA_MAX_NODES */
@@ -497,7 +498,7 @@ size_t medusa_cache_workspace_size(const medusa_cache* cache);
 medusa_status medusa_cache_get_status(const medusa_cache* cache, void* stream, uint32_t* flags);
 
 /* Rows for the cache.  k, v: element e of head h of row r at [r * row + h * head + e] (strides
- * in elements).  Items are the rows as they are appended; `rows` is how many item places there
+ * in elements; heads less than 2^31 bytes apart).  Items are the rows as they are appended; `rows` is how many item places there
  * are, and they belong to the sequences in one of two ways:
  *   packed  start: device [B+1], items start[b] .. start[b+1]-1 are sequence b's; places
  *           before start[0] and from start[B] on belong to none and are skipped

@@ -94,7 +94,7 @@ medusa_status check_cache(const medusa_cache_dims* d) {
   if (d->capacity < 1 || d->page_size < 0 || d->max_nodes < 1) return MEDUSA_ERR_INVALID;
   if (d->page_size > 0 && (d->capacity % d->page_size != 0 || d->num_pages < 1)) return MEDUSA_ERR_INVALID;
   if (d->dh != 32 && d->dh != 64 && d->dh != 128) return MEDUSA_ERR_UNSUPPORTED;
-  if (d->max_nodes > MEDUSA_MAX_NODES) return MEDUSA_ERR_UNSUPPORTED;
+  if (d->max_nodes > MEDUSA_MAX_NODES || d->capacity > MEDUSA_MAX_CAPACITY) return MEDUSA_ERR_UNSUPPORTED;
   if (d->format == MEDUSA_KV4 && (d->page_size > 0 ? d->page_size : d->capacity) % 16 != 0)
     return MEDUSA_ERR_UNSUPPORTED;
   return MEDUSA_OK;
@@ -109,7 +109,8 @@ medusa_status check_kv(const medusa_cache* c, const medusa_kv* kv, bool out) {
 }
 
 medusa_status check_scales(const medusa_cache* c, float gk, float gv) {
-  if (c->d.format == MEDUSA_KV4 && (!finite_pos(gk) || !finite_pos(gv))) return MEDUSA_ERR_INVALID;
+  auto ok = [](float g) { return g >= 1e-20f && g <= 1e20f; };
+  if (c->d.format == MEDUSA_KV4 && (!ok(gk) || !ok(gv))) return MEDUSA_ERR_INVALID;
   return MEDUSA_OK;
 }
 
@@ -139,6 +140,9 @@ template <typename T> medusa_status check_items(const medusa_cache* c, const T* 
   if (!r || !is_dtype(r->dtype) || r->rows < 0 || (r->rows > 0 && (!r->k || !r->v))) return MEDUSA_ERR_INVALID;
   if (!aligned(r->k, elem(r->dtype)) || !aligned(r->v, elem(r->dtype))) return MEDUSA_ERR_INVALID;
   if (r->k_row < 0 || r->k_head < 0 || r->v_row < 0 || r->v_head < 0) return MEDUSA_ERR_INVALID;
+  constexpr long long kApart = 1ll << 31;                  // heads lie less than this many bytes apart
+  if (r->k_head * (long long)elem(r->dtype) >= kApart || r->v_head * (long long)elem(r->dtype) >= kApart)
+    return MEDUSA_ERR_UNSUPPORTED;
   if (!r->start && (r->per_seq < 1 || (long long)r->per_seq * c->d.B != r->rows)) return MEDUSA_ERR_INVALID;
   m->rows = r->rows;
   m->per_seq = r->start ? 0 : r->per_seq;

@@ -13,7 +13,7 @@ namespace medusa {
 template <typename T>
 __device__ __forceinline__ void load_turned(const T* row, int d0, bool vec, const RopeTable& t, const float* cs,
                                             float (&f)[16]) {
-  load16(row + d0, vec, f);
+  load_n(row + d0, vec, f);
   if (!cs || d0 >= t.rot) return;
   const int h = t.rot / 2;
   if (t.layout == MEDUSA_ROPE_HALF) {
@@ -81,22 +81,41 @@ __device__ __forceinline__ const float* append_angles(const AppendArgs& a, int i
   if (lead) set_flag(a.c.status, MEDUSA_FLAG_POS_RANGE);
   return nullptr;
 }
-// 16 elements of head h from element 16 grp on into the cache.
-template <int FMT>
-__device__ __forceinline__ void put16(const CacheView& c, bool values, const Target& o, int h, int grp, float (&f)[16]) {
-  if (FMT == MEDUSA_KV4) {
-    uint8_t* block = static_cast<uint8_t*>(values ? c.v : c.k) + kv4_offset(c, o.unit, o.in, h);
-    const int slot = o.in % KV4_SLOTS;
+// 8 or 16 elements into the cache: at points to them in a plain cache, in a 4-bit one to their
+// codes, with sc at their group's scale.
+template <int FMT, int N>
+__device__ __forceinline__ void put(const CacheView& c, const Kv4Divisors& d, void* at, uint8_t* sc, const float (&f)[N]) {
+  if constexpr (FMT == MEDUSA_KV4) {
     uint2 codes;
     uint8_t scale;
-    if (!kv4_encode(f, values ? c.gv : c.gk, codes, scale)) set_flag(c.status, MEDUSA_FLAG_NONFINITE);
-    *reinterpret_cast<uint2*>(block + slot * (c.dh / 2) + grp * 8) = codes;
-    block[8 * c.dh + slot * (c.dh / 16) + grp] = scale;
-  } else if (FMT == MEDUSA_BF16) {
-    store16(static_cast<bf16*>(values ? c.v : c.k) + plain_offset(c, o.unit, o.in, h) + grp * 16, true, f);
+    if (!kv4_encode(f, d, codes, scale)) set_flag(c.status, MEDUSA_FLAG_NONFINITE);
+    *static_cast<uint2*>(at) = codes;
+    *sc = scale;
+  } else if constexpr (FMT == MEDUSA_BF16) {
+    store_n(static_cast<bf16*>(at), true, f);
   } else {
-    store16(static_cast<float*>(values ? c.v : c.k) + plain_offset(c, o.unit, o.in, h) + grp * 16, true, f);
+    store_n(static_cast<float*>(at), true, f);
   }
+}
+// The block's tables of divisors, for keys and values (256 threads; 4-bit format only).
+template <int FMT, int N> __device__ __forceinline__ void fill_divisors(const CacheView& c, float2 (&t)[2][N]) {
+  if constexpr (FMT == MEDUSA_KV4) {
+    t[threadIdx.x >> 7][threadIdx.x & 127] = kv4_divisor(threadIdx.x & 127, threadIdx.x >> 7 ? c.gv : c.gk);
+    __syncthreads();
+  }
+}
+template <int N> __device__ __forceinline__ Kv4Divisors divisors_of(const CacheView& c, const float2 (&t)[2][N], bool values) {
+  const float six = 6.f * (values ? c.gv : c.gk);
+  return {t[values ? 1 : 0], six, __frcp_rn(six)};
+}
+// Byte offset of slot `in` of a unit, head 0: its first element, or its block's first byte.
+template <int FMT> __device__ __forceinline__ long slot_bytes(const CacheView& c, long unit, int in) {
+  return FMT == MEDUSA_KV4 ? kv4_offset(c, unit, in, 0) : plain_offset(c, unit, in, 0) * (FMT == MEDUSA_BF16 ? 2 : 4);
+}
+// Bytes from a head to the next.
+template <int FMT> __device__ __forceinline__ long head_bytes(const CacheView& c) {
+  return FMT == MEDUSA_KV4 ? (long)((c.page_table ? c.page_size : c.capacity) / KV4_SLOTS) * kv4_block(c.dh)
+                           : (long)c.dh * (FMT == MEDUSA_BF16 ? 2 : 4);
 }
 __device__ __forceinline__ void append_lengths(const CacheView& c, const ItemMap& m, long tid, long threads) {
   if (c.len_out == c.len) return;
@@ -104,73 +123,178 @@ __device__ __forceinline__ void append_lengths(const CacheView& c, const ItemMap
     c.len_out[b] = min(clamp_len(c, c.len[b]) + item_count(m, (int)b), c.capacity);
 }
 
-// 16 angles of a row of the table from pair p0 on.
-__device__ __forceinline__ void load_angles(const float* cs, int p0, int h, float (&c)[16], float (&s)[16]) {
+// How warps share rows x (keys, values): a warp takes `places` rows of one kind and every
+// slices-th 32 tasks of them, tasks being numbered (head, row, piece of a head): four rows of a
+// 4-bit cache fill whole sectors of codes and of scales.
+constexpr int KV_PLACES = 4;
+struct WarpShare {
+  int places, slices;
+};
+// Many rows: several a warp, so that finding them (three dependent loads, one lane a row) is
+// paid once; few rows: a row over several warps.
+static WarpShare warp_share(long rows, int tasks) {
+  const long wave = 152l * 48;                         // warps that keep the GPU busy
+  if (rows * 2 >= wave * KV_PLACES) return {KV_PLACES, 1};
+  const int most = (tasks + 31) / 32;
+  const long want = wave / (rows * 2 > 0 ? rows * 2 : 1);
+  return {1, (int)(want < 1 ? 1 : want < most ? want : most)};
+}
+// A warp's place in that numbering: task e0 + lane, then every step-th.
+struct TaskWalk {
+  int u, j, h, du, dj, dh, tasks, places;
+  __device__ __forceinline__ TaskWalk(int e, int step, int tasks_, int places_) : tasks(tasks_), places(places_) {
+    u = e % tasks;
+    j = e / tasks % places;
+    h = e / tasks / places;
+    du = step % tasks;
+    dj = step / tasks % places;
+    dh = step / tasks / places;
+  }
+  __device__ __forceinline__ void next() {
+    u += du;
+    j += dj;
+    h += dh;
+    if (u >= tasks) { u -= tasks; ++j; }
+    if (j >= places) { j -= places; ++h; }
+  }
+};
+// A row found: its elements outside the cache, its slot in it (head 0: elements, or codes and
+// scales), its angles.  Heads are less than 2^31 bytes apart everywhere (checked by the caller).
+struct PlaceInfo {
+  char* rows;             // null: no such row
+  char* at;
+  char* sc;
+  const float* cs;
+};
+template <int FMT>
+__device__ __forceinline__ PlaceInfo place_info(const CacheView& c, const void* pool, long unit, int in) {
+  PlaceInfo p;
+  p.rows = nullptr;
+  p.cs = nullptr;
+  p.at = const_cast<char*>(static_cast<const char*>(pool)) + slot_bytes<FMT>(c, unit, in);
+  p.sc = p.at + 8 * c.dh + in % KV4_SLOTS * (c.dh / 16);
+  if (FMT == MEDUSA_KV4) p.at += in % KV4_SLOTS * (c.dh / 2);
+  return p;
+}
+
+// Two pairs turned: (x1, x2) -> (x1 c - x2 s, x2 c + x1 s), each operation rounded by itself.
+__device__ __forceinline__ void turn2(F2 c, F2 s, float* x1, float* x2) {
+  const F2 a = f2(x1[0], x1[1]), b = f2(x2[0], x2[1]);
+  unf2(fma2(mul2(b, s), f2(-1.f, -1.f), mul2(a, c)), x1[0], x1[1]);
+  unf2(add2(mul2(b, c), mul2(a, s)), x2[0], x2[1]);
+}
+template <int N> struct Raw16 {
+  uint4 v[N];
+};
+template <typename T, int N> __device__ __forceinline__ void load_raw(const char* p, Raw16<N * sizeof(T) / 16>& r) {
 #pragma unroll
-  for (int e = 0; e < 16; e += 4) {
-    const float4 x = *reinterpret_cast<const float4*>(cs + p0 + e), y = *reinterpret_cast<const float4*>(cs + h + p0 + e);
-    c[e] = x.x; c[e + 1] = x.y; c[e + 2] = x.z; c[e + 3] = x.w;
-    s[e] = y.x; s[e + 1] = y.y; s[e + 2] = y.z; s[e + 3] = y.w;
+  for (int i = 0; i < (int)(N * sizeof(T) / 16); ++i) r.v[i] = reinterpret_cast<const uint4*>(p)[i];
+}
+template <typename T, int N> __device__ __forceinline__ void unpack_raw(const Raw16<N * sizeof(T) / 16>& r, float (&f)[N]) {
+  constexpr int E = 16 / sizeof(T);
+#pragma unroll
+  for (int i = 0; i < N / E; ++i) {
+    float t[E];
+    unpack16(r.v[i], t);
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[E * i + e] = t[e];
   }
 }
 
 // Aligned rows whose rotation pairs whole groups of 16 elements (HALF with rot a multiple of
-// 32, or INTERLEAVED with rot one of 16, or none): a warp takes one item's keys or its values,
-// found once for the warp, and its lanes go over the heads' groups; with HALF a lane takes a
-// group and its partner, so that every key and angle is read once.
+// 32, or INTERLEAVED with rot one of 16, or none).  A task is N elements of a head, with HALF
+// together with their partners, so that every key and angle is read once: a group of 16 for the
+// 4-bit format, 8 for the others (whole 16 or 32 bytes written by neighbouring lanes).  The next
+// task's elements are under way while one is encoded.
 template <typename T, int FMT>
-__global__ void __launch_bounds__(256) kv_append_vec_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(256, 3) kv_append_vec_kernel(const __grid_constant__ AppendArgs a, const WarpShare ws) {
+  constexpr int N = FMT == MEDUSA_KV4 ? 16 : 8, ES = FMT == MEDUSA_F32 ? 4 : 2;
+  using Raw = Raw16<N * sizeof(T) / 16>;
+  __shared__ PlaceInfo info[8][KV_PLACES];
+  __shared__ float2 table[2][FMT == MEDUSA_KV4 ? 128 : 1];
   const CacheView& c = a.c;
-  const int lane = threadIdx.x & 31, groups = c.dh / 16, h2 = a.t.rot / 2;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h2 = a.t.rot / 2;
+  fill_divisors<FMT>(c, table);
   append_lengths(c, a.m, (long)blockIdx.x * blockDim.x + threadIdx.x, (long)gridDim.x * blockDim.x);
-  const long wid = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int i = (int)(wid >> 1);
+  long wid = (long)blockIdx.x * 8 + warp;
+  const int slice = (int)(wid % ws.slices);
+  wid /= ws.slices;
   const bool values = wid & 1;
-  if (i >= a.m.rows) return;
-  const int2 it = item_of_warp(a.m, c.B, i);
-  Target o;
-  const bool lead = lane == 0 && !values;
-  if (!append_target(a, i, it, lead, o)) return;
-  const T* src = values ? static_cast<const T*>(a.v) + o.row * a.v_row : static_cast<const T*>(a.k) + o.row * a.k_row;
-  const long head = values ? a.v_head : a.k_head;
-  const float* cs = values ? nullptr : append_angles(a, i, o.t, lead);
-  const bool half = cs && a.t.layout == MEDUSA_ROPE_HALF;
-  // tasks of a head: pairs of groups, then single groups
-  const int pairs = half ? a.t.rot / 32 : 0, tasks = half ? groups - pairs : groups;
-  const int n = c.Hkv * tasks;
-  for (int e = lane; e < n; e += 32) {
-    const int h = e / tasks, u = e - h * tasks;
-    const T* row = src + h * head;
-    const int g0 = u < pairs ? u : pairs + u;
-    float f[16];
-    load16(row + g0 * 16, true, f);
-    if (u < pairs) {
-      float f2[16], cc[16], ss[16];
-      load16(row + g0 * 16 + h2, true, f2);
-      load_angles(cs, g0 * 16, h2, cc, ss);
+  const int i0 = (int)(wid >> 1) * ws.places;
+  if (i0 >= a.m.rows) return;
+  if (lane < ws.places) {
+    const bool lead = !values && slice == 0;
+    PlaceInfo p{};
+    Target o;
+    if (i0 + lane < a.m.rows && append_target(a, i0 + lane, item_of(a.m, c.B, i0 + lane), lead, o)) {
+      p = place_info<FMT>(c, values ? c.v : c.k, o.unit, o.in);
+      p.rows = const_cast<char*>(static_cast<const char*>(values ? a.v : a.k)) +
+               o.row * (values ? a.v_row : a.k_row) * (long)sizeof(T);
+      if (!values) p.cs = append_angles(a, i0 + lane, o.t, lead);
+    }
+    info[warp][lane] = p;
+  }
+  __syncwarp();
+  const int head_b = (int)((values ? a.v_head : a.k_head) * (long)sizeof(T)), step = (int)head_bytes<FMT>(c);
+  // tasks of a row's head: pairs of pieces (rows that are not turned copy both), then single ones
+  const bool half = a.turn && !values && a.t.layout == MEDUSA_ROPE_HALF;
+  const int pairs = half ? h2 / N : 0, tasks = c.dh / N - pairs;
+  const Kv4Divisors dv = divisors_of(c, table, values);
+  TaskWalk w(32 * slice + lane, 32 * ws.slices, tasks, ws.places);
+  Raw ahead, ahead2;
+  auto fetch = [&]() {                     // the task's elements, if there is such a task
+    while (w.h < c.Hkv && !info[warp][w.j].rows) w.next();
+    if (w.h >= c.Hkv) return;
+    const char* x = info[warp][w.j].rows + (long)w.h * head_b + N * (int)sizeof(T) * (w.u < pairs ? w.u : w.u + pairs);
+    load_raw<T, N>(x, ahead);
+    if (w.u < pairs) load_raw<T, N>(x + h2 * sizeof(T), ahead2);
+  };
+  fetch();
+  while (w.h < c.Hkv) {
+    const PlaceInfo& p = info[warp][w.j];
+    const bool paired = w.u < pairs;
+    const int d0 = N * (paired ? w.u : w.u + pairs);
+    char* at = p.at + (long)w.h * step + (FMT == MEDUSA_KV4 ? d0 / 2 : d0 * ES);
+    uint8_t* sc = reinterpret_cast<uint8_t*>(p.sc) + (long)w.h * step + d0 / 16;      // 4-bit only
+    const float* cs = p.cs;
+    float f[N], g[N];
+    unpack_raw<T, N>(ahead, f);
+    if (paired) unpack_raw<T, N>(ahead2, g);
+    w.next();
+    fetch();
+    if (paired) {
+      if (cs) {
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float x1 = f[k], x2 = f2[k];
-        f[k] = __fsub_rn(__fmul_rn(x1, cc[k]), __fmul_rn(x2, ss[k]));
-        f2[k] = __fadd_rn(__fmul_rn(x2, cc[k]), __fmul_rn(x1, ss[k]));
+        for (int k4 = 0; k4 < N; k4 += 4) {
+          float ck[4], sk[4];
+          load_n(cs + d0 + k4, true, ck);
+          load_n(cs + h2 + d0 + k4, true, sk);
+#pragma unroll
+          for (int k = 0; k < 4; k += 2) turn2(f2(ck[k], ck[k + 1]), f2(sk[k], sk[k + 1]), f + k4 + k, g + k4 + k);
+        }
       }
-      put16<FMT>(c, values, o, h, g0 + pairs, f2);
-    } else if (cs && !half && g0 * 16 < a.t.rot) {
+      put<FMT, N>(c, dv, at + (FMT == MEDUSA_KV4 ? h2 / 2 : h2 * ES), sc + h2 / 16, g);
+    } else if (cs && !half && d0 < a.t.rot) {
+      float ck[N / 2], sk[N / 2];
+      load_n(cs + d0 / 2, true, ck);
+      load_n(cs + h2 + d0 / 2, true, sk);
 #pragma unroll
-      for (int k = 0; k < 16; k += 2) {
-        const float ck = cs[g0 * 8 + k / 2], sk = cs[h2 + g0 * 8 + k / 2], x1 = f[k], x2 = f[k + 1];
-        f[k] = __fsub_rn(__fmul_rn(x1, ck), __fmul_rn(x2, sk));
-        f[k + 1] = __fadd_rn(__fmul_rn(x2, ck), __fmul_rn(x1, sk));
+      for (int k = 0; k < N; k += 2) {
+        const float x1 = f[k], x2 = f[k + 1];
+        f[k] = __fsub_rn(__fmul_rn(x1, ck[k / 2]), __fmul_rn(x2, sk[k / 2]));
+        f[k + 1] = __fadd_rn(__fmul_rn(x2, ck[k / 2]), __fmul_rn(x1, sk[k / 2]));
       }
     }
-    put16<FMT>(c, values, o, h, g0, f);
+    put<FMT, N>(c, dv, at, sc, f);
   }
 }
 
 // Any alignment and any rotation: one thread per (item, keys or values, head, 16 elements).
 template <typename T, int FMT>
 __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ AppendArgs a) {
+  __shared__ float2 table[2][FMT == MEDUSA_KV4 ? 128 : 1];
   const CacheView& c = a.c;
+  fill_divisors<FMT>(c, table);
   const int groups = c.dh / 16;
   const long tid = (long)blockIdx.x * blockDim.x + threadIdx.x;
   append_lengths(c, a.m, tid, (long)gridDim.x * blockDim.x);
@@ -187,12 +311,16 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
     if (!append_target(a, i, item_of(a.m, c.B, i), lead, o)) continue;
     float f[16];
     if (values) {
-      load16(static_cast<const T*>(a.v) + o.row * a.v_row + h * a.v_head + grp * 16, a.vec, f);
+      load_n(static_cast<const T*>(a.v) + o.row * a.v_row + h * a.v_head + grp * 16, a.vec, f);
     } else {
       const float* cs = append_angles(a, i, o.t, lead);
       load_turned(static_cast<const T*>(a.k) + o.row * a.k_row + h * a.k_head, grp * 16, a.vec, a.t, cs, f);
     }
-    put16<FMT>(c, values, o, h, grp, f);
+    char* at = static_cast<char*>(values ? c.v : c.k) + slot_bytes<FMT>(c, o.unit, o.in) + h * head_bytes<FMT>(c);
+    const int slot = o.in % KV4_SLOTS;
+    uint8_t* sc = reinterpret_cast<uint8_t*>(at) + 8 * c.dh + slot * groups + grp;
+    at += FMT == MEDUSA_KV4 ? slot * (c.dh / 2) + grp * 8 : grp * (FMT == MEDUSA_BF16 ? 32 : 64);
+    put<FMT, 16>(c, divisors_of(c, table, values), at, sc, f);
   }
 }
 
@@ -208,8 +336,9 @@ static cudaError_t append_go(const AppendArgs& a, int format, cudaStream_t st) {
   if (a.vec && (!a.turn || a.t.rot % (a.t.layout == MEDUSA_ROPE_HALF ? 32 : 16) == 0)) {
     auto kern = format == MEDUSA_KV4 ? kv_append_vec_kernel<T, MEDUSA_KV4>
                 : format == MEDUSA_BF16 ? kv_append_vec_kernel<T, MEDUSA_BF16> : kv_append_vec_kernel<T, MEDUSA_F32>;
-    const unsigned ctas = (unsigned)(((long)a.m.rows * 2 + 7) / 8);
-    return launch_kernel(kern, dim3(ctas ? ctas : 1), dim3(256), 0, st, 1, a);
+    const WarpShare ws = warp_share(a.m.rows, a.c.Hkv * (a.c.dh / (format == MEDUSA_KV4 ? 16 : 8)));
+    const long warps = (long)(a.m.rows + ws.places - 1) / ws.places * 2 * ws.slices;
+    return launch_kernel(kern, dim3((unsigned)(warps < 1 ? 1 : (warps + 7) / 8)), dim3(256), 0, st, 1, a, ws);
   }
   const long n = (long)a.m.rows * 2 * a.c.Hkv * (a.c.dh / 16);
   const long want = (n + 255) / 256;
@@ -225,68 +354,81 @@ cudaError_t launch_kv_append(const AppendArgs& a, int src_dtype, int format, cud
   return launch_kernel(kv_length_kernel, dim3((a.c.B + 255) / 256), dim3(256), 0, st, 1, a.c, a.m);
 }
 
-// A warp takes one place's keys or its values, found once for the warp; its lanes go over the
-// heads' groups of 16 elements, UNROLL at a time with all loads before the first use.
+// A task is 16 bytes of the result; a lane has UNROLL of them under way.
 template <typename T, int FMT>
-__global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ ReadArgs a) {
-  constexpr int UNROLL = FMT == MEDUSA_KV4 ? 4 : 1;
+__global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ ReadArgs a, const WarpShare ws) {
+  constexpr int N = 16 / sizeof(T), UNROLL = 4, ES = FMT == MEDUSA_F32 ? 4 : 2;
+  __shared__ PlaceInfo info[8][KV_PLACES];
   const CacheView& c = a.c;
-  const int lane = threadIdx.x & 31, groups = c.dh / 16;
-  const long wid = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int i = (int)(wid >> 1);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long wid = (long)blockIdx.x * 8 + warp;
+  const int slice = (int)(wid % ws.slices);
+  wid /= ws.slices;
   const bool values = wid & 1;
-  if (i >= a.m.rows) return;
-  const int2 it = item_of_warp(a.m, c.B, i);
-  if (it.x < 0) return;
-  const long t = (long)it.y + (a.first ? a.first[it.x] : 0);
-  uint32_t flag = 0;
-  long unit = 0;
-  int in = 0;
-  if (t < 0 || t >= clamp_len(c, c.len[it.x])) flag = MEDUSA_FLAG_KV_CAPACITY;
-  else if (!unit_of(c, it.x, (int)t, unit, in)) flag = MEDUSA_FLAG_PAGE_RANGE;
-  if (flag) {
-    if (lane == 0) set_flag(c.status, flag);
-    return;
+  const int i0 = (int)(wid >> 1) * ws.places;
+  if (i0 >= a.m.rows) return;
+  if (lane < ws.places) {
+    PlaceInfo p{};
+    const int2 it = i0 + lane < a.m.rows ? item_of(a.m, c.B, i0 + lane) : make_int2(-1, 0);
+    if (it.x >= 0) {
+      const long t = (long)it.y + (a.first ? a.first[it.x] : 0);
+      long unit;
+      int in;
+      uint32_t flag = 0;
+      if (t < 0 || t >= clamp_len(c, c.len[it.x])) flag = MEDUSA_FLAG_KV_CAPACITY;
+      else if (!unit_of(c, it.x, (int)t, unit, in)) flag = MEDUSA_FLAG_PAGE_RANGE;
+      if (flag) {
+        if (!values && slice == 0) set_flag(c.status, flag);
+      } else {
+        p = place_info<FMT>(c, values ? c.v : c.k, unit, in);
+        p.rows = static_cast<char*>(values ? a.v : a.k) + (long)(i0 + lane) * (values ? a.v_row : a.k_row) * (long)sizeof(T);
+      }
+    }
+    info[warp][lane] = p;
   }
-  T* dst = values ? static_cast<T*>(a.v) + i * a.v_row : static_cast<T*>(a.k) + i * a.k_row;
-  const long head = values ? a.v_head : a.k_head;
-  const void* pool = values ? c.v : c.k;
+  __syncwarp();
+  const int head_b = (int)((values ? a.v_head : a.k_head) * (long)sizeof(T)), step = (int)head_bytes<FMT>(c);
   const float g = values ? c.gv : c.gk;
-  const int n = c.Hkv * groups, slot = in % KV4_SLOTS;
-  const uint8_t* block0 = static_cast<const uint8_t*>(pool) + kv4_offset(c, unit, in, 0);
-  const long step = (long)((c.page_table ? c.page_size : c.capacity) / KV4_SLOTS) * kv4_block(c.dh);   // to the next head
-  for (int e0 = lane; e0 < n; e0 += 32 * UNROLL) {
-    uint2 codes[UNROLL];
+  TaskWalk w(32 * slice + lane, 32 * ws.slices, c.dh / N, ws.places);
+  while (w.h < c.Hkv) {
+    uint32_t codes[UNROLL];
     uint8_t scale[UNROLL];
-    if (FMT == MEDUSA_KV4) {
+    float f[UNROLL][N];
+    T* dst[UNROLL];
 #pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
-        const int e = e0 + 32 * u, h = e / groups, grp = e - h * groups;
-        if (e >= n) break;
-        const uint8_t* block = block0 + h * step;
-        codes[u] = *reinterpret_cast<const uint2*>(block + slot * (c.dh / 2) + grp * 8);
-        scale[u] = block[8 * c.dh + slot * groups + grp];
+    for (int u = 0; u < UNROLL; ++u, w.next()) {
+      dst[u] = nullptr;
+      if (w.h >= c.Hkv) continue;
+      const PlaceInfo& p = info[warp][w.j];
+      if (!p.rows) continue;
+      const int d0 = w.u * N;
+      const char* at = p.at + (long)w.h * step;
+      dst[u] = reinterpret_cast<T*>(p.rows + (long)w.h * head_b) + d0;
+      if (FMT == MEDUSA_KV4) {
+        codes[u] = N == 8 ? *reinterpret_cast<const uint32_t*>(at + d0 / 2) : *reinterpret_cast<const uint16_t*>(at + d0 / 2);
+        scale[u] = static_cast<uint8_t>(p.sc[(long)w.h * step + d0 / 16]);
+      } else if (FMT == MEDUSA_BF16) {
+        load_n(reinterpret_cast<const bf16*>(at + d0 * ES), N == 8, f[u]);
+      } else {
+        load_n(reinterpret_cast<const float*>(at + d0 * ES), true, f[u]);
       }
     }
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
-      const int e = e0 + 32 * u, h = e / groups, grp = e - h * groups;
-      if (e >= n) break;
-      float f[16];
-      if (FMT == MEDUSA_KV4) kv4_decode(codes[u], scale[u], g, f);
-      else if (FMT == MEDUSA_BF16) load16(static_cast<const bf16*>(pool) + plain_offset(c, unit, in, h) + grp * 16, true, f);
-      else load16(static_cast<const float*>(pool) + plain_offset(c, unit, in, h) + grp * 16, true, f);
-      store16(dst + h * head + grp * 16, a.vec, f);
+      if (!dst[u]) continue;
+      if (FMT == MEDUSA_KV4) kv4_decode<N>(codes[u], scale[u], g, f[u]);
+      store_n(dst[u], a.vec, f[u]);
     }
   }
 }
 
 template <typename T>
 static cudaError_t read_go(const ReadArgs& a, int format, cudaStream_t st) {
-  const unsigned ctas = (unsigned)(((long)a.m.rows * 2 + 7) / 8);
+  const WarpShare ws = warp_share(a.m.rows, a.c.Hkv * a.c.dh * (int)sizeof(T) / 16);
+  const long warps = (long)(a.m.rows + ws.places - 1) / ws.places * 2 * ws.slices;
   auto kern = format == MEDUSA_KV4 ? kv_read_kernel<T, MEDUSA_KV4>
               : format == MEDUSA_BF16 ? kv_read_kernel<T, MEDUSA_BF16> : kv_read_kernel<T, MEDUSA_F32>;
-  return launch_kernel(kern, dim3(ctas), dim3(256), 0, st, 1, a);
+  return launch_kernel(kern, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st, 1, a, ws);
 }
 
 cudaError_t launch_kv_read(const ReadArgs& a, int dst_dtype, int format, cudaStream_t st) {

@@ -28,21 +28,6 @@ __device__ __forceinline__ int2 item_of(const ItemMap& m, int B, int i) {
   const int s0 = m.start[lo];
   return make_int2(i >= s0 && i < m.start[lo + 1] ? lo : -1, i - s0);
 }
-// The same with the whole warp on one item: 32 sequences' offsets at a time.
-__device__ __forceinline__ int2 item_of_warp(const ItemMap& m, int B, int i) {
-  if (!m.start) return item_of(m, B, i);
-  const int lane = threadIdx.x & 31;
-  for (int b0 = 0; b0 < B; b0 += 32) {
-    const int b = b0 + lane;
-    const int s0 = b < B ? m.start[b] : 0, s1 = b < B ? m.start[b + 1] : 0;
-    const uint32_t hit = __ballot_sync(0xffffffffu, b < B && i >= s0 && i < s1);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      return make_int2(b0 + l, i - __shfl_sync(0xffffffffu, s0, l));
-    }
-  }
-  return make_int2(-1, 0);
-}
 __device__ __forceinline__ int item_count(const ItemMap& m, int b) {
   const int n = m.start ? m.start[b + 1] - m.start[b] : (m.count ? min(m.count[b], m.per_seq) : m.per_seq);
   return max(n, 0);
@@ -75,11 +60,11 @@ __device__ __forceinline__ long kv4_offset(const CacheView& c, long unit, int in
   return ((unit * c.Hkv + h) * per + in / KV4_SLOTS) * kv4_block(c.dh);
 }
 
-// 16 consecutive elements, in 16-byte units when vec.
-__device__ __forceinline__ void load16(const bf16* p, bool vec, float (&f)[16]) {
+// N consecutive elements (whole 16-byte units), vec: 16-byte aligned.
+template <int N> __device__ __forceinline__ void load_n(const bf16* p, bool vec, float (&f)[N]) {
   if (vec) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < N / 8; ++i) {
       float t[8];
       unpack16(reinterpret_cast<const uint4*>(p)[i], t);
 #pragma unroll
@@ -87,45 +72,71 @@ __device__ __forceinline__ void load16(const bf16* p, bool vec, float (&f)[16]) 
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) f[e] = to_f32(p[e]);
+    for (int e = 0; e < N; ++e) f[e] = to_f32(p[e]);
   }
 }
-__device__ __forceinline__ void load16(const float* p, bool vec, float (&f)[16]) {
+template <int N> __device__ __forceinline__ void load_n(const float* p, bool vec, float (&f)[N]) {
   if (vec) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N / 4; ++i) {
       const float4 t = reinterpret_cast<const float4*>(p)[i];
       f[4 * i] = t.x; f[4 * i + 1] = t.y; f[4 * i + 2] = t.z; f[4 * i + 3] = t.w;
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) f[e] = p[e];
+    for (int e = 0; e < N; ++e) f[e] = p[e];
   }
 }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&p);
 }
-__device__ __forceinline__ void store16(bf16* p, bool vec, const float (&f)[16]) {
+template <int N> __device__ __forceinline__ void store_n(bf16* p, bool vec, const float (&f)[N]) {
   if (vec) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < N / 8; ++i)
       reinterpret_cast<uint4*>(p)[i] = make_uint4(pack2(f[8 * i], f[8 * i + 1]), pack2(f[8 * i + 2], f[8 * i + 3]),
                                                   pack2(f[8 * i + 4], f[8 * i + 5]), pack2(f[8 * i + 6], f[8 * i + 7]));
   } else {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) p[e] = from_f32<bf16>(f[e]);
+    for (int e = 0; e < N; ++e) p[e] = from_f32<bf16>(f[e]);
   }
 }
-__device__ __forceinline__ void store16(float* p, bool vec, const float (&f)[16]) {
+template <int N> __device__ __forceinline__ void store_n(float* p, bool vec, const float (&f)[N]) {
   if (vec) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < N / 4; ++i)
       reinterpret_cast<float4*>(p)[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
   } else {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) p[e] = f[e];
+    for (int e = 0; e < N; ++e) p[e] = f[e];
   }
+}
+
+// Two floats in one register pair: each half is one IEEE operation, as by itself.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unf2(F2 a, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v)); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
 }
 
 // Eight floats to a word of e2m1 codes (nearest, ties to even, 6 at most).
@@ -141,44 +152,55 @@ __device__ __forceinline__ uint32_t e2m1x8(const float* y) {
       : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
   return w;
 }
+// Magnitude bits of the largest of 16; a NaN stays one, which fmaxf would drop.
+__device__ __forceinline__ uint32_t largest_bits(const float (&f)[16]) {
+  float m = fabsf(f[0]);
+#pragma unroll
+  for (int e = 1; e < 15; e += 2)
+    asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(fabsf(f[e])), "f"(fabsf(f[e + 1])));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(f[15])));
+  return __float_as_uint(m);
+}
+// What one number's 16-element groups are divided by: for each e4m3 scale byte, s = e4m3 * g and
+// its correctly rounded reciprocal (0 for 0), in shared memory; and 6 g with its reciprocal.
+struct Kv4Divisors {
+  const float2* by_scale;                   // [128] (s, 1/s)
+  float six, inv_six;
+};
+__device__ __forceinline__ float2 kv4_divisor(uint32_t byte, float g) {
+  const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3))) * g;
+  return make_float2(s, s > 0.f ? __frcp_rn(s) : 0.f);
+}
 // 16 elements -> 8 bytes of e2m1 pairs and one e4m3 scale.  The scale is the nearest e4m3 to
 // max|x| / (6 g), each code the nearest to x / (g s): the correctly rounded quotients, because a
 // bf16 element divided by a 4-bit scale is often exactly half way between two codes, and a
 // quotient off by one unit in the last place would send it the wrong way.  16 divisions took
-// longer than the group's memory traffic, so the quotients come from one correctly rounded
+// longer than the group's memory traffic, so the quotients come from a correctly rounded
 // reciprocal r and Markstein's correction (IBM J. Res. Dev. 34, 1990): q = x r, then
 // q + r (x - q s) with the residual exact in one fused multiply-add is the rounded quotient.
-__device__ __forceinline__ bool kv4_encode(float (&x)[16], float g, uint2& codes, uint8_t& scale) {
-  uint32_t bits = 0;                        // of the largest magnitude; NaN above all
-#pragma unroll
-  for (int e = 0; e < 16; ++e) bits = max(bits, __float_as_uint(x[e]) & 0x7fffffffu);
+// (g lies in 1e-20..1e20, so residuals neither vanish nor overflow where they matter.)
+__device__ __forceinline__ bool kv4_encode(const float (&x)[16], const Kv4Divisors& d, uint2& codes, uint8_t& scale) {
+  const uint32_t bits = largest_bits(x);
   if (bits >= 0x7f800000u) {                // the whole group reads back as NaN
     codes = make_uint2(0x22222222u, 0x22222222u);
     scale = 0x7f;
     return false;
   }
-  scale = __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(bits), 6.f * g), __NV_SATFINITE, __NV_E4M3);
-  const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(scale, __NV_E4M3))) * g;
-  if (s > 1e-25f && s < 1e25f) {            // residuals neither vanish nor overflow
-    const float r = __frcp_rn(s);
+  const float top = __uint_as_float(bits), q = top * d.inv_six;
+  scale = __nv_cvt_float_to_fp8(fmaf(fmaf(-q, d.six, top), d.inv_six, q), __NV_SATFINITE, __NV_E4M3);
+  const float2 sr = d.by_scale[scale];
+  const F2 s = f2(-sr.x, -sr.x), r = f2(sr.y, sr.y);
+  float y[16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float q = x[e] * r;
-      x[e] = fmaf(fmaf(-q, s, x[e]), r, q);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = s > 0.f ? __fdiv_rn(x[e], s) : 0.f;
+  for (int e = 0; e < 16; e += 2) {
+    const F2 v = f2(x[e], x[e + 1]), w = mul2(v, r);
+    unf2(fma2(fma2(w, s, v), r, w), y[e], y[e + 1]);
   }
-  codes = make_uint2(e2m1x8(x), e2m1x8(x + 8));
+  codes = make_uint2(e2m1x8(y), e2m1x8(y + 8));
   return true;
 }
 
-// Two e2m1 codes (one byte) as halves, exactly.
-__device__ __forceinline__ __half2 kv4_pair(uint32_t byte) {
-  return __half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)byte, __NV_E2M1));
-}
-// The four bytes of a word, two codes each.
+// The four bytes of a word, two e2m1 codes each, as halves (exactly).
 __device__ __forceinline__ void kv4_pairs(uint32_t w, __half2 (&y)[4]) {
   uint32_t* r = reinterpret_cast<uint32_t*>(y);
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
@@ -197,15 +219,16 @@ __device__ __forceinline__ __half2 kv4_scales(uint16_t s) {
 // An e4m3 scale as a half, exactly (NaN for a group that held none of the numbers).
 __device__ __forceinline__ __half kv4_scale(uint8_t s) { return __half(__nv_cvt_fp8_to_halfraw(s, __NV_E4M3)); }
 
-// What 16 elements of a block stand for: e2m1 * e4m3 is exact in a half (6 bits, 2^-10..2688).
-__device__ __forceinline__ void kv4_decode(uint2 codes, uint8_t scale, float g, float (&f)[16]) {
-  const __half2 s2 = __half2half2(kv4_scale(scale));
-  const uint32_t w[2] = {codes.x, codes.y};
+// What N elements of a group stand for: codes are exact halves, the group's factor is one float.
+template <int N> __device__ __forceinline__ void kv4_decode(uint32_t codes, uint8_t scale, float g, float (&f)[N]) {
+  const float s = __half2float(kv4_scale(scale)) * g;
+  __half2 y[4];
+  kv4_pairs(codes, y);
+  const F2 s2 = f2(s, s);
 #pragma unroll
-  for (int e = 0; e < 16; e += 2) {
-    const float2 v = __half22float2(__hmul2(kv4_pair((w[e >> 3] >> (4 * (e & 7))) & 0xffu), s2));
-    f[e] = v.x * g;
-    f[e + 1] = v.y * g;
+  for (int e = 0; e < N; e += 2) {
+    const float2 v = __half22float2(y[e / 2]);
+    unf2(mul2(f2(v.x, v.y), s2), f[e], f[e + 1]);
   }
 }
 
