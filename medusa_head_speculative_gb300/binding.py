@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 import numpy as np
 
@@ -74,11 +75,6 @@ class RopeDesc(C.Structure):
     _fields_ = [("rot", C.c_int), ("layout", C.c_int), ("max_pos", C.c_int), ("scaling", C.c_int),
                 ("base", C.c_double), ("factor", C.c_double), ("orig_pos", C.c_double),
                 ("low", C.c_double), ("high", C.c_double), ("attn", C.c_double)]
-
-
-class RopeRows(C.Structure):
-    _fields_ = [("x", C.c_void_p), ("y", C.c_void_p), ("heads", C.c_int), ("x_row", C.c_longlong),
-                ("x_head", C.c_longlong), ("y_row", C.c_longlong), ("y_head", C.c_longlong)]
 
 
 class CacheDims(C.Structure):
@@ -160,7 +156,7 @@ def lib():
         "medusa_rope_create": (I, [C.POINTER(RopeDesc), C.POINTER(P)]),
         "medusa_rope_destroy": (None, [P]),
         "medusa_rope_get_status": (I, [P, P, C.POINTER(C.c_uint32)]),
-        "medusa_rope_apply": (I, [P, I, I, I, P, C.POINTER(RopeRows), I, I, P]),
+        "medusa_rope_apply": (I, [P, I, I, I, P, C.c_char_p, I, I, P]),   # medusa_rope_rows as bytes
         "medusa_cache_create": (I, [C.POINTER(CacheDims), C.POINTER(P)]),
         "medusa_cache_destroy": (None, [P]),
         "medusa_cache_pool_bytes": (SZ, [P]),
@@ -188,10 +184,23 @@ def ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_current = None     # address of the current device's current stream
+
+
 def _stream(stream):
-    import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    global _current
+    if _current is None:
+        import torch
+        try:        # a Stream object takes longer to make than a kernel to launch
+            raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            _current = lambda: raw(device())  # noqa: E731
+            torch.cuda.current_stream()       # (initialises CUDA)
+            _current()
+        except (AttributeError, TypeError):
+            _current = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _current()
 
 
 # ------------------------------------------------------------------ host tree builders
@@ -456,37 +465,56 @@ def _status(fn, handle, stream):
     return flags.value
 
 
-_DTYPES = {}
+# These calls are made once a layer and token, where the host's part is what takes time: each
+# tensor is asked once for its shape, strides, dtype and device.
+_DTYPES = {}        # torch dtype -> F32 or BF16; _INT32: torch.int32
+_INT32 = None
 
 
-def _dtype(*tensors):
-    """F32 or BF16, the same for every tensor given (None: none)."""
+def _load_dtypes():
+    global _INT32
+    import torch
+    _DTYPES.update({torch.float32: F32, torch.bfloat16: BF16})
+    _INT32 = torch.int32
+
+
+def _dtype(x):
     if not _DTYPES:
-        import torch
-        _DTYPES.update({torch.float32: F32, torch.bfloat16: BF16})
-    t = _DTYPES.get(tensors[0].dtype)
-    if t is None or any(x is not None and x.dtype != tensors[0].dtype for x in tensors[1:]):
-        raise TypeError("float32 or bfloat16 tensors of one dtype are needed: "
-                        + ", ".join(str(x.dtype) for x in tensors if x is not None))
+        _load_dtypes()
+    t = _DTYPES.get(x.dtype)
+    if t is None:
+        raise TypeError(f"float32 or bfloat16 is needed, got {x.dtype}")
     return t
 
 
-def _ints(what, t, n):
+def _same(x, *others):
+    """The others (None: none) have x's dtype and device."""
+    t, d = x.dtype, x.get_device()
+    for y in others:
+        if y is not None and (y.dtype != t or y.get_device() != d):
+            raise TypeError(f"tensors of one dtype on one device are needed: {t} on {x.device}, "
+                            f"{y.dtype} on {y.device}")
+
+
+def _ints(what, t, n, device):
     """Address of an int32 tensor of at least n entries in order, or None."""
     if t is None:
         return None
-    if t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous() or t.numel() < n:
-        raise ValueError(f"{what}: a contiguous int32 tensor of at least {n} entries is needed")
+    if _INT32 is None:
+        _load_dtypes()
+    if t.dtype is not _INT32 or t.numel() < n or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{what}: a contiguous int32 tensor of at least {n} entries on the cache's "
+                         f"device is needed, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
 def _rows(what, x, rows, heads, dh):
     """(row, head) strides of [rows][heads][dh] whose elements lie together."""
-    if x.dim() != 3 or x.shape[0] < rows or x.shape[1] != heads or x.shape[2] != dh or \
-            (x.stride(2) != 1 and dh > 1):
+    shape, strides = x.shape, x.stride()
+    if len(shape) != 3 or shape[0] < rows or shape[1] != heads or shape[2] != dh or strides[2] != 1:
         raise ValueError(f"{what}: [{rows}][{heads}][{dh}] with elements in order is needed, got "
-                         f"shape {tuple(x.shape)}, strides {x.stride()}")
-    return x.stride(0), x.stride(1)
+                         f"shape {tuple(shape)}, strides {strides}")
+    return strides[0], strides[1]
 
 
 class Rope:
@@ -515,20 +543,30 @@ class Rope:
             pass
 
 
+# n medusa_rope_rows as bytes: x, y, heads, x_row, x_head, y_row, y_head
+_ROPE_ROWS = {n: struct.Struct("PPiqqqq" * n) for n in range(1, 5)}
+
+
 def rope_apply(rope, pos, parts, inverse=False, stream=None):
     """medusa_rope_apply: `parts` holds (x, y) pairs of [rows][heads][dh] tensors (any strides
     between rows and heads); y may be x."""
-    rows, dh = pos.numel(), parts[0][0].shape[2]
-    dtype = _dtype(*(t for p in parts for t in p))
-    arr = (RopeRows * len(parts))()
-    for a, (x, y) in zip(arr, parts):
-        a.heads = x.shape[1]
-        a.x_row, a.x_head = _rows("x", x, rows, a.heads, dh)
-        a.y_row, a.y_head = _rows("y", y, rows, a.heads, dh)
-        a.x, a.y = x.data_ptr(), y.data_ptr()
-    _check("medusa_rope_apply",
-           lib().medusa_rope_apply(rope.handle, dtype, dh, rows, _ints("pos", pos, rows), arr,
-                                   len(parts), int(inverse), _stream(stream)))
+    rows, first = pos.numel(), parts[0][0]
+    dh, dtype, t, device = first.shape[-1], _dtype(first), first.dtype, first.get_device()
+    args = []
+    for x, y in parts:
+        xs, xt, ys, yt = x.shape, x.stride(), y.shape, y.stride()
+        if len(xs) != 3 or xs != ys or xs[0] < rows or xs[2] != dh or xt[2] != 1 or yt[2] != 1:
+            raise ValueError(f"x, y: [{rows}][heads][{dh}] with elements in order is needed, got shapes "
+                             f"{tuple(xs)}, {tuple(ys)}, strides {xt}, {yt}")
+        if x.dtype is not t or y.dtype is not t or x.get_device() != device or y.get_device() != device:
+            _same(first, x, y)
+        args += (x.data_ptr(), y.data_ptr(), xs[1], xt[0], xt[1], yt[0], yt[1])
+    n = len(parts)
+    code = MEDUSA_ERR_INVALID
+    if n in _ROPE_ROWS:
+        code = lib().medusa_rope_apply(rope.handle, dtype, dh, rows, _ints("pos", pos, rows, device),
+                                       _ROPE_ROWS[n].pack(*args), n, 1 if inverse else 0, _stream(stream))
+    _check("medusa_rope_apply", code)
 
 
 class Cache:
@@ -558,12 +596,15 @@ class Cache:
             pass
 
 
-def _items(cache, k, v, start, rows, per_seq, count):
-    """rows, start, per_seq and count of medusa_kv_rows / medusa_kv_places."""
+def _items(cache, n, start, rows, per_seq, count, device):
+    """rows, start, per_seq and count of medusa_kv_rows / medusa_kv_places; n: places there are."""
+    if rows is None:
+        rows = n
     if start is not None:
-        return k.shape[0] if rows is None else rows, _ints("start", start, cache.B + 1), 0, None
-    per_seq = (k.shape[0] if rows is None else rows) // cache.B if per_seq is None else per_seq
-    return cache.B * per_seq, None, per_seq, _ints("count", count, cache.B)
+        return rows, _ints("start", start, cache.B + 1, device), 0, None
+    if per_seq is None:
+        per_seq = rows // cache.B
+    return cache.B * per_seq, None, per_seq, _ints("count", count, cache.B, device)
 
 
 def kv_append(cache, kv, k, v, start=None, per_seq=None, count=None, index=None, index_rows=0,
@@ -571,25 +612,30 @@ def kv_append(cache, kv, k, v, start=None, per_seq=None, count=None, index=None,
     """medusa_kv_append: k, v [rows][Hkv][dh] (any strides between rows and heads).  Packed
     batches give `start`, padded ones `per_seq` (default: an equal share of the rows) and
     `count`; with `index` the item places are index's and k, v the rows they name."""
-    n, start, per_seq, count = _items(cache, k if index is None else index, v, start, rows, per_seq, count)
+    device = k.get_device()
+    n, start, per_seq, count = _items(cache, k.shape[0] if index is None else index.numel(), start,
+                                      rows, per_seq, count, device)
     need = n if index is None else cache.B * index_rows
     kr, kh = _rows("k", k, need, cache.Hkv, cache.dh)
     vr, vh = _rows("v", v, need, cache.Hkv, cache.dh)
-    r = KVRows(k.data_ptr(), v.data_ptr(), _dtype(k, v), kr, kh, vr, vh, n, start, per_seq, count,
-               _ints("index", index, n), index_rows, _ints("pos", pos, n))
+    _same(k, v)
+    r = KVRows(k.data_ptr(), v.data_ptr(), _dtype(k), kr, kh, vr, vh, n, start, per_seq, count,
+               _ints("index", index, n, device), index_rows, _ints("pos", pos, n, device))
     _check("medusa_kv_append",
-           lib().medusa_kv_append(cache.handle, kv, r, rope.handle if rope is not None else None,
+           lib().medusa_kv_append(cache.handle, kv, r, None if rope is None else rope.handle,
                                   k_scale, v_scale, _stream(stream)))
 
 
 def kv_read(cache, kv, k, v, start=None, per_seq=None, count=None, first=None, k_scale=1.0,
             v_scale=1.0, rows=None, stream=None):
     """medusa_kv_read into k, v [rows][Hkv][dh]; batches as in kv_append."""
-    n, start, per_seq, count = _items(cache, k, v, start, rows, per_seq, count)
+    device = k.get_device()
+    n, start, per_seq, count = _items(cache, k.shape[0], start, rows, per_seq, count, device)
     kr, kh = _rows("k", k, n, cache.Hkv, cache.dh)
     vr, vh = _rows("v", v, n, cache.Hkv, cache.dh)
-    r = KVPlaces(k.data_ptr(), v.data_ptr(), _dtype(k, v), kr, kh, vr, vh, n, start, per_seq, count,
-                 _ints("first", first, cache.B))
+    _same(k, v)
+    r = KVPlaces(k.data_ptr(), v.data_ptr(), _dtype(k), kr, kh, vr, vh, n, start, per_seq, count,
+                 _ints("first", first, cache.B, device))
     _check("medusa_kv_read",
            lib().medusa_kv_read(cache.handle, kv, r, k_scale, v_scale, _stream(stream)))
 
@@ -598,22 +644,23 @@ def kv4_attention(cache, kv, q, o, ws, tree_k=None, tree_v=None, mask=None, scal
                   v_scale=1.0, stream=None):
     """medusa_kv4_attention: q, o [B][n1][Hq][dh] (rows evenly spaced), tree_k, tree_v
     [B][n1][Hkv][dh] contiguous or None, mask int32 [n1][8] or None."""
-    B, n1 = q.shape[0], q.shape[1]
-    if B != cache.B or o.shape != q.shape:
-        raise ValueError(f"q, o: [{cache.B}][n1][Hq][dh] is needed, got {tuple(q.shape)}, {tuple(o.shape)}")
-    if (B > 1 and n1 > 1) and (q.stride(0) != n1 * q.stride(1) or o.stride(0) != n1 * o.stride(1)):
-        raise ValueError("q, o: the B * n1 rows have to be evenly spaced")
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != cache.B or shape[2] != cache.Hq or shape[3] != cache.dh or o.shape != shape:
+        raise ValueError(f"q, o: [{cache.B}][n1][{cache.Hq}][{cache.dh}] is needed, got {tuple(shape)}, "
+                         f"{tuple(o.shape)}")
+    B, n1 = shape[0], shape[1]
     at = 0 if n1 == 1 else 1
-    for x in (q, o):
-        if x.shape[2] != cache.Hq or x.shape[3] != cache.dh or x.stride(3) != 1:
-            raise ValueError(f"q, o: [{cache.B}][n1][{cache.Hq}][{cache.dh}] with elements in order is needed")
-    dtype = _dtype(q, o, tree_k, tree_v)
+    qs, os_ = q.stride(), o.stride()
+    for s in (qs, os_):
+        if s[3] != 1 or (at and B > 1 and s[0] != n1 * s[1]):
+            raise ValueError(f"q, o: elements in order and evenly spaced rows are needed, got strides {s}")
+    _same(q, o, tree_k, tree_v)
     for t in (tree_k, tree_v):
-        if t is not None and (tuple(t.shape) != (B, n1, cache.Hkv, cache.dh) or not t.is_contiguous()):
+        if t is not None and (t.shape != (B, n1, cache.Hkv, cache.dh) or not t.is_contiguous()):
             raise ValueError(f"tree_k, tree_v: contiguous [{B}][{n1}][{cache.Hkv}][{cache.dh}] is needed")
-    a = KV4Query(q.data_ptr(), o.data_ptr(), dtype, n1, q.stride(at), q.stride(2), o.stride(at),
-                 o.stride(2), ptr(tree_k), ptr(tree_v), _ints("mask", mask, 8 * n1), scale, k_scale,
-                 v_scale)
+    a = KV4Query(q.data_ptr(), o.data_ptr(), _dtype(q), n1, qs[at], qs[2], os_[at], os_[2],
+                 None if tree_k is None else tree_k.data_ptr(), None if tree_v is None else tree_v.data_ptr(),
+                 _ints("mask", mask, 8 * n1, q.get_device()), scale, k_scale, v_scale)
     _check("medusa_kv4_attention",
-           lib().medusa_kv4_attention(cache.handle, kv, a, ptr(ws), ws.numel() * ws.element_size(),
+           lib().medusa_kv4_attention(cache.handle, kv, a, ws.data_ptr(), ws.numel() * ws.element_size(),
                                       _stream(stream)))

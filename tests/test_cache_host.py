@@ -47,8 +47,7 @@ def test_cache_creation_refuses(bad, code):
 def test_calls_without_a_handle_are_refused():
     L = Bnd.lib()
     kv, rows, places, q = Bnd.KV(), Bnd.KVRows(), Bnd.KVPlaces(), Bnd.KV4Query()
-    part = (Bnd.RopeRows * 1)()
-    assert L.medusa_rope_apply(None, 0, 64, 1, None, part, 1, 0, None) == -1
+    assert L.medusa_rope_apply(None, 0, 64, 1, None, bytes(56), 1, 0, None) == -1
     assert L.medusa_kv_append(None, kv, rows, None, 1.0, 1.0, None) == -1
     assert L.medusa_kv_read(None, kv, places, 1.0, 1.0, None) == -1
     assert L.medusa_kv4_attention(None, kv, q, None, 0, None) == -1
