@@ -25,6 +25,7 @@
 // row's largest.  Float queries and their P go as two halves (22 bits) in two MMAs.
 #include "cache.h"
 #include "common.cuh"
+#include "kv4_attn.cuh"
 #include "kvcache.cuh"
 #include "launch.cuh"
 #include "tc_ptx.cuh"
@@ -35,22 +36,7 @@ constexpr int KD_WARPS = 4, KD_ROWS = 16, KD_STAGES = 2;
 template <int NR> constexpr int KD_CTAS = NR == 1 ? 4 : 3;     // resident CTAs per SM (registers, shared memory)
 constexpr int KD_CTAS_MOST = 4;
 constexpr int KD_KEYS = 2 * KV4_SLOTS;              // slots a warp takes at a time: two blocks
-constexpr int KD_CHUNK = KD_WARPS * KD_KEYS;
-// P is taken against a reference 2^KD_TOP below a half's range: a row's reference starts KD_BACK
-// (log2) below its running maximum and is raised, O rescaled, only once a score passes it by
-// KD_TOP.  Small probabilities then stay normal halves down to 2^(-14 - back) of the largest; with
-// two halves for P (float inputs) that floor matters most, so the reference lies lower and
-// moves more often.
-constexpr float KD_TOP = 15.f;
-template <bool SPLIT> constexpr float KD_BACK = SPLIT ? 13.f : 7.f;
-
-struct Kv4Work {
-  Kv4AttnArgs a;
-  int R, rb, nrb;                     // rows of a head, rows of a block, row blocks
-  float* part_o;                      // [slots][rb][dh]
-  float2* part_ml;                    // [slots][rb] (reference in base-2 units, sum)
-  int2* span;                         // [B * Hkv * nrb]: first slot and one past the last
-};
+static_assert(KD_CHUNK == KD_WARPS * KD_KEYS, "a chunk is the warps' slots");
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t pol) {
   asm volatile(
@@ -63,63 +49,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-__device__ __forceinline__ uint32_t half_pair(float lo, float hi) { return h2u(__floats2half2_rn(lo, hi)); }
-
-// Chunks of sequence b.
-__device__ __forceinline__ int kd_chunks(const CacheView& c, int b) {
-  return (clamp_len(c, c.len[b]) + KD_CHUNK - 1) / KD_CHUNK;
-}
-// All chunks of the call, and where the walk through them stands at chunk w: sequence b, its
-// triple q of Hkv * nrb, chunk j, and nb chunks of b.
-struct KdCursor {
-  int b, q, j, nb;
-};
-__device__ __forceinline__ long kd_total(const CacheView& c, int per) {
-  long sum = 0;
-  for (int b = threadIdx.x & 31; b < c.B; b += 32) sum += kd_chunks(c, b);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return sum * per;
-}
-__device__ __forceinline__ KdCursor kd_seek(const CacheView& c, int per, long w) {
-  const int lane = threadIdx.x & 31;
-  long before = 0;
-  for (int b0 = 0;; b0 += 32) {
-    const int mine = b0 + lane < c.B ? kd_chunks(c, b0 + lane) : 0;
-    long upto = mine;                              // chunks of the sequences b0 .. b0 + lane
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
-    }
-    const uint32_t hit = __ballot_sync(0xffffffffu, (before + upto) * per > w);
-    if (hit || b0 + 32 >= c.B) {
-      const int l = hit ? __ffs(hit) - 1 : 31;
-      const int nb = __shfl_sync(0xffffffffu, mine, l);
-      const long first = (before + __shfl_sync(0xffffffffu, upto, l) - nb) * per;
-      KdCursor k;
-      k.b = b0 + l;
-      k.nb = max(nb, 1);
-      const long in = w - first;
-      k.q = (int)(in / k.nb);
-      k.j = (int)(in - (long)k.q * k.nb);
-      return k;
-    }
-    before += __shfl_sync(0xffffffffu, upto, 31);
-  }
-}
-__device__ __forceinline__ void kd_next(const CacheView& c, int per, KdCursor& k) {
-  if (++k.j < k.nb) return;
-  k.j = 0;
-  if (++k.q < per) return;
-  k.q = 0;
-  do {
-    ++k.b;
-    k.nb = k.b < c.B ? kd_chunks(c, k.b) : 1;
-  } while (k.nb == 0);
-}
-
 // Q as column operands: for MMA step s and 8-row tile n, lane (g, t) holds row 8 n + g, elements
 // e, e + 1 and e + 2, e + 3 with e = t dh/4 + 4 s; kept in shared memory as the lanes read it.
 template <typename T, int DH, int NR, bool SPLIT>
@@ -141,9 +70,8 @@ __device__ __forceinline__ void kd_load_q(const Kv4Work& w, int b, int g, int rb
     }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    // 2^-e with the row's largest element in [2^e, 2^(e+1)), and 2^e for the scores
-    const int eb = top > 0.f ? min(max((int)(__float_as_uint(top) >> 23), 1), 253) : 127;
-    const float down = __uint_as_float((uint32_t)(254 - eb) << 23), up = __uint_as_float((uint32_t)eb << 23);
+    float down, up;
+    row_scale(top, down, up);
     if (li == 0) rs[r] = up * (w.a.scale * w.a.c.gk) * 1.4426950408889634f;
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
@@ -634,17 +562,28 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant_
 }
 
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-static size_t kd_slots(int B, int Hkv, int nrb, int num_sms) { return (size_t)num_sms * KD_CTAS_MOST + (size_t)B * Hkv * nrb; }
+// Row blocks, and how many CTAs a launch can have, of R rows a head.
+static void blocks_of(int dtype, int dh, int R, int num_sms, int* rb, int* nrb, int* ctas) {
+  if (kv4_tree_takes(dtype, dh, R)) {
+    kv4_tree_blocks(R, rb, nrb);
+    *ctas = num_sms;
+  } else {
+    *rb = R < KD_ROWS ? R : KD_ROWS;
+    *nrb = (R + *rb - 1) / *rb;
+    *ctas = num_sms * KD_CTAS_MOST;
+  }
+}
 
 size_t kv4_workspace(int B, int Hq, int Hkv, int dh, int max_nodes, int num_sms) {
   size_t most = 0;
-  // the largest over the rows a call may have: the slots of 16 rows, or fewer rows in one
-  for (int R = Hq / Hkv, n = 1; n <= max_nodes; ++n, R += Hq / Hkv) {
-    const int rb = R < KD_ROWS ? R : KD_ROWS, nrb = (R + rb - 1) / rb;
-    const size_t slots = kd_slots(B, Hkv, nrb, num_sms);
-    const size_t s = up256(slots * rb * dh * 4) + up256(slots * rb * 8) + up256((size_t)B * Hkv * nrb * 8);
-    most = s > most ? s : most;
-  }
+  for (int dtype : {MEDUSA_F32, MEDUSA_BF16})
+    for (int R = Hq / Hkv, n = 1; n <= max_nodes; ++n, R += Hq / Hkv) {
+      int rb, nrb, ctas;
+      blocks_of(dtype, dh, R, num_sms, &rb, &nrb, &ctas);
+      const size_t pairs = (size_t)B * Hkv * nrb, slots = ctas + pairs;
+      const size_t s = up256(slots * rb * dh * 4) + up256(slots * rb * 8) + up256(pairs * 8);
+      most = s > most ? s : most;
+    }
   return most;
 }
 
@@ -652,11 +591,16 @@ template <typename T, int DH, int NR, bool SPLIT>
 static cudaError_t rows_go(const Kv4Work& w, int num_sms, cudaStream_t st) {
   const size_t smem = (size_t)KD_WARPS * KD_STAGES * 4 * kv4_block(DH) + (size_t)2 * w.rb * (DH + 4) * 4;
   auto kern = kv4_rows_kernel<T, DH, NR, SPLIT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static unsigned long long done = 0;
+  const size_t most = (size_t)KD_WARPS * KD_STAGES * 4 * kv4_block(DH) + (size_t)2 * 8 * NR * (DH + 4) * 4;
+  cudaError_t e = allow_smem(kern, most, &done);
   if (e != cudaSuccess) return e;
-  if ((e = launch_kernel(kern, dim3(num_sms * KD_CTAS<NR>), dim3(KD_WARPS * 32), smem, st, 1, w)) != cudaSuccess) return e;
+  return launch_kernel(kern, dim3(num_sms * KD_CTAS<NR>), dim3(KD_WARPS * 32), smem, st, 1, w);
+}
+template <typename T> static cudaError_t combine(const Kv4Work& w, cudaStream_t st) {
   const long rows = (long)w.a.c.B * w.a.n1 * w.a.Hq;
-  return launch_kernel(kv4_combine_kernel<T, DH>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, 1, w);
+  auto kern = w.a.c.dh == 32 ? kv4_combine_kernel<T, 32> : w.a.c.dh == 64 ? kv4_combine_kernel<T, 64> : kv4_combine_kernel<T, 128>;
+  return launch_kernel(kern, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, 1, w);
 }
 template <typename T, bool SPLIT>
 static cudaError_t rows_dh(const Kv4Work& w, int num_sms, cudaStream_t st) {
@@ -672,16 +616,19 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, int dtype, void* ws, int 
   Kv4Work w{};
   w.a = a;
   w.R = a.n1 * a.G;
-  w.rb = w.R < KD_ROWS ? w.R : KD_ROWS;
-  w.nrb = (w.R + w.rb - 1) / w.rb;
-  const size_t slots = kd_slots(a.c.B, a.c.Hkv, w.nrb, num_sms);
+  int ctas;
+  blocks_of(dtype, a.c.dh, w.R, num_sms, &w.rb, &w.nrb, &ctas);
+  const size_t slots = ctas + (size_t)a.c.B * a.c.Hkv * w.nrb;
   char* p = static_cast<char*>(ws);
   w.part_o = reinterpret_cast<float*>(p);
   p += up256(slots * w.rb * a.c.dh * 4);
   w.part_ml = reinterpret_cast<float2*>(p);
   p += up256(slots * w.rb * 8);
   w.span = reinterpret_cast<int2*>(p);
-  return dtype == MEDUSA_F32 ? rows_dh<float, true>(w, num_sms, st) : rows_dh<bf16, false>(w, num_sms, st);
+  cudaError_t e = kv4_tree_takes(dtype, a.c.dh, w.R) ? launch_kv4_tree(w, num_sms, st)
+                  : dtype == MEDUSA_F32 ? rows_dh<float, true>(w, num_sms, st) : rows_dh<bf16, false>(w, num_sms, st);
+  if (e != cudaSuccess) return e;
+  return dtype == MEDUSA_F32 ? combine<float>(w, st) : combine<bf16>(w, st);
 }
 
 }  // namespace medusa
