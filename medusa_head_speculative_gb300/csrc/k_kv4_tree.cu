@@ -7,9 +7,11 @@
 // 128 cached slots, a (sequence, head, row block) at a time, and writes a partial for each it
 // leaves.  A row block is one 128-row tile, or two when a head has more rows.  In the CTA
 //
-//   warps 8-15   decode: a thread takes 64 elements of one slot (32 bytes of codes, 4 scales),
-//                loaded a chunk ahead into registers, and writes them as halves (exact) into a
-//                128-byte-swizzled tile: K and V chunks in rings of two or three stages
+//   warp 17      copies: the eight blocks of a chunk's keys, then of its values, by the copy engine
+//                into a ring of staging slots
+//   warps 8-15   decode: a thread takes 32 elements of one slot (16 bytes of codes, 2 scales) and
+//                writes them as halves (exact) into a 128-byte-swizzled tile: K and V chunks in
+//                rings of two or three stages
 //   warp 16      (one lane) MMAs for two "slots", each with S (128 columns) and O (dh columns) in
 //                tensor memory: S = Q K^T, then O += P V with P read from tensor memory (the A
 //                operand) and V from shared memory (MN-major)
@@ -30,11 +32,12 @@
 
 namespace medusa {
 
-constexpr int KT_ROWS = 128, KT_KEYS = KD_CHUNK, KT_MAXST = 3;
-constexpr int KT_MMA_WARP = 16, KT_THREADS = 5 * 128;   // five warpgroups; of the last one warp works
-// Registers a thread: 96 at launch (5 x 128 x 96 = 61440), then 136 for softmax, 80 for decode and
-// 48 for the MMA warpgroup: 2 x 136 + 2 x 80 + 48 = 5 x 96.
-constexpr int KT_REG_SOFTMAX = 136, KT_REG_DECODE = 80, KT_REG_MMA = 48;
+constexpr int KT_ROWS = 128, KT_KEYS = KD_CHUNK, KT_ST = 2, KT_MAXLD = 6;
+constexpr int KT_DECODERS = 8, KT_MMA_WARP = 16, KT_LOAD_WARP = 17;
+constexpr int KT_THREADS = 5 * 128;                 // five warpgroups; of the last one two warps work
+// Registers a thread: 96 at launch (5 x 128 x 96 = 61440), then 152 for softmax, 56 for decode and
+// 64 for the MMA and copy warps: 2 x 152 + 2 x 56 + 64 = 5 x 96.
+constexpr int KT_REG_SOFTMAX = 152, KT_REG_DECODE = 56, KT_REG_MMA = 64;
 static_assert(2 * KT_REG_SOFTMAX + 2 * KT_REG_DECODE + KT_REG_MMA == 5 * 96, "what the launch holds");
 constexpr uint32_t KT_SLOT_COLS = 256;               // per slot: S / P [0, 128), O [128, 128 + dh)
 constexpr int KT_MIN_ROWS = 17;                      // rows a head from which this kernel is taken
@@ -46,26 +49,20 @@ void kv4_tree_blocks(int R, int* rb, int* nrb) {
   *nrb = (R + most - 1) / most;
 }
 
-// Barriers.  QF / QE: query tiles written / no longer read.  KF / KE and VF / VE: K and V stages
+// Barriers.  LF / LE: a staging slot has landed / been read.  QF / QE: query tiles written / no
+// longer read.  KF / KE and VF / VE: K and V stages
 // full / free.  Per slot: SF (S written), PR (P written), OF (P V done).  MRG / MFR: the second
 // slot's (reference, sum) are in shared memory / consumed.  END: every MMA issued has completed.
 enum {
-  TB_QF = 0, TB_QE = 1, TB_KF = 2, TB_KE = TB_KF + KT_MAXST, TB_VF = TB_KE + KT_MAXST, TB_VE = TB_VF + KT_MAXST,
-  TB_SF = TB_VE + KT_MAXST, TB_PR = TB_SF + 2, TB_OF = TB_PR + 2, TB_MRG = TB_OF + 2, TB_MFR = TB_MRG + 1,
-  TB_END = TB_MFR + 1, TB_COUNT = TB_END + 1
-};
-
-struct Kv4TreeArgs {
-  Kv4Work w;
-  int nt, kst, vst;                   // query tiles of a block, stages of the K and V rings
+  TB_QF = 0, TB_QE = 1, TB_KF = 2, TB_KE = TB_KF + KT_ST, TB_VF = TB_KE + KT_ST, TB_VE = TB_VF + KT_ST,
+  TB_SF = TB_VE + KT_ST, TB_PR = TB_SF + 2, TB_OF = TB_PR + 2, TB_MRG = TB_OF + 2, TB_MFR = TB_MRG + 1,
+  TB_END = TB_MFR + 1, TB_LF = TB_END + 1, TB_LE = TB_LF + KT_MAXLD, TB_COUNT = TB_LE + KT_MAXLD
 };
 
 // Instruction descriptor, kind::f16: fp32 D, half A and B, both K-major, M x N.
 constexpr uint32_t idesc_f16(int M, int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24); }
-// D[tmem] (+)= A(smem) B(smem)^T and A(tmem) B(smem), kind::f16.
-__device__ __forceinline__ void kt_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  umma_bf16(d, a, b, idesc, acc);     // the descriptor says which 16-bit type the operands are
-}
+// D[tmem] (+)= A(tmem) B(smem), kind::f16 (umma_bf16 is the one with A in shared memory: the
+// descriptor says which 16-bit type the operands are).
 __device__ __forceinline__ void kt_mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -96,8 +93,8 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t 
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-template <int DH>
-__global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_constant__ Kv4TreeArgs ta) {
+template <int DH, int NT>
+__global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_constant__ Kv4Work w) {
   constexpr int H = DH / 64;                         // 64-element halves of a head
   constexpr int BLK = kv4_block(DH);
   constexpr uint32_t TILE = 128 * 128;               // one half of a tile: 128 rows of 128 bytes
@@ -106,13 +103,14 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
   __shared__ uint64_t bars[TB_COUNT];
   __shared__ uint32_t tmem_slot;
   __shared__ int s_abort;
+  __shared__ int s_valid[KT_MAXLD];                  // slots of the chunk there are
   __shared__ float2 s_ml[KT_ROWS];                   // second slot's (reference, sum) per row
-  const Kv4Work& w = ta.w;
   const CacheView& c = w.a.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int nt = ta.nt, SK = ta.kst, SV = ta.vst;
+  constexpr int nt = NT, SK = KT_ST, SV = KT_ST, SL = NT == 2 ? 3 : 6;   // tiles, stages of the K, V and staging rings
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t qs = base, k0s = base + nt * CHUNK, v0s = k0s + SK * CHUNK;
+  const uint32_t qs = base, k0s = base + nt * CHUNK, v0s = k0s + SK * CHUNK, l0s = v0s + SV * CHUNK;
+  constexpr uint32_t STAGE = 8 * BLK;                // the blocks of 128 slots
   const uint32_t bar0 = smem_u32(bars);
   auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   const int per = c.Hkv * w.nrb;
@@ -127,11 +125,15 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
   if (tid == 0) {
     mbar_init(bar(TB_QF), 2 * KT_ROWS);
     mbar_init(bar(TB_QE), 1);
-    for (int i = 0; i < KT_MAXST; ++i) {
-      mbar_init(bar(TB_KF + i), 128 * H);
+    for (int i = 0; i < KT_ST; ++i) {
+      mbar_init(bar(TB_KF + i), KT_DECODERS);
       mbar_init(bar(TB_KE + i), 1);
-      mbar_init(bar(TB_VF + i), 128 * H);
+      mbar_init(bar(TB_VF + i), KT_DECODERS);
       mbar_init(bar(TB_VE + i), 1);
+    }
+    for (int i = 0; i < KT_MAXLD; ++i) {
+      mbar_init(bar(TB_LF + i), 1);
+      mbar_init(bar(TB_LE + i), KT_DECODERS);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(TB_SF + s), 1);
@@ -156,96 +158,70 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
   if (warp >= 8 && warp < KT_MMA_WARP) {
     // ------------------------------------------------------------ decode
     reg_fewer<KT_REG_DECODE>();
-    // dh 128: 256 threads take the two halves of 128 slots, keys then values; dh 64: one half
-    // of the threads takes the keys, the other the values
-    const int slot = (warp & 3) * 32 + lane, half = (warp - 8) >> 2;
-    const int eh = H == 2 ? half : 0;                 // 64-element half of the head
-    const bool do_k = H == 2 || half == 0, do_v = H == 2 || half == 1;
-    const int upp = (c.page_table ? c.page_size : c.capacity) / KV4_SLOTS;
-    struct Piece {
-      uint4 a, b;
-      uint32_t sc;
-    };
-    Piece kp, vp;
-    // two walks: one chunk ahead the codes are loaded, two chunks ahead the page is looked up
-    KdCursor lk = kd_seek(c, per, w0);
-    long lw = w0;
-    int len_b = -1, len = 0;
-    long blk = 0;                                     // this slot's block for lk (head 0)
-    auto look = [&]() {                               // of chunk lw, if there is one
-      if (lw >= w1) return;
-      if (lk.b != len_b) {
-        len_b = lk.b;
-        len = clamp_len(c, c.len[lk.b]);
-      }
-      const int t = lk.j * KT_KEYS + slot;
-      blk = -1;
-      if (t < len) {
-        long unit;
-        int in;
-        if (!unit_of(c, lk.b, t, unit, in)) {
-          set_flag(c.status, MEDUSA_FLAG_PAGE_RANGE);
-          unit = 0;
-        }
-        blk = (unit * c.Hkv + lk.q / w.nrb) * upp + in / KV4_SLOTS;
-      }
-    };
-    auto step = [&]() {
-      if (++lw < w1) kd_next(c, per, lk);
-    };
-    const int in16 = slot % KV4_SLOTS;                // chunks start on a block's first slot
-    auto load = [&](Piece& p, const void* pool, long b) {
-      if (b < 0) {                                    // past the length: zeros, whatever lies there
-        p.a = p.b = make_uint4(0u, 0u, 0u, 0u);
-        p.sc = 0u;
-        return;
-      }
-      const uint8_t* s = static_cast<const uint8_t*>(pool) + b * BLK;
-      const uint4* q = reinterpret_cast<const uint4*>(s + in16 * (DH / 2) + eh * 32);
-      p.a = __ldg(q);
-      p.b = __ldg(q + 1);
-      p.sc = __ldg(reinterpret_cast<const uint32_t*>(s + 8 * DH + in16 * (DH / 16) + eh * 4));
-    };
-    auto store = [&](const Piece& p, uint32_t tile) {
-      const uint32_t wd[8] = {p.a.x, p.a.y, p.a.z, p.a.w, p.b.x, p.b.y, p.b.z, p.b.w};
-      const __half2 s01 = kv4_scales((uint16_t)(p.sc & 0xffffu)), s23 = kv4_scales((uint16_t)(p.sc >> 16));
-      const uint32_t row = tile + eh * TILE + slot * 128;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const __half2 s = i < 2 ? __low2half2(s01) : i < 4 ? __high2half2(s01) : i < 6 ? __low2half2(s23) : __high2half2(s23);
-        __half2 y[4];
-        kv4_pairs(wd[i], y);
-        st_shared16(row + ((i ^ (slot & 7)) << 4), h2u(__hmul2(y[0], s)), h2u(__hmul2(y[1], s)), h2u(__hmul2(y[2], s)),
-                    h2u(__hmul2(y[3], s)));
-      }
-      fence_proxy_async();
-    };
-    look();
-    long cur = blk;
-    step();
-    look();                                           // blk: chunk w0 + 1
-    if (do_k) load(kp, c.k, cur);
-    if (do_v) load(vp, c.v, cur);
-    for (long x = w0; x < w1; ++x) {
+    // 16 bytes of codes a lane: neighbouring lanes the quarters (dh 64: halves) of a slot, so that
+    // reading a staging slot takes every bank once; and so does writing the tile, with the upper
+    // half of a head (16 KB further on: the same banks) written two 16-byte units out of step.
+    constexpr int Q = DH / 32, KEYS = 32 / Q;         // lanes a slot, slots a warp at a time
+    const int quarter = lane % Q, eh = quarter >> 1, twist = eh;
+    const int dw = warp - 8;
+    int u = 0;                                        // staging units (K and V of each chunk)
+    bool dead = false;
+    for (long x = w0; x < w1 && !dead; ++x) {
       const int i = (int)(x - w0);
-      const long next = blk;
-      const bool more = x + 1 < w1;
-      step();
-      look();                                         // chunk x + 2
-      if (do_k) {
-        if (!kt_warp_wait(bar(TB_KE + i % SK), ((i / SK) & 1) ^ 1)) { timed_out = true; break; }
-        store(kp, k0s + (i % SK) * CHUNK);
-        mbar_arrive(bar(TB_KF + i % SK));
-        if (more) load(kp, c.k, next);
-      }
-      if (do_v) {
-        if (!kt_warp_wait(bar(TB_VE + i % SV), ((i / SV) & 1) ^ 1)) { timed_out = true; break; }
-        store(vp, v0s + (i % SV) * CHUNK);
-        mbar_arrive(bar(TB_VF + i % SV));
-        if (more) load(vp, c.v, next);
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part, ++u) {
+        const int st = u % SL;
+        if (!kt_warp_wait(bar(TB_LF + st), (u / SL) & 1)) { dead = true; break; }
+        const int valid = s_valid[st];
+        uint4 cw[Q / 2];
+        uint32_t sc[Q / 2];
+#pragma unroll
+        for (int y = 0; y < Q / 2; ++y) {
+          const int key = (dw * (Q / 2) + y) * KEYS + lane / Q;
+          cw[y] = make_uint4(0u, 0u, 0u, 0u);         // past the length: zeros, whatever lies there
+          sc[y] = 0u;
+          if (key < valid) {
+            const uint32_t blk = l0s + st * STAGE + (key >> 4) * BLK;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(cw[y].x), "=r"(cw[y].y), "=r"(cw[y].z), "=r"(cw[y].w)
+                         : "r"(blk + (key & 15) * (DH / 2) + quarter * 16));
+            uint16_t two;
+            asm volatile("ld.shared.b16 %0, [%1];" : "=h"(two) : "r"(blk + 8 * DH + (key & 15) * (DH / 16) + quarter * 2));
+            sc[y] = two;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(TB_LE + st));
+        const int S = part ? SV : SK, full = (part ? TB_VF : TB_KF) + i % S;
+        if (!kt_warp_wait(bar((part ? TB_VE : TB_KE) + i % S), ((i / S) & 1) ^ 1)) { dead = true; break; }
+        const uint32_t tile = (part ? v0s : k0s) + (i % S) * CHUNK + eh * TILE;
+#pragma unroll
+        for (int y = 0; y < Q / 2; ++y) {
+          const int key = (dw * (Q / 2) + y) * KEYS + lane / Q;
+          const __half2 s2 = kv4_scales((uint16_t)sc[y]);
+          const __half2 slo = __low2half2(s2), shi = __high2half2(s2);
+          // units 0, 1 have the first scale, 2, 3 the second; a twisted lane takes 2, 3 first
+          const uint32_t wd[4] = {twist ? cw[y].z : cw[y].x, twist ? cw[y].w : cw[y].y, twist ? cw[y].x : cw[y].z,
+                                  twist ? cw[y].y : cw[y].w};
+          const __half2 s0 = twist ? shi : slo, s1 = twist ? slo : shi;
+          const uint32_t row = tile + key * 128;
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const __half2 s = z < 2 ? s0 : s1;
+            const int unit = (quarter & 1) * 4 + (z ^ (twist << 1));
+            __half2 h[4];
+            kv4_pairs(wd[z], h);
+            st_shared16(row + ((unit ^ (key & 7)) << 4), h2u(__hmul2(h[0], s)), h2u(__hmul2(h[1], s)), h2u(__hmul2(h[2], s)),
+                        h2u(__hmul2(h[3], s)));
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(full));
       }
       if (aborted()) break;
     }
+    timed_out = dead;
   } else if (warp >= KT_MMA_WARP) {
     // ------------------------------------------------------------ MMA issuer
     reg_fewer<KT_REG_MMA>();
@@ -265,14 +241,16 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
         tc_fence_after();
         return true;
       };
+      // descriptors hold addresses in 16-byte units: an offset is added to them
+      const uint64_t dq = sw128_desc(qs), dk = sw128_desc(k0s), dv = sw128_desc_mn(v0s, TILE);
       auto issue_qk = [&](int slot, int tile, int x) {
-        const uint32_t ks = k0s + (x % SK) * CHUNK, d = tmem + slot * KT_SLOT_COLS;
+        const uint32_t d = tmem + slot * KT_SLOT_COLS;
+        const uint64_t a = dq + tile * (CHUNK >> 4), b = dk + (x % SK) * (CHUNK >> 4);
 #pragma unroll
-        for (int h = 0; h < H; ++h)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            kt_mma(d, sw128_desc(qs + tile * CHUNK + h * TILE) + 2 * kk, sw128_desc(ks + h * TILE) + 2 * kk, id_qk,
-                   (h | kk) != 0);
+        for (int kk = 0; kk < 4 * H; ++kk) {
+          const uint32_t at = (kk >> 2) * (TILE >> 4) + 2 * (kk & 3);
+          umma_bf16(d, a + at, b + at, id_qk, kk != 0);
+        }
         umma_commit(bar(TB_SF + slot));
       };
       auto wait_p = [&](int slot) -> bool {
@@ -281,10 +259,11 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
         return true;
       };
       auto issue_pv = [&](int slot, int x, bool acc) {
-        const uint32_t vs = v0s + (x % SV) * CHUNK, pa = tmem + slot * KT_SLOT_COLS, d = pa + KT_KEYS;
+        const uint32_t pa = tmem + slot * KT_SLOT_COLS, d = pa + KT_KEYS;
+        const uint64_t b = dv + (x % SV) * (CHUNK >> 4);
 #pragma unroll
         for (int kk = 0; kk < KT_KEYS / 16; ++kk)      // 16 keys per MMA: 8 columns of P
-          kt_mma_tmem_a(d, pa + 8 * kk, sw128_desc_mn(vs + kk * 2048, TILE), id_pv, acc || kk > 0);
+          kt_mma_tmem_a(d, pa + 8 * kk, b + kk * (2048 >> 4), id_pv, acc || kk > 0);
         umma_commit(bar(TB_OF + slot));
         if (slot) ++js1;
         else ++js0;
@@ -297,56 +276,37 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
         if (!mbar_wait(bar(TB_QF), qn & 1, TC_TIMEOUT_NS)) { dead = true; break; }
         ++qn;
         tc_fence_after();
-        if (nt == 2) {
-          // every chunk goes to each active tile's slot
-          if (!wait_k(gc)) { dead = true; break; }
-          for (int s = 0; s < nta; ++s) issue_qk(s, s, gc);
-          umma_commit(bar(TB_KE + gc % SK));
-          if (n == 1) umma_commit(bar(TB_QE));
-          for (int i = 0; i < n && !dead; ++i) {
-            const int x = gc + i;
-            if (!wait_v(x)) { dead = true; break; }
-            for (int s = 0; s < nta; ++s) {
+        // Job y: nt 2: chunk y, both tiles; nt 1: chunk y to slot y & 1.  Each turn issues the P V of
+        // job i and the S of job i + LEAD, so that one slot's MMAs run while the other's S is
+        // exponentiated.
+        constexpr int LEAD = nt == 2 ? 1 : 2;
+#pragma unroll 1
+        for (int i = -LEAD; i < n && !dead; ++i) {
+          const int x = gc + i, y = i + LEAD;
+          if (i >= 0 && !wait_v(x)) { dead = true; break; }
+          // one tile: slot 1's O may be overwritten only after the first warpgroup has merged it
+          // into the previous block's partial
+          if (nt == 1 && i == 1 && mc > 0 && !mbar_wait(bar(TB_MFR), (mc - 1) & 1, TC_TIMEOUT_NS)) { dead = true; break; }
+#pragma unroll 1
+          for (int t = 0; t < nta; ++t) {
+            const int s = nt == 2 ? t : i & 1;         // i + LEAD has the same slot
+            if (i >= 0) {
               if (!wait_p(s)) { dead = true; break; }
-              issue_pv(s, x, i > 0);
-              if (i + 1 < n) {
-                if (s == 0 && !wait_k(x + 1)) { dead = true; break; }
-                issue_qk(s, s, x + 1);
-                if (s == nta - 1) {
-                  umma_commit(bar(TB_KE + (x + 1) % SK));   // both tiles' S of chunk x + 1
-                  if (i + 2 == n) umma_commit(bar(TB_QE));
-                }
-              }
+              issue_pv(s, x, i >= (nt == 2 ? 1 : 2));
             }
-            if (!dead) umma_commit(bar(TB_VE + x % SV));     // both tiles' P V of chunk x
-          }
-        } else {
-          // one tile: chunk i goes to slot i & 1; slot 1's O may be overwritten only after the
-          // first warpgroup has merged it into the previous block's partial
-          if (!wait_k(gc)) { dead = true; break; }
-          issue_qk(0, 0, gc);
-          umma_commit(bar(TB_KE + gc % SK));
-          if (n > 1) {
-            if (!wait_k(gc + 1)) { dead = true; break; }
-            issue_qk(1, 0, gc + 1);
-            umma_commit(bar(TB_KE + (gc + 1) % SK));
-          }
-          if (n <= 2) umma_commit(bar(TB_QE));
-          for (int i = 0; i < n; ++i) {
-            const int s = i & 1, x = gc + i;
-            if (!wait_v(x) || !wait_p(s)) { dead = true; break; }
-            if (i == 1 && mc > 0 && !mbar_wait(bar(TB_MFR), (mc - 1) & 1, TC_TIMEOUT_NS)) { dead = true; break; }
-            issue_pv(s, x, i > 1);
-            umma_commit(bar(TB_VE + x % SV));
-            if (i + 2 < n) {
-              if (!wait_k(x + 2)) { dead = true; break; }
-              issue_qk(s, 0, x + 2);
-              umma_commit(bar(TB_KE + (x + 2) % SK));
-              if (i + 3 == n) umma_commit(bar(TB_QE));
+            if (y < n) {
+              if (t == 0 && !wait_k(x + LEAD)) { dead = true; break; }
+              issue_qk(s, nt == 2 ? t : 0, x + LEAD);
             }
           }
-          ++mc;
+          if (dead) break;
+          if (i >= 0) umma_commit(bar(TB_VE + x % SV));
+          if (y < n) {
+            umma_commit(bar(TB_KE + (x + LEAD) % SK));
+            if (y + 1 == n) umma_commit(bar(TB_QE));
+          }
         }
+        if (nt == 1) ++mc;
         gc += n;
         wi += n;
         k.j += n - 1;
@@ -355,6 +315,50 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
       }
       timed_out = dead;
       umma_commit(bar(TB_END));           // arrives once every MMA issued above is done
+    }
+    else if (warp == KT_LOAD_WARP) {
+      // ---------------------------------------------------------- copies: lane l < 8 block l
+      const int upp = (c.page_table ? c.page_size : c.capacity) / KV4_SLOTS;
+      const uint64_t pol = policy_evict_first();
+      int u = 0, waited = 0, len_b = -1, len = 0;
+      for (long x = w0; x < w1; ++x) {
+        if (k.b != len_b) {
+          len_b = k.b;
+          len = clamp_len(c, c.len[k.b]);
+        }
+        const int t = k.j * KT_KEYS + lane * KV4_SLOTS, valid = min(len - k.j * KT_KEYS, KT_KEYS);
+        const bool mine = lane < 8 && t < len;
+        long off = 0;
+        if (mine) {
+          long unit;
+          int in;
+          if (!unit_of(c, k.b, t, unit, in)) {
+            set_flag(c.status, MEDUSA_FLAG_PAGE_RANGE);
+            unit = 0;
+          }
+          off = ((unit * c.Hkv + k.q / w.nrb) * upp + in / KV4_SLOTS) * BLK;
+        }
+        bool ok = true;
+        for (int part = 0; part < 2 && ok; ++part, ++u) {
+          const int st = u % SL;
+          ok = kt_warp_wait(bar(TB_LE + st), ((u / SL) & 1) ^ 1);
+          if (!ok) break;
+          if (lane == 0) {
+            s_valid[st] = valid;
+            mbar_expect_tx(bar(TB_LF + st), (valid + KV4_SLOTS - 1) / KV4_SLOTS * BLK);
+          }
+          __syncwarp();
+          if (mine)
+            bulk_load(l0s + st * STAGE + lane * BLK, static_cast<const uint8_t*>(part ? c.v : c.k) + off, BLK,
+                      bar(TB_LF + st), pol);
+        }
+        if (!ok) { timed_out = true; break; }
+        if (x + 1 < w1) kd_next(c, per, k);
+        if (aborted()) break;
+      }
+      // copies still under way when the block gives up (bounded): the last SL units at most
+      for (waited = max(0, u - SL); (timed_out || aborted()) && waited < u; ++waited)
+        mbar_wait(bar(TB_LF + waited % SL), (waited / SL) & 1, TC_TIMEOUT_NS / 16);
     }
   } else {
     // ------------------------------------------------------------ softmax warpgroups
@@ -383,7 +387,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
                                                           ((long)k.b * w.a.n1 + node) * w.a.q_row + hq * w.a.q_head);
         float top = 0.f;
         if (row_ok) {
-#pragma unroll
+#pragma unroll 8
           for (int i = 0; i < DH / 8; ++i) {
             float f[8];
             unpack16(src[i], f);
@@ -398,6 +402,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
         ++qn;
         if (nt == 2 || H == 2 || slot == 0) {
           const int h0 = nt == 2 ? 0 : slot, h1 = nt == 2 || H == 1 ? H : slot + 1;
+#pragma unroll 1
           for (int h = h0; h < h1; ++h) {
             const uint32_t row = qs + tile * CHUNK + h * TILE + r * 128;
 #pragma unroll
@@ -421,7 +426,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
         tc_fence_after();
         if (live) {
           const int t0 = (k.j + i) * KT_KEYS;
-#pragma unroll
+#pragma unroll 1
           for (int hf = 0; hf < 2; ++hf) {
             float s[64];
             tmem_ld64(scol + 64 * hf, s);
@@ -446,7 +451,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
               // MMA of the same issuer), so O may be rescaled here; in a block's first chunk
               // there is no O yet.
               if (jj > 0) {
-#pragma unroll
+#pragma unroll 1
                 for (int x = 0; x < DH; x += 16) {
                   float v[16];
                   tmem_ld16(ocol + x, v);
@@ -457,7 +462,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
               }
               if (hf == 1) {                         // and the first half's P, already written
                 const __half2 fh = __float2half2_rn(f);
-#pragma unroll
+#pragma unroll 1
                 for (int x = 0; x < 32; x += 16) {
                   float v[16];
                   tmem_ld16(scol + x, v);
@@ -505,7 +510,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
         if (njobs > 0 && live) {
           if (!kt_warp_wait(bar(TB_OF + slot), (js - 1) & 1)) { timed_out = true; break; }
           tc_fence_after();
-#pragma unroll
+#pragma unroll 2
           for (int x = 0; x < DH; x += 16) {
             float v[16];
             tmem_ld16(ocol + x, v);
@@ -538,7 +543,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
         const float f1 = ml1.x == -INFINITY ? 0.f : ex2_approx(ml1.x - m);
         const uint32_t ocol1 = lane_base + KT_SLOT_COLS + KT_KEYS;
         if (live) {
-#pragma unroll
+#pragma unroll 2
           for (int x = 0; x < DH; x += 16) {
             float v0[16], v1[16];
             tmem_ld16(ocol + x, v0);
@@ -578,18 +583,19 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
   if (warp == KT_MMA_WARP) tmem_dealloc(tmem, 2 * KT_SLOT_COLS);
 }
 
-cudaError_t launch_kv4_tree(const Kv4Work& w, int num_sms, cudaStream_t st) {
-  Kv4TreeArgs a;
-  a.w = w;
-  a.nt = w.R > KT_ROWS ? 2 : 1;
-  a.kst = a.nt == 2 ? 2 : 3;
-  a.vst = 2;
-  const size_t chunk = (size_t)w.a.c.dh / 64 * 128 * 128, most = 1024 + 6 * chunk;   // both forms hold six tiles
-  static unsigned long long done128 = 0, done64 = 0;
-  auto kern = w.a.c.dh == 128 ? kv4_tree_kernel<128> : kv4_tree_kernel<64>;
-  const cudaError_t e = allow_smem(kern, most, w.a.c.dh == 128 ? &done128 : &done64);
+template <int DH, int NT> static cudaError_t tree_go(const Kv4Work& w, int num_sms, cudaStream_t st) {
+  constexpr size_t CHUNK = DH / 64 * 128 * 128, STAGE = 8 * kv4_block(DH);
+  constexpr size_t smem = 1024 + (NT + 2 * KT_ST) * CHUNK + (NT == 2 ? 3 : 6) * STAGE;
+  static unsigned long long done = 0;
+  const cudaError_t e = allow_smem(kv4_tree_kernel<DH, NT>, smem, &done);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3(num_sms), dim3(KT_THREADS), most, st, 1, a);
+  return launch_kernel(kv4_tree_kernel<DH, NT>, dim3(num_sms), dim3(KT_THREADS), smem, st, 1, w);
+}
+
+cudaError_t launch_kv4_tree(const Kv4Work& w, int num_sms, cudaStream_t st) {
+  const bool two = w.R > KT_ROWS;
+  if (w.a.c.dh == 128) return two ? tree_go<128, 2>(w, num_sms, st) : tree_go<128, 1>(w, num_sms, st);
+  return two ? tree_go<64, 2>(w, num_sms, st) : tree_go<64, 1>(w, num_sms, st);
 }
 
 }  // namespace medusa

@@ -37,6 +37,14 @@ __device__ __forceinline__ void row_scale(float top, float& down, float& up) {
   up = __uint_as_float((uint32_t)eb << 23);
 }
 
+// Contiguous bytes (multiples of 16) to shared memory by the copy engine.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
+      ::"r"(dst), "l"(src), "r"(bytes), "r"(bar), "l"(pol)
+      : "memory");
+}
+
 // Chunks of sequence b.
 __device__ __forceinline__ int kd_chunks(const CacheView& c, int b) {
   return (clamp_len(c, c.len[b]) + KD_CHUNK - 1) / KD_CHUNK;
