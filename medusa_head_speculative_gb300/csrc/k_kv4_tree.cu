@@ -7,14 +7,15 @@
 // 128 cached slots, a (sequence, head, row block) at a time, and writes a partial for each it
 // leaves.  A row block is one 128-row tile, or two when a head has more rows.  In the CTA
 //
-//   warp 17      copies: the eight blocks of a chunk's keys, then of its values, by the copy engine
+//   warp 18      copies: the eight blocks of a chunk's keys, then of its values, by the copy engine
 //                into a ring of staging slots
 //   warps 8-15   decode: a thread takes 32 elements of one slot (16 bytes of codes, 2 scales) and
 //                writes them as halves (exact) into a 128-byte-swizzled tile: K and V chunks in
 //                rings of two or three stages
-//   warp 16      (one lane) MMAs for two "slots", each with S (128 columns) and O (dh columns) in
+//   warps 16, 17 MMAs, a warp for each of two "slots" with S (128 columns) and O (dh columns) in
 //                tensor memory: S = Q K^T, then O += P V with P read from tensor memory (the A
-//                operand) and V from shared memory (MN-major)
+//                operand) and V from shared memory (MN-major).  Issuing blocks while the tensor
+//                cores are busy, so one warp for both slots left them idle whenever it waited
 //   warps 0-3,   two softmax warpgroups, one per slot, one query row per thread: they load the
 //   4-7          block's queries (scaled by a power of two into a half's range), read S 64 columns
 //                at a time, exponentiate and write P over S as pairs of halves
@@ -33,8 +34,8 @@
 namespace medusa {
 
 constexpr int KT_ROWS = 128, KT_KEYS = KD_CHUNK, KT_ST = 2, KT_MAXLD = 6;
-constexpr int KT_DECODERS = 8, KT_MMA_WARP = 16, KT_LOAD_WARP = 17;
-constexpr int KT_THREADS = 5 * 128;                 // five warpgroups; of the last one two warps work
+constexpr int KT_DECODERS = 8, KT_MMA_WARP = 16, KT_LOAD_WARP = 18;
+constexpr int KT_THREADS = 5 * 128;                 // five warpgroups; of the last one three warps work
 // Registers a thread: 96 at launch (5 x 128 x 96 = 61440), then 152 for softmax, 56 for decode and
 // 64 for the MMA and copy warps: 2 x 152 + 2 x 56 + 64 = 5 x 96.
 constexpr int KT_REG_SOFTMAX = 152, KT_REG_DECODE = 56, KT_REG_MMA = 64;
@@ -61,15 +62,42 @@ enum {
 
 // Instruction descriptor, kind::f16: fp32 D, half A and B, both K-major, M x N.
 constexpr uint32_t idesc_f16(int M, int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24); }
-// D[tmem] (+)= A(tmem) B(smem), kind::f16 (umma_bf16 is the one with A in shared memory: the
-// descriptor says which 16-bit type the operands are).
-__device__ __forceinline__ void kt_mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
+// The MMAs of one S = Q K^T (4 a 64-element half) and of one O += P V (8 x 16 keys), kind::f16
+// (the descriptor says which 16-bit type the operands are), and their commits.  The whole warp
+// comes here and lane 0 issues, by predicate and not in a branch: in a divergent branch every
+// operand of every MMA is moved to a uniform register by itself, and issuing 8 MMAs took longer
+// (1000 cycles) than executing them (512).
+#define KT_QK(OFF, ACC)                                  \
+  "add.s64 x, %1, " OFF ";\n\tadd.s64 y, %2, " OFF ";\n\t" \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, " ACC ";\n\t"
+template <int H>
+__device__ __forceinline__ void kt_qk(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t lead) {
+  if constexpr (H == 2)
+    asm volatile("{\n\t.reg .pred e, no, yes;\n\t.reg .b64 x, y;\n\t"
+                 "setp.ne.b32 e, %4, 0;\n\tsetp.ne.b32 no, 0, 0;\n\tsetp.eq.b32 yes, 0, 0;\n\t"
+                 KT_QK("0", "no") KT_QK("2", "yes") KT_QK("4", "yes") KT_QK("6", "yes")
+                 KT_QK("1024", "yes") KT_QK("1026", "yes") KT_QK("1028", "yes") KT_QK("1030", "yes") "}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(lead) : "memory");
+  else
+    asm volatile("{\n\t.reg .pred e, no, yes;\n\t.reg .b64 x, y;\n\t"
+                 "setp.ne.b32 e, %4, 0;\n\tsetp.ne.b32 no, 0, 0;\n\tsetp.eq.b32 yes, 0, 0;\n\t"
+                 KT_QK("0", "no") KT_QK("2", "yes") KT_QK("4", "yes") KT_QK("6", "yes") "}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(lead) : "memory");
+}
+#define KT_PV(AOFF, BOFF, ACC)                             \
+  "add.u32 x, %1, " AOFF ";\n\tadd.s64 y, %2, " BOFF ";\n\t" \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, " ACC ";\n\t"
+__device__ __forceinline__ void kt_pv(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
+  asm volatile("{\n\t.reg .pred e, first, yes;\n\t.reg .b32 x;\n\t.reg .b64 y;\n\t"
+               "setp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 first, %4, 0;\n\tsetp.eq.b32 yes, 0, 0;\n\t"
+               KT_PV("0", "0", "first") KT_PV("8", "128", "yes") KT_PV("16", "256", "yes") KT_PV("24", "384", "yes")
+               KT_PV("32", "512", "yes") KT_PV("40", "640", "yes") KT_PV("48", "768", "yes") KT_PV("56", "896", "yes") "}"
+               ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead) : "memory");
+}
+__device__ __forceinline__ void kt_commit(uint32_t bar, uint32_t lead) {
+  asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+               "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+               ::"r"(bar), "r"(lead) : "memory");
 }
 // 32 columns of 32 bits of this thread's TMEM lane, without and with the wait.
 __device__ __forceinline__ void kt_st32(uint32_t taddr, const uint32_t (&v)[32]) {
@@ -124,12 +152,12 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
 
   if (tid == 0) {
     mbar_init(bar(TB_QF), 2 * KT_ROWS);
-    mbar_init(bar(TB_QE), 1);
+    mbar_init(bar(TB_QE), 2);
     for (int i = 0; i < KT_ST; ++i) {
       mbar_init(bar(TB_KF + i), KT_DECODERS);
-      mbar_init(bar(TB_KE + i), 1);
+      mbar_init(bar(TB_KE + i), nt);
       mbar_init(bar(TB_VF + i), KT_DECODERS);
-      mbar_init(bar(TB_VE + i), 1);
+      mbar_init(bar(TB_VE + i), nt);
     }
     for (int i = 0; i < KT_MAXLD; ++i) {
       mbar_init(bar(TB_LF + i), 1);
@@ -142,7 +170,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
     }
     mbar_init(bar(TB_MRG), KT_ROWS);
     mbar_init(bar(TB_MFR), KT_ROWS);
-    mbar_init(bar(TB_END), 1);
+    mbar_init(bar(TB_END), 2);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -226,87 +254,63 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
     // ------------------------------------------------------------ MMA issuer
     reg_fewer<KT_REG_MMA>();
     KdCursor k = kd_seek(c, per, w0);
-    if (warp == KT_MMA_WARP && lane == 0) {
+    if (warp < KT_LOAD_WARP) {
+      // ---------------------------------------------------------- MMAs of one slot
+      const int slot = warp - KT_MMA_WARP;
+      const uint32_t lead = lane == 0;
       const uint32_t id_qk = idesc_f16(KT_ROWS, KT_KEYS);
       const uint32_t id_pv = idesc_f16(KT_ROWS, DH) | IDESC_B_MN_MAJOR;
-      int gc = 0, qn = 0, mc = 0;
-      int js0 = 0, js1 = 0;               // jobs (chunk x slot) issued per slot
-      auto wait_k = [&](int x) -> bool {
-        if (!mbar_wait(bar(TB_KF + x % SK), (x / SK) & 1, TC_TIMEOUT_NS)) return false;
-        tc_fence_after();
-        return true;
-      };
-      auto wait_v = [&](int x) -> bool {
-        if (!mbar_wait(bar(TB_VF + x % SV), (x / SV) & 1, TC_TIMEOUT_NS)) return false;
-        tc_fence_after();
-        return true;
-      };
       // descriptors hold addresses in 16-byte units: an offset is added to them
-      const uint64_t dq = sw128_desc(qs), dk = sw128_desc(k0s), dv = sw128_desc_mn(v0s, TILE);
-      auto issue_qk = [&](int slot, int tile, int x) {
-        const uint32_t d = tmem + slot * KT_SLOT_COLS;
-        const uint64_t a = dq + tile * (CHUNK >> 4), b = dk + (x % SK) * (CHUNK >> 4);
-#pragma unroll
-        for (int kk = 0; kk < 4 * H; ++kk) {
-          const uint32_t at = (kk >> 2) * (TILE >> 4) + 2 * (kk & 3);
-          umma_bf16(d, a + at, b + at, id_qk, kk != 0);
-        }
-        umma_commit(bar(TB_SF + slot));
-      };
-      auto wait_p = [&](int slot) -> bool {
-        if (!mbar_wait(bar(TB_PR + slot), (slot ? js1 : js0) & 1, TC_TIMEOUT_NS)) return false;
-        tc_fence_after();
-        return true;
-      };
-      auto issue_pv = [&](int slot, int x, bool acc) {
-        const uint32_t pa = tmem + slot * KT_SLOT_COLS, d = pa + KT_KEYS;
-        const uint64_t b = dv + (x % SV) * (CHUNK >> 4);
-#pragma unroll
-        for (int kk = 0; kk < KT_KEYS / 16; ++kk)      // 16 keys per MMA: 8 columns of P
-          kt_mma_tmem_a(d, pa + 8 * kk, b + kk * (2048 >> 4), id_pv, acc || kk > 0);
-        umma_commit(bar(TB_OF + slot));
-        if (slot) ++js1;
-        else ++js0;
-      };
+      const uint64_t dq = sw128_desc(qs + (nt == 2 ? slot : 0) * CHUNK), dk = sw128_desc(k0s), dv = sw128_desc_mn(v0s, TILE);
+      const uint32_t sp = tmem + slot * KT_SLOT_COLS, od = sp + KT_KEYS;
+      int gc = 0, qn = 0, js = 0;         // chunks, blocks and this slot's jobs so far
       bool dead = false;
+      auto wait_k = [&](int x) { return kt_warp_wait(bar(TB_KF + x % SK), (x / SK) & 1); };
+      auto wait_v = [&](int x) { return kt_warp_wait(bar(TB_VF + x % SV), (x / SV) & 1); };
+      auto scores = [&](int x) {
+        kt_qk<H>(sp, dq, dk + (x % SK) * (CHUNK >> 4), id_qk, lead);
+        kt_commit(bar(TB_SF + slot), lead);
+        kt_commit(bar(TB_KE + x % SK), lead);
+      };
       for (long wi = w0; wi < w1 && !dead;) {
         const int n = (int)min((long)(k.nb - k.j), w1 - wi);
-        const int row0 = (k.q % w.nrb) * KT_ROWS * nt;
-        const int nta = nt == 2 ? (row0 + KT_ROWS < w.R ? 2 : 1) : 1;
-        if (!mbar_wait(bar(TB_QF), qn & 1, TC_TIMEOUT_NS)) { dead = true; break; }
-        ++qn;
+        const bool idle = nt == 2 && (k.q % w.nrb) * KT_ROWS * nt + slot * KT_ROWS >= w.R;
+        constexpr int STEP = nt == 2 ? 1 : 2;            // two tiles: every chunk; one: alternate ones
+        const int i0 = nt == 2 ? 0 : slot;
+        if (!kt_warp_wait(bar(TB_QF), qn & 1)) { dead = true; break; }
         tc_fence_after();
-        // Job y: nt 2: chunk y, both tiles; nt 1: chunk y to slot y & 1.  Each turn issues the P V of
-        // job i and the S of job i + LEAD, so that one slot's MMAs run while the other's S is
-        // exponentiated.
-        constexpr int LEAD = nt == 2 ? 1 : 2;
-#pragma unroll 1
-        for (int i = -LEAD; i < n && !dead; ++i) {
-          const int x = gc + i, y = i + LEAD;
-          if (i >= 0 && !wait_v(x)) { dead = true; break; }
-          // one tile: slot 1's O may be overwritten only after the first warpgroup has merged it
-          // into the previous block's partial
-          if (nt == 1 && i == 1 && mc > 0 && !mbar_wait(bar(TB_MFR), (mc - 1) & 1, TC_TIMEOUT_NS)) { dead = true; break; }
-#pragma unroll 1
-          for (int t = 0; t < nta; ++t) {
-            const int s = nt == 2 ? t : i & 1;         // i + LEAD has the same slot
-            if (i >= 0) {
-              if (!wait_p(s)) { dead = true; break; }
-              issue_pv(s, x, i >= (nt == 2 ? 1 : 2));
-            }
-            if (y < n) {
-              if (t == 0 && !wait_k(x + LEAD)) { dead = true; break; }
-              issue_qk(s, nt == 2 ? t : 0, x + LEAD);
-            }
+        if (idle) {                                      // no rows: only let the stages go
+          for (int i = 0; i < n; ++i) {
+            if (!wait_k(gc + i) || !wait_v(gc + i)) { dead = true; break; }
+            kt_commit(bar(TB_KE + (gc + i) % SK), lead);
+            kt_commit(bar(TB_VE + (gc + i) % SV), lead);
           }
-          if (dead) break;
-          if (i >= 0) umma_commit(bar(TB_VE + x % SV));
-          if (y < n) {
-            umma_commit(bar(TB_KE + (x + LEAD) % SK));
-            if (y + 1 == n) umma_commit(bar(TB_QE));
+        } else if (i0 < n) {
+          if (!wait_k(gc + i0)) { dead = true; break; }
+          scores(gc + i0);
+          if (i0 + STEP >= n) kt_commit(bar(TB_QE), lead);
+#pragma unroll 1
+          for (int i = i0; i < n; i += STEP) {
+            const int x = gc + i;
+            if (!wait_v(x)) { dead = true; break; }
+            // one tile: slot 1's O may be overwritten only after the first warpgroup has merged it
+            // into the previous block's partial
+            if (nt == 1 && i == 1 && qn > 0 && !kt_warp_wait(bar(TB_MFR), (qn - 1) & 1)) { dead = true; break; }
+            if (!kt_warp_wait(bar(TB_PR + slot), js & 1)) { dead = true; break; }
+            tc_fence_after();
+            ++js;
+            kt_pv(od, sp, dv + (x % SV) * (CHUNK >> 4), id_pv, i != i0, lead);
+            kt_commit(bar(TB_OF + slot), lead);
+            kt_commit(bar(TB_VE + x % SV), lead);
+            if (i + STEP < n) {
+              if (!wait_k(x + STEP)) { dead = true; break; }
+              scores(x + STEP);
+              if (i + 2 * STEP >= n) kt_commit(bar(TB_QE), lead);
+            }
           }
         }
-        if (nt == 1) ++mc;
+        if (idle || i0 >= n) kt_commit(bar(TB_QE), lead);
+        ++qn;
         gc += n;
         wi += n;
         k.j += n - 1;
@@ -314,7 +318,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
         if (aborted()) break;
       }
       timed_out = dead;
-      umma_commit(bar(TB_END));           // arrives once every MMA issued above is done
+      kt_commit(bar(TB_END), lead);                      // arrives once this warp's MMAs are done
     }
     else if (warp == KT_LOAD_WARP) {
       // ---------------------------------------------------------- copies: lane l < 8 block l
