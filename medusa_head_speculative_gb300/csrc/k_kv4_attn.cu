@@ -418,25 +418,6 @@ __global__ void __launch_bounds__(KD_WARPS * 32, KD_CTAS<NR>) kv4_rows_kernel(co
 }
 
 // N = 1, 2 or 4 consecutive elements of a lane.
-template <int N> __device__ __forceinline__ void load_f(const float* p, float (&f)[N]) {
-  if constexpr (N == 4) *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(p);
-  else if constexpr (N == 2) *reinterpret_cast<float2*>(f) = *reinterpret_cast<const float2*>(p);
-  else f[0] = p[0];
-}
-template <int N> __device__ __forceinline__ void load_f(const bf16* p, float (&f)[N]) {
-  if constexpr (N == 1) {
-    f[0] = to_f32(p[0]);
-  } else {
-    uint32_t u[N / 2];
-    if constexpr (N == 4) *reinterpret_cast<uint2*>(u) = *reinterpret_cast<const uint2*>(p);
-    else u[0] = *reinterpret_cast<const uint32_t*>(p);
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-      f[2 * i] = __uint_as_float(u[i] << 16);
-      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-  }
-}
 template <int N> __device__ __forceinline__ void store_f(float* p, const float (&f)[N]) {
   if constexpr (N == 4) *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
   else if constexpr (N == 2) *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
@@ -448,13 +429,30 @@ template <int N> __device__ __forceinline__ void store_f(bf16* p, const float (&
   else p[0] = from_f32<bf16>(f[0]);
 }
 
-// One warp a query row: joins the prefix's partials (o, max, sum), adds the call's own rows the
-// row sees, one at a time in float, and rounds the quotient once.  A tree row sees its
-// ancestors only (at most 9), so going through the set bits beats a masked product with all n1.
-template <typename T, int DH>
+// 4, 2 or 1 elements of a lane as loaded: bf16 pairs stay packed until they are used.
+template <typename T, int N> struct LaneRow {
+  uint32_t u[(N * sizeof(T) + 3) / 4];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (N * sizeof(T) == 16) *reinterpret_cast<uint4*>(u) = *reinterpret_cast<const uint4*>(p);
+    else if constexpr (N * sizeof(T) == 8) *reinterpret_cast<uint2*>(u) = *reinterpret_cast<const uint2*>(p);
+    else if constexpr (N * sizeof(T) == 4) u[0] = *reinterpret_cast<const uint32_t*>(p);
+    else u[0] = *reinterpret_cast<const uint16_t*>(p);
+  }
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(u[i]);
+    else return __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+  }
+};
+
+// One warp a query row: joins the prefix's partials (o, reference, sum), adds the call's own rows
+// the row sees in float, and rounds the quotient once.  A tree row sees its ancestors only (at
+// most 9), so going through the set bits beats a masked product with all n1.  The kernel waits
+// for loads and nothing else, so what they depend on comes in two rounds: query, span and mask
+// first; then the first partials and, with them, the first four visible rows' keys and values.
+// SB partials in a round: few slots a row (many rows a head) need few registers, many need them.
+template <typename T, int DH, int SB>
 __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant__ Kv4Work w) {
   constexpr int C = DH / 32;
-  pdl_wait();
   const Kv4AttnArgs& a = w.a;
   const CacheView& c = a.c;
   const long row = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -465,26 +463,61 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant_
   const int node = (int)(bn % a.n1), b = (int)(bn / a.n1);
   const int g = hq / a.G, r = node * a.G + hq - g * a.G;
   const int rb = r / w.rb, in = r - rb * w.rb;
+  const int len = clamp_len(c, c.len[b]);
+  // lane i < 8: word i of the row's visible bits
+  uint32_t mine = 0;
+  if (a.tk && lane < (a.n1 + 31) / 32) {
+    const int first = 32 * lane;
+    mine = a.mask ? a.mask[(long)node * 8 + lane]
+                  : (node >= first + 31 ? 0xffffffffu : node < first ? 0u : (2u << (node - first)) - 1u);
+    if (a.n1 < first + 32) mine &= (1u << (a.n1 - first)) - 1u;
+  }
+  LaneRow<T, C> q;
+  if (a.tk) q.load(static_cast<const T*>(a.q) + bn * a.q_row + hq * a.q_head + lane * C);
+  int wd = 0;
+  uint32_t bits = __shfl_sync(0xffffffffu, mine, 0);
+  auto next_row = [&]() {                  // the next visible row, -1: none
+    while (!bits && ++wd < 8) bits = __shfl_sync(0xffffffffu, mine, wd);
+    if (!bits) return -1;
+    const int j = 32 * wd + __ffs(bits) - 1;
+    bits &= bits - 1;
+    return j;
+  };
+  LaneRow<T, C> tk[4], tv[4];
+  int seen = 0;                            // of the four, how many there are
+  auto load_rows = [&]() {
+    seen = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = next_row();
+      if (j < 0) continue;
+      const long off = (((long)b * a.n1 + j) * c.Hkv + g) * DH + lane * C;
+      tk[u].load(static_cast<const T*>(a.tk) + off);
+      tv[u].load(static_cast<const T*>(a.tv) + off);
+      seen = u + 1;
+    }
+  };
+  if (a.tk) load_rows();
+  pdl_wait();                              // the partials come from the kernel before; the above does not
   float m = -INFINITY, l = 0.f, o[C];
 #pragma unroll
   for (int i = 0; i < C; ++i) o[i] = 0.f;
-  if (clamp_len(c, c.len[b]) > 0) {
-    // eight slots in one round trip; the reference moves once for them
+  if (len > 0) {
     const int2 sp = w.span[((long)b * c.Hkv + g) * w.nrb + rb];
-    for (int s0 = sp.x; s0 < sp.y; s0 += 8) {
-      float2 y[8];
-      float v[8][C];
+#pragma unroll 1
+    for (int s0 = sp.x; s0 < sp.y; s0 += SB) {
+      float2 y[SB];
+      LaneRow<float, C> v[SB];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const long at = (long)(s0 + u) * w.rb + in;
-        y[u] = s0 + u < sp.y ? w.part_ml[at] : make_float2(-INFINITY, 0.f);
-#pragma unroll
-        for (int i = 0; i < C; ++i) v[u][i] = 0.f;
-        if (s0 + u < sp.y) load_f<C>(w.part_o + at * DH + lane * C, v[u]);
+      for (int u = 0; u < SB; ++u) {
+        const long at = (long)min(s0 + u, sp.y - 1) * w.rb + in;
+        y[u] = w.part_ml[at];
+        v[u].load(w.part_o + at * DH + lane * C);
+        if (s0 + u >= sp.y) y[u] = make_float2(-INFINITY, 0.f);
       }
       float mn = m;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) mn = fmaxf(mn, y[u].x);
+      for (int u = 0; u < SB; ++u) mn = fmaxf(mn, y[u].x);
       if (mn == -INFINITY) continue;
       const float f = ex2_approx(m - mn);
       m = mn;
@@ -492,7 +525,7 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant_
 #pragma unroll
       for (int i = 0; i < C; ++i) o[i] *= f;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < SB; ++u) {
         const float h = ex2_approx(y[u].x - mn);
         l += y[u].y * h;
 #pragma unroll
@@ -503,55 +536,48 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant_
 #pragma unroll
   for (int i = 0; i < C; ++i) o[i] *= c.gv;
   if (a.tk) {
-    const T* q = static_cast<const T*>(a.q) + bn * a.q_row + hq * a.q_head + lane * C;
-    float x[C];
-    load_f<C>(q, x);
+    const float scale = a.scale * 1.4426950408889634f;
+#pragma unroll 1
+    while (seen > 0) {
+      float sc[4];
 #pragma unroll
-    for (int i = 0; i < C; ++i) x[i] *= a.scale * 1.4426950408889634f;
-    for (int wd = 0; wd < (a.n1 + 31) / 32; ++wd) {
-      uint32_t bits = a.mask ? a.mask[(long)node * 8 + wd]
-                             : (node >= 32 * wd + 31 ? 0xffffffffu : node < 32 * wd ? 0u : (2u << (node - 32 * wd)) - 1u);
-      if (a.n1 < 32 * wd + 32) bits &= (1u << (a.n1 - 32 * wd)) - 1u;
-      while (bits) {
-        // four visible rows in one round trip
-        float sc[4], v[4][C];
+      for (int u = 0; u < 4; ++u) {
+        sc[u] = 0.f;
+        if (u < seen) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          sc[u] = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < C; ++i) v[u][i] = 0.f;
-          if (bits) {
-            const int j = 32 * wd + __ffs(bits) - 1;
-            bits &= bits - 1;
-            const long off = (((long)b * a.n1 + j) * c.Hkv + g) * DH + lane * C;
-            float kx[C];
-            load_f<C>(static_cast<const T*>(a.tk) + off, kx);
-            load_f<C>(static_cast<const T*>(a.tv) + off, v[u]);
-            sc[u] = 0.f;
-#pragma unroll
-            for (int i = 0; i < C; ++i) sc[u] = fmaf(x[i], kx[i], sc[u]);
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) sc[u] = warp_sum(sc[u]);
-        const float mn = fmaxf(fmaxf(m, fmaxf(sc[0], sc[1])), fmaxf(sc[2], sc[3])), f = ex2_approx(m - mn);
-        m = mn;
-        l *= f;
-#pragma unroll
-        for (int i = 0; i < C; ++i) o[i] *= f;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float p = ex2_approx(sc[u] - mn);
-          l += p;
-#pragma unroll
-          for (int i = 0; i < C; ++i) o[i] = fmaf(p, v[u][i], o[i]);
+          for (int i = 0; i < C; ++i) sc[u] = fmaf(q[i], tk[u][i], sc[u]);
         }
       }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sc[u] += __shfl_xor_sync(0xffffffffu, sc[u], d);
+      float mn = m;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        sc[u] = u < seen ? sc[u] * scale : -INFINITY;
+        mn = fmaxf(mn, sc[u]);
+      }
+      const float f = ex2_approx(m - mn);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < C; ++i) o[i] *= f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (u >= seen) continue;
+        const float p = ex2_approx(sc[u] - mn);
+        l += p;
+#pragma unroll
+        for (int i = 0; i < C; ++i) o[i] = fmaf(p, tv[u][i], o[i]);
+      }
+      load_rows();
     }
   }
   T* y = static_cast<T*>(a.o) + bn * a.o_row + hq * a.o_head + lane * C;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
-  for (int i = 0; i < C; ++i) o[i] = l > 0.f ? o[i] / l : 0.f;
+  for (int i = 0; i < C; ++i) o[i] = l > 0.f ? o[i] * inv : 0.f;
   store_f<C>(y, o);
 }
 
@@ -591,9 +617,11 @@ static cudaError_t rows_go(const Kv4Work& w, int num_sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   return launch_kernel(kern, dim3(num_sms * KD_CTAS<NR>), dim3(KD_WARPS * 32), smem, st, 1, w);
 }
-template <typename T> static cudaError_t combine(const Kv4Work& w, cudaStream_t st) {
+template <typename T, int SB> static cudaError_t combine(const Kv4Work& w, cudaStream_t st) {
   const long rows = (long)w.a.c.B * w.a.n1 * w.a.Hq;
-  auto kern = w.a.c.dh == 32 ? kv4_combine_kernel<T, 32> : w.a.c.dh == 64 ? kv4_combine_kernel<T, 64> : kv4_combine_kernel<T, 128>;
+  auto kern = w.a.c.dh == 32   ? kv4_combine_kernel<T, 32, SB>
+              : w.a.c.dh == 64 ? kv4_combine_kernel<T, 64, SB>
+                               : kv4_combine_kernel<T, 128, SB>;
   return launch_kernel(kern, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, 1, w);
 }
 template <typename T, bool SPLIT>
@@ -622,7 +650,9 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, int dtype, void* ws, int 
   cudaError_t e = kv4_tree_takes(dtype, a.c.dh, w.R) ? launch_kv4_tree(w, num_sms, st)
                   : dtype == MEDUSA_F32 ? rows_dh<float, true>(w, num_sms, st) : rows_dh<bf16, false>(w, num_sms, st);
   if (e != cudaSuccess) return e;
-  return dtype == MEDUSA_F32 ? combine<float>(w, st) : combine<bf16>(w, st);
+  // a head with up to 16 rows is shared out over many CTAs, one with more over a few
+  if (w.R <= KD_ROWS) return dtype == MEDUSA_F32 ? combine<float, 8>(w, st) : combine<bf16, 8>(w, st);
+  return dtype == MEDUSA_F32 ? combine<float, 2>(w, st) : combine<bf16, 2>(w, st);
 }
 
 }  // namespace medusa
