@@ -94,6 +94,7 @@ medusa_status check_cache(const medusa_cache_dims* d) {
   if (d->capacity < 1 || d->page_size < 0 || d->max_nodes < 1) return MEDUSA_ERR_INVALID;
   if (d->page_size > 0 && (d->capacity % d->page_size != 0 || d->num_pages < 1)) return MEDUSA_ERR_INVALID;
   if (d->dh != 32 && d->dh != 64 && d->dh != 128) return MEDUSA_ERR_UNSUPPORTED;
+  if (d->Hq > 65535 || d->B > (1 << 22)) return MEDUSA_ERR_UNSUPPORTED;         // launch grids
   if (d->max_nodes > MEDUSA_MAX_NODES || d->capacity > MEDUSA_MAX_CAPACITY) return MEDUSA_ERR_UNSUPPORTED;
   if (d->format == MEDUSA_KV4 && (d->page_size > 0 ? d->page_size : d->capacity) % 16 != 0)
     return MEDUSA_ERR_UNSUPPORTED;

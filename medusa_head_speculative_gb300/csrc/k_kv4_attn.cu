@@ -455,14 +455,13 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant_
   constexpr int C = DH / 32;
   const Kv4AttnArgs& a = w.a;
   const CacheView& c = a.c;
-  const long row = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= (long)c.B * a.n1 * a.Hq) return;
+  // block (sequence and node, query heads)
   const int lane = threadIdx.x & 31;
-  const int hq = (int)(row % a.Hq);
-  const long bn = row / a.Hq;
-  const int node = (int)(bn % a.n1), b = (int)(bn / a.n1);
+  const int hq = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (hq >= a.Hq) return;
+  const int bn = blockIdx.x, b = bn / a.n1, node = bn - b * a.n1;
   const int g = hq / a.G, r = node * a.G + hq - g * a.G;
-  const int rb = r / w.rb, in = r - rb * w.rb;
+  const int rb = w.nrb == 1 ? 0 : r / w.rb, in = r - rb * w.rb;
   const int len = clamp_len(c, c.len[b]);
   // lane i < 8: word i of the row's visible bits
   uint32_t mine = 0;
@@ -473,7 +472,7 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant_
     if (a.n1 < first + 32) mine &= (1u << (a.n1 - first)) - 1u;
   }
   LaneRow<T, C> q;
-  if (a.tk) q.load(static_cast<const T*>(a.q) + bn * a.q_row + hq * a.q_head + lane * C);
+  if (a.tk) q.load(static_cast<const T*>(a.q) + (long)bn * a.q_row + hq * a.q_head + lane * C);
   int wd = 0;
   uint32_t bits = __shfl_sync(0xffffffffu, mine, 0);
   auto next_row = [&]() {                  // the next visible row, -1: none
@@ -483,6 +482,8 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant_
     bits &= bits - 1;
     return j;
   };
+  const long tree0 = ((long)b * a.n1 * c.Hkv + g) * DH + lane * C;
+  const int tree_row = c.Hkv * DH;
   LaneRow<T, C> tk[4], tv[4];
   int seen = 0;                            // of the four, how many there are
   auto load_rows = [&]() {
@@ -491,7 +492,7 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant_
     for (int u = 0; u < 4; ++u) {
       const int j = next_row();
       if (j < 0) continue;
-      const long off = (((long)b * a.n1 + j) * c.Hkv + g) * DH + lane * C;
+      const long off = tree0 + (long)j * tree_row;
       tk[u].load(static_cast<const T*>(a.tk) + off);
       tv[u].load(static_cast<const T*>(a.tv) + off);
       seen = u + 1;
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant_
       for (int u = 0; u < SB; ++u) {
         const long at = (long)min(s0 + u, sp.y - 1) * w.rb + in;
         y[u] = w.part_ml[at];
-        v[u].load(w.part_o + at * DH + lane * C);
+        v[u].load(w.part_o + (at * DH + lane * C));
         if (s0 + u >= sp.y) y[u] = make_float2(-INFINITY, 0.f);
       }
       float mn = m;
@@ -574,7 +575,7 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant_
       load_rows();
     }
   }
-  T* y = static_cast<T*>(a.o) + bn * a.o_row + hq * a.o_head + lane * C;
+  T* y = static_cast<T*>(a.o) + (long)bn * a.o_row + hq * a.o_head + lane * C;
   const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
   for (int i = 0; i < C; ++i) o[i] = l > 0.f ? o[i] * inv : 0.f;
@@ -618,11 +619,12 @@ static cudaError_t rows_go(const Kv4Work& w, int num_sms, cudaStream_t st) {
   return launch_kernel(kern, dim3(num_sms * KD_CTAS<NR>), dim3(KD_WARPS * 32), smem, st, 1, w);
 }
 template <typename T, int SB> static cudaError_t combine(const Kv4Work& w, cudaStream_t st) {
-  const long rows = (long)w.a.c.B * w.a.n1 * w.a.Hq;
+  const int warps = w.a.Hq < 8 ? w.a.Hq : 8;
+  const dim3 grid((unsigned)w.a.c.B * w.a.n1, (unsigned)((w.a.Hq + warps - 1) / warps));
   auto kern = w.a.c.dh == 32   ? kv4_combine_kernel<T, 32, SB>
               : w.a.c.dh == 64 ? kv4_combine_kernel<T, 64, SB>
                                : kv4_combine_kernel<T, 128, SB>;
-  return launch_kernel(kern, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, 1, w);
+  return launch_kernel(kern, grid, dim3(32 * warps), 0, st, 1, w);
 }
 template <typename T, bool SPLIT>
 static cudaError_t rows_dh(const Kv4Work& w, int num_sms, cudaStream_t st) {

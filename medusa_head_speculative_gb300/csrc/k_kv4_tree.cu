@@ -112,6 +112,11 @@ __device__ __forceinline__ void kt_st32(uint32_t taddr, const uint32_t (&v)[32])
       : "memory");
 }
 __device__ __forceinline__ void kt_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ bool kt_warp_wait(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, TC_TIMEOUT_NS));
 }
@@ -130,7 +135,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t bars[TB_COUNT];
   __shared__ uint32_t tmem_slot;
-  __shared__ int s_abort;
+  __shared__ int s_abort, s_turn;                    // s_turn: an MMA warp is issuing
   __shared__ int s_valid[KT_MAXLD];                  // slots of the chunk there are
   __shared__ float2 s_ml[KT_ROWS];                   // second slot's (reference, sum) per row
   const CacheView& c = w.a.c;
@@ -148,7 +153,8 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
     pdl_trigger();
     return;
   }
-  const long w0 = W * blockIdx.x / ctas, w1 = W * (blockIdx.x + 1) / ctas;
+  const long w0 = W * blockIdx.x / ctas;
+  const int total = (int)(W * (blockIdx.x + 1) / ctas - w0);   // this CTA's chunks
 
   if (tid == 0) {
     mbar_init(bar(TB_QF), 2 * KT_ROWS);
@@ -171,7 +177,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
     mbar_init(bar(TB_MRG), KT_ROWS);
     mbar_init(bar(TB_MFR), KT_ROWS);
     mbar_init(bar(TB_END), 2);
-    s_abort = 0;
+    s_abort = s_turn = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == KT_MMA_WARP) tmem_alloc(smem_u32(&tmem_slot), 2 * KT_SLOT_COLS);
@@ -189,63 +195,64 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
     // 16 bytes of codes a lane: neighbouring lanes the quarters (dh 64: halves) of a slot, so that
     // reading a staging slot takes every bank once; and so does writing the tile, with the upper
     // half of a head (16 KB further on: the same banks) written two 16-byte units out of step.
-    constexpr int Q = DH / 32, KEYS = 32 / Q;         // lanes a slot, slots a warp at a time
-    const int quarter = lane % Q, eh = quarter >> 1, twist = eh;
-    const int dw = warp - 8;
-    int u = 0;                                        // staging units (K and V of each chunk)
-    bool dead = false;
-    for (long x = w0; x < w1 && !dead; ++x) {
-      const int i = (int)(x - w0);
-#pragma unroll 1
-      for (int part = 0; part < 2; ++part, ++u) {
-        const int st = u % SL;
-        if (!kt_warp_wait(bar(TB_LF + st), (u / SL) & 1)) { dead = true; break; }
-        const int valid = s_valid[st];
-        uint4 cw[Q / 2];
-        uint32_t sc[Q / 2];
+    // A warp has one block (16 slots) of each chunk; all its addresses are fixed but for the stage.
+    constexpr int Q = DH / 32, PIECES = Q / 2;        // lanes a slot, pieces (8 slots on) a lane
+    const int quarter = lane % Q, eh = quarter >> 1, dw = warp - 8, key0 = dw * KV4_SLOTS + lane / Q;
+    const uint32_t codes_at = l0s + dw * BLK + lane / Q * (DH / 2) + quarter * 16;
+    const uint32_t scales_at = l0s + dw * BLK + 8 * DH + lane / Q * (DH / 16) + quarter * 2;
+    uint32_t out_at[4];                               // of words 0..3 in the order they are written
 #pragma unroll
-        for (int y = 0; y < Q / 2; ++y) {
-          const int key = (dw * (Q / 2) + y) * KEYS + lane / Q;
-          cw[y] = make_uint4(0u, 0u, 0u, 0u);         // past the length: zeros, whatever lies there
-          sc[y] = 0u;
-          if (key < valid) {
-            const uint32_t blk = l0s + st * STAGE + (key >> 4) * BLK;
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(cw[y].x), "=r"(cw[y].y), "=r"(cw[y].z), "=r"(cw[y].w)
-                         : "r"(blk + (key & 15) * (DH / 2) + quarter * 16));
-            uint16_t two;
-            asm volatile("ld.shared.b16 %0, [%1];" : "=h"(two) : "r"(blk + 8 * DH + (key & 15) * (DH / 16) + quarter * 2));
-            sc[y] = two;
-          }
+    for (int z = 0; z < 4; ++z)
+      out_at[z] = eh * TILE + key0 * 128 + ((((quarter & 1) * 4 + (z ^ (eh << 1))) ^ (key0 & 7)) << 4);
+    const uint32_t first = eh ? 8 : 0, swap = eh ? 0x4401u : 0x4410u;   // an upper half's lane: words 2, 3 first
+    int st = 0;
+    uint32_t ph = 0;                                  // staging slot and its phase
+    bool dead = false;
+    for (int i = 0; i < total && !dead; ++i) {
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part) {
+        if (!kt_warp_wait(bar(TB_LF + st), ph)) { dead = true; break; }
+        const int valid = s_valid[st];
+        uint32_t cw[PIECES][4], sc[PIECES];
+#pragma unroll
+        for (int y = 0; y < PIECES; ++y) {
+          const uint32_t at = codes_at + st * STAGE + y * 8 * (DH / 2);
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(cw[y][0]), "=r"(cw[y][1]) : "r"(at + first));
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(cw[y][2]), "=r"(cw[y][3]) : "r"(at + (first ^ 8)));
+          uint16_t two;
+          asm volatile("ld.shared.b16 %0, [%1];" : "=h"(two) : "r"(scales_at + st * STAGE + y * 8 * (DH / 16)));
+          sc[y] = __byte_perm(two, 0, swap);
+        }
+        if (valid < KT_KEYS) {                        // past the length: zeros, whatever lies there
+#pragma unroll
+          for (int y = 0; y < PIECES; ++y)
+            if (key0 + 8 * y >= valid) cw[y][0] = cw[y][1] = cw[y][2] = cw[y][3] = sc[y] = 0u;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(TB_LE + st));
-        const int S = part ? SV : SK, full = (part ? TB_VF : TB_KF) + i % S;
-        if (!kt_warp_wait(bar((part ? TB_VE : TB_KE) + i % S), ((i / S) & 1) ^ 1)) { dead = true; break; }
-        const uint32_t tile = (part ? v0s : k0s) + (i % S) * CHUNK + eh * TILE;
+        if (++st == SL) {
+          st = 0;
+          ph ^= 1;
+        }
+        const int stage = i & 1;
+        if (!kt_warp_wait(bar((part ? TB_VE : TB_KE) + stage), ((i >> 1) & 1) ^ 1)) { dead = true; break; }
+        const uint32_t tile = (part ? v0s : k0s) + stage * CHUNK;
 #pragma unroll
-        for (int y = 0; y < Q / 2; ++y) {
-          const int key = (dw * (Q / 2) + y) * KEYS + lane / Q;
+        for (int y = 0; y < PIECES; ++y) {
           const __half2 s2 = kv4_scales((uint16_t)sc[y]);
-          const __half2 slo = __low2half2(s2), shi = __high2half2(s2);
-          // units 0, 1 have the first scale, 2, 3 the second; a twisted lane takes 2, 3 first
-          const uint32_t wd[4] = {twist ? cw[y].z : cw[y].x, twist ? cw[y].w : cw[y].y, twist ? cw[y].x : cw[y].z,
-                                  twist ? cw[y].y : cw[y].w};
-          const __half2 s0 = twist ? shi : slo, s1 = twist ? slo : shi;
-          const uint32_t row = tile + key * 128;
+          const __half2 s0 = __low2half2(s2), s1 = __high2half2(s2);
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
             const __half2 s = z < 2 ? s0 : s1;
-            const int unit = (quarter & 1) * 4 + (z ^ (twist << 1));
             __half2 h[4];
-            kv4_pairs(wd[z], h);
-            st_shared16(row + ((unit ^ (key & 7)) << 4), h2u(__hmul2(h[0], s)), h2u(__hmul2(h[1], s)), h2u(__hmul2(h[2], s)),
+            kv4_pairs(cw[y][z], h);
+            st_shared16(tile + out_at[z] + y * 1024, h2u(__hmul2(h[0], s)), h2u(__hmul2(h[1], s)), h2u(__hmul2(h[2], s)),
                         h2u(__hmul2(h[3], s)));
           }
         }
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(full));
+        if (lane == 0) mbar_arrive(bar((part ? TB_VF : TB_KF) + stage));
       }
       if (aborted()) break;
     }
@@ -267,13 +274,31 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
       bool dead = false;
       auto wait_k = [&](int x) { return kt_warp_wait(bar(TB_KF + x % SK), (x / SK) & 1); };
       auto wait_v = [&](int x) { return kt_warp_wait(bar(TB_VF + x % SV), (x / SV) & 1); };
+      // Two tiles: one warp at a time issues.  Interleaved, both slots' products would end late
+      // together and both softmaxes start together, with the tensor cores idle meanwhile; one after
+      // the other the slots stay half a turn apart.  (One tile's slots take alternate chunks and
+      // are apart already.)
+      auto take_turn = [&]() -> bool {
+        if (nt == 1) return true;
+        bool ok = true;
+        if (lane == 0 && atomicCAS(&s_turn, 0, 1) != 0) {
+          const uint64_t t0 = gtimer();
+          while (ok && atomicCAS(&s_turn, 0, 1) != 0) ok = gtimer() - t0 < TC_TIMEOUT_NS;
+        }
+        return __all_sync(0xffffffffu, ok);
+      };
+      auto end_turn = [&]() {
+        if (nt == 1) return;
+        if (lane == 0) atomicExch(&s_turn, 0);
+        __syncwarp();
+      };
       auto scores = [&](int x) {
         kt_qk<H>(sp, dq, dk + (x % SK) * (CHUNK >> 4), id_qk, lead);
         kt_commit(bar(TB_SF + slot), lead);
         kt_commit(bar(TB_KE + x % SK), lead);
       };
-      for (long wi = w0; wi < w1 && !dead;) {
-        const int n = (int)min((long)(k.nb - k.j), w1 - wi);
+      for (int wi = 0; wi < total && !dead;) {
+        const int n = min(k.nb - k.j, total - wi);
         const bool idle = nt == 2 && (k.q % w.nrb) * KT_ROWS * nt + slot * KT_ROWS >= w.R;
         constexpr int STEP = nt == 2 ? 1 : 2;            // two tiles: every chunk; one: alternate ones
         const int i0 = nt == 2 ? 0 : slot;
@@ -286,8 +311,9 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
             kt_commit(bar(TB_VE + (gc + i) % SV), lead);
           }
         } else if (i0 < n) {
-          if (!wait_k(gc + i0)) { dead = true; break; }
+          if (!wait_k(gc + i0) || !take_turn()) { dead = true; break; }
           scores(gc + i0);
+          end_turn();
           if (i0 + STEP >= n) kt_commit(bar(TB_QE), lead);
 #pragma unroll 1
           for (int i = i0; i < n; i += STEP) {
@@ -299,12 +325,23 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
             if (!kt_warp_wait(bar(TB_PR + slot), js & 1)) { dead = true; break; }
             tc_fence_after();
             ++js;
+            // the next S in the same turn where its keys are there (waiting for them with the turn
+            // taken could wait for the other slot)
+            const bool more = i + STEP < n;
+            const int xn = x + STEP;
+            const bool now = more && __all_sync(0xffffffffu, mbar_test(bar(TB_KF + xn % SK), (xn / SK) & 1));
+            if (!take_turn()) { dead = true; break; }
             kt_pv(od, sp, dv + (x % SV) * (CHUNK >> 4), id_pv, i != i0, lead);
             kt_commit(bar(TB_OF + slot), lead);
             kt_commit(bar(TB_VE + x % SV), lead);
-            if (i + STEP < n) {
-              if (!wait_k(x + STEP)) { dead = true; break; }
-              scores(x + STEP);
+            if (now) scores(xn);
+            end_turn();
+            if (more) {
+              if (!now) {
+                if (!wait_k(xn) || !take_turn()) { dead = true; break; }
+                scores(xn);
+                end_turn();
+              }
               if (i + 2 * STEP >= n) kt_commit(bar(TB_QE), lead);
             }
           }
@@ -314,7 +351,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
         gc += n;
         wi += n;
         k.j += n - 1;
-        if (wi < w1) kd_next(c, per, k);
+        if (wi < total) kd_next(c, per, k);
         if (aborted()) break;
       }
       timed_out = dead;
@@ -325,7 +362,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
       const int upp = (c.page_table ? c.page_size : c.capacity) / KV4_SLOTS;
       const uint64_t pol = policy_evict_first();
       int u = 0, waited = 0, len_b = -1, len = 0;
-      for (long x = w0; x < w1; ++x) {
+      for (int x = 0; x < total; ++x) {
         if (k.b != len_b) {
           len_b = k.b;
           len = clamp_len(c, c.len[k.b]);
@@ -357,7 +394,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
                       bar(TB_LF + st), pol);
         }
         if (!ok) { timed_out = true; break; }
-        if (x + 1 < w1) kd_next(c, per, k);
+        if (x + 1 < total) kd_next(c, per, k);
         if (aborted()) break;
       }
       // copies still under way when the block gives up (bounded): the last SL units at most
@@ -375,8 +412,8 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
     KdCursor k = kd_seek(c, per, w0);
     int js = 0, mc = 0, qn = 0;
     int js1 = 0;                                     // slot 1's jobs (merging warpgroup)
-    for (long wi = w0; wi < w1;) {
-      const int n = (int)min((long)(k.nb - k.j), w1 - wi);
+    for (int wi = 0; wi < total;) {
+      const int n = min(k.nb - k.j, total - wi);
       const int g = k.q / w.nrb, rblk = k.q - g * w.nrb, len = clamp_len(c, c.len[k.b]);
       const int row0 = rblk * KT_ROWS * nt, tile = nt == 2 ? slot : 0;
       const int gr = row0 + tile * KT_ROWS + r;
@@ -443,8 +480,8 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
             float x0 = fmaxf(s[0], s[1]), x1 = fmaxf(s[2], s[3]);
 #pragma unroll
             for (int j = 4; j < 64; j += 4) {
-              x0 = fmaxf(x0, fmaxf(s[j], s[j + 1]));
-              x1 = fmaxf(x1, fmaxf(s[j + 2], s[j + 3]));
+              x0 = max3(x0, s[j], s[j + 1]);
+              x1 = max3(x1, s[j + 2], s[j + 3]);
             }
             const float mx = fmaxf(x0, x1) * rs;     // the row's factor is positive
             const bool raise = mx > m_use + KD_TOP;
@@ -482,19 +519,20 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
               l_acc *= f;
               m_use = mn;
             }
-            float l0 = 0.f, l1 = 0.f;
+            F2 ls = f2(0.f, 0.f);
             uint32_t pk[32];
             const float nm = -m_use;
 #pragma unroll
             for (int j = 0; j < 64; j += 2) {
-              const float p0 = ex2_approx(fmaf(s[j], rs, nm)), p1 = ex2_approx(fmaf(s[j + 1], rs, nm));
-              l0 += p0;
-              l1 += p1;
+              float p0, p1;
+              unf2(fma2(f2(s[j], s[j + 1]), f2(rs, rs), f2(nm, nm)), p0, p1);
+              p0 = ex2_approx(p0); p1 = ex2_approx(p1);
+              ls = add2(ls, f2(p0, p1));
               pk[j / 2] = half_pair(p0, p1);
             }
             kt_st32(scol + 32 * hf, pk);
             kt_st_wait();
-            l_acc += l0 + l1;
+            float l0, l1; unf2(ls, l0, l1); l_acc += l0 + l1;
           }
         }
         tc_fence_before();
@@ -573,7 +611,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
       }
       wi += n;
       k.j += n - 1;
-      if (wi < w1) kd_next(c, per, k);
+      if (wi < total) kd_next(c, per, k);
     }
   }
   if (timed_out) {
