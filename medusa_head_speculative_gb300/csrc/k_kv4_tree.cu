@@ -138,6 +138,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
   __shared__ int s_abort, s_turn;                    // s_turn: an MMA warp is issuing
   __shared__ int s_valid[KT_MAXLD];                  // slots of the chunk there are
   __shared__ float2 s_ml[KT_ROWS];                   // second slot's (reference, sum) per row
+  __shared__ float s_rs[2][KT_ROWS];                 // one tile: the rows' score factors, two blocks
   const CacheView& c = w.a.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int nt = NT, SK = KT_ST, SV = KT_ST, SL = NT == 2 ? 3 : 6;   // tiles, stages of the K, V and staging rings
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
   const int total = (int)(W * (blockIdx.x + 1) / ctas - w0);   // this CTA's chunks
 
   if (tid == 0) {
-    mbar_init(bar(TB_QF), 2 * KT_ROWS);
+    mbar_init(bar(TB_QF), nt * KT_ROWS);
     mbar_init(bar(TB_QE), 2);
     for (int i = 0; i < KT_ST; ++i) {
       mbar_init(bar(TB_KF + i), KT_DECODERS);
@@ -419,41 +420,38 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
       const int gr = row0 + tile * KT_ROWS + r;
       const bool row_ok = gr < w.R;
       const bool live = row0 + tile * KT_ROWS + wl * 32 < w.R;     // the warp has rows
-      // ---- the block's queries: scaled into [1, 2) by a power of two, as halves.  One tile:
-      // the warpgroups write a 64-element half each (dh 64: the first all of it)
-      float rs;
-      {
+      // ---- the block's queries: scaled into [1, 2) by a power of two, as halves.  Two tiles: each
+      // slot its own; one: the second slot, which is done with the block before sooner, while the
+      // first one writes that block's partial (and finds the rows' factors in shared memory)
+      float rs = 0.f;
+      if (nt == 2 || slot == 1) {
         const int node = row_ok ? gr / w.a.G : 0, hq = g * w.a.G + (row_ok ? gr - node * w.a.G : 0);
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const bf16*>(w.a.q) +
                                                           ((long)k.b * w.a.n1 + node) * w.a.q_row + hq * w.a.q_head);
-        float top = 0.f;
-        if (row_ok) {
-#pragma unroll 8
-          for (int i = 0; i < DH / 8; ++i) {
-            float f[8];
-            unpack16(src[i], f);
+        uint4 raw[DH / 8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
-          }
+        for (int u = 0; u < DH / 8; ++u) raw[u] = row_ok ? src[u] : make_uint4(0u, 0u, 0u, 0u);
+        float top = 0.f;
+#pragma unroll
+        for (int u = 0; u < DH / 8; ++u) {
+          float f[8];
+          unpack16(raw[u], f);
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) top = max3(top, fabsf(f[e]), fabsf(f[e + 1]));
         }
         float down, up;
         row_scale(top, down, up);
         rs = up * (w.a.scale * c.gk) * 1.4426950408889634f;
+        if (nt == 1) s_rs[qn & 1][r] = rs;
         if (qn > 0 && !kt_warp_wait(bar(TB_QE), (qn - 1) & 1)) { timed_out = true; break; }
-        ++qn;
-        if (nt == 2 || H == 2 || slot == 0) {
-          const int h0 = nt == 2 ? 0 : slot, h1 = nt == 2 || H == 1 ? H : slot + 1;
-#pragma unroll 1
-          for (int h = h0; h < h1; ++h) {
-            const uint32_t row = qs + tile * CHUNK + h * TILE + r * 128;
+        const uint32_t row = qs + tile * CHUNK + r * 128;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              float f[8];
-              unpack16(row_ok ? src[h * 8 + u] : make_uint4(0u, 0u, 0u, 0u), f);
-              st_shared16(row + ((u ^ (r & 7)) << 4), half_pair(f[0] * down, f[1] * down), half_pair(f[2] * down, f[3] * down),
-                          half_pair(f[4] * down, f[5] * down), half_pair(f[6] * down, f[7] * down));
-            }
-          }
+        for (int u = 0; u < DH / 8; ++u) {
+          float f[8];
+          unpack16(raw[u], f);
+          st_shared16(row + (u >> 3) * TILE + (((u & 7) ^ (r & 7)) << 4), half_pair(f[0] * down, f[1] * down),
+                      half_pair(f[2] * down, f[3] * down), half_pair(f[4] * down, f[5] * down),
+                      half_pair(f[6] * down, f[7] * down));
         }
         fence_proxy_async();
         mbar_arrive(bar(TB_QF));
@@ -465,6 +463,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
         const int i = nt == 2 ? jj : 2 * jj + slot;
         if (!kt_warp_wait(bar(TB_SF + slot), js & 1)) { timed_out = true; break; }
         tc_fence_after();
+        if (nt == 1 && slot == 0 && jj == 0) rs = s_rs[qn & 1][r];
         if (live) {
           const int t0 = (k.j + i) * KT_KEYS;
 #pragma unroll 1
@@ -540,6 +539,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
         ++js;
       }
       if (timed_out) break;
+      ++qn;
       // ---- the block's partial
       const long pair = (long)k.b * per + k.q, part = pair + blockIdx.x;
       const long prow = part * w.rb + tile * KT_ROWS + r;
