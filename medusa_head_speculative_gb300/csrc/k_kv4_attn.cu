@@ -35,6 +35,8 @@ namespace medusa {
 constexpr int KD_WARPS = 4, KD_ROWS = 16, KD_STAGES = 2;
 template <int NR> constexpr int KD_CTAS = NR == 1 ? 4 : 3;     // resident CTAs per SM (registers, shared memory)
 constexpr int KD_CTAS_MOST = 4;
+constexpr int KD_CLUSTER = 8;         // CTAs of a cluster that share one triple (small calls)
+constexpr int KD_SMALL_CTAS = 3, KD_SMALL_SLOTS = 8192;   // see kd_small()
 constexpr int KD_KEYS = 2 * KV4_SLOTS;              // slots a warp takes at a time: two blocks
 static_assert(KD_CHUNK == KD_WARPS * KD_KEYS, "a chunk is the warps' slots");
 
@@ -81,13 +83,153 @@ __device__ __forceinline__ void kd_load_q(const Kv4Work& w, int b, int g, int rb
     }
   }
 }
+// Thread-block cluster: all of its threads meet; 1, 2 or 4 floats of CTA `rank`'s shared memory.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+template <int N> __device__ __forceinline__ void peer_load(uint32_t addr, uint32_t rank, float (&v)[N]) {
+  asm("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(addr) : "r"(rank));
+  if constexpr (N == 4)
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(addr) : "memory");
+  else if constexpr (N == 2)
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "r"(addr) : "memory");
+  else
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[0]) : "r"(addr) : "memory");
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 
-template <typename T, int DH, int NR, bool SPLIT>
+// 4, 2 or 1 elements of a lane as loaded: bf16 pairs stay packed until they are used.
+template <typename T, int N> struct LaneRow {
+  uint32_t u[(N * sizeof(T) + 3) / 4];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (N * sizeof(T) == 16) *reinterpret_cast<uint4*>(u) = *reinterpret_cast<const uint4*>(p);
+    else if constexpr (N * sizeof(T) == 8) *reinterpret_cast<uint2*>(u) = *reinterpret_cast<const uint2*>(p);
+    else if constexpr (N * sizeof(T) == 4) u[0] = *reinterpret_cast<const uint32_t*>(p);
+    else u[0] = *reinterpret_cast<const uint16_t*>(p);
+  }
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(u[i]);
+    else return __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+  }
+};
+
+// N = 1, 2 or 4 consecutive elements of a lane.
+template <int N> __device__ __forceinline__ void store_f(float* p, const float (&f)[N]) {
+  if constexpr (N == 4) *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  else if constexpr (N == 2) *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
+  else p[0] = f[0];
+}
+template <int N> __device__ __forceinline__ void store_f(bf16* p, const float (&f)[N]) {
+  if constexpr (N == 4) *reinterpret_cast<uint2*>(p) = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
+  else if constexpr (N == 2) *reinterpret_cast<uint32_t*>(p) = pack2(f[0], f[1]);
+  else p[0] = from_f32<bf16>(f[0]);
+}
+
+// One warp finishes a query row: the prefix's (o, reference, sum) from join(m, l, o), the call's own
+// rows the row sees added in float, and the quotient rounded once.  A tree row sees its
+// ancestors only (at most 9), so going through the set bits beats a masked product with all n1.
+// The first four visible rows' keys and values are loaded before join, which waits for loads too.
+template <typename T, int DH, typename Join>
+__device__ __forceinline__ void finish_row(const Kv4Work& w, int b, int node, int hq, Join join) {
+  constexpr int C = DH / 32;
+  const Kv4AttnArgs& a = w.a;
+  const CacheView& c = a.c;
+  const int lane = threadIdx.x & 31, bn = b * a.n1 + node;
+  const int g = hq / a.G;
+  // lane i < 8: word i of the row's visible bits
+  uint32_t mine = 0;
+  if (a.tk && lane < (a.n1 + 31) / 32) {
+    const int first = 32 * lane;
+    mine = a.mask ? a.mask[(long)node * 8 + lane]
+                  : (node >= first + 31 ? 0xffffffffu : node < first ? 0u : (2u << (node - first)) - 1u);
+    if (a.n1 < first + 32) mine &= (1u << (a.n1 - first)) - 1u;
+  }
+  LaneRow<T, C> q;
+  if (a.tk) q.load(static_cast<const T*>(a.q) + (long)bn * a.q_row + hq * a.q_head + lane * C);
+  int wd = 0;
+  uint32_t bits = __shfl_sync(0xffffffffu, mine, 0);
+  auto next_row = [&]() {                  // the next visible row, -1: none
+    while (!bits && ++wd < 8) bits = __shfl_sync(0xffffffffu, mine, wd);
+    if (!bits) return -1;
+    const int j = 32 * wd + __ffs(bits) - 1;
+    bits &= bits - 1;
+    return j;
+  };
+  const long tree0 = ((long)b * a.n1 * c.Hkv + g) * DH + lane * C;
+  const int tree_row = c.Hkv * DH;
+  LaneRow<T, C> tk[4], tv[4];
+  int seen = 0;                            // of the four, how many there are
+  auto load_rows = [&]() {
+    seen = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = next_row();
+      if (j < 0) continue;
+      const long off = tree0 + (long)j * tree_row;
+      tk[u].load(static_cast<const T*>(a.tk) + off);
+      tv[u].load(static_cast<const T*>(a.tv) + off);
+      seen = u + 1;
+    }
+  };
+  if (a.tk) load_rows();
+  float m = -INFINITY, l = 0.f, o[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) o[i] = 0.f;
+  join(m, l, o);
+#pragma unroll
+  for (int i = 0; i < C; ++i) o[i] *= c.gv;
+  if (a.tk) {
+    const float scale = a.scale * 1.4426950408889634f;
+#pragma unroll 1
+    while (seen > 0) {
+      float sc[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        sc[u] = 0.f;
+        if (u < seen) {
+#pragma unroll
+          for (int i = 0; i < C; ++i) sc[u] = fmaf(q[i], tk[u][i], sc[u]);
+        }
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sc[u] += __shfl_xor_sync(0xffffffffu, sc[u], d);
+      float mn = m;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        sc[u] = u < seen ? sc[u] * scale : -INFINITY;
+        mn = fmaxf(mn, sc[u]);
+      }
+      const float f = ex2_approx(m - mn);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < C; ++i) o[i] *= f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (u >= seen) continue;
+        const float p = ex2_approx(sc[u] - mn);
+        l += p;
+#pragma unroll
+        for (int i = 0; i < C; ++i) o[i] = fmaf(p, tv[u][i], o[i]);
+      }
+      load_rows();
+    }
+  }
+  T* y = static_cast<T*>(a.o) + (long)bn * a.o_row + hq * a.o_head + lane * C;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int i = 0; i < C; ++i) o[i] = l > 0.f ? o[i] * inv : 0.f;
+  store_f<C>(y, o);
+}
+
+template <typename T, int DH, int NR, bool SPLIT, bool CLUSTER>
 __global__ void __launch_bounds__(KD_WARPS * 32, KD_CTAS<NR>) kv4_rows_kernel(const __grid_constant__ Kv4Work w) {
   constexpr int BLK = kv4_block(DH), STEPS = DH / 16, MT = DH / 16;   // MT: 16-element tiles of O^T
   constexpr int QW = STEPS * NR * 64 * (SPLIT ? 2 : 1);
@@ -96,18 +238,33 @@ __global__ void __launch_bounds__(KD_WARPS * 32, KD_CTAS<NR>) kv4_rows_kernel(co
   __shared__ __align__(16) uint32_t qf[QW];
   __shared__ float rs[8 * NR];
   __shared__ float2 ml[KD_WARPS][8 * NR];
+  __shared__ float2 whole[CLUSTER ? 8 * NR : 1];       // the CTA's (reference, sum)
   const CacheView& c = w.a.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
   const int per = c.Hkv * w.nrb;
   uint8_t* ring = smem + warp * KD_STAGES * 4 * BLK;
   float* merge = reinterpret_cast<float*>(smem + KD_WARPS * KD_STAGES * 4 * BLK);   // [2 warps][rb][DH + 4]
   constexpr int ML = DH + 4;
-  const long W = kd_total(c, per);
-  // every CTA that takes part has at least one chunk, so a triple's slots have no gaps
-  const long ctas = W < (long)gridDim.x ? W : (long)gridDim.x;
-  pdl_trigger();
-  if (blockIdx.x >= ctas) return;
-  const long w0 = W * blockIdx.x / ctas, w1 = W * (blockIdx.x + 1) / ctas;
+  long w0, w1;
+  KdCursor k;
+  if constexpr (CLUSTER) {
+    // block (triple, rank): the ranks of a cluster share one triple's chunks
+    k.b = blockIdx.x / per;
+    k.q = blockIdx.x - k.b * per;
+    k.nb = kd_chunks(c, k.b);
+    w0 = k.nb * blockIdx.y / KD_CLUSTER;
+    w1 = k.nb * (blockIdx.y + 1) / KD_CLUSTER;
+    k.j = (int)w0;
+  } else {
+    const long W = kd_total(c, per);
+    // every CTA that takes part has at least one chunk, so a triple's slots have no gaps
+    const long ctas = W < (long)gridDim.x ? W : (long)gridDim.x;
+    pdl_trigger();
+    if (blockIdx.x >= ctas) return;
+    w0 = W * blockIdx.x / ctas;
+    w1 = W * (blockIdx.x + 1) / ctas;
+    k = kd_seek(c, per, w0);
+  }
   if (lane == 0)
     for (int s = 0; s < KD_STAGES; ++s) mbar_init(smem_u32(&bars[warp][s]), 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -116,7 +273,7 @@ __global__ void __launch_bounds__(KD_WARPS * 32, KD_CTAS<NR>) kv4_rows_kernel(co
 
   // ---- this warp's blocks, in order: the copies run up to KD_STAGES ahead.  Lane 2 i + x knows
   // where block x of the warp's chunk win0 + i lies (head 0's) and issues its copies.
-  KdCursor pc = kd_seek(c, per, w0), k = pc;
+  KdCursor pc = k;
   int left = (int)(w1 - w0);               // chunks to copy
   int issued = 0, taken = 0, drain = 0;
   int win_b = -1, win0 = 0, plen = 0, head = pc.q / w.nrb;
@@ -165,6 +322,9 @@ __global__ void __launch_bounds__(KD_WARPS * 32, KD_CTAS<NR>) kv4_rows_kernel(co
   };
   for (int s = 0; s < KD_STAGES; ++s) copy_next();
 
+  if constexpr (CLUSTER) {
+    if (w0 == w1 && tid < w.rb) whole[tid] = make_float2(-INFINITY, -1.f);   // no chunks, no sums
+  }
   long wi = w0;
   while (wi < w1) {
     // ---- one (sequence, head, row block)
@@ -392,6 +552,14 @@ __global__ void __launch_bounds__(KD_WARPS * 32, KD_CTAS<NR>) kv4_rows_kernel(co
       }
       __syncthreads();
     }
+    if constexpr (CLUSTER) {                 // to this CTA's own shared memory: the cluster joins it
+      for (int e = tid; e < w.rb * DH; e += KD_WARPS * 32) {
+        const int r = e / DH, col = e - r * DH;
+        merge[r * ML + col] += merge[(w.rb + r) * ML + col];
+        if (col == 0) whole[r] = joined(r);
+      }
+      break;
+    }
     const long pair = (long)b * per + q, slot = pair + blockIdx.x;
     for (int e = tid; e < w.rb * (DH / 4); e += KD_WARPS * 32) {
       const int r = e / (DH / 4), col = (e - r * (DH / 4)) * 4;
@@ -415,41 +583,39 @@ __global__ void __launch_bounds__(KD_WARPS * 32, KD_CTAS<NR>) kv4_rows_kernel(co
     for (; drain < issued; ++drain)          // copies in flight (bounded)
       mbar_wait(smem_u32(&bars[warp][drain % KD_STAGES]), (drain / KD_STAGES) & 1, TC_TIMEOUT_NS / 16);
   }
-}
-
-// N = 1, 2 or 4 consecutive elements of a lane.
-template <int N> __device__ __forceinline__ void store_f(float* p, const float (&f)[N]) {
-  if constexpr (N == 4) *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-  else if constexpr (N == 2) *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
-  else p[0] = f[0];
-}
-template <int N> __device__ __forceinline__ void store_f(bf16* p, const float (&f)[N]) {
-  if constexpr (N == 4) *reinterpret_cast<uint2*>(p) = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
-  else if constexpr (N == 2) *reinterpret_cast<uint32_t*>(p) = pack2(f[0], f[1]);
-  else p[0] = from_f32<bf16>(f[0]);
-}
-
-// 4, 2 or 1 elements of a lane as loaded: bf16 pairs stay packed until they are used.
-template <typename T, int N> struct LaneRow {
-  uint32_t u[(N * sizeof(T) + 3) / 4];
-  __device__ __forceinline__ void load(const T* p) {
-    if constexpr (N * sizeof(T) == 16) *reinterpret_cast<uint4*>(u) = *reinterpret_cast<const uint4*>(p);
-    else if constexpr (N * sizeof(T) == 8) *reinterpret_cast<uint2*>(u) = *reinterpret_cast<const uint2*>(p);
-    else if constexpr (N * sizeof(T) == 4) u[0] = *reinterpret_cast<const uint32_t*>(p);
-    else u[0] = *reinterpret_cast<const uint16_t*>(p);
+  if constexpr (CLUSTER) {
+    // every CTA of the cluster comes here: the rows are dealt out over its warps
+    constexpr int C = DH / 32;
+    cluster_sync();
+    const int r = blockIdx.y * KD_WARPS + warp, g = k.q / w.nrb, gr = (k.q - g * w.nrb) * w.rb + r;
+    if (r < w.rb && gr < w.R) {
+      const int node = gr / w.a.G;
+      finish_row<T, DH>(w, k.b, node, g * w.a.G + gr - node * w.a.G, [&](float& m, float& l, float (&o)[C]) {
+        float2 y[KD_CLUSTER];
+        float v[KD_CLUSTER][C];
+#pragma unroll
+        for (int x = 0; x < KD_CLUSTER; ++x) {
+          peer_load(smem_u32(&whole[r]), x, reinterpret_cast<float(&)[2]>(y[x]));
+          peer_load(smem_u32(merge + r * ML + lane * C), x, v[x]);
+          m = fmaxf(m, y[x].x);
+        }
+#pragma unroll
+        for (int x = 0; x < KD_CLUSTER; ++x) {
+          if (y[x].y < 0.f) continue;          // a CTA without chunks: its sums were never written
+          const float f = ex2_approx(y[x].x - m);
+          l += f * y[x].y;
+#pragma unroll
+          for (int i = 0; i < C; ++i) o[i] = fmaf(f, v[x][i], o[i]);
+        }
+      });
+    }
+    cluster_sync();                          // nobody leaves while its shared memory is read
   }
-  __device__ __forceinline__ float operator[](int i) const {
-    if constexpr (sizeof(T) == 4) return __uint_as_float(u[i]);
-    else return __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
-  }
-};
+}
 
-// One warp a query row: joins the prefix's partials (o, reference, sum), adds the call's own rows
-// the row sees in float, and rounds the quotient once.  A tree row sees its ancestors only (at
-// most 9), so going through the set bits beats a masked product with all n1.  The kernel waits
-// for loads and nothing else, so what they depend on comes in two rounds: query, span and mask
-// first; then the first partials and, with them, the first four visible rows' keys and values.
-// SB partials in a round: few slots a row (many rows a head) need few registers, many need them.
+// Joins the partials: one warp a query row.  What its loads depend on comes in two rounds: query,
+// span and mask first, then the first partials and the first visible rows.  SB partials in a
+// round: few slots a row (many rows a head) need few registers, many need them.
 template <typename T, int DH, int SB>
 __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant__ Kv4Work w) {
   constexpr int C = DH / 32;
@@ -463,123 +629,40 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant_
   const int g = hq / a.G, r = node * a.G + hq - g * a.G;
   const int rb = w.nrb == 1 ? 0 : r / w.rb, in = r - rb * w.rb;
   const int len = clamp_len(c, c.len[b]);
-  // lane i < 8: word i of the row's visible bits
-  uint32_t mine = 0;
-  if (a.tk && lane < (a.n1 + 31) / 32) {
-    const int first = 32 * lane;
-    mine = a.mask ? a.mask[(long)node * 8 + lane]
-                  : (node >= first + 31 ? 0xffffffffu : node < first ? 0u : (2u << (node - first)) - 1u);
-    if (a.n1 < first + 32) mine &= (1u << (a.n1 - first)) - 1u;
-  }
-  LaneRow<T, C> q;
-  if (a.tk) q.load(static_cast<const T*>(a.q) + (long)bn * a.q_row + hq * a.q_head + lane * C);
-  int wd = 0;
-  uint32_t bits = __shfl_sync(0xffffffffu, mine, 0);
-  auto next_row = [&]() {                  // the next visible row, -1: none
-    while (!bits && ++wd < 8) bits = __shfl_sync(0xffffffffu, mine, wd);
-    if (!bits) return -1;
-    const int j = 32 * wd + __ffs(bits) - 1;
-    bits &= bits - 1;
-    return j;
-  };
-  const long tree0 = ((long)b * a.n1 * c.Hkv + g) * DH + lane * C;
-  const int tree_row = c.Hkv * DH;
-  LaneRow<T, C> tk[4], tv[4];
-  int seen = 0;                            // of the four, how many there are
-  auto load_rows = [&]() {
-    seen = 0;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int j = next_row();
-      if (j < 0) continue;
-      const long off = tree0 + (long)j * tree_row;
-      tk[u].load(static_cast<const T*>(a.tk) + off);
-      tv[u].load(static_cast<const T*>(a.tv) + off);
-      seen = u + 1;
-    }
-  };
-  if (a.tk) load_rows();
-  pdl_wait();                              // the partials come from the kernel before; the above does not
-  float m = -INFINITY, l = 0.f, o[C];
-#pragma unroll
-  for (int i = 0; i < C; ++i) o[i] = 0.f;
-  if (len > 0) {
-    const int2 sp = w.span[((long)b * c.Hkv + g) * w.nrb + rb];
+  finish_row<T, DH>(w, b, node, hq, [&](float& m, float& l, float (&o)[C]) {
+    pdl_wait();                            // the partials come from the kernel before
+    if (len > 0) {
+      const int2 sp = w.span[((long)b * c.Hkv + g) * w.nrb + rb];
 #pragma unroll 1
-    for (int s0 = sp.x; s0 < sp.y; s0 += SB) {
-      float2 y[SB];
-      LaneRow<float, C> v[SB];
+      for (int s0 = sp.x; s0 < sp.y; s0 += SB) {
+        float2 y[SB];
+        LaneRow<float, C> v[SB];
 #pragma unroll
-      for (int u = 0; u < SB; ++u) {
-        const long at = (long)min(s0 + u, sp.y - 1) * w.rb + in;
-        y[u] = w.part_ml[at];
-        v[u].load(w.part_o + (at * DH + lane * C));
-        if (s0 + u >= sp.y) y[u] = make_float2(-INFINITY, 0.f);
-      }
-      float mn = m;
+        for (int u = 0; u < SB; ++u) {
+          const long at = (long)min(s0 + u, sp.y - 1) * w.rb + in;
+          y[u] = w.part_ml[at];
+          v[u].load(w.part_o + (at * DH + lane * C));
+          if (s0 + u >= sp.y) y[u] = make_float2(-INFINITY, 0.f);
+        }
+        float mn = m;
 #pragma unroll
-      for (int u = 0; u < SB; ++u) mn = fmaxf(mn, y[u].x);
-      if (mn == -INFINITY) continue;
-      const float f = ex2_approx(m - mn);
-      m = mn;
-      l *= f;
+        for (int u = 0; u < SB; ++u) mn = fmaxf(mn, y[u].x);
+        if (mn == -INFINITY) continue;
+        const float f = ex2_approx(m - mn);
+        m = mn;
+        l *= f;
 #pragma unroll
-      for (int i = 0; i < C; ++i) o[i] *= f;
+        for (int i = 0; i < C; ++i) o[i] *= f;
 #pragma unroll
-      for (int u = 0; u < SB; ++u) {
-        const float h = ex2_approx(y[u].x - mn);
-        l += y[u].y * h;
+        for (int u = 0; u < SB; ++u) {
+          const float h = ex2_approx(y[u].x - mn);
+          l += y[u].y * h;
 #pragma unroll
-        for (int i = 0; i < C; ++i) o[i] = fmaf(v[u][i], h, o[i]);
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < C; ++i) o[i] *= c.gv;
-  if (a.tk) {
-    const float scale = a.scale * 1.4426950408889634f;
-#pragma unroll 1
-    while (seen > 0) {
-      float sc[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        sc[u] = 0.f;
-        if (u < seen) {
-#pragma unroll
-          for (int i = 0; i < C; ++i) sc[u] = fmaf(q[i], tk[u][i], sc[u]);
+          for (int i = 0; i < C; ++i) o[i] = fmaf(v[u][i], h, o[i]);
         }
       }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1)
-#pragma unroll
-        for (int u = 0; u < 4; ++u) sc[u] += __shfl_xor_sync(0xffffffffu, sc[u], d);
-      float mn = m;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        sc[u] = u < seen ? sc[u] * scale : -INFINITY;
-        mn = fmaxf(mn, sc[u]);
-      }
-      const float f = ex2_approx(m - mn);
-      m = mn;
-      l *= f;
-#pragma unroll
-      for (int i = 0; i < C; ++i) o[i] *= f;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (u >= seen) continue;
-        const float p = ex2_approx(sc[u] - mn);
-        l += p;
-#pragma unroll
-        for (int i = 0; i < C; ++i) o[i] = fmaf(p, tv[u][i], o[i]);
-      }
-      load_rows();
     }
-  }
-  T* y = static_cast<T*>(a.o) + (long)bn * a.o_row + hq * a.o_head + lane * C;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int i = 0; i < C; ++i) o[i] = l > 0.f ? o[i] * inv : 0.f;
-  store_f<C>(y, o);
+  });
 }
 
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -608,13 +691,29 @@ size_t kv4_workspace(int B, int Hq, int Hkv, int dh, int max_nodes, int num_sms)
   return most;
 }
 
+// Few triples in caches that are not long: a cluster of eight CTAs each, joined through
+// distributed shared memory in the same launch.  All clusters have to be resident together, at
+// three CTAs an SM.  Single tokens, dh 128, one launch against two (us): 32 triples, 64 slots
+// 5.4 against 7.3, 2048 slots 7.3 / 9.8, 8192 slots 14.7 / 16.5; 8 triples, 8192 slots 12.6 / 14.7,
+// but 16384 slots 20.5 / 18.3 (64 CTAs of a possible 608); 56 triples, 64 slots 6.0 / 6.6, 8192 slots
+// 20.8 / 21.6, 16384 slots 37.0 / 34.1; 80 triples, which take two rounds, 9.9 / 6.6.
+static bool kd_small(const Kv4Work& w, int num_sms) {
+  return (long)w.a.c.B * w.a.c.Hkv * w.nrb * KD_CLUSTER <= (long)num_sms * KD_SMALL_CTAS && w.a.c.capacity <= KD_SMALL_SLOTS;
+}
 template <typename T, int DH, int NR, bool SPLIT>
 static cudaError_t rows_go(const Kv4Work& w, int num_sms, cudaStream_t st) {
-  const size_t smem = (size_t)KD_WARPS * KD_STAGES * 4 * kv4_block(DH) + (size_t)2 * w.rb * (DH + 4) * 4;
-  auto kern = kv4_rows_kernel<T, DH, NR, SPLIT>;
-  static unsigned long long done = 0;
-  const size_t most = (size_t)KD_WARPS * KD_STAGES * 4 * kv4_block(DH) + (size_t)2 * 8 * NR * (DH + 4) * 4;
-  cudaError_t e = allow_smem(kern, most, &done);
+  const size_t ring = (size_t)KD_WARPS * KD_STAGES * 4 * kv4_block(DH);
+  const size_t smem = ring + (size_t)2 * w.rb * (DH + 4) * 4, most = ring + (size_t)2 * 8 * NR * (DH + 4) * 4;
+  static unsigned long long done = 0, done_small = 0;
+  if (kd_small(w, num_sms)) {
+    auto kern = kv4_rows_kernel<T, DH, NR, SPLIT, true>;
+    const cudaError_t e = allow_smem(kern, most, &done_small);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(kern, dim3((unsigned)(w.a.c.B * w.a.c.Hkv * w.nrb), KD_CLUSTER), dim3(KD_WARPS * 32), smem, st,
+                         KD_CLUSTER, w);
+  }
+  auto kern = kv4_rows_kernel<T, DH, NR, SPLIT, false>;
+  const cudaError_t e = allow_smem(kern, most, &done);
   if (e != cudaSuccess) return e;
   return launch_kernel(kern, dim3(num_sms * KD_CTAS<NR>), dim3(KD_WARPS * 32), smem, st, 1, w);
 }
@@ -649,9 +748,10 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, int dtype, void* ws, int 
   w.part_ml = reinterpret_cast<float2*>(p);
   p += up256(slots * w.rb * 8);
   w.span = reinterpret_cast<int2*>(p);
-  cudaError_t e = kv4_tree_takes(dtype, a.c.dh, w.R) ? launch_kv4_tree(w, num_sms, st)
+  const bool tree = kv4_tree_takes(dtype, a.c.dh, w.R);
+  cudaError_t e = tree ? launch_kv4_tree(w, num_sms, st)
                   : dtype == MEDUSA_F32 ? rows_dh<float, true>(w, num_sms, st) : rows_dh<bf16, false>(w, num_sms, st);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || (!tree && kd_small(w, num_sms))) return e;
   // a head with up to 16 rows is shared out over many CTAs, one with more over a few
   if (w.R <= KD_ROWS) return dtype == MEDUSA_F32 ? combine<float, 8>(w, st) : combine<bf16, 8>(w, st);
   return dtype == MEDUSA_F32 ? combine<float, 2>(w, st) : combine<bf16, 2>(w, st);

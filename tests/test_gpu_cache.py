@@ -557,6 +557,15 @@ def test_attention_long_and_ragged(n1, Hq, Hkv):
     run_attention("f32", Hq, Hkv, 64, n1, (2500, 7), 0, "chain", capacity=4096)
 
 
+@pytest.mark.parametrize("capacity", [8192, 8208])
+@pytest.mark.parametrize("dtype,dh,n1", [("bf16", 128, 1), ("bf16", 64, 9), ("f32", 32, 5), ("f32", 128, 12)])
+def test_attention_few_rows_in_short_and_long_caches(capacity, dtype, dh, n1):
+    """Small calls share a head out over a fixed number of blocks, in long caches over all: with
+    fewer chunks than blocks, one short of and one past a multiple, empty and full ones."""
+    run_attention(dtype, 2, 2, dh, n1, (1025, 0, 1, 1023, 130), 16, "tree", capacity=capacity, strided=True)
+    run_attention(dtype, 3, 1, dh, n1, (0, 8192), 0, None, capacity=capacity)
+
+
 def test_attention_many_sequences():
     lens = [int(x) for x in np.random.default_rng(2).integers(0, 90, 70)]
     run_attention("bf16", 2, 1, 64, 1, lens, 16, "chain")
