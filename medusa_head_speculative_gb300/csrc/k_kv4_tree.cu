@@ -34,7 +34,7 @@
 namespace medusa {
 
 constexpr int KT_ROWS = 128, KT_KEYS = KD_CHUNK, KT_ST = 2, KT_MAXLD = 6;
-constexpr int KT_DECODERS = 8, KT_MMA_WARP = 16, KT_LOAD_WARP = 18;
+constexpr int KT_DECODERS = 4, KT_MMA_WARP = 16, KT_LOAD_WARP = 18;
 constexpr int KT_THREADS = 5 * 128;                 // five warpgroups; of the last one three warps work
 // Registers a thread: 96 at launch (5 x 128 x 96 = 61440), then 152 for softmax, 56 for decode and
 // 64 for the MMA and copy warps: 2 x 152 + 2 x 56 + 64 = 5 x 96.
@@ -56,7 +56,7 @@ void kv4_tree_blocks(int R, int* rb, int* nrb) {
 // slot's (reference, sum) are in shared memory / consumed.  END: every MMA issued has completed.
 enum {
   TB_QF = 0, TB_QE = 1, TB_KF = 2, TB_KE = TB_KF + KT_ST, TB_VF = TB_KE + KT_ST, TB_VE = TB_VF + KT_ST,
-  TB_SF = TB_VE + KT_ST, TB_PR = TB_SF + 2, TB_OF = TB_PR + 2, TB_MRG = TB_OF + 2, TB_MFR = TB_MRG + 1,
+  TB_SF = TB_VE + KT_ST, TB_PR = TB_SF + 4, TB_OF = TB_PR + 4, TB_MRG = TB_OF + 4, TB_MFR = TB_MRG + 1,
   TB_END = TB_MFR + 1, TB_LF = TB_END + 1, TB_LE = TB_LF + KT_MAXLD, TB_COUNT = TB_LE + KT_MAXLD
 };
 
@@ -90,8 +90,7 @@ __device__ __forceinline__ void kt_qk(uint32_t d, uint64_t a, uint64_t b, uint32
 __device__ __forceinline__ void kt_pv(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
   asm volatile("{\n\t.reg .pred e, first, yes;\n\t.reg .b32 x;\n\t.reg .b64 y;\n\t"
                "setp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 first, %4, 0;\n\tsetp.eq.b32 yes, 0, 0;\n\t"
-               KT_PV("0", "0", "first") KT_PV("8", "128", "yes") KT_PV("16", "256", "yes") KT_PV("24", "384", "yes")
-               KT_PV("32", "512", "yes") KT_PV("40", "640", "yes") KT_PV("48", "768", "yes") KT_PV("56", "896", "yes") "}"
+               KT_PV("0", "0", "first") KT_PV("8", "128", "yes") KT_PV("16", "256", "yes") KT_PV("24", "384", "yes") "}"
                ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead) : "memory");
 }
 __device__ __forceinline__ void kt_commit(uint32_t bar, uint32_t lead) {
@@ -135,7 +134,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t bars[TB_COUNT];
   __shared__ uint32_t tmem_slot;
-  __shared__ int s_abort, s_turn;                    // s_turn: an MMA warp is issuing
+  __shared__ int s_abort;
   __shared__ int s_valid[KT_MAXLD];                  // slots of the chunk there are
   __shared__ float2 s_ml[KT_ROWS];                   // second slot's (reference, sum) per row
   __shared__ float s_rs[2][KT_ROWS];                 // one tile: the rows' score factors, two blocks
@@ -170,7 +169,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
       mbar_init(bar(TB_LF + i), 1);
       mbar_init(bar(TB_LE + i), KT_DECODERS);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < 4; ++s) {
       mbar_init(bar(TB_SF + s), 1);
       mbar_init(bar(TB_PR + s), KT_ROWS);
       mbar_init(bar(TB_OF + s), 1);
@@ -178,7 +177,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
     mbar_init(bar(TB_MRG), KT_ROWS);
     mbar_init(bar(TB_MFR), KT_ROWS);
     mbar_init(bar(TB_END), 2);
-    s_abort = s_turn = 0;
+    s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == KT_MMA_WARP) tmem_alloc(smem_u32(&tmem_slot), 2 * KT_SLOT_COLS);
@@ -198,7 +197,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
     // half of a head (16 KB further on: the same banks) written two 16-byte units out of step.
     // A warp has one block (16 slots) of each chunk; all its addresses are fixed but for the stage.
     constexpr int Q = DH / 32, PIECES = Q / 2;        // lanes a slot, pieces (8 slots on) a lane
-    const int quarter = lane % Q, eh = quarter >> 1, dw = warp - 8, key0 = dw * KV4_SLOTS + lane / Q;
+    const int quarter = lane % Q, eh = quarter >> 1, part = (warp - 8) >> 2, dw = 2 * ((warp - 8) & 3), key0 = dw * KV4_SLOTS + lane / Q;
     const uint32_t codes_at = l0s + dw * BLK + lane / Q * (DH / 2) + quarter * 16;
     const uint32_t scales_at = l0s + dw * BLK + 8 * DH + lane / Q * (DH / 16) + quarter * 2;
     uint32_t out_at[4];                               // of words 0..3 in the order they are written
@@ -206,40 +205,35 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
     for (int z = 0; z < 4; ++z)
       out_at[z] = eh * TILE + key0 * 128 + ((((quarter & 1) * 4 + (z ^ (eh << 1))) ^ (key0 & 7)) << 4);
     const uint32_t first = eh ? 8 : 0, swap = eh ? 0x4401u : 0x4410u;   // an upper half's lane: words 2, 3 first
-    int st = 0;
-    uint32_t ph = 0;                                  // staging slot and its phase
     bool dead = false;
     for (int i = 0; i < total && !dead; ++i) {
-#pragma unroll 1
-      for (int part = 0; part < 2; ++part) {
-        if (!kt_warp_wait(bar(TB_LF + st), ph)) { dead = true; break; }
+        const int u = 2 * i + part, st = u % SL;
+        if (!kt_warp_wait(bar(TB_LF + st), (u / SL) & 1)) { dead = true; break; }
         const int valid = s_valid[st];
-        uint32_t cw[PIECES][4], sc[PIECES];
+        constexpr int PP = 2 * PIECES;
+        uint32_t cw[PP][4], sc[PP];
 #pragma unroll
-        for (int y = 0; y < PIECES; ++y) {
-          const uint32_t at = codes_at + st * STAGE + y * 8 * (DH / 2);
+        for (int y = 0; y < PP; ++y) {
+          const int bo = y / PIECES * BLK + y % PIECES * 8 * (DH / 2), so = y / PIECES * BLK + y % PIECES * 8 * (DH / 16);
+          const uint32_t at = codes_at + st * STAGE + bo;
           asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(cw[y][0]), "=r"(cw[y][1]) : "r"(at + first));
           asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(cw[y][2]), "=r"(cw[y][3]) : "r"(at + (first ^ 8)));
           uint16_t two;
-          asm volatile("ld.shared.b16 %0, [%1];" : "=h"(two) : "r"(scales_at + st * STAGE + y * 8 * (DH / 16)));
+          asm volatile("ld.shared.b16 %0, [%1];" : "=h"(two) : "r"(scales_at + st * STAGE + so));
           sc[y] = __byte_perm(two, 0, swap);
         }
         if (valid < KT_KEYS) {                        // past the length: zeros, whatever lies there
 #pragma unroll
-          for (int y = 0; y < PIECES; ++y)
-            if (key0 + 8 * y >= valid) cw[y][0] = cw[y][1] = cw[y][2] = cw[y][3] = sc[y] = 0u;
+          for (int y = 0; y < PP; ++y)
+            if (key0 + (DH == 128 ? 8 * y : 16 * y) >= valid) cw[y][0] = cw[y][1] = cw[y][2] = cw[y][3] = sc[y] = 0u;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(TB_LE + st));
-        if (++st == SL) {
-          st = 0;
-          ph ^= 1;
-        }
-        const int stage = i & 1;
-        if (!kt_warp_wait(bar((part ? TB_VE : TB_KE) + stage), ((i >> 1) & 1) ^ 1)) { dead = true; break; }
+        const int NS = part ? SV : SK, stage = i % NS, turn = i / NS;
+        if (!kt_warp_wait(bar((part ? TB_VE : TB_KE) + stage), (turn & 1) ^ 1)) { dead = true; break; }
         const uint32_t tile = (part ? v0s : k0s) + stage * CHUNK;
 #pragma unroll
-        for (int y = 0; y < PIECES; ++y) {
+        for (int y = 0; y < PP; ++y) {
           const __half2 s2 = kv4_scales((uint16_t)sc[y]);
           const __half2 s0 = __low2half2(s2), s1 = __high2half2(s2);
 #pragma unroll
@@ -247,14 +241,13 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
             const __half2 s = z < 2 ? s0 : s1;
             __half2 h[4];
             kv4_pairs(cw[y][z], h);
-            st_shared16(tile + out_at[z] + y * 1024, h2u(__hmul2(h[0], s)), h2u(__hmul2(h[1], s)), h2u(__hmul2(h[2], s)),
+            st_shared16(tile + out_at[z] + (DH == 128 ? y * 1024 : y * 2048), h2u(__hmul2(h[0], s)), h2u(__hmul2(h[1], s)), h2u(__hmul2(h[2], s)),
                         h2u(__hmul2(h[3], s)));
           }
         }
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar((part ? TB_VF : TB_KF) + stage));
-      }
       if (aborted()) break;
     }
     timed_out = dead;
@@ -266,7 +259,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
       // ---------------------------------------------------------- MMAs of one slot
       const int slot = warp - KT_MMA_WARP;
       const uint32_t lead = lane == 0;
-      const uint32_t id_qk = idesc_f16(KT_ROWS, KT_KEYS);
+      const uint32_t id_qk = idesc_f16(KT_ROWS, KT_KEYS / 2);
       const uint32_t id_pv = idesc_f16(KT_ROWS, DH) | IDESC_B_MN_MAJOR;
       // descriptors hold addresses in 16-byte units: an offset is added to them
       const uint64_t dq = sw128_desc(qs + (nt == 2 ? slot : 0) * CHUNK), dk = sw128_desc(k0s), dv = sw128_desc_mn(v0s, TILE);
@@ -275,28 +268,9 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
       bool dead = false;
       auto wait_k = [&](int x) { return kt_warp_wait(bar(TB_KF + x % SK), (x / SK) & 1); };
       auto wait_v = [&](int x) { return kt_warp_wait(bar(TB_VF + x % SV), (x / SV) & 1); };
-      // Two tiles: one warp at a time issues.  Interleaved, both slots' products would end late
-      // together and both softmaxes start together, with the tensor cores idle meanwhile; one after
-      // the other the slots stay half a turn apart.  (One tile's slots take alternate chunks and
-      // are apart already.)
-      auto take_turn = [&]() -> bool {
-        if (nt == 1) return true;
-        bool ok = true;
-        if (lane == 0 && atomicCAS(&s_turn, 0, 1) != 0) {
-          const uint64_t t0 = gtimer();
-          while (ok && atomicCAS(&s_turn, 0, 1) != 0) ok = gtimer() - t0 < TC_TIMEOUT_NS;
-        }
-        return __all_sync(0xffffffffu, ok);
-      };
-      auto end_turn = [&]() {
-        if (nt == 1) return;
-        if (lane == 0) atomicExch(&s_turn, 0);
-        __syncwarp();
-      };
-      auto scores = [&](int x) {
-        kt_qk<H>(sp, dq, dk + (x % SK) * (CHUNK >> 4), id_qk, lead);
-        kt_commit(bar(TB_SF + slot), lead);
-        kt_commit(bar(TB_KE + x % SK), lead);
+      auto scores = [&](int x, int hf) {
+        kt_qk<H>(sp + 64 * hf, dq, dk + (x % SK) * (CHUNK >> 4) + 512 * hf, id_qk, lead);
+        kt_commit(bar(TB_SF + 2 * slot + hf), lead);
       };
       for (int wi = 0; wi < total && !dead;) {
         const int n = min(k.nb - k.j, total - wi);
@@ -312,39 +286,43 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
             kt_commit(bar(TB_VE + (gc + i) % SV), lead);
           }
         } else if (i0 < n) {
-          if (!wait_k(gc + i0) || !take_turn()) { dead = true; break; }
-          scores(gc + i0);
-          end_turn();
+          if (!wait_k(gc + i0)) { dead = true; break; }
+          scores(gc + i0, 0);
+          scores(gc + i0, 1);
+          kt_commit(bar(TB_KE + (gc + i0) % SK), lead);
           if (i0 + STEP >= n) kt_commit(bar(TB_QE), lead);
 #pragma unroll 1
-          for (int i = i0; i < n; i += STEP) {
-            const int x = gc + i;
+          for (int i = i0; i < n && !dead; i += STEP) {
+            const int x = gc + i, xn = x + STEP;
             if (!wait_v(x)) { dead = true; break; }
             // one tile: slot 1's O may be overwritten only after the first warpgroup has merged it
             // into the previous block's partial
             if (nt == 1 && i == 1 && qn > 0 && !kt_warp_wait(bar(TB_MFR), (qn - 1) & 1)) { dead = true; break; }
-            if (!kt_warp_wait(bar(TB_PR + slot), js & 1)) { dead = true; break; }
-            tc_fence_after();
-            ++js;
-            // the next S in the same turn where its keys are there (waiting for them with the turn
-            // taken could wait for the other slot)
-            const bool more = i + STEP < n;
-            const int xn = x + STEP;
-            const bool now = more && __all_sync(0xffffffffu, mbar_test(bar(TB_KF + xn % SK), (xn / SK) & 1));
-            if (!take_turn()) { dead = true; break; }
-            kt_pv(od, sp, dv + (x % SV) * (CHUNK >> 4), id_pv, i != i0, lead);
-            kt_commit(bar(TB_OF + slot), lead);
-            kt_commit(bar(TB_VE + x % SV), lead);
-            if (now) scores(xn);
-            end_turn();
-            if (more) {
-              if (!now) {
-                if (!wait_k(xn) || !take_turn()) { dead = true; break; }
-                scores(xn);
-                end_turn();
+            // each half of P as it comes, and in its place the next chunk's scores
+            int next = i + STEP < n ? 0 : 2;             // halves of the next chunk's scores issued
+#pragma unroll 1
+            for (int hf = 0; hf < 2; ++hf) {
+              if (!kt_warp_wait(bar(TB_PR + 2 * slot + hf), js & 1)) { dead = true; break; }
+              tc_fence_after();
+              kt_pv(od, sp + 64 * hf, dv + (x % SV) * (CHUNK >> 4) + 512 * hf, id_pv, i != i0 || hf, lead);
+              kt_commit(bar(TB_OF + 2 * slot + hf), lead);
+              if (hf == 1) kt_commit(bar(TB_VE + x % SV), lead);
+              if (next == 0) {
+                // the first half's scores wait for P's second half where their keys are not there yet
+                const bool now = hf == 1 ? wait_k(xn) : __all_sync(0xffffffffu, mbar_test(bar(TB_KF + xn % SK), (xn / SK) & 1));
+                if (hf == 1 && !now) { dead = true; break; }
+                if (now) {
+                  scores(xn, 0);
+                  next = 1;
+                }
               }
-              if (i + 2 * STEP >= n) kt_commit(bar(TB_QE), lead);
+              if (hf == 1 && next == 1) {
+                scores(xn, 1);
+                kt_commit(bar(TB_KE + xn % SK), lead);
+                if (i + 2 * STEP >= n) kt_commit(bar(TB_QE), lead);
+              }
             }
+            ++js;
           }
         }
         if (idle || i0 >= n) kt_commit(bar(TB_QE), lead);
@@ -360,25 +338,35 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
     }
     else if (warp == KT_LOAD_WARP) {
       // ---------------------------------------------------------- copies: lane l < 8 block l
+      // Blocks of one page lie side by side, so a page's (a contiguous cache's: the chunk's) go in
+      // one copy, by the lane of the first.  The next chunk's pages are looked up a chunk ahead.
       const int upp = (c.page_table ? c.page_size : c.capacity) / KV4_SLOTS;
       const uint64_t pol = policy_evict_first();
-      int u = 0, waited = 0, len_b = -1, len = 0;
+      int u = 0, waited = 0, len_b = k.b, len = clamp_len(c, c.len[k.b]);
+      auto page_of = [&]() {
+        const int t = k.j * KT_KEYS + lane * KV4_SLOTS;
+        return c.page_table && lane < 8 && t < len ? c.page_table[(long)k.b * c.pages_per_seq + t / c.page_size] : 0;
+      };
+      int page = page_of();
       for (int x = 0; x < total; ++x) {
-        if (k.b != len_b) {
-          len_b = k.b;
-          len = clamp_len(c, c.len[k.b]);
+        const int j = k.j, t = j * KT_KEYS + lane * KV4_SLOTS, valid = min(len - j * KT_KEYS, KT_KEYS);
+        const int blocks = (valid + KV4_SLOTS - 1) / KV4_SLOTS;
+        const int in = (c.page_table ? t % c.page_size : t) / KV4_SLOTS;
+        const bool lead = lane < blocks && (lane == 0 || in == 0);
+        const uint32_t bytes = lead ? min(upp - in, blocks - lane) * BLK : 0;
+        long unit = c.page_table ? page : k.b;
+        if (lead && c.page_table && (page < 0 || page >= c.num_pages)) {
+          set_flag(c.status, MEDUSA_FLAG_PAGE_RANGE);
+          unit = 0;
         }
-        const int t = k.j * KT_KEYS + lane * KV4_SLOTS, valid = min(len - k.j * KT_KEYS, KT_KEYS);
-        const bool mine = lane < 8 && t < len;
-        long off = 0;
-        if (mine) {
-          long unit;
-          int in;
-          if (!unit_of(c, k.b, t, unit, in)) {
-            set_flag(c.status, MEDUSA_FLAG_PAGE_RANGE);
-            unit = 0;
+        const long off = ((unit * c.Hkv + k.q / w.nrb) * upp + in) * BLK;
+        if (x + 1 < total) {
+          kd_next(c, per, k);
+          if (k.b != len_b) {
+            len_b = k.b;
+            len = clamp_len(c, c.len[k.b]);
           }
-          off = ((unit * c.Hkv + k.q / w.nrb) * upp + in / KV4_SLOTS) * BLK;
+          page = page_of();
         }
         bool ok = true;
         for (int part = 0; part < 2 && ok; ++part, ++u) {
@@ -387,15 +375,14 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
           if (!ok) break;
           if (lane == 0) {
             s_valid[st] = valid;
-            mbar_expect_tx(bar(TB_LF + st), (valid + KV4_SLOTS - 1) / KV4_SLOTS * BLK);
+            mbar_expect_tx(bar(TB_LF + st), blocks * BLK);
           }
           __syncwarp();
-          if (mine)
-            bulk_load(l0s + st * STAGE + lane * BLK, static_cast<const uint8_t*>(part ? c.v : c.k) + off, BLK,
+          if (lead)
+            bulk_load(l0s + st * STAGE + lane * BLK, static_cast<const uint8_t*>(part ? c.v : c.k) + off, bytes,
                       bar(TB_LF + st), pol);
         }
         if (!ok) { timed_out = true; break; }
-        if (x + 1 < total) kd_next(c, per, k);
         if (aborted()) break;
       }
       // copies still under way when the block gives up (bounded): the last SL units at most
@@ -461,13 +448,13 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
       float m_use = -INFINITY, l_acc = 0.f;
       for (int jj = 0; jj < njobs; ++jj) {
         const int i = nt == 2 ? jj : 2 * jj + slot;
-        if (!kt_warp_wait(bar(TB_SF + slot), js & 1)) { timed_out = true; break; }
-        tc_fence_after();
-        if (nt == 1 && slot == 0 && jj == 0) rs = s_rs[qn & 1][r];
-        if (live) {
-          const int t0 = (k.j + i) * KT_KEYS;
+        const int t0 = (k.j + i) * KT_KEYS;
 #pragma unroll 1
-          for (int hf = 0; hf < 2; ++hf) {
+        for (int hf = 0; hf < 2; ++hf) {
+          if (!kt_warp_wait(bar(TB_SF + 2 * slot + hf), js & 1)) { timed_out = true; break; }
+          tc_fence_after();
+          if (nt == 1 && slot == 0 && jj == 0 && hf == 0) rs = s_rs[qn & 1][r];
+          if (live) {
             float s[64];
             tmem_ld64(scol + 64 * hf, s);
             const int valid = len - t0 - 64 * hf;    // keys of this half there are
@@ -487,10 +474,10 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
             if (__any_sync(0xffffffffu, raise)) {
               const float mn = raise ? mx - KD_BACK<false> : m_use;
               const float f = !raise ? 1.f : m_use == -INFINITY ? 0.f : ex2_approx(m_use - mn);
-              // The P V of this slot's previous chunk has completed (this S comes from a later
-              // MMA of the same issuer), so O may be rescaled here; in a block's first chunk
-              // there is no O yet.
-              if (jj > 0) {
+              // O is rescaled once the half before has been added to it; a block's first half finds none
+              if (jj > 0 || hf == 1) {
+                if (!kt_warp_wait(bar(TB_OF + 2 * slot + (hf ^ 1)), (hf ? js : js - 1) & 1)) { timed_out = true; break; }
+                tc_fence_after();
 #pragma unroll 1
                 for (int x = 0; x < DH; x += 16) {
                   float v[16];
@@ -498,21 +485,6 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
 #pragma unroll
                   for (int e = 0; e < 16; ++e) v[e] *= f;
                   tmem_st16(ocol + x, v);
-                }
-              }
-              if (hf == 1) {                         // and the first half's P, already written
-                const __half2 fh = __float2half2_rn(f);
-#pragma unroll 1
-                for (int x = 0; x < 32; x += 16) {
-                  float v[16];
-                  tmem_ld16(scol + x, v);
-#pragma unroll
-                  for (int e = 0; e < 16; ++e) {
-                    uint32_t u = __float_as_uint(v[e]);
-                    u = h2u(__hmul2(*reinterpret_cast<__half2*>(&u), fh));
-                    v[e] = __uint_as_float(u);
-                  }
-                  tmem_st16(scol + x, v);
                 }
               }
               l_acc *= f;
@@ -529,13 +501,14 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
               ls = add2(ls, f2(p0, p1));
               pk[j / 2] = half_pair(p0, p1);
             }
-            kt_st32(scol + 32 * hf, pk);
+            kt_st32(scol + 64 * hf, pk);
             kt_st_wait();
             float l0, l1; unf2(ls, l0, l1); l_acc += l0 + l1;
           }
+          tc_fence_before();
+          mbar_arrive(bar(TB_PR + 2 * slot + hf));
         }
-        tc_fence_before();
-        mbar_arrive(bar(TB_PR + slot));
+        if (timed_out) break;
         ++js;
       }
       if (timed_out) break;
@@ -550,7 +523,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
       }
       if (nt == 2) {
         if (njobs > 0 && live) {
-          if (!kt_warp_wait(bar(TB_OF + slot), (js - 1) & 1)) { timed_out = true; break; }
+          if (!kt_warp_wait(bar(TB_OF + 2 * slot + 1), (js - 1) & 1)) { timed_out = true; break; }
           tc_fence_after();
 #pragma unroll 2
           for (int x = 0; x < DH; x += 16) {
@@ -574,8 +547,8 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
       } else {
         const int nj1 = n / 2;                       // slot 1's chunks in this block
         js1 += nj1;
-        bool ok = kt_warp_wait(bar(TB_OF), (js - 1) & 1);
-        if (ok && nj1 > 0) ok = kt_warp_wait(bar(TB_OF + 1), (js1 - 1) & 1);
+        bool ok = kt_warp_wait(bar(TB_OF + 1), (js - 1) & 1);
+        if (ok && nj1 > 0) ok = kt_warp_wait(bar(TB_OF + 3), (js1 - 1) & 1);
         if (ok) ok = kt_warp_wait(bar(TB_MRG), mc & 1);
         if (!ok) { timed_out = true; break; }
         tc_fence_after();
