@@ -572,6 +572,15 @@ def test_attention_many_sequences():
     run_attention("bf16", 2, 1, 64, 17, lens[:40], 16, "tree")
 
 
+@pytest.mark.parametrize("Hq,Hkv,dh,n1", [(32, 8, 128, 43), (32, 8, 64, 43), (64, 8, 128, 40), (24, 24, 128, 65),
+                                           (32, 8, 64, 20)])
+def test_attention_blocks_that_do_many_heads(Hq, Hkv, dh, n1):
+    """More (sequence, head) pairs than there are blocks on the GPU: each goes from head to head."""
+    lens = [int(x) for x in np.random.default_rng(n1).integers(1, 420, 24)]
+    lens[3] = 0
+    run_attention("bf16", Hq, Hkv, dh, n1, lens, 16, "tree", seed=n1)
+
+
 def test_attention_on_another_stream_and_repeated():
     run_attention("bf16", 8, 2, 128, 20, (300, 100), 16, "tree", stream=torch.cuda.Stream())
     case = Case("kv4", 3, 2, 128, 512, 16, Hq=8, max_nodes=43)
