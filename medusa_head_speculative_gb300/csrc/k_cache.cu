@@ -97,10 +97,10 @@ __device__ __forceinline__ void put(const CacheView& c, const Kv4Divisors& d, vo
     store_n(static_cast<float*>(at), true, f);
   }
 }
-// The block's tables of divisors, for keys and values (256 threads; 4-bit format only).
+// The block's tables of divisors, for keys and values (4-bit format only).
 template <int FMT, int N> __device__ __forceinline__ void fill_divisors(const CacheView& c, float2 (&t)[2][N]) {
   if constexpr (FMT == MEDUSA_KV4) {
-    t[threadIdx.x >> 7][threadIdx.x & 127] = kv4_divisor(threadIdx.x & 127, threadIdx.x >> 7 ? c.gv : c.gk);
+    for (int i = threadIdx.x; i < 256; i += blockDim.x) t[i >> 7][i & 127] = kv4_divisor(i & 127, i >> 7 ? c.gv : c.gk);
     __syncthreads();
   }
 }
@@ -126,15 +126,18 @@ __device__ __forceinline__ void append_lengths(const CacheView& c, const ItemMap
 // How warps share rows x (keys, values): a warp takes `places` rows of one kind and every
 // slices-th 32 tasks of them, tasks being numbered (head, row, piece of a head): four rows of a
 // 4-bit cache fill whole sectors of codes and of scales.
-constexpr int KV_PLACES = 4;
+constexpr int KV_PLACES = 8, KV_SHARE_ELEMS = 8192, KV_APPEND_WARPS = 4;
 struct WarpShare {
   int places, slices;
 };
 // Many rows: several a warp, so that finding them (three dependent loads, one lane a row) is
 // paid once; few rows: a row over several warps.
-static WarpShare warp_share(long rows, int tasks) {
+static WarpShare warp_share(long rows, int row_elems, int tasks) {
   const long wave = 152l * 48;                         // warps that keep the GPU busy
-  if (rows * 2 >= wave * KV_PLACES) return {KV_PLACES, 1};
+  if (rows * 2 >= 2 * wave) {
+    const int places = KV_SHARE_ELEMS / row_elems;
+    return {places < 1 ? 1 : places < KV_PLACES ? places : KV_PLACES, 1};
+  }
   const int most = (tasks + 31) / 32;
   const long want = wave / (rows * 2 > 0 ? rows * 2 : 1);
   return {1, (int)(want < 1 ? 1 : want < most ? want : most)};
@@ -207,16 +210,16 @@ template <typename T, int N> __device__ __forceinline__ void unpack_raw(const Ra
 // 4-bit format, 8 for the others (whole 16 or 32 bytes written by neighbouring lanes).  The next
 // task's elements are under way while one is encoded.
 template <typename T, int FMT>
-__global__ void __launch_bounds__(256, 3) kv_append_vec_kernel(const __grid_constant__ AppendArgs a, const WarpShare ws) {
+__global__ void __launch_bounds__(KV_APPEND_WARPS * 32, 5) kv_append_vec_kernel(const __grid_constant__ AppendArgs a, const WarpShare ws) {
   constexpr int N = FMT == MEDUSA_KV4 ? 16 : 8, ES = FMT == MEDUSA_F32 ? 4 : 2;
   using Raw = Raw16<N * sizeof(T) / 16>;
-  __shared__ PlaceInfo info[8][KV_PLACES];
+  __shared__ PlaceInfo info[KV_APPEND_WARPS][KV_PLACES];
   __shared__ float2 table[2][FMT == MEDUSA_KV4 ? 128 : 1];
   const CacheView& c = a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h2 = a.t.rot / 2;
   fill_divisors<FMT>(c, table);
   append_lengths(c, a.m, (long)blockIdx.x * blockDim.x + threadIdx.x, (long)gridDim.x * blockDim.x);
-  long wid = (long)blockIdx.x * 8 + warp;
+  long wid = (long)blockIdx.x * KV_APPEND_WARPS + warp;
   const int slice = (int)(wid % ws.slices);
   wid /= ws.slices;
   const bool values = wid & 1;
@@ -336,9 +339,9 @@ static cudaError_t append_go(const AppendArgs& a, int format, cudaStream_t st) {
   if (a.vec && (!a.turn || a.t.rot % (a.t.layout == MEDUSA_ROPE_HALF ? 32 : 16) == 0)) {
     auto kern = format == MEDUSA_KV4 ? kv_append_vec_kernel<T, MEDUSA_KV4>
                 : format == MEDUSA_BF16 ? kv_append_vec_kernel<T, MEDUSA_BF16> : kv_append_vec_kernel<T, MEDUSA_F32>;
-    const WarpShare ws = warp_share(a.m.rows, a.c.Hkv * (a.c.dh / (format == MEDUSA_KV4 ? 16 : 8)));
+    const WarpShare ws = warp_share(a.m.rows, a.c.Hkv * a.c.dh, a.c.Hkv * (a.c.dh / (format == MEDUSA_KV4 ? 16 : 8)));
     const long warps = (long)(a.m.rows + ws.places - 1) / ws.places * 2 * ws.slices;
-    return launch_kernel(kern, dim3((unsigned)(warps < 1 ? 1 : (warps + 7) / 8)), dim3(256), 0, st, 1, a, ws);
+    return launch_kernel(kern, dim3((unsigned)(warps < 1 ? 1 : (warps + KV_APPEND_WARPS - 1) / KV_APPEND_WARPS)), dim3(KV_APPEND_WARPS * 32), 0, st, 1, a, ws);
   }
   const long n = (long)a.m.rows * 2 * a.c.Hkv * (a.c.dh / 16);
   const long want = (n + 255) / 256;
@@ -424,7 +427,7 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ Re
 
 template <typename T>
 static cudaError_t read_go(const ReadArgs& a, int format, cudaStream_t st) {
-  const WarpShare ws = warp_share(a.m.rows, a.c.Hkv * a.c.dh * (int)sizeof(T) / 16);
+  const WarpShare ws = warp_share(a.m.rows, a.c.Hkv * a.c.dh, a.c.Hkv * a.c.dh * (int)sizeof(T) / 16);
   const long warps = (long)(a.m.rows + ws.places - 1) / ws.places * 2 * ws.slices;
   auto kern = format == MEDUSA_KV4 ? kv_read_kernel<T, MEDUSA_KV4>
               : format == MEDUSA_BF16 ? kv_read_kernel<T, MEDUSA_BF16> : kv_read_kernel<T, MEDUSA_F32>;

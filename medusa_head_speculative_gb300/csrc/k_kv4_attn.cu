@@ -752,8 +752,7 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, int dtype, void* ws, int 
   cudaError_t e = tree ? launch_kv4_tree(w, num_sms, st)
                   : dtype == MEDUSA_F32 ? rows_dh<float, true>(w, num_sms, st) : rows_dh<bf16, false>(w, num_sms, st);
   if (e != cudaSuccess || (!tree && kd_small(w, num_sms))) return e;
-  // a head with up to 16 rows is shared out over many CTAs, one with more over a few
-  if (w.R <= KD_ROWS) return dtype == MEDUSA_F32 ? combine<float, 8>(w, st) : combine<bf16, 8>(w, st);
+  if (ctas >= 3l * a.c.B * a.c.Hkv * w.nrb) return dtype == MEDUSA_F32 ? combine<float, 8>(w, st) : combine<bf16, 8>(w, st);
   return dtype == MEDUSA_F32 ? combine<float, 2>(w, st) : combine<bf16, 2>(w, st);
 }
 
