@@ -163,21 +163,19 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeA
   }
 }
 
-template <typename T, int HPT>
+template <typename T, int LAYOUT, int HPT>
 static cudaError_t rope_vec(const RopeArgs& a, cudaStream_t st) {
   constexpr int N = Vec<T>::N;
   long most = 0;
   for (int i = 0; i < a.n_parts; ++i) {
     const medusa_rope_rows& p = a.part[i];
-    const int turned = a.t.layout == MEDUSA_ROPE_HALF ? a.t.rot / 2 / N : a.t.rot / N;
+    const int turned = LAYOUT == MEDUSA_ROPE_HALF ? a.t.rot / 2 / N : a.t.rot / N;
     const int units = turned + (p.x == p.y ? 0 : (a.dh - a.t.rot) / N);
     const long n = (long)a.rows * units * ((p.heads + HPT - 1) / HPT);
     most = n > most ? n : most;
   }
   const dim3 grid((unsigned)((most + 255) / 256), (unsigned)a.n_parts);
-  return launch_kernel(a.t.layout == MEDUSA_ROPE_HALF ? rope_vec_kernel<T, MEDUSA_ROPE_HALF, HPT>
-                                                      : rope_vec_kernel<T, MEDUSA_ROPE_INTERLEAVED, HPT>,
-                       grid, dim3(256), 0, st, 1, a);
+  return launch_kernel(rope_vec_kernel<T, LAYOUT, HPT>, grid, dim3(256), 0, st, 1, a);
 }
 
 template <typename T>
@@ -189,8 +187,14 @@ static cudaError_t rope_go(const RopeArgs& a, cudaStream_t st) {
     vec = vec && reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && reinterpret_cast<uintptr_t>(p.y) % 16 == 0 &&
           p.x_row % N == 0 && p.x_head % N == 0 && p.y_row % N == 0 && p.y_head % N == 0;
   }
-  // four heads a thread share the angles' loads; too few rows for that leave the GPU idle
-  if (vec) return (long)a.rows * a.heads * a.dh >= 4l << 20 ? rope_vec<T, 4>(a, st) : rope_vec<T, 1>(a, st);
+  // Heads of a thread share its angles' loads, but too few threads leave the GPU idle.  40 heads of
+  // 128 bf16 elements, 1 / 2 / 4 heads a thread (us): HALF 65 rows 2.0 / 2.3 / 2.9, 512 rows 3.5 / 3.4 /
+  // 3.9, 4096 rows 14.5 / 12.1 / 13.3; INTERLEAVED 65 rows 2.0 /
+  // 2.0 / 2.3, 512 rows 4.1 / 3.4 / 3.3, 4096 rows 21.8 / 14.2 / 11.1.
+  const bool many = (long)a.rows * a.heads * a.dh >= 2l << 20;
+  constexpr int H = MEDUSA_ROPE_HALF, I = MEDUSA_ROPE_INTERLEAVED;
+  if (vec && a.t.layout == H) return many ? rope_vec<T, H, 2>(a, st) : rope_vec<T, H, 1>(a, st);
+  if (vec) return many ? rope_vec<T, I, 4>(a, st) : rope_vec<T, I, 1>(a, st);
   const long n = (long)a.rows * a.heads * (a.dh - a.t.rot / 2);
   const int blocks = (int)((n + 255) / 256 < 1 << 20 ? (n + 255) / 256 : 1 << 20);
   return launch_kernel(rope_kernel<T>, dim3(blocks), dim3(256), 0, st, 1, a);
