@@ -3,26 +3,42 @@
 // Acceleration Framework with Multiple Decoding Heads" §3.4 Tree Attention, Steps 3 and 5, over
 // the format of include/medusa.h).
 //
+// For each row r of a head, with s_j = scale q_r . k_j over the cached slots j:
+// o_r = sum_j 2^(s'_j - m_r) v_j and l_r = sum_j 2^(s'_j - m_r), s' in base-2 units, m_r a running
+// reference at or below the maximum (kv4_attn.cuh), o and l in float; the joining kernel of
+// k_kv4_attn.cu adds the partials and the call's own rows up and divides.
+//
 // The work is dealt out as in k_kv4_attn.cu: one CTA per SM takes an even share of the chunks of
 // 128 cached slots, a (sequence, head, row block) at a time, and writes a partial for each it
 // leaves.  A row block is one 128-row tile, or two when a head has more rows.  In the CTA
 //
-//   warp 18      copies: the eight blocks of a chunk's keys, then of its values, by the copy engine
-//                into a ring of staging slots
-//   warps 8-15   decode: a thread takes 32 elements of one slot (16 bytes of codes, 2 scales) and
-//                writes them as halves (exact) into a 128-byte-swizzled tile: K and V chunks in
-//                rings of two or three stages
+//   warp 18      copies: the blocks of a chunk's keys, then of its values, by the copy engine into a
+//                ring of staging slots, one copy for each page (eight 1152-byte copies cost its
+//                issue half as much again as one)
+//   warps 8-11,  decode keys and values: a thread takes 32 elements of one slot at a time (16 bytes
+//   12-15        of codes, 2 scales) and writes them as halves (exact) into a 128-byte-swizzled tile;
+//                K and V have two tiles each.  Warps of their own, because in one order a value
+//                tile still in use held up the next keys (long 65-node trees 134 -> 121 us)
 //   warps 16, 17 MMAs, a warp for each of two "slots" with S (128 columns) and O (dh columns) in
 //                tensor memory: S = Q K^T, then O += P V with P read from tensor memory (the A
-//                operand) and V from shared memory (MN-major).  Issuing blocks while the tensor
-//                cores are busy, so one warp for both slots left them idle whenever it waited
+//                operand) and V from shared memory (MN-major), in halves of 64 slots: while the
+//                softmax has one half, the other half's P is multiplied with V and the next
+//                chunk's scores take its place (43 x 4 rows: 154 us with whole chunks, 146 so)
 //   warps 0-3,   two softmax warpgroups, one per slot, one query row per thread: they load the
-//   4-7          block's queries (scaled by a power of two into a half's range), read S 64 columns
-//                at a time, exponentiate and write P over S as pairs of halves
+//   4-7          block's queries (scaled by a power of two into a half's range), read a half of S,
+//                exponentiate and write P over it as pairs of halves
 //
 // With two tiles the slots are the tiles and share every chunk; with one both slots work on it
 // and take alternate chunks, and the first warpgroup merges the second's (O, reference, sum)
-// before it writes the partial.  The call's own tree rows are added by the joining kernel.
+// before it writes the partial.
+//
+// Measured: 8 sequences x 40 heads x 65 nodes over 2048-4096 slots each (161 MB, 24 us at copy
+// bandwidth) 99 us; 16 x 8 heads x 172 rows over 8192 slots (165 MB; 92 GFLOP, 73 us of tensor time
+// on whole tiles) 144 us; 8 us of either for joining.  No single part bounds it: a chunk takes
+// 2000 cycles (two tiles: 3900), with copies and signals alone 1250 (2500), and besides these
+// with only the softmax 1500 (2700), the decoding 1650 (2700) or the MMAs 1650 (3300): the parts
+// wait for one another.
+//
 // Every wait is bounded; on expiry MEDUSA_FLAG_TIMEOUT is set, the CTA stops taking work, lets
 // its MMAs end and frees its tensor memory.
 #include <cuda.h>
@@ -41,7 +57,11 @@ constexpr int KT_THREADS = 5 * 128;                 // five warpgroups; of the l
 constexpr int KT_REG_SOFTMAX = 152, KT_REG_DECODE = 56, KT_REG_MMA = 64;
 static_assert(2 * KT_REG_SOFTMAX + 2 * KT_REG_DECODE + KT_REG_MMA == 5 * 96, "what the launch holds");
 constexpr uint32_t KT_SLOT_COLS = 256;               // per slot: S / P [0, 128), O [128, 128 + dh)
-constexpr int KT_MIN_ROWS = 17;                      // rows a head from which this kernel is taken
+// Rows a head from which this kernel is taken; k_kv4_attn.cu, in blocks of 16 rows, against this
+// one (us): 8 x 40 heads of 128, 3100 slots: 17 rows 85 / 78, 32 rows 87 / 82, 64 rows 162 / 88 (16 rows
+// there: 50); 16 x 8 heads of 128, 6000 slots: 24 rows 65 / 57, 64 rows 121 / 61; 4 x 8 heads of 64, 2000
+// slots: 17 rows 14.5 / 14.1, 64 rows 17.2 / 14.9.
+constexpr int KT_MIN_ROWS = 17;
 
 bool kv4_tree_takes(int dtype, int dh, int R) { return dtype == MEDUSA_BF16 && dh >= 64 && R >= KT_MIN_ROWS; }
 void kv4_tree_blocks(int R, int* rb, int* nrb) {
@@ -64,9 +84,8 @@ enum {
 constexpr uint32_t idesc_f16(int M, int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24); }
 // The MMAs of one S = Q K^T (4 a 64-element half) and of one O += P V (8 x 16 keys), kind::f16
 // (the descriptor says which 16-bit type the operands are), and their commits.  The whole warp
-// comes here and lane 0 issues, by predicate and not in a branch: in a divergent branch every
-// operand of every MMA is moved to a uniform register by itself, and issuing 8 MMAs took longer
-// (1000 cycles) than executing them (512).
+// comes here and lane 0 issues, by predicate and not in a branch, so that the operands stay in
+// uniform registers.
 #define KT_QK(OFF, ACC)                                  \
   "add.s64 x, %1, " OFF ";\n\tadd.s64 y, %2, " OFF ";\n\t" \
   "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, " ACC ";\n\t"

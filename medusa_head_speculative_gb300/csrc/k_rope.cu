@@ -5,6 +5,11 @@
 // y1 = x1 c - x2 s, y2 = x2 c + x1 s with every product and sum rounded by itself (no fused
 // multiply-add), so that the result depends on the inputs alone and not on how a kernel
 // groups the operations: medusa_kv_append quantises the same values.
+//
+// Bound by what it moves.  Measured: 16,381 rows of 40 heads of 128 bf16 elements, 64 of them turned
+// (340 MB, 50 us at copy bandwidth) 57 us, 5.9 TB/s; 65 rows of 64 heads 2.1 us (latency).  The kernel for
+// any alignment takes 265 us where the one for 16-byte units takes 61 (16,384 rows, all turned), 2.6 for
+// 2.0 at 65 rows: it is for rows that cannot be read in 16-byte units.
 #include "cache.h"
 #include "common.cuh"
 #include "launch.cuh"
