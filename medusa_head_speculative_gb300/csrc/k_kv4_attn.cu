@@ -229,9 +229,9 @@ __device__ __forceinline__ void finish_row(const Kv4Work& w, int b, int node, in
     }
   }
   T* y = static_cast<T*>(a.o) + (long)bn * a.o_row + hq * a.o_head + lane * C;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;            // nothing seen: 0; a NaN stays one
 #pragma unroll
-  for (int i = 0; i < C; ++i) o[i] = l > 0.f ? o[i] * inv : 0.f;
+  for (int i = 0; i < C; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;
   store_f<C>(y, o);
 }
 
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(KD_WARPS * 32, KD_CTAS<NR>) kv4_rows_kernel(co
 #pragma unroll
         for (int e = 0; e < 2; ++e) {       // the rows' factors are positive
           top[x][e] = fmaxf(fmaxf(s[0][x][e], s[0][x][e + 2]), fmaxf(s[1][x][e], s[1][x][e + 2])) * f[x][e];
-          raise = raise || top[x][e] > m[x][e] + KD_TOP;
+          raise = raise || !(top[x][e] <= m[x][e] + KD_TOP);
         }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -648,12 +648,10 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant_
           const long at = (long)min(s0 + u, sp.y - 1) * w.rb + in;
           y[u] = w.part_ml[at];
           v[u].load(w.part_o + (at * DH + lane * C));
-          if (s0 + u >= sp.y) y[u] = make_float2(-INFINITY, 0.f);
         }
-        float mn = m;
+        float mn = m;                      // stays -inf only where every score was NaN: so is the sum, then
 #pragma unroll
         for (int u = 0; u < SB; ++u) mn = fmaxf(mn, y[u].x);
-        if (mn == -INFINITY) continue;
         const float f = ex2_approx(m - mn);
         m = mn;
         l *= f;
@@ -661,6 +659,7 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant_
         for (int i = 0; i < C; ++i) o[i] *= f;
 #pragma unroll
         for (int u = 0; u < SB; ++u) {
+          if (s0 + u >= sp.y) continue;    // the last partial once more
           const float h = ex2_approx(y[u].x - mn);
           l += y[u].y * h;
 #pragma unroll

@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
               x1 = max3(x1, s[j + 2], s[j + 3]);
             }
             const float mx = fmaxf(x0, x1) * rs;     // the row's factor is positive
-            const bool raise = mx > m_use + KD_TOP;
+            const bool raise = !(mx <= m_use + KD_TOP);
             if (__any_sync(0xffffffffu, raise)) {
               const float mn = raise ? mx - KD_BACK<false> : m_use;
               const float f = !raise ? 1.f : m_use == -INFINITY ? 0.f : ex2_approx(m_use - mn);

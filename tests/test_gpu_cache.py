@@ -572,6 +572,53 @@ def test_attention_many_sequences():
     run_attention("bf16", 2, 1, 64, 17, lens[:40], 16, "tree")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n1,capacity", [(1, 512), (1, 8208), (9, 512), (40, 512), (160, 512)])
+def test_attention_not_a_number(dtype, n1, capacity):
+    """A NaN that a row sees (in its query, a key, a value, a call's own row) makes that row's head
+    NaN and nothing else; one that it does not see changes nothing."""
+    B, H, dh = 6, 2, 64
+    case = Case("kv4", B, H, dh, capacity, 16, max_nodes=n1)
+    lens = [1, 300, 300, 300, 300, 0]
+    case.fill(lens)
+    ws = torch.full((case.cache.workspace_size,), 0xff, dtype=torch.uint8, device="cuda")
+    q = rnd(1, (B, n1, H, dh), dtype).cuda()
+    tk, tv = rnd(2, (B, n1, H, dh), dtype).cuda(), rnd(3, (B, n1, H, dh), dtype).cuda()
+    see = np.eye(n1, dtype=bool)                       # each node sees itself
+    last = see.copy()
+    last[n1 - 1] = False                               # the last one nothing
+
+    def run(see):
+        o = torch.empty_like(q)
+        Bnd.kv4_attention(case.cache, case.kv(i32(lens)), q, o, ws, tree_k=tk, tree_v=tv, mask=mask_of(see),
+                          k_scale=case.gk, v_scale=case.gv)
+        assert case.cache.status() == 0
+        return o
+
+    good, hidden = run(see), run(last)
+    assert torch.isfinite(good.float()).all() and torch.isfinite(hidden.float()).all()
+    assert (hidden[5, n1 - 1] == 0).all()
+    # the scale of the first 16 elements of head 1: slot 0 of sequence 0 (keys), slot 299 of 1 (keys), of 2 (values)
+    for pool, b, t in ((0, 0, 0), (0, 1, 299), (1, 2, 299)):
+        block = (int(case.pages[b, t // 16]) * H + 1) * 9 * dh
+        case.pool[pool][block + 8 * dh + t % 16 * (dh // 16)] = 0x7f
+    q[3, n1 - 1, 0, 5] = float("nan")
+    tk[4, n1 - 1, 1, 7] = float("nan")
+    tv[5, n1 - 1, 0, 7] = float("nan")
+    bad, hidden2 = run(see).float(), run(last).float()
+    want = torch.zeros(B, n1, H, dh, dtype=torch.bool, device="cuda")
+    want[0, :, 1] = want[1, :, 1] = True
+    want[2, :, 1, :16] = True
+    want[3, n1 - 1, 0] = True
+    unseen = want.clone()
+    want[4, n1 - 1, 1] = True
+    want[5, n1 - 1, 0, 7] = True
+    assert torch.equal(bad.isnan(), want)
+    assert torch.equal(bad[~want], good.float()[~want])
+    assert torch.equal(hidden2.isnan(), unseen)
+    assert torch.equal(hidden2[~unseen], hidden.float()[~unseen])
+
+
 @pytest.mark.parametrize("Hq,Hkv,dh,n1", [(32, 8, 128, 43), (32, 8, 64, 43), (64, 8, 128, 40), (24, 24, 128, 65),
                                            (32, 8, 64, 20)])
 def test_attention_blocks_that_do_many_heads(Hq, Hkv, dh, n1):
