@@ -498,8 +498,9 @@ size_t medusa_cache_workspace_size(const medusa_cache* cache);
 medusa_status medusa_cache_get_status(const medusa_cache* cache, void* stream, uint32_t* flags);
 
 /* Rows for the cache.  k, v: element e of head h of row r at [r * row + h * head + e] (strides
- * in elements; heads less than 2^31 bytes apart).  Items are the rows as they are appended; `rows` is how many item places there
- * are, and they belong to the sequences in one of two ways:
+ * in elements; heads less than 2^31 bytes apart), outside the pools.  Items are the rows as they
+ * are appended; `rows` is how many item places there are, and they belong to the sequences in
+ * one of two ways:
  *   packed  start: device [B+1], items start[b] .. start[b+1]-1 are sequence b's; places
  *           before start[0] and from start[B] on belong to none and are skipped
  *   padded  start NULL: rows = B * per_seq, sequence b has the first count[b] (device [B],
@@ -555,14 +556,15 @@ medusa_status medusa_kv_read(const medusa_cache* cache, const medusa_kv* kv,
  * rows j that n sees: bit j of mask row n (medusa_tree_build's mask), or j <= n without a mask.
  *   o = sum_j p_j v_j,  p = softmax(scale q . k_j)
  * One row (n1 = 1) is plain decoding: tree_k, tree_v are that token's keys/values, or NULL when
- * it has been appended already.  A row that sees nothing gives zeros.  Slots from len[b] on
- * may hold anything.
+ * it has been appended already.  A row that sees nothing gives zeros, one that sees a NaN gives
+ * NaN.  Slots from len[b] on and rows that are not seen may hold anything.  Calls that may run at
+ * the same time need workspaces of their own.
  *   q: [B * n1] rows of Hq heads, element strides q_row, q_head; o: as q, strides o_row, o_head
  *   tree_k, tree_v: [B][n1][Hkv][dh]; q, o, tree_k, tree_v all of dtype (MEDUSA_F32 or
  *   MEDUSA_BF16), 16-byte aligned with strides of whole 16 bytes
  * Scores, softmax statistics and sums are 32 bits wide.  With MEDUSA_F32 the products keep
- * 22 bits of queries and probabilities, with MEDUSA_BF16 the queries are exact and the
- * probabilities keep 11 bits. */
+ * 22 bits of queries and probabilities, with MEDUSA_BF16 the queries are exact (elements below
+ * 2^-17 of a row's largest to 2^-25 of it) and the probabilities keep 11 bits. */
 typedef struct {
   const void* q;
   void* o;

@@ -40,9 +40,9 @@ medusa_status done(cudaError_t e) { return e == cudaSuccess ? MEDUSA_OK : MEDUSA
 
 medusa_status read_status(uint32_t* word, void* stream, uint32_t* flags) {
   uint32_t v = 0;
-  if (cudaStreamSynchronize(S(stream)) != cudaSuccess) return MEDUSA_ERR_CUDA;
-  if (cudaMemcpy(&v, word, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return MEDUSA_ERR_CUDA;
-  if (cudaMemset(word, 0, sizeof(v)) != cudaSuccess) return MEDUSA_ERR_CUDA;
+  if (cudaMemcpyAsync(&v, word, sizeof(v), cudaMemcpyDeviceToHost, S(stream)) != cudaSuccess ||
+      cudaMemsetAsync(word, 0, sizeof(v), S(stream)) != cudaSuccess || cudaStreamSynchronize(S(stream)) != cudaSuccess)
+    return MEDUSA_ERR_CUDA;
   *flags = v;
   return v ? MEDUSA_ERR_DEVICE : MEDUSA_OK;
 }
@@ -96,6 +96,11 @@ medusa_status check_cache(const medusa_cache_dims* d) {
   if (d->dh != 32 && d->dh != 64 && d->dh != 128) return MEDUSA_ERR_UNSUPPORTED;
   if (d->Hq > 65535 || d->B > (1 << 22)) return MEDUSA_ERR_UNSUPPORTED;         // launch grids
   if (d->max_nodes > MEDUSA_MAX_NODES || d->capacity > MEDUSA_MAX_CAPACITY) return MEDUSA_ERR_UNSUPPORTED;
+  // far beyond any memory: sizes in bytes stay below 2^63
+  const double slots = d->page_size > 0 ? (double)d->num_pages * d->page_size : (double)d->B * d->capacity;
+  const double most = 1125899906842624.0;                                      // 2^50 elements
+  if (slots * d->Hkv * d->dh > most || (double)d->B * d->Hq * d->max_nodes * d->dh > most)
+    return MEDUSA_ERR_UNSUPPORTED;
   if (d->format == MEDUSA_KV4 && (d->page_size > 0 ? d->page_size : d->capacity) % 16 != 0)
     return MEDUSA_ERR_UNSUPPORTED;
   return MEDUSA_OK;
@@ -253,7 +258,8 @@ medusa_status medusa_cache_create(const medusa_cache_dims* dims, medusa_cache** 
   bool ok = cudaGetDevice(&c->device) == cudaSuccess &&
             cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, c->device) == cudaSuccess &&
             cudaMalloc(&c->status, sizeof(uint32_t)) == cudaSuccess &&
-            cudaMemset(c->status, 0, sizeof(uint32_t)) == cudaSuccess;
+            cudaMemset(c->status, 0, sizeof(uint32_t)) == cudaSuccess &&
+            cudaStreamSynchronize(nullptr) == cudaSuccess;   // before a call on any other stream
   if (!ok) {
     cudaGetLastError();
     medusa_cache_destroy(c);

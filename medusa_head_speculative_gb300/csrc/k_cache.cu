@@ -235,8 +235,8 @@ __global__ void __launch_bounds__(KV_APPEND_WARPS * 32, 5) kv_append_vec_kernel(
   const int slice = (int)(wid % ws.slices);
   wid /= ws.slices;
   const bool values = wid & 1;
+  if ((wid >> 1) * ws.places >= a.m.rows) return;
   const int i0 = (int)(wid >> 1) * ws.places;
-  if (i0 >= a.m.rows) return;
   if (lane < ws.places) {
     const bool lead = !values && slice == 0;
     PlaceInfo p{};
@@ -382,8 +382,8 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ Re
   const int slice = (int)(wid % ws.slices);
   wid /= ws.slices;
   const bool values = wid & 1;
+  if ((wid >> 1) * ws.places >= a.m.rows) return;
   const int i0 = (int)(wid >> 1) * ws.places;
-  if (i0 >= a.m.rows) return;
   if (lane < ws.places) {
     PlaceInfo p{};
     const int2 it = i0 + lane < a.m.rows ? item_of(a.m, c.B, i0 + lane) : make_int2(-1, 0);

@@ -44,6 +44,17 @@ def test_cache_creation_refuses(bad, code):
     assert e.value.code == code
 
 
+@pytest.mark.parametrize("kw", [
+    dict(B=1 << 22, Hq=65535, Hkv=65535, dh=128, format=Bnd.BF16, capacity=1 << 24),
+    dict(B=1, Hq=65535, Hkv=65535, dh=128, format=Bnd.KV4, capacity=1 << 24, page_size=1 << 24, num_pages=(1 << 31) - 1),
+    dict(B=1 << 22, Hq=65535, Hkv=1, dh=128, format=Bnd.KV4, capacity=16, max_nodes=256),
+])
+def test_caches_whose_sizes_pass_64_bits_are_refused(kw):
+    with pytest.raises(Bnd.MedusaError) as e:
+        Bnd.Cache(**kw)
+    assert e.value.code == -2
+
+
 def test_calls_without_a_handle_are_refused():
     L = Bnd.lib()
     kv, rows, places, q = Bnd.KV(), Bnd.KVRows(), Bnd.KVPlaces(), Bnd.KV4Query()
