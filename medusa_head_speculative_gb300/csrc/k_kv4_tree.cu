@@ -12,9 +12,10 @@
 // 128 cached slots, a (sequence, head, row block) at a time, and writes a partial for each it
 // leaves.  A row block is one 128-row tile, or two when a head has more rows.  In the CTA
 //
-//   warp 18      copies: the blocks of a chunk's keys, then of its values, by the copy engine into a
-//                ring of staging slots, one copy for each page (eight 1152-byte copies cost its
-//                issue half as much again as one)
+//   warp 18      copies: the blocks of a chunk's keys, then of its values, by the copy engine into
+//                rings of staging slots, one copy for each page (eight 1152-byte copies cost its
+//                issue half as much again as one; copies issued by the decode warps, a ring each,
+//                were slower: 112 us for 98)
 //   warps 8-11,  decode keys and values: a thread takes 32 elements of one slot at a time (16 bytes
 //   12-15        of codes, 2 scales) and writes them as halves (exact) into a 128-byte-swizzled tile;
 //                K and V have two tiles each.  Warps of their own, because in one order a value
@@ -33,8 +34,8 @@
 // before it writes the partial.
 //
 // Measured: 8 sequences x 40 heads x 65 nodes over 2048-4096 slots each (161 MB, 24 us at copy
-// bandwidth) 99 us; 16 x 8 heads x 172 rows over 8192 slots (165 MB; 92 GFLOP, 73 us of tensor time
-// on whole tiles) 144 us; 8 us of either for joining.  No single part bounds it: a chunk takes
+// bandwidth) 98 us; 16 x 8 heads x 172 rows over 8192 slots (165 MB; 92 GFLOP, 73 us of tensor time
+// on whole tiles) 143 us; 8 us of either for joining.  No single part bounds it: a chunk takes
 // 2000 cycles (two tiles: 3900), with copies and signals alone 1250 (2500), and besides these
 // with only the softmax 1500 (2700), the decoding 1650 (2700) or the MMAs 1650 (3300): the parts
 // wait for one another.
@@ -70,6 +71,10 @@ void kv4_tree_blocks(int R, int* rb, int* nrb) {
   *nrb = (R + most - 1) / most;
 }
 
+// A wait names a phase by its parity, which tells it from its neighbours only: a waiter has to have
+// seen the phase before, or something that implies it.  So keys and values are staged in rings of
+// their own (in one ring of three a slot's next user skipped a phase), and where the slots of one
+// tile share a barrier the order of the waits matters (see the comments there).
 // Barriers.  LF / LE: a staging slot has landed / been read.  QF / QE: query tiles written / no
 // longer read.  KF / KE and VF / VE: K and V stages
 // full / free.  Per slot: SF (S written), PR (P written), OF (P V done).  MRG / MFR: the second
@@ -159,7 +164,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
   __shared__ float s_rs[2][KT_ROWS];                 // one tile: the rows' score factors, two blocks
   const CacheView& c = w.a.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int nt = NT, SK = KT_ST, SV = KT_ST, SL = NT == 2 ? 3 : 6;   // tiles, stages of the K, V and staging rings
+  constexpr int nt = NT, SK = KT_ST, SV = KT_ST, SLK = NT == 2 ? 2 : 3, SLV = NT == 2 ? 1 : 3;   // tiles, stages of the rings: K, V, staged K and V
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t qs = base, k0s = base + nt * CHUNK, v0s = k0s + SK * CHUNK, l0s = v0s + SV * CHUNK;
   constexpr uint32_t STAGE = 8 * BLK;                // the blocks of 128 slots
@@ -224,10 +229,11 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
     for (int z = 0; z < 4; ++z)
       out_at[z] = eh * TILE + key0 * 128 + ((((quarter & 1) * 4 + (z ^ (eh << 1))) ^ (key0 & 7)) << 4);
     const uint32_t first = eh ? 8 : 0, swap = eh ? 0x4401u : 0x4410u;   // an upper half's lane: words 2, 3 first
+    const int slots = part ? SLV : SLK, slot0 = part ? SLK : 0;
     bool dead = false;
     for (int i = 0; i < total && !dead; ++i) {
-        const int u = 2 * i + part, st = u % SL;
-        if (!kt_warp_wait(bar(TB_LF + st), (u / SL) & 1)) { dead = true; break; }
+        const int st = slot0 + i % slots;
+        if (!kt_warp_wait(bar(TB_LF + st), (i / slots) & 1)) { dead = true; break; }
         const int valid = s_valid[st];
         constexpr int PP = 2 * PIECES;
         uint32_t cw[PP][4], sc[PP];
@@ -313,10 +319,11 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
 #pragma unroll 1
           for (int i = i0; i < n && !dead; i += STEP) {
             const int x = gc + i, xn = x + STEP;
-            if (!wait_v(x)) { dead = true; break; }
             // one tile: slot 1's O may be overwritten only after the first warpgroup has merged it
-            // into the previous block's partial
+            // into the previous block's partial (which also means that chunk x - 2's values, perhaps the
+            // other slot's, have been there: without that the wait for this chunk's could end early)
             if (nt == 1 && i == 1 && qn > 0 && !kt_warp_wait(bar(TB_MFR), (qn - 1) & 1)) { dead = true; break; }
+            if (!wait_v(x)) { dead = true; break; }
             // each half of P as it comes, and in its place the next chunk's scores
             int next = i + STEP < n ? 0 : 2;             // halves of the next chunk's scores issued
 #pragma unroll 1
@@ -361,7 +368,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
       // one copy, by the lane of the first.  The next chunk's pages are looked up a chunk ahead.
       const int upp = (c.page_table ? c.page_size : c.capacity) / KV4_SLOTS;
       const uint64_t pol = policy_evict_first();
-      int u = 0, waited = 0, len_b = k.b, len = clamp_len(c, c.len[k.b]);
+      int issued[2] = {0, 0}, len_b = k.b, len = clamp_len(c, c.len[k.b]);
       auto page_of = [&]() {
         const int t = k.j * KT_KEYS + lane * KV4_SLOTS;
         return c.page_table && lane < 8 && t < len ? c.page_table[(long)k.b * c.pages_per_seq + t / c.page_size] : 0;
@@ -388,9 +395,9 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
           page = page_of();
         }
         bool ok = true;
-        for (int part = 0; part < 2 && ok; ++part, ++u) {
-          const int st = u % SL;
-          ok = kt_warp_wait(bar(TB_LE + st), ((u / SL) & 1) ^ 1);
+        for (int part = 0; part < 2 && ok; ++part) {
+          const int slots = part ? SLV : SLK, st = (part ? SLK : 0) + x % slots;
+          ok = kt_warp_wait(bar(TB_LE + st), ((x / slots) & 1) ^ 1);
           if (!ok) break;
           if (lane == 0) {
             s_valid[st] = valid;
@@ -400,13 +407,18 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
           if (lead)
             bulk_load(l0s + st * STAGE + lane * BLK, static_cast<const uint8_t*>(part ? c.v : c.k) + off, bytes,
                       bar(TB_LF + st), pol);
+          ++issued[part];
         }
         if (!ok) { timed_out = true; break; }
         if (aborted()) break;
       }
-      // copies still under way when the block gives up (bounded): the last SL units at most
-      for (waited = max(0, u - SL); (timed_out || aborted()) && waited < u; ++waited)
-        mbar_wait(bar(TB_LF + waited % SL), (waited / SL) & 1, TC_TIMEOUT_NS / 16);
+      // copies still under way when the block gives up (bounded): the last of each ring at most
+      if (timed_out || aborted())
+        for (int part = 0; part < 2; ++part) {
+          const int slots = part ? SLV : SLK;
+          for (int x = max(0, issued[part] - slots); x < issued[part]; ++x)
+            mbar_wait(bar(TB_LF + (part ? SLK : 0) + x % slots), (x / slots) & 1, TC_TIMEOUT_NS / 16);
+        }
     }
   } else {
     // ------------------------------------------------------------ softmax warpgroups
@@ -567,8 +579,9 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
         const int nj1 = n / 2;                       // slot 1's chunks in this block
         js1 += nj1;
         bool ok = kt_warp_wait(bar(TB_OF + 1), (js - 1) & 1);
-        if (ok && nj1 > 0) ok = kt_warp_wait(bar(TB_OF + 3), (js1 - 1) & 1);
+        // the second slot's softmax first: it ends once all of its products but the last are done
         if (ok) ok = kt_warp_wait(bar(TB_MRG), mc & 1);
+        if (ok && nj1 > 0) ok = kt_warp_wait(bar(TB_OF + 3), (js1 - 1) & 1);
         if (!ok) { timed_out = true; break; }
         tc_fence_after();
         const float2 ml1 = s_ml[r];

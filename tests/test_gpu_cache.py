@@ -628,6 +628,32 @@ def test_attention_blocks_that_do_many_heads(Hq, Hkv, dh, n1):
     run_attention("bf16", Hq, Hkv, dh, n1, lens, 16, "tree", seed=n1)
 
 
+@pytest.mark.parametrize("Hq,Hkv,dh,n1,B,most,page", [
+    (32, 8, 64, 43, 24, 420, 16), (32, 8, 128, 43, 24, 420, 16), (64, 8, 64, 40, 24, 420, 16),
+    (24, 24, 64, 65, 24, 420, 0), (40, 40, 128, 65, 8, 4000, 0), (40, 40, 64, 65, 8, 2000, 16),
+    (32, 8, 128, 43, 16, 4000, 16), (40, 40, 128, 8, 8, 1000, 0)])
+def test_attention_repeats_bit_for_bit(Hq, Hkv, dh, n1, B, most, page):
+    """The same call gives the same bits every time: blocks that go from head to head, with odd
+    and even numbers of chunks, wait for what they read."""
+    rng = np.random.default_rng(n1)
+    lens = [int(x) for x in rng.integers(1, most, B)]
+    capacity = (max(lens) + 15) // 16 * 16
+    case = Case("kv4", B, Hkv, dh, capacity, page, Hq=Hq, max_nodes=n1)
+    for pool in case.pool:                             # any codes, scales from 0.5 to 1.875
+        scales = pool.view(-1, 9 * dh)[:, 8 * dh:]
+        scales.copy_(torch.randint(0x30, 0x40, scales.shape, dtype=torch.uint8, device="cuda"))
+    q = rnd(1, (B, n1, Hq, dh), "bf16").cuda()
+    ws = torch.empty(case.cache.workspace_size, dtype=torch.uint8, device="cuda")
+    kv, outs = case.kv(i32(lens)), []
+    for _ in range(60):
+        o = torch.empty_like(q)
+        Bnd.kv4_attention(case.cache, kv, q, o, ws, k_scale=case.gk, v_scale=case.gv)
+        outs.append(o)
+    assert case.cache.status() == 0
+    assert torch.isfinite(outs[0].float()).all()
+    assert all(torch.equal(o, outs[0]) for o in outs[1:])
+
+
 def test_attention_on_another_stream_and_repeated():
     run_attention("bf16", 8, 2, 128, 20, (300, 100), 16, "tree", stream=torch.cuda.Stream())
     case = Case("kv4", 3, 2, 128, 512, 16, Hq=8, max_nodes=43)
