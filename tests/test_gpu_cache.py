@@ -671,6 +671,50 @@ def test_attention_on_another_stream_and_repeated():
     assert torch.equal(outs[3], outs[4]) and torch.equal(outs[3], outs[5])
 
 
+def test_two_streams_and_two_graphs_with_one_handle():
+    """Calls on one cache handle at the same time, each with its own workspace and outputs, eager
+    and as two captured graphs replayed side by side."""
+    case = Case("kv4", 4, 4, 128, 1024, 16, Hq=8, max_nodes=40)
+    lens = [1000, 3, 517, 1024]
+    case.fill(lens)
+    length = i32(lens)
+    kv = case.kv(length)
+    q = [rnd(i, (4, n1, 8, 128), "bf16").cuda() for i, n1 in enumerate((40, 1))]
+    o = [torch.empty_like(x) for x in q]
+    ws = [torch.empty(case.cache.workspace_size, dtype=torch.uint8, device="cuda") for _ in q]
+    start = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    rows = [torch.empty(2, sum(lens), 4, 128, dtype=torch.bfloat16, device="cuda") for _ in q]
+
+    def call(i, stream=None):
+        Bnd.kv4_attention(case.cache, kv, q[i], o[i], ws[i], k_scale=case.gk, v_scale=case.gv, stream=stream)
+        Bnd.kv_read(case.cache, kv, rows[i][0], rows[i][1], start=start, k_scale=case.gk, v_scale=case.gv, stream=stream)
+
+    for i in (0, 1):
+        call(i)
+    torch.cuda.synchronize()
+    want = [x.clone() for x in o + rows]
+    streams = [torch.cuda.Stream() for _ in q]
+    for _ in range(20):
+        for i in (0, 1):
+            call(i, streams[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, o + rows))
+    graphs = [torch.cuda.CUDAGraph() for _ in q]
+    for i in (0, 1):
+        with torch.cuda.graph(graphs[i], stream=streams[i]):
+            call(i)
+    for x in o + rows:
+        x.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, o + rows))
+    assert case.cache.status() == 0
+
+
 def test_attention_bad_lengths_and_pages_are_reported():
     case = Case("kv4", 2, 1, 64, 64, 16, Hq=2, max_nodes=30)
     case.fill([64, 64])
