@@ -458,7 +458,7 @@ typedef struct {
  * is outside the table is passed through unturned and sets MEDUSA_FLAG_POS_RANGE.  rows = 0
  * does nothing.  Any alignment of whole elements works; rows whose pointers and strides are
  * multiples of 16 bytes (and rot/2 of 16 bytes for HALF, rot for INTERLEAVED) move in 16-byte
- * units. */
+ * units, bf16 rows for which 8 bytes are such a multiple in 8-byte units. */
 medusa_status medusa_rope_apply(const medusa_rope* rope, int dtype, int dh, int rows,
                                 const int32_t* pos, const medusa_rope_rows* parts, int n_parts,
                                 int inverse, void* stream);

@@ -7,9 +7,9 @@
 // groups the operations: medusa_kv_append quantises the same values.
 //
 // Bound by what it moves.  Measured: 16,381 rows of 40 heads of 128 bf16 elements, 64 of them turned
-// (340 MB, 50 us at copy bandwidth) 57 us, 5.9 TB/s; 65 rows of 64 heads 2.1 us (latency).  The kernel for
-// any alignment takes 265 us where the one for 16-byte units takes 61 (16,384 rows, all turned), 2.6 for
-// 2.0 at 65 rows: it is for rows that cannot be read in 16-byte units.
+// (340 MB, 50 us at copy bandwidth) 57 us, 5.9 TB/s; 65 rows of 64 heads 2.1 us (latency).  Units of 16
+// bytes where alignment and rot allow, of 8 for the bf16 rows that allow only these (halves of 36
+// elements, 16,384 rows of 40 heads: 94 us), single elements for the rest (394 us there).
 #include "cache.h"
 #include "common.cuh"
 #include "launch.cuh"
@@ -39,27 +39,42 @@ __device__ __forceinline__ void turn(float c, float s, float x1, float x2, float
   y1 = __fsub_rn(__fmul_rn(x1, c), __fmul_rn(x2, s));
   y2 = __fadd_rn(__fmul_rn(x2, c), __fmul_rn(x1, s));
 }
-template <typename T> struct Vec { static constexpr int N = 16 / sizeof(T); };   // elements of 16 bytes
-__device__ __forceinline__ uint4 pack16(const float (&f)[8]) {
-  uint32_t r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    r[i] = *reinterpret_cast<const uint32_t*>(&p);
+// N elements of a row, loaded and stored in one access of 8 or 16 bytes.
+template <typename T, int N> struct RowUnit {
+  static constexpr int WORDS = N * sizeof(T) / 4;
+  uint32_t w[WORDS];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (WORDS == 4) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
+    else *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
   }
-  return make_uint4(r[0], r[1], r[2], r[3]);
-}
-__device__ __forceinline__ uint4 pack16(const float (&f)[4]) {
-  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-}
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (WORDS == 4) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(w);
+    else *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(w);
+  }
+  __device__ __forceinline__ void unpack(float (&f)[N]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      f[i] = __uint_as_float(sizeof(T) == 4 ? w[i] : i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+  }
+  __device__ __forceinline__ void pack(const float (&f)[N]) {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        w[i] = __float_as_uint(f[i]);
+      } else {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&p);
+      }
+    }
+  }
+};
 
-// Rows in 16-byte units (grid y: the part).  A thread takes one unit (HALF: 16 bytes and their
-// partners rot/2 further on; INTERLEAVED: 16 bytes; past rot: 16 bytes to copy) of HPT heads of
-// one row, which share its cosines and sines, all loads before the first use.  Neighbouring
+// Rows in units of N elements, 16 or 8 bytes (grid y: the part).  A thread takes one unit (HALF: N
+// elements and their partners rot/2 further on; INTERLEAVED: N; past rot: N to copy) of HPT heads
+// of one row, which share its cosines and sines, all loads before the first use.  Neighbouring
 // threads take neighbouring units, then neighbouring heads.
-template <typename T, int LAYOUT, int HPT>
+template <typename T, int LAYOUT, int HPT, int N>
 __global__ void __launch_bounds__(256) rope_vec_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr int N = Vec<T>::N;
   const medusa_rope_rows& p = a.part[blockIdx.y];
   const int h = a.t.rot / 2, turned = LAYOUT == MEDUSA_ROPE_HALF ? h / N : a.t.rot / N;
   const bool place = p.x == p.y;
@@ -73,13 +88,13 @@ __global__ void __launch_bounds__(256) rope_vec_kernel(const __grid_constant__ R
   const T* x = static_cast<const T*>(p.x) + r * p.x_row;
   T* y = static_cast<T*>(p.y) + r * p.y_row;
   const int at = u < turned ? u * N : a.t.rot + (u - turned) * N;
-  uint4 v[HPT][2];
+  RowUnit<T, N> v[HPT][2];
 #pragma unroll
   for (int i = 0; i < HPT; ++i) {
     const int hd = hg + i * groups;
     if (hd >= p.heads) break;
-    v[i][0] = *reinterpret_cast<const uint4*>(x + hd * p.x_head + at);
-    if (LAYOUT == MEDUSA_ROPE_HALF && u < turned) v[i][1] = *reinterpret_cast<const uint4*>(x + hd * p.x_head + at + h);
+    v[i][0].load(x + hd * p.x_head + at);
+    if (LAYOUT == MEDUSA_ROPE_HALF && u < turned) v[i][1].load(x + hd * p.x_head + at + h);
   }
   if (u < turned) {
     const int pos = a.pos[r];
@@ -100,9 +115,9 @@ __global__ void __launch_bounds__(256) rope_vec_kernel(const __grid_constant__ R
 #pragma unroll
       for (int i = 0; i < HPT; ++i) {
         float f[N], g[N];
-        unpack16(v[i][0], f);
+        v[i][0].unpack(f);
         if (LAYOUT == MEDUSA_ROPE_HALF) {
-          unpack16(v[i][1], g);
+          v[i][1].unpack(g);
 #pragma unroll
           for (int k = 0; k < N; ++k) {
             float y1, y2;
@@ -110,7 +125,7 @@ __global__ void __launch_bounds__(256) rope_vec_kernel(const __grid_constant__ R
             f[k] = y1;
             g[k] = y2;
           }
-          v[i][1] = pack16(g);
+          v[i][1].pack(g);
         } else {
 #pragma unroll
           for (int k = 0; k < N; k += 2) {
@@ -120,7 +135,7 @@ __global__ void __launch_bounds__(256) rope_vec_kernel(const __grid_constant__ R
             f[k + 1] = y2;
           }
         }
-        v[i][0] = pack16(f);
+        v[i][0].pack(f);
       }
     }
   }
@@ -128,8 +143,8 @@ __global__ void __launch_bounds__(256) rope_vec_kernel(const __grid_constant__ R
   for (int i = 0; i < HPT; ++i) {
     const int hd = hg + i * groups;
     if (hd >= p.heads) break;
-    *reinterpret_cast<uint4*>(y + hd * p.y_head + at) = v[i][0];
-    if (LAYOUT == MEDUSA_ROPE_HALF && u < turned) *reinterpret_cast<uint4*>(y + hd * p.y_head + at + h) = v[i][1];
+    v[i][0].store(y + hd * p.y_head + at);
+    if (LAYOUT == MEDUSA_ROPE_HALF && u < turned) v[i][1].store(y + hd * p.y_head + at + h);
   }
 }
 
@@ -168,9 +183,8 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeA
   }
 }
 
-template <typename T, int LAYOUT, int HPT>
+template <typename T, int LAYOUT, int HPT, int N>
 static cudaError_t rope_vec(const RopeArgs& a, cudaStream_t st) {
-  constexpr int N = Vec<T>::N;
   long most = 0;
   for (int i = 0; i < a.n_parts; ++i) {
     const medusa_rope_rows& p = a.part[i];
@@ -180,26 +194,38 @@ static cudaError_t rope_vec(const RopeArgs& a, cudaStream_t st) {
     most = n > most ? n : most;
   }
   const dim3 grid((unsigned)((most + 255) / 256), (unsigned)a.n_parts);
-  return launch_kernel(rope_vec_kernel<T, LAYOUT, HPT>, grid, dim3(256), 0, st, 1, a);
+  return launch_kernel(rope_vec_kernel<T, LAYOUT, HPT, N>, grid, dim3(256), 0, st, 1, a);
+}
+
+// Whether all rows can be taken in units of n elements.
+template <typename T> static bool units_fit(const RopeArgs& a, int n) {
+  const size_t bytes = n * sizeof(T);
+  bool fit = a.dh % n == 0 && a.t.rot % n == 0 && (a.t.layout != MEDUSA_ROPE_HALF || a.t.rot / 2 % n == 0);
+  for (int i = 0; i < a.n_parts; ++i) {
+    const medusa_rope_rows& p = a.part[i];
+    fit = fit && reinterpret_cast<uintptr_t>(p.x) % bytes == 0 && reinterpret_cast<uintptr_t>(p.y) % bytes == 0 &&
+          p.x_row % n == 0 && p.x_head % n == 0 && p.y_row % n == 0 && p.y_head % n == 0;
+  }
+  return fit;
+}
+// Heads of a thread share its angles' loads, but too few threads leave the GPU idle.  40 heads of
+// 128 bf16 elements, 1 / 2 / 4 heads a thread (us): HALF 65 rows 2.0 / 2.3 / 2.9, 512 rows 3.5 / 3.4 /
+// 3.9, 4096 rows 14.5 / 12.1 / 13.3; INTERLEAVED 65 rows 2.0 / 2.0 / 2.3, 512 rows 4.1 / 3.4 / 3.3, 4096
+// rows 21.8 / 14.2 / 11.1.
+template <typename T, int N> static cudaError_t rope_units(const RopeArgs& a, cudaStream_t st) {
+  const bool many = (long)a.rows * a.heads * a.dh >= 2l << 20;
+  constexpr int H = MEDUSA_ROPE_HALF, I = MEDUSA_ROPE_INTERLEAVED;
+  if (a.t.layout == H) return many ? rope_vec<T, H, 2, N>(a, st) : rope_vec<T, H, 1, N>(a, st);
+  return many ? rope_vec<T, I, 4, N>(a, st) : rope_vec<T, I, 1, N>(a, st);
 }
 
 template <typename T>
 static cudaError_t rope_go(const RopeArgs& a, cudaStream_t st) {
-  constexpr int N = Vec<T>::N;
-  bool vec = a.dh % N == 0 && a.t.rot % N == 0 && (a.t.layout != MEDUSA_ROPE_HALF || a.t.rot / 2 % N == 0);
-  for (int i = 0; i < a.n_parts; ++i) {
-    const medusa_rope_rows& p = a.part[i];
-    vec = vec && reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && reinterpret_cast<uintptr_t>(p.y) % 16 == 0 &&
-          p.x_row % N == 0 && p.x_head % N == 0 && p.y_row % N == 0 && p.y_head % N == 0;
+  constexpr int N = 16 / sizeof(T);
+  if (units_fit<T>(a, N)) return rope_units<T, N>(a, st);
+  if constexpr (N == 8) {                  // partial rotations whose halves are no whole 16 bytes
+    if (units_fit<T>(a, 4)) return rope_units<T, 4>(a, st);
   }
-  // Heads of a thread share its angles' loads, but too few threads leave the GPU idle.  40 heads of
-  // 128 bf16 elements, 1 / 2 / 4 heads a thread (us): HALF 65 rows 2.0 / 2.3 / 2.9, 512 rows 3.5 / 3.4 /
-  // 3.9, 4096 rows 14.5 / 12.1 / 13.3; INTERLEAVED 65 rows 2.0 /
-  // 2.0 / 2.3, 512 rows 4.1 / 3.4 / 3.3, 4096 rows 21.8 / 14.2 / 11.1.
-  const bool many = (long)a.rows * a.heads * a.dh >= 2l << 20;
-  constexpr int H = MEDUSA_ROPE_HALF, I = MEDUSA_ROPE_INTERLEAVED;
-  if (vec && a.t.layout == H) return many ? rope_vec<T, H, 2>(a, st) : rope_vec<T, H, 1>(a, st);
-  if (vec) return many ? rope_vec<T, I, 4>(a, st) : rope_vec<T, I, 1>(a, st);
   const long n = (long)a.rows * a.heads * (a.dh - a.t.rot / 2);
   const int blocks = (int)((n + 255) / 256 < 1 << 20 ? (n + 255) / 256 : 1 << 20);
   return launch_kernel(rope_kernel<T>, dim3(blocks), dim3(256), 0, st, 1, a);

@@ -56,6 +56,9 @@ ROPES = [
     ("f32", 33, 2, "interleaved", (2,), 3, {}),
     ("bf16", 128, 96, "half", (40, 40), 65, {}),
     ("bf16", 256, 256, "half", (2, 1), 17, RAMP),
+    ("bf16", 128, 72, "half", (32, 8), 520, {}),           # halves of 36: 8-byte units, two heads a thread
+    ("bf16", 128, 100, "interleaved", (32, 8), 515, {}),
+    ("bf16", 128, 128, "interleaved", (31, 7), 600, {}),
 ]
 
 
