@@ -35,7 +35,7 @@
 //
 // Measured: 8 sequences x 40 heads x 65 nodes over 2048-4096 slots each (161 MB, 24 us at copy
 // bandwidth) 98 us; 16 x 8 heads x 172 rows over 8192 slots (165 MB; 92 GFLOP, 73 us of tensor time
-// on whole tiles) 143 us; 8 us of either for joining.  No single part bounds it: a chunk takes
+// on whole tiles) 139.5 us; 8 us of either for joining.  No single part bounds it: a chunk takes
 // 2000 cycles (two tiles: 3900), with copies and signals alone 1250 (2500), and besides these
 // with only the softmax 1500 (2700), the decoding 1650 (2700) or the MMAs 1650 (3300): the parts
 // wait for one another.
@@ -431,6 +431,37 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
     KdCursor k = kd_seek(c, per, w0);
     int js = 0, mc = 0, qn = 0;
     int js1 = 0;                                     // slot 1's jobs (merging warpgroup)
+    // 16 columns of the warp's 32 rows to global memory: the four lanes of a quad trade 16-byte
+    // pieces so that each store writes 64 bytes of a row (a row a lane: 16, four times the lines).
+    // dst: the quad's first row; rows: how many there are from it on.  Two tiles: 143 -> 139.5 us (43 x 4
+    // rows); with one, where one warpgroup alone writes and the other goes on, 98 -> 102, so not there.
+    auto store_rows = [&](float* dst, int rows, const float (&v)[16]) {
+      const bool up2 = lane & 2, up1 = lane & 1;
+      float lo[2][4], hi[2][4];
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float a0 = v[4 * y + e], a1 = v[4 * y + 8 + e];
+          const float got = __shfl_xor_sync(0xffffffffu, up2 ? a0 : a1, 2);
+          lo[y][e] = up2 ? got : a0;
+          hi[y][e] = up2 ? a1 : got;
+        }
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        float r0[4], r1[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float a0 = z ? hi[0][e] : lo[0][e], a1 = z ? hi[1][e] : lo[1][e];
+          const float got = __shfl_xor_sync(0xffffffffu, up1 ? a0 : a1, 1);
+          r0[e] = up1 ? got : a0;
+          r1[e] = up1 ? a1 : got;
+        }
+        float* at = dst + 2 * z * DH + (lane & 3) * 4;
+        if (2 * z < rows) *reinterpret_cast<float4*>(at) = make_float4(r0[0], r0[1], r0[2], r0[3]);
+        if (2 * z + 1 < rows) *reinterpret_cast<float4*>(at + DH) = make_float4(r1[0], r1[1], r1[2], r1[3]);
+      }
+    };
     for (int wi = 0; wi < total;) {
       const int n = min(k.nb - k.j, total - wi);
       const int g = k.q / w.nrb, rblk = k.q - g * w.nrb, len = clamp_len(c, c.len[k.b]);
@@ -560,11 +591,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
           for (int x = 0; x < DH; x += 16) {
             float v[16];
             tmem_ld16(ocol + x, v);
-            if (row_ok) {
-#pragma unroll
-              for (int e = 0; e < 16; e += 4)
-                *reinterpret_cast<float4*>(dst + x + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-            }
+            store_rows(dst - (lane & 3) * DH + x, w.R - (gr - (lane & 3)), v);
           }
           if (row_ok) w.part_ml[prow] = make_float2(m_use, l_acc);
         }
