@@ -202,10 +202,15 @@ __device__ __forceinline__ void finish_row(const Kv4Work& w, int b, int node, in
           for (int i = 0; i < C; ++i) sc[u] = fmaf(q[i], tk[u][i], sc[u]);
         }
       }
+      // The four sums over the warp: lanes trade rows until each eight of them have one (10 shuffles for 20)
+      const bool h16 = lane & 16, h8 = lane & 8;
+      const float s0 = (h16 ? sc[2] : sc[0]) + __shfl_xor_sync(0xffffffffu, h16 ? sc[0] : sc[2], 16);
+      const float s1 = (h16 ? sc[3] : sc[1]) + __shfl_xor_sync(0xffffffffu, h16 ? sc[1] : sc[3], 16);
+      float sum = (h8 ? s1 : s0) + __shfl_xor_sync(0xffffffffu, h8 ? s0 : s1, 8);
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1)
+      for (int d = 4; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) sc[u] += __shfl_xor_sync(0xffffffffu, sc[u], d);
+      for (int u = 0; u < 4; ++u) sc[u] = __shfl_sync(0xffffffffu, sum, 8 * u);
       float mn = m;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
