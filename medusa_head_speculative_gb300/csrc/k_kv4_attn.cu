@@ -625,7 +625,10 @@ __global__ void __launch_bounds__(KD_WARPS * 32, KD_CTAS<NR>) kv4_rows_kernel(co
 }
 
 // Joins the partials: one warp a query row.  What its loads depend on comes in two rounds: query,
-// span and mask first, then the first partials and the first visible rows.  SB partials in a
+// span and mask first, then the first partials and the first visible rows.  Bound by its
+// instructions where the call brings rows of its own (two thirds of the issue slots; 20,800 rows, of
+// which each sees up to six: 17 us, without such rows 8), else by latency (2.6 us for 512 rows).  Two or
+// more rows a warp, 16 bytes a lane, took 1 to 2 us off the trees and put 0.2 to 0.4 on small calls.  SB partials in a
 // round: few slots a row (many rows a head) need few registers, many need them.
 template <typename T, int DH, int SB>
 __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant__ Kv4Work w) {
