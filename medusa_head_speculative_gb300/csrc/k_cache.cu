@@ -113,7 +113,7 @@ template <int FMT, int N> __device__ __forceinline__ void fill_divisors(const Ca
 }
 template <int N> __device__ __forceinline__ Kv4Divisors divisors_of(const CacheView& c, const float2 (&t)[2][N], bool values) {
   const float six = 6.f * (values ? c.gv : c.gk);
-  return {t[values ? 1 : 0], six, __frcp_rn(six)};
+  return {t[values ? 1 : 0], six, __frcp_rn(six), __float_as_uint(448.f * six)};
 }
 // Byte offset of slot `in` of a unit, head 0: its first element, or its block's first byte.
 template <int FMT> __device__ __forceinline__ long slot_bytes(const CacheView& c, long unit, int in) {

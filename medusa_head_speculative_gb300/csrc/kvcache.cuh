@@ -162,10 +162,12 @@ __device__ __forceinline__ uint32_t largest_bits(const float (&f)[16]) {
   return __float_as_uint(m);
 }
 // What one number's 16-element groups are divided by: for each e4m3 scale byte, s = e4m3 * g and
-// its correctly rounded reciprocal (0 for 0), in shared memory; and 6 g with its reciprocal.
+// its correctly rounded reciprocal (0 for 0), in shared memory; 6 g with its reciprocal; and the bits of
+// 448 * 6 g, from which on a group has the largest scale (below infinity's: g is at most 1e20).
 struct Kv4Divisors {
   const float2* by_scale;                   // [128] (s, 1/s)
   float six, inv_six;
+  uint32_t beyond;
 };
 __device__ __forceinline__ float2 kv4_divisor(uint32_t byte, float g) {
   const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3))) * g;
@@ -178,22 +180,33 @@ __device__ __forceinline__ float2 kv4_divisor(uint32_t byte, float g) {
 // longer than the group's memory traffic, so the quotients come from a correctly rounded
 // reciprocal r and Markstein's correction (IBM J. Res. Dev. 34, 1990): q = x r, then
 // q + r (x - q s) with the residual exact in one fused multiply-add is the rounded quotient.
-// (g lies in 1e-20..1e20, so residuals neither vanish nor overflow where they matter.)
+// (g lies in 1e-20..1e20, so no residual vanishes where it matters.)  A group whose largest element
+// reaches 448 * 6 g has the largest scale whatever its quotient, which may pass a float's range and
+// leave the correction infinity minus infinity; its elements are first cut to 8 s, which rounds to the
+// largest code.  In any other group s is 0 or |x| < 10 s.
 __device__ __forceinline__ bool kv4_encode(const float (&x)[16], const Kv4Divisors& d, uint2& codes, uint8_t& scale) {
   const uint32_t bits = largest_bits(x);
-  if (bits >= 0x7f800000u) {                // the whole group reads back as NaN
-    codes = make_uint2(0x22222222u, 0x22222222u);
-    scale = 0x7f;
-    return false;
-  }
   const float top = __uint_as_float(bits), q = top * d.inv_six;
   scale = __nv_cvt_float_to_fp8(fmaf(fmaf(-q, d.six, top), d.inv_six, q), __NV_SATFINITE, __NV_E4M3);
-  const float2 sr = d.by_scale[scale];
-  const F2 s = f2(-sr.x, -sr.x), r = f2(sr.y, sr.y);
   float y[16];
 #pragma unroll
+  for (int e = 0; e < 16; ++e) y[e] = x[e];
+  if (bits >= d.beyond) {
+    if (bits >= 0x7f800000u) {              // the whole group reads back as NaN
+      codes = make_uint2(0x22222222u, 0x22222222u);
+      scale = 0x7f;
+      return false;
+    }
+    scale = 0x7e;
+    const float most = 8.f * d.by_scale[scale].x;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) y[e] = fminf(fmaxf(y[e], -most), most);
+  }
+  const float2 sr = d.by_scale[scale];
+  const F2 s = f2(-sr.x, -sr.x), r = f2(sr.y, sr.y);
+#pragma unroll
   for (int e = 0; e < 16; e += 2) {
-    const F2 v = f2(x[e], x[e + 1]), w = mul2(v, r);
+    const F2 v = f2(y[e], y[e + 1]), w = mul2(v, r);
     unf2(fma2(fma2(w, s, v), r, w), y[e], y[e + 1]);
   }
   codes = make_uint2(e2m1x8(y), e2m1x8(y + 8));

@@ -1,0 +1,59 @@
+"""Edges of the cache operators' documented ranges, against the 64-bit forms in kv4_ref.py.
+Tolerances as in test_gpu_cache.py, or exact."""
+import numpy as np
+import pytest
+import torch
+
+import kv4_ref as R
+from harness import ensure_built
+from medusa_head_speculative_gb300 import binding as Bnd
+from test_gpu_cache import DT, U, Case, f64, i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    ensure_built()
+
+
+def off_by_one(x):
+    """The same rows one element off every 16-byte boundary."""
+    n, h, d = x.shape
+    buf = torch.zeros(n * h * (d + 1) + 1, dtype=x.dtype, device=x.device)
+    v = torch.as_strided(buf, (n, h, d), (h * (d + 1), d + 1, 1), 1)
+    return v.copy_(x)
+
+
+# ------------------------------------------------------------------ values past the 4-bit scales
+@pytest.mark.parametrize("src", ["bf16", "f32"])
+@pytest.mark.parametrize("aligned", [True, False])
+@pytest.mark.parametrize("g", [1e-20, 1e-3, 0.05, 1.0, 1e20])
+def test_append_beyond_the_largest_scale(g, aligned, src):
+    """Finite groups whose largest element passes 6 * 448 g, up to a float's end: scale 448, elements
+    beyond it the largest code of their sign, the others (none nearer than 8 % to a border between two codes, bf16
+    rounding moves them by 0.4 %) their nearest code.  Nothing of it is not finite."""
+    g = float(np.float32(g))
+    case = Case("kv4", 1, 1, 64, 16, gk=g, gv=g)
+    codes = [.1, -.4, .6, -.9, 1.1, -1.4, 1.6, -1.9, 2.2, -2.8, 3.2, -3.9, 4.4, -5.5]
+    x = np.zeros((4, 1, 64))
+    for i, big in enumerate((3.3e38, min(2e39 * g, 1e38), 2800 * g, 1e5 * g)):
+        for part, ends in enumerate(((big, -big), (-big, 0.0), (0.0, big), (-big, -big))):
+            x[i, 0, 16 * part:16 * part + 16] = [448 * g * c for c in codes] + list(ends)
+    x = torch.from_numpy(x.astype(np.float32)).to(DT[src]).cuda()
+    k = x if aligned else off_by_one(x)
+    out = i32([0])
+    Bnd.kv_append(case.cache, case.kv(i32([0]), out), k, k, per_seq=4, k_scale=g, v_scale=g)
+    assert case.cache.status() == 0 and out.tolist() == [4]
+    want_codes, want_scales = R.encode(f64(x), g)
+    assert (want_scales == 0x7e).all()
+    for which in (0, 1):
+        raw = case.host(which)
+        for t in range(4):
+            got_codes, got_scales = case.view.slot(raw, 0, t)
+            np.testing.assert_array_equal(got_scales, want_scales[t])
+            np.testing.assert_array_equal(got_codes, want_codes[t])
+    rk, rv = (torch.empty(4, 1, 64, device="cuda") for _ in "kv")
+    Bnd.kv_read(case.cache, case.kv(out), rk, rv, per_seq=4, k_scale=g, v_scale=g)
+    held = R.decode(want_codes, want_scales, g)
+    assert (np.abs(f64(rk) - held) <= 4 * U * np.abs(held)).all() and torch.equal(rk, rv)
