@@ -562,7 +562,8 @@ medusa_status medusa_kv_read(const medusa_cache* cache, const medusa_kv* kv,
  *   q: [B * n1] rows of Hq heads, element strides q_row, q_head; o: as q, strides o_row, o_head
  *   tree_k, tree_v: [B][n1][Hkv][dh]; q, o, tree_k, tree_v all of dtype (MEDUSA_F32 or
  *   MEDUSA_BF16), 16-byte aligned with strides of whole 16 bytes
- * Scores, softmax statistics and sums are 32 bits wide.  With MEDUSA_F32 the products keep
+ * Scores, softmax statistics and sums are 32 bits wide; scores beyond 2^107 in size may give any
+ * result of that row's head.  With MEDUSA_F32 the products keep
  * 22 bits of queries and probabilities, with MEDUSA_BF16 the queries are exact (elements below
  * 2^-17 of a row's largest to 2^-25 of it) and the probabilities keep 11 bits. */
 typedef struct {

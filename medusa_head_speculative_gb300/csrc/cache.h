@@ -69,6 +69,8 @@ struct Kv4AttnArgs {
   const uint32_t* mask;
   int n1, Hq, G;                                  // G = Hq / Hkv query heads per KV head
   float scale;                                    // of the scores, without gk
+  float factor_m;                                 // scale gk log2(e) = factor_m 2^factor_e, factor_m in [1, 2)
+  int factor_e;
 };
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, int dtype, void* ws, int num_sms, cudaStream_t st);
 size_t kv4_workspace(int B, int Hq, int Hkv, int dh, int max_nodes, int num_sms);

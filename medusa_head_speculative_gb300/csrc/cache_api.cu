@@ -368,6 +368,12 @@ medusa_status medusa_kv4_attention(const medusa_cache* c, const medusa_kv* kv, c
   a.Hq = c->d.Hq;
   a.G = c->d.Hq / c->d.Hkv;
   a.scale = q->scale > 0 ? q->scale : 1.0f / std::sqrt((float)c->d.dh);
+  a.factor_m = (float)(2.0 * std::frexp((double)a.scale * q->k_scale * 1.4426950408889634, &a.factor_e));
+  --a.factor_e;
+  if (a.factor_m >= 2.0f) {                       // rounded up
+    a.factor_m = 1.0f;
+    ++a.factor_e;
+  }
   return done(launch_kv4_attention(a, q->dtype, ws, c->num_sms, S(stream)));
 }
 

@@ -72,9 +72,9 @@ __device__ __forceinline__ void kd_load_q(const Kv4Work& w, int b, int g, int rb
     }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float down, up;
-    row_scale(top, down, up);
-    if (li == 0) rs[r] = up * (w.a.scale * w.a.c.gk) * 1.4426950408889634f;
+    float down;
+    const float factor = row_scale(w.a, top, down);
+    if (li == 0) rs[r] = factor;
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
       const int e = li * N + i, t = e / (DH / 4), in = e % (DH / 4), s = in >> 2, hi = (in >> 1) & 1;

@@ -488,9 +488,8 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
 #pragma unroll
           for (int e = 0; e < 8; e += 2) top = max3(top, fabsf(f[e]), fabsf(f[e + 1]));
         }
-        float down, up;
-        row_scale(top, down, up);
-        rs = up * (w.a.scale * c.gk) * 1.4426950408889634f;
+        float down;
+        rs = row_scale(w.a, top, down);
         if (nt == 1) s_rs[qn & 1][r] = rs;
         if (qn > 0 && !kt_warp_wait(bar(TB_QE), (qn - 1) & 1)) { timed_out = true; break; }
         const uint32_t row = qs + tile * CHUNK + r * 128;

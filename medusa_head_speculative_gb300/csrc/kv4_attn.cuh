@@ -30,11 +30,15 @@ template <bool SPLIT> constexpr float KD_BACK = SPLIT ? 13.f : 7.f;
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ uint32_t half_pair(float lo, float hi) { return h2u(__floats2half2_rn(lo, hi)); }
 
-// 2^-e that brings a row whose largest element is top into [1, 2), and 2^e.
-__device__ __forceinline__ void row_scale(float top, float& down, float& up) {
+// down: 2^-e, which brings a row whose largest element is top into [1, 2).  Returned: what its scores,
+// taken with that row and with keys without gk, are multiplied by (base-2 units): 2^e scale gk log2(e).
+// Put together from exponents, as the product of its parts can leave a float's range where it does
+// not, and kept within 2^-126 .. 2^107: not 0 and not infinite for any row, and with |score| < 2^20 (128 x
+// 2 x 448 x 6) neither is a product.  A factor of 0 would turn a masked score's -infinity into NaN.
+__device__ __forceinline__ float row_scale(const Kv4AttnArgs& a, float top, float& down) {
   const int eb = top > 0.f ? min(max((int)(__float_as_uint(top) >> 23), 1), 253) : 127;
   down = __uint_as_float((uint32_t)(254 - eb) << 23);
-  up = __uint_as_float((uint32_t)eb << 23);
+  return __uint_as_float(__float_as_uint(a.factor_m) + ((uint32_t)min(max(eb - 127 + a.factor_e, -126), 107) << 23));
 }
 
 // Contiguous bytes (multiples of 16) to shared memory by the copy engine.

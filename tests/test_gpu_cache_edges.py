@@ -7,7 +7,7 @@ import torch
 import kv4_ref as R
 from harness import ensure_built
 from medusa_head_speculative_gb300 import binding as Bnd
-from test_gpu_cache import DT, U, Case, f64, i32
+from test_gpu_cache import DT, U, Case, attn_bound, f64, i32, mask_of, rnd, see_matrix
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +57,39 @@ def test_append_beyond_the_largest_scale(g, aligned, src):
     Bnd.kv_read(case.cache, case.kv(out), rk, rv, per_seq=4, k_scale=g, v_scale=g)
     held = R.decode(want_codes, want_scales, g)
     assert (np.abs(f64(rk) - held) <= 4 * U * np.abs(held)).all() and torch.equal(rk, rv)
+
+
+# ------------------------------------------------------------------ scores at the ends of a float's range
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n1", [1, 20, 70])
+@pytest.mark.parametrize("kind", [None, "tree"])
+@pytest.mark.parametrize("qgain,scale,g,kvgain", [
+    (1e-30, 1e-10, 1e-20, 1e-18),          # scale, k_scale and the row's largest query multiply to 0 in float
+    (1e-38, 1e27, 1e14, 1e14),             # scale * k_scale alone passes a float's range, the scores do not
+    (1e30, 1e-20, 1e-20, 1e-18),
+])
+def test_attention_factors_outside_a_float(qgain, scale, g, kvgain, kind, n1, dtype):
+    Hq, Hkv, dh, lens, page, capacity = 4, 2, 64, (90, 257, 16), 16, 512
+    g = float(np.float32(g))
+    case = Case("kv4", len(lens), Hkv, dh, capacity, page, Hq=Hq, max_nodes=n1, gk=g, gv=g)
+    case.fill(lens, 1, kvgain)
+    q = rnd(2, (3, n1, Hq, dh), dtype, qgain).cuda()
+    tk = tv = see = mask = None
+    if kind:
+        see = see_matrix(n1, kind)
+        tk, tv = rnd(3, (3, n1, Hkv, dh), dtype, kvgain).cuda(), rnd(4, (3, n1, Hkv, dh), dtype, kvgain).cuda()
+        mask = mask_of(see)
+    ws = torch.full((case.cache.workspace_size,), 0xff, dtype=torch.uint8, device="cuda")
+    o = torch.empty_like(q)
+    Bnd.kv4_attention(case.cache, case.kv(i32(lens)), q, o, ws, tree_k=tk, tree_v=tv, mask=mask, scale=scale, k_scale=g,
+                      v_scale=g)
+    assert case.cache.status() == 0
+    raw = case.host(0), case.host(1)
+    for b, n in enumerate(lens):
+        K, V = (case.view.prefix(raw[i], b, n, g) for i in (0, 1))
+        w, spread, reach = R.attention(f64(q[b]), K, V, None if tk is None else f64(tk[b]),
+                                       None if tv is None else f64(tv[b]), see, float(np.float32(scale)))
+        vmax = max(np.abs(V).max(), 0 if tv is None else np.abs(f64(tv[b])).max())
+        got = f64(o[b])
+        assert np.isfinite(got).all()
+        assert (np.abs(got - w) <= attn_bound(dtype, w, spread, reach, dh, n + n1, vmax)).all()
