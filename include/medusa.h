@@ -496,6 +496,13 @@ size_t medusa_cache_pool_bytes(const medusa_cache* cache);
 size_t medusa_cache_workspace_size(const medusa_cache* cache);
 /* As medusa_get_status, for the cache's own status word. */
 medusa_status medusa_cache_get_status(const medusa_cache* cache, void* stream, uint32_t* flags);
+/* Failure-path testing, as medusa_plan_expire_wait_once: in the next medusa_kv4_attention call on this
+ * cache (a captured one: in every replay) a warp of each block first waits, for at most `ns` nanoseconds,
+ * on a barrier that nothing arrives on, and then takes the path of a copy that never landed:
+ * MEDUSA_FLAG_TIMEOUT is set, the other waits run to their ~1 s limits, and the call returns with a
+ * meaningless o and a usable context.  MEDUSA_ERR_INVALID for ns = 0 or above 10 s,
+ * MEDUSA_ERR_UNSUPPORTED for other formats. */
+medusa_status medusa_cache_expire_wait_once(medusa_cache* cache, unsigned long long ns);
 
 /* Rows for the cache.  k, v: element e of head h of row r at [r * row + h * head + e] (strides
  * in elements; heads less than 2^31 bytes apart), outside the pools.  Items are the rows as they

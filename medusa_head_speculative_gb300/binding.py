@@ -162,6 +162,7 @@ def lib():
         "medusa_cache_pool_bytes": (SZ, [P]),
         "medusa_cache_workspace_size": (SZ, [P]),
         "medusa_cache_get_status": (I, [P, P, C.POINTER(C.c_uint32)]),
+        "medusa_cache_expire_wait_once": (I, [P, C.c_ulonglong]),
         "medusa_kv_append": (I, [P, C.POINTER(KV), C.POINTER(KVRows), P, C.c_float, C.c_float, P]),
         "medusa_kv_read": (I, [P, C.POINTER(KV), C.POINTER(KVPlaces), C.c_float, C.c_float, P]),
         "medusa_kv4_attention": (I, [P, C.POINTER(KV), C.POINTER(KV4Query), P, SZ, P]),
@@ -583,6 +584,10 @@ class Cache:
 
     def status(self, stream=None):
         return _status("medusa_cache_get_status", self.handle, stream)
+
+    def expire_wait_once(self, ns):
+        """Failure-path testing: see medusa_cache_expire_wait_once."""
+        _check("medusa_cache_expire_wait_once", lib().medusa_cache_expire_wait_once(self.handle, int(ns)))
 
     def close(self):
         if getattr(self, "handle", None):

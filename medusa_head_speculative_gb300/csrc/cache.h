@@ -71,6 +71,7 @@ struct Kv4AttnArgs {
   float scale;                                    // of the scores, without gk
   float factor_m;                                 // scale gk log2(e) = factor_m 2^factor_e, factor_m in [1, 2)
   int factor_e;
+  unsigned long long test_wait_ns;                // failure-path tests only (0 otherwise): a wait that runs out
 };
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, int dtype, void* ws, int num_sms, cudaStream_t st);
 size_t kv4_workspace(int B, int Hq, int Hkv, int dh, int max_nodes, int num_sms);

@@ -2,6 +2,7 @@
 // every call keeps to are in include/medusa.h.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <new>
 
@@ -23,6 +24,7 @@ struct medusa_cache {
   uint32_t* status = nullptr;
   int device = 0, num_sms = 152;
   size_t pool_bytes = 0, ws_bytes = 0;
+  mutable std::atomic<unsigned long long> test_wait_ns{0};
 };
 
 namespace {
@@ -286,6 +288,13 @@ medusa_status medusa_cache_get_status(const medusa_cache* c, void* stream, uint3
   return read_status(c->status, stream, flags);
 }
 
+medusa_status medusa_cache_expire_wait_once(medusa_cache* c, unsigned long long ns) {
+  if (!c || ns == 0 || ns > 10000000000ull) return MEDUSA_ERR_INVALID;
+  if (c->d.format != MEDUSA_KV4) return MEDUSA_ERR_UNSUPPORTED;
+  c->test_wait_ns.store(ns);
+  return MEDUSA_OK;
+}
+
 medusa_status medusa_kv_append(const medusa_cache* c, const medusa_kv* kv, const medusa_kv_rows* rows,
                                const medusa_rope* rope, float k_scale, float v_scale, void* stream) {
   EntryScope scope("medusa_kv_append");
@@ -374,6 +383,7 @@ medusa_status medusa_kv4_attention(const medusa_cache* c, const medusa_kv* kv, c
     a.factor_m = 1.0f;
     ++a.factor_e;
   }
+  if (c->test_wait_ns.load(std::memory_order_relaxed)) a.test_wait_ns = c->test_wait_ns.exchange(0);
   return done(launch_kv4_attention(a, q->dtype, ws, c->num_sms, S(stream)));
 }
 

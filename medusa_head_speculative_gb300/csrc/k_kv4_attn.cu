@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(KD_WARPS * 32, KD_CTAS<NR>) kv4_rows_kernel(co
   constexpr int BLK = kv4_block(DH), STEPS = DH / 16, MT = DH / 16;   // MT: 16-element tiles of O^T
   constexpr int QW = STEPS * NR * 64 * (SPLIT ? 2 : 1);
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t bars[KD_WARPS][KD_STAGES];
+  __shared__ uint64_t bars[KD_WARPS][KD_STAGES], never;
   __shared__ __align__(16) uint32_t qf[QW];
   __shared__ float rs[8 * NR];
   __shared__ float2 ml[KD_WARPS][8 * NR];
@@ -335,6 +335,14 @@ __global__ void __launch_bounds__(KD_WARPS * 32, KD_CTAS<NR>) kv4_rows_kernel(co
 
   if constexpr (CLUSTER) {
     if (w0 == w1 && tid < w.rb) whole[tid] = make_float2(-INFINITY, -1.f);   // no chunks, no sums
+  }
+  if constexpr (!CLUSTER) {                // failure-path tests; in the one-launch form it would cost 0.12 us
+    if (w.a.test_wait_ns && warp == 0) {
+      if (lane == 0) mbar_init(smem_u32(&never), 1);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      __syncwarp();
+      dead = !__all_sync(0xffffffffu, mbar_wait(smem_u32(&never), 0, w.a.test_wait_ns));
+    }
   }
   long wi = w0;
   while (wi < w1) {
@@ -711,7 +719,7 @@ size_t kv4_workspace(int B, int Hq, int Hkv, int dh, int max_nodes, int num_sms)
 // but 16384 slots 20.5 / 18.3 (64 CTAs of a possible 608); 56 triples, 64 slots 6.0 / 6.6, 8192 slots
 // 20.8 / 21.6, 16384 slots 37.0 / 34.1; 80 triples, which take two rounds, 9.9 / 6.6.
 static bool kd_small(const Kv4Work& w, int num_sms) {
-  return (long)w.a.c.B * w.a.c.Hkv * w.nrb * KD_CLUSTER <= (long)num_sms * KD_SMALL_CTAS && w.a.c.capacity <= KD_SMALL_SLOTS;
+  return !w.a.test_wait_ns && (long)w.a.c.B * w.a.c.Hkv * w.nrb * KD_CLUSTER <= (long)num_sms * KD_SMALL_CTAS && w.a.c.capacity <= KD_SMALL_SLOTS;
 }
 template <typename T, int DH, int NR, bool SPLIT>
 static cudaError_t rows_go(const Kv4Work& w, int num_sms, cudaStream_t st) {

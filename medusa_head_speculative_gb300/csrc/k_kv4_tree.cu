@@ -12,6 +12,8 @@
 // 128 cached slots, a (sequence, head, row block) at a time, and writes a partial for each it
 // leaves.  A row block is one 128-row tile, or two when a head has more rows.  In the CTA
 //
+//   warp 19      writes down where each triple's partials lie, before and without any wait: the joining
+//                kernel reads by it, also after a wait of this one expired
 //   warp 18      copies: the blocks of a chunk's keys, then of its values, by the copy engine into
 //                rings of staging slots, one copy for each page (eight 1152-byte copies cost its
 //                issue half as much again as one; copies issued by the decode warps, a ring each,
@@ -79,10 +81,11 @@ void kv4_tree_blocks(int R, int* rb, int* nrb) {
 // longer read.  KF / KE and VF / VE: K and V stages
 // full / free.  Per slot: SF (S written), PR (P written), OF (P V done).  MRG / MFR: the second
 // slot's (reference, sum) are in shared memory / consumed.  END: every MMA issued has completed.
+// NEVER: for failure-path tests, nothing arrives there.
 enum {
   TB_QF = 0, TB_QE = 1, TB_KF = 2, TB_KE = TB_KF + KT_ST, TB_VF = TB_KE + KT_ST, TB_VE = TB_VF + KT_ST,
   TB_SF = TB_VE + KT_ST, TB_PR = TB_SF + 4, TB_OF = TB_PR + 4, TB_MRG = TB_OF + 4, TB_MFR = TB_MRG + 1,
-  TB_END = TB_MFR + 1, TB_LF = TB_END + 1, TB_LE = TB_LF + KT_MAXLD, TB_COUNT = TB_LE + KT_MAXLD
+  TB_END = TB_MFR + 1, TB_NEVER = TB_END + 1, TB_LF = TB_NEVER + 1, TB_LE = TB_LF + KT_MAXLD, TB_COUNT = TB_LE + KT_MAXLD
 };
 
 // Instruction descriptor, kind::f16: fp32 D, half A and B, both K-major, M x N.
@@ -201,6 +204,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
     mbar_init(bar(TB_MRG), KT_ROWS);
     mbar_init(bar(TB_MFR), KT_ROWS);
     mbar_init(bar(TB_END), 2);
+    mbar_init(bar(TB_NEVER), 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -412,13 +416,25 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
         if (!ok) { timed_out = true; break; }
         if (aborted()) break;
       }
-      // copies still under way when the block gives up (bounded): the last of each ring at most
-      if (timed_out || aborted())
-        for (int part = 0; part < 2; ++part) {
-          const int slots = part ? SLV : SLK;
-          for (int x = max(0, issued[part] - slots); x < issued[part]; ++x)
-            mbar_wait(bar(TB_LF + (part ? SLK : 0) + x % slots), (x / slots) & 1, TC_TIMEOUT_NS / 16);
+      // the last copies of each ring: if the block gives up nobody else waits for them (bounded)
+      for (int part = 0; part < 2; ++part) {
+        const int slots = part ? SLV : SLK;
+        for (int x = max(0, issued[part] - slots); x < issued[part]; ++x)
+          mbar_wait(bar(TB_LF + (part ? SLK : 0) + x % slots), (x / slots) & 1, TC_TIMEOUT_NS / 16);
+      }
+    } else {
+      // ---------------------------------------------------------- slots of the partials
+      for (int wi = 0; wi < total;) {
+        const int n = min(k.nb - k.j, total - wi);
+        const long pair = (long)k.b * per + k.q;
+        if (lane == 0) {
+          if (k.j == 0) w.span[pair].x = (int)(pair + blockIdx.x);
+          if (k.j + n == k.nb) w.span[pair].y = (int)(pair + blockIdx.x) + 1;
         }
+        wi += n;
+        k.j += n - 1;
+        if (wi < total) kd_next(c, per, k);
+      }
     }
   } else {
     // ------------------------------------------------------------ softmax warpgroups
@@ -462,7 +478,9 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
         if (2 * z + 1 < rows) *reinterpret_cast<float4*>(at + DH) = make_float4(r1[0], r1[1], r1[2], r1[3]);
       }
     };
-    for (int wi = 0; wi < total;) {
+    if (w.a.test_wait_ns && slot == 0)
+      timed_out = !__all_sync(0xffffffffu, mbar_wait(bar(TB_NEVER), 0, w.a.test_wait_ns));
+    for (int wi = timed_out ? total : 0; wi < total;) {
       const int n = min(k.nb - k.j, total - wi);
       const int g = k.q / w.nrb, rblk = k.q - g * w.nrb, len = clamp_len(c, c.len[k.b]);
       const int row0 = rblk * KT_ROWS * nt, tile = nt == 2 ? slot : 0;
@@ -578,10 +596,6 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
       const long pair = (long)k.b * per + k.q, part = pair + blockIdx.x;
       const long prow = part * w.rb + tile * KT_ROWS + r;
       float* dst = w.part_o + prow * DH;
-      if (tid == 0) {
-        if (k.j == 0) w.span[pair].x = (int)part;
-        if (k.j + n == k.nb) w.span[pair].y = (int)part + 1;
-      }
       if (nt == 2) {
         if (njobs > 0 && live) {
           if (!kt_warp_wait(bar(TB_OF + 2 * slot + 1), (js - 1) & 1)) { timed_out = true; break; }

@@ -1,5 +1,7 @@
 """Edges of the cache operators' documented ranges, against the 64-bit forms in kv4_ref.py.
 Tolerances as in test_gpu_cache.py, or exact."""
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -93,3 +95,52 @@ def test_attention_factors_outside_a_float(qgain, scale, g, kvgain, kind, n1, dt
         got = f64(o[b])
         assert np.isfinite(got).all()
         assert (np.abs(got - w) <= attn_bound(dtype, w, spread, reach, dh, n + n1, vmax)).all()
+
+
+# ------------------------------------------------------------------ waits that run out
+@pytest.mark.parametrize("dtype,Hq,Hkv,dh,n1,capacity,page", [
+    ("bf16", 4, 4, 128, 1, 512, 16), ("f32", 4, 2, 64, 9, 512, 0),         # few rows, short caches
+    ("bf16", 8, 2, 128, 1, 8208, 16), ("f32", 4, 4, 32, 20, 8208, 0),      # and long ones
+    ("bf16", 4, 4, 128, 65, 4096, 16), ("bf16", 2, 2, 64, 20, 512, 0),     # one tile of rows
+    ("bf16", 8, 2, 128, 43, 4096, 16), ("bf16", 4, 1, 64, 100, 512, 0),    # two tiles, several of them
+])
+def test_expired_wait_is_reported_and_nothing_else_is_lost(dtype, Hq, Hkv, dh, n1, capacity, page):
+    """A bounded wait of the attention kernels is made to run out: the call returns with
+    MEDUSA_FLAG_TIMEOUT, whatever the workspace held, and the next one is as before."""
+    B = 3
+    case = Case("kv4", B, Hkv, dh, capacity, page, Hq=Hq, max_nodes=n1)
+    lens = [min(capacity, 1500), 0, 129]
+    for pool in case.pool:                             # any codes, scales from 0.5 to 1.875
+        pool.view(-1, 9 * dh)[:, 8 * dh:] = 0x35
+    q = rnd(1, (B, n1, Hq, dh), dtype).cuda()
+    tk, tv = rnd(2, (B, n1, Hkv, dh), dtype).cuda(), rnd(3, (B, n1, Hkv, dh), dtype).cuda()
+    ws = torch.empty(case.cache.workspace_size, dtype=torch.uint8, device="cuda")
+    kv = case.kv(i32(lens))
+
+    def call():
+        ws.fill_(0x7f)                                 # what another program may have left there
+        o = torch.empty_like(q)
+        t0 = time.perf_counter()
+        Bnd.kv4_attention(case.cache, kv, q, o, ws, tree_k=tk, tree_v=tv, k_scale=case.gk, v_scale=case.gv)
+        torch.cuda.synchronize()
+        return o, time.perf_counter() - t0
+
+    clean, _ = call()
+    assert case.cache.status() == 0 and torch.isfinite(clean.float()).all()
+    case.cache.expire_wait_once(2_000_000)
+    assert call()[1] < 30.0
+    assert case.cache.status() == Bnd.FLAG_TIMEOUT
+    assert case.cache.status() == 0
+    again, _ = call()
+    assert case.cache.status() == 0 and torch.equal(again, clean)
+
+
+def test_expire_wait_argument_checks():
+    case = Case("kv4", 1, 1, 64, 16)
+    for ns in (0, 10**10 + 1):
+        with pytest.raises(Bnd.MedusaError) as e:
+            case.cache.expire_wait_once(ns)
+        assert e.value.code == Bnd.MEDUSA_ERR_INVALID
+    with pytest.raises(Bnd.MedusaError) as e:
+        Case("bf16", 1, 1, 64, 16).cache.expire_wait_once(1000)
+    assert e.value.code == Bnd.MEDUSA_ERR_UNSUPPORTED
