@@ -508,10 +508,13 @@ medusa_status medusa_cache_expire_wait_once(medusa_cache* cache, unsigned long l
  * in elements; heads less than 2^31 bytes apart), outside the pools.  Items are the rows as they
  * are appended; `rows` is how many item places there are, and they belong to the sequences in
  * one of two ways:
- *   packed  start: device [B+1], items start[b] .. start[b+1]-1 are sequence b's; places
- *           before start[0] and from start[B] on belong to none and are skipped
+ *   packed  start: device [B+1], ascending, items start[b] .. start[b+1]-1 are sequence b's;
+ *           places before start[0] and from start[B] on belong to none and are skipped
  *   padded  start NULL: rows = B * per_seq, sequence b has the first count[b] (device [B],
  *           NULL: all) of the per_seq places from b * per_seq
+ * Offsets outside 0..rows and counts outside 0..per_seq are taken as the nearer end and set
+ * MEDUSA_FLAG_ROW_RANGE, and so do offsets that fall (len_out may then count slots that were not
+ * written).
  * index (device [rows], NULL: item i is row i): item i of sequence b is row
  * b * index_rows + index[i], 0 <= index[i] < index_rows; items outside are skipped and set
  * MEDUSA_FLAG_ROW_RANGE.  With per_seq = K+1, count = n_acc, index = path_nodes, index_rows =

@@ -124,10 +124,13 @@ template <int FMT> __device__ __forceinline__ long head_bytes(const CacheView& c
   return FMT == MEDUSA_KV4 ? (long)((c.page_table ? c.page_size : c.capacity) / KV4_SLOTS) * kv4_block(c.dh)
                            : (long)c.dh * (FMT == MEDUSA_BF16 ? 2 : 4);
 }
+__device__ __forceinline__ int append_length(const CacheView& c, const ItemMap& m, int b) {
+  return (int)min((long)clamp_len(c, c.len[b]) + item_count(m, b, c.status), (long)c.capacity);
+}
 __device__ __forceinline__ void append_lengths(const CacheView& c, const ItemMap& m, long tid, long threads) {
   if (c.len_out == c.len) return;
   for (long b = tid; b < c.B; b += threads)
-    c.len_out[b] = min(clamp_len(c, c.len[b]) + item_count(m, (int)b), c.capacity);
+    c.len_out[b] = append_length(c, m, (int)b);
 }
 
 // How warps share rows x (keys, values): a warp takes `places` rows of one kind and every
@@ -343,7 +346,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
 __global__ void kv_length_kernel(CacheView c, ItemMap m) {
   pdl_wait();
   for (int b = blockIdx.x * blockDim.x + threadIdx.x; b < c.B; b += gridDim.x * blockDim.x)
-    c.len_out[b] = min(clamp_len(c, c.len[b]) + item_count(m, b), c.capacity);
+    c.len_out[b] = append_length(c, m, b);
 }
 
 // The kernel for aligned rows against the other (4-bit, 8 heads of 128, us): 16 rows 3.7 / 4.5, 4096 rows
@@ -378,6 +381,8 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ Re
   __shared__ PlaceInfo info[8][KV_PLACES];
   const CacheView& c = a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (long b = (long)blockIdx.x * blockDim.x + threadIdx.x; b < c.B; b += (long)gridDim.x * blockDim.x)
+    item_count(a.m, (int)b, c.status);      // reports what is out of range
   long wid = (long)blockIdx.x * 8 + warp;
   const int slice = (int)(wid % ws.slices);
   wid /= ws.slices;

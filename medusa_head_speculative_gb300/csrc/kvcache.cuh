@@ -13,7 +13,8 @@ namespace medusa {
 constexpr int KV4_SLOTS = 16;                           // slots of a block
 __host__ __device__ constexpr int kv4_block(int dh) { return 9 * dh; }   // its bytes
 
-// Sequence (< 0: none) and place within it of item i.
+// Sequence (< 0: none) and place within it of item i.  Places are 0 .. rows - 1: an offset outside counts as
+// the nearer end, here and in item_count(), so that a sequence has as many items as are found for it.
 __device__ __forceinline__ int2 item_of(const ItemMap& m, int B, int i) {
   if (!m.start) {
     const int b = i / m.per_seq, j = i - b * m.per_seq;
@@ -25,12 +26,24 @@ __device__ __forceinline__ int2 item_of(const ItemMap& m, int B, int i) {
     if (m.start[mid] <= i) lo = mid;
     else hi = mid;
   }
-  const int s0 = m.start[lo];
+  const int s0 = max(m.start[lo], 0);                   // (i < rows)
   return make_int2(i >= s0 && i < m.start[lo + 1] ? lo : -1, i - s0);
 }
-__device__ __forceinline__ int item_count(const ItemMap& m, int b) {
-  const int n = m.start ? m.start[b + 1] - m.start[b] : (m.count ? min(m.count[b], m.per_seq) : m.per_seq);
-  return max(n, 0);
+// Items of sequence b; an offset or a count out of range sets MEDUSA_FLAG_ROW_RANGE.
+__device__ __forceinline__ int item_count(const ItemMap& m, int b, uint32_t* status) {
+  int n = m.per_seq;
+  bool ok = true;
+  if (m.start) {
+    const int s0 = m.start[b], s1 = m.start[b + 1];
+    ok = 0 <= s0 && s0 <= s1 && s1 <= m.rows;
+    n = max(min(max(s1, 0), m.rows) - min(max(s0, 0), m.rows), 0);
+  } else if (m.count) {
+    const int x = m.count[b];
+    n = min(max(x, 0), m.per_seq);
+    ok = n == x;
+  }
+  if (!ok) set_flag(status, MEDUSA_FLAG_ROW_RANGE);
+  return n;
 }
 
 // A length as the calls take it: outside 0..capacity the nearer end.

@@ -9,7 +9,7 @@ import torch
 import kv4_ref as R
 from harness import ensure_built
 from medusa_head_speculative_gb300 import binding as Bnd
-from test_gpu_cache import DT, U, Case, attn_bound, f64, i32, mask_of, rnd, see_matrix
+from test_gpu_cache import DT, U, Case, attn_bound, f64, i32, mask_of, rnd, see_matrix, want_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -144,3 +144,59 @@ def test_expire_wait_argument_checks():
     with pytest.raises(Bnd.MedusaError) as e:
         Case("bf16", 1, 1, 64, 16).cache.expire_wait_once(1000)
     assert e.value.code == Bnd.MEDUSA_ERR_UNSUPPORTED
+
+
+# ------------------------------------------------------------------ offsets, counts and row numbers
+@pytest.mark.parametrize("fmt", ["bf16", "kv4"])
+@pytest.mark.parametrize("alias", [False, True])
+@pytest.mark.parametrize("aligned", [True, False])
+@pytest.mark.parametrize("start,rows,items", [
+    ([0, 3, 9], 5, (range(0, 3), range(3, 5))),            # past the last row
+    ([-2, 2, 4], 5, (range(0, 2), range(2, 4))),           # before the first
+    ([7, 9, 12], 5, ((), ())),                             # nothing there at all
+    ([-2**31, 2, 2**31 - 1], 5, (range(0, 2), range(2, 5))),
+    ([4, 2, 5], 5, ((), range(2, 5))),                     # not ascending: the first has no items
+])
+def test_packed_offsets_out_of_range(start, rows, items, aligned, alias, fmt):
+    """Only items there are count: len_out grows by what was written, and the offsets are reported."""
+    case = Case(fmt, 2, 1, 32, 32)
+    x = rnd(1, (rows, 1, 32), "bf16").cuda()
+    if not aligned:
+        x = off_by_one(x)
+    length = i32([1, 6])
+    out = length if alias else torch.zeros_like(length)
+    Bnd.kv_append(case.cache, case.kv(length, out), x, x, start=i32(start), k_scale=case.gk, v_scale=case.gv)
+    assert out.tolist() == [1 + len(items[0]), 6 + len(items[1])]
+    assert case.cache.status() == Bnd.FLAG_ROW_RANGE
+    raw = case.host(1)
+    for b, at in ((0, 1), (1, 6)):
+        for j, i in enumerate(items[b]):
+            np.testing.assert_array_equal(case.view.value(raw, b, at + j, case.gv), want_rows(case, f64(x[i]), case.gv, fmt))
+    if fmt == "kv4":
+        case.fill([8, 8])
+    lens = i32([8, 8])
+    k, v = (torch.full((rows, 1, 32), 7.0, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    Bnd.kv_read(case.cache, case.kv(lens), k, v, start=i32(start), k_scale=case.gk, v_scale=case.gv)
+    assert case.cache.status() == Bnd.FLAG_ROW_RANGE
+    raw, seen = case.host(1), set()
+    for b in (0, 1):
+        for j, i in enumerate(items[b]):
+            seen.add(i)
+            np.testing.assert_array_equal(f64(v[i]), case.view.value(raw, b, j, case.gv))
+    for i in set(range(rows)) - seen:
+        assert (v[i] == 7).all() and (k[i] == 7).all()
+
+
+@pytest.mark.parametrize("alias", [False, True])
+def test_counts_out_of_range(alias):
+    case = Case("bf16", 3, 1, 32, 32)
+    x = rnd(1, (6, 1, 32), "bf16").cuda()
+    length = i32([0, 4, 8])
+    out = length if alias else torch.zeros_like(length)
+    Bnd.kv_append(case.cache, case.kv(length, out), x, x, per_seq=2, count=i32([5, -1, 1]))
+    assert out.tolist() == [2, 4, 9] and case.cache.status() == Bnd.FLAG_ROW_RANGE
+    k, v = torch.zeros_like(x), torch.zeros_like(x)
+    Bnd.kv_read(case.cache, case.kv(out), k, v, per_seq=2, count=i32([1, 3, 2]), first=i32([0, 0, 7]))
+    assert case.cache.status() == Bnd.FLAG_ROW_RANGE
+    Bnd.kv_read(case.cache, case.kv(out), k, v, per_seq=2, count=i32([1, 2, 0]))
+    assert case.cache.status() == 0
