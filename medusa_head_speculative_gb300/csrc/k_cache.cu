@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(KV_APPEND_WARPS * 32, 5) kv_append_vec_kernel(
     const bool lead = !values && slice == 0;
     PlaceInfo p{};
     Target o;
-    if (i0 + lane < a.m.rows && append_target(a, i0 + lane, item_of(a.m, c.B, i0 + lane), lead, o)) {
+    if (lane < a.m.rows - i0 && append_target(a, i0 + lane, item_of(a.m, c.B, i0 + lane), lead, o)) {
       p = place_info<FMT>(c, values ? c.v : c.k, o.unit, o.in);
       p.rows = const_cast<char*>(static_cast<const char*>(values ? a.v : a.k)) +
                o.row * (values ? a.v_row : a.k_row) * (long)sizeof(T);
@@ -357,7 +357,7 @@ static cudaError_t append_go(const AppendArgs& a, int format, cudaStream_t st) {
     auto kern = format == MEDUSA_KV4 ? kv_append_vec_kernel<T, MEDUSA_KV4>
                 : format == MEDUSA_BF16 ? kv_append_vec_kernel<T, MEDUSA_BF16> : kv_append_vec_kernel<T, MEDUSA_F32>;
     const WarpShare ws = warp_share(a.m.rows, a.c.Hkv * a.c.dh, a.c.Hkv * (a.c.dh / (format == MEDUSA_KV4 ? 16 : 8)));
-    const long warps = (long)(a.m.rows + ws.places - 1) / ws.places * 2 * ws.slices;
+    const long warps = ((long)a.m.rows + ws.places - 1) / ws.places * 2 * ws.slices;
     return launch_kernel(kern, dim3((unsigned)(warps < 1 ? 1 : (warps + KV_APPEND_WARPS - 1) / KV_APPEND_WARPS)), dim3(KV_APPEND_WARPS * 32), 0, st, 1, a, ws);
   }
   const long n = (long)a.m.rows * 2 * a.c.Hkv * (a.c.dh / 16);
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ Re
   const int i0 = (int)(wid >> 1) * ws.places;
   if (lane < ws.places) {
     PlaceInfo p{};
-    const int2 it = i0 + lane < a.m.rows ? item_of(a.m, c.B, i0 + lane) : make_int2(-1, 0);
+    const int2 it = lane < a.m.rows - i0 ? item_of(a.m, c.B, i0 + lane) : make_int2(-1, 0);
     if (it.x >= 0) {
       const long t = (long)it.y + (a.first ? a.first[it.x] : 0);
       long unit;
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ Re
 template <typename T>
 static cudaError_t read_go(const ReadArgs& a, int format, cudaStream_t st) {
   const WarpShare ws = warp_share(a.m.rows, a.c.Hkv * a.c.dh, a.c.Hkv * a.c.dh * (int)sizeof(T) / 16);
-  const long warps = (long)(a.m.rows + ws.places - 1) / ws.places * 2 * ws.slices;
+  const long warps = ((long)a.m.rows + ws.places - 1) / ws.places * 2 * ws.slices;
   auto kern = format == MEDUSA_KV4 ? kv_read_kernel<T, MEDUSA_KV4>
               : format == MEDUSA_BF16 ? kv_read_kernel<T, MEDUSA_BF16> : kv_read_kernel<T, MEDUSA_F32>;
   return launch_kernel(kern, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st, 1, a, ws);

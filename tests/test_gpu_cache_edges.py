@@ -200,3 +200,17 @@ def test_counts_out_of_range(alias):
     assert case.cache.status() == Bnd.FLAG_ROW_RANGE
     Bnd.kv_read(case.cache, case.kv(out), k, v, per_seq=2, count=i32([1, 2, 0]))
     assert case.cache.status() == 0
+
+
+def test_append_of_two_thousand_million_places():
+    """Row counts up to a 32-bit integer's end: the last places of all are found."""
+    rows = 2**31 - 1
+    case = Case("bf16", 2, 1, 32, 32)
+    x = rnd(1, (1, 1, 32), "bf16").cuda()
+    length, out = i32([3, 0]), i32([0, 0])
+    Bnd.kv_append(case.cache, case.kv(length, out), x.expand(rows, 1, 32), x.expand(rows, 1, 32),
+                  start=i32([rows - 5, rows - 1, rows]))
+    assert out.tolist() == [7, 1] and case.cache.status() == 0
+    raw = case.host(0)
+    for b, t in ((0, 3), (0, 4), (0, 5), (0, 6), (1, 0)):
+        np.testing.assert_array_equal(case.view.value(raw, b, t), f64(x[0]))
