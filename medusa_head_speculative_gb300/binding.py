@@ -608,7 +608,9 @@ def _items(cache, n, start, rows, per_seq, count, device):
     if start is not None:
         return rows, _ints("start", start, cache.B + 1, device), 0, None
     if per_seq is None:
-        per_seq = rows // cache.B
+        per_seq, rest = divmod(rows, cache.B)
+        if rest:
+            raise ValueError(f"{rows} rows are no equal shares of {cache.B} sequences: per_seq or start is needed")
     return cache.B * per_seq, None, per_seq, _ints("count", count, cache.B, device)
 
 

@@ -1,8 +1,10 @@
 """Rotary and cache handles: what creation refuses, and the 4-bit reference's own pins (CPU)."""
 import ctypes as C
+from types import SimpleNamespace
 
 import numpy as np
 import pytest
+import torch
 
 import kv4_ref as R
 from harness import ensure_built
@@ -93,3 +95,29 @@ def test_reference_rotation_depends_on_distance_only():
         assert abs(a - b) < 1e-12
         back = R.rope(R.rope(q, [77], 24, layout), [77], 24, layout, inverse=True)
         assert np.abs(back - q).max() < 1e-14
+
+
+def unopened(cls, **kw):
+    """A handle object without a handle: calls that pass the binding's own checks are refused by the library."""
+    h = cls.__new__(cls)
+    h.handle = None
+    for name, value in dict(kw, device=-1).items():          # a CPU tensor's device
+        setattr(h, name, value)
+    return h
+
+
+NO_STREAM = SimpleNamespace(cuda_stream=None)
+
+
+def test_rows_that_are_no_equal_shares_are_refused():
+    cache = unopened(Bnd.Cache, B=4, Hq=1, Hkv=1, dh=32, format=Bnd.BF16)
+    rows, ints = torch.zeros(10, 1, 32), torch.zeros(12, dtype=torch.int32)
+    for call in (lambda **kw: Bnd.kv_append(cache, Bnd.KV(), rows, rows, stream=NO_STREAM, **kw),
+                 lambda **kw: Bnd.kv_append(cache, Bnd.KV(), rows, rows, index=ints[:10], index_rows=2, stream=NO_STREAM, **kw),
+                 lambda **kw: Bnd.kv_read(cache, Bnd.KV(), rows, rows, stream=NO_STREAM, **kw)):
+        with pytest.raises(ValueError, match="equal shares"):
+            call()
+        with pytest.raises(Bnd.MedusaError):                 # as far as the library
+            call(per_seq=2)
+        with pytest.raises(Bnd.MedusaError):
+            call(rows=8)

@@ -214,3 +214,16 @@ def test_append_of_two_thousand_million_places():
     raw = case.host(0)
     for b, t in ((0, 3), (0, 4), (0, 5), (0, 6), (1, 0)):
         np.testing.assert_array_equal(case.view.value(raw, b, t), f64(x[0]))
+
+
+def test_rows_that_are_no_equal_shares_are_refused():
+    case = Case("bf16", 4, 1, 32, 16)
+    rows, length, out = rnd(1, (10, 1, 32), "bf16").cuda(), i32([0] * 4), i32([-5] * 4)
+    with pytest.raises(ValueError):
+        Bnd.kv_append(case.cache, case.kv(length, out), rows, rows)
+    with pytest.raises(ValueError):
+        Bnd.kv_read(case.cache, case.kv(i32([3] * 4)), rows, rows.clone())
+    assert out.tolist() == [-5] * 4
+    Bnd.kv_append(case.cache, case.kv(length, out), rows[:8], rows[:8])
+    Bnd.kv_append(case.cache, case.kv(length, out), rows, rows, per_seq=2)      # the rows behind are the caller's
+    assert out.tolist() == [2] * 4
