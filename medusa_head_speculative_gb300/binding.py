@@ -497,6 +497,19 @@ def _same(x, *others):
                             f"{y.dtype} on {y.device}")
 
 
+def _device():
+    """The current device, where a handle's memory is made."""
+    import torch
+    return torch.cuda.current_device()
+
+
+def _on(handle, *tensors):
+    """The tensors (None: none) are on the handle's device: the kernels take their addresses as they are."""
+    for t in tensors:
+        if t is not None and t.get_device() != handle.device:
+            raise ValueError(f"tensors on cuda:{handle.device}, the handle's device, are needed, got one on {t.device}")
+
+
 def _ints(what, t, n, device):
     """Address of an int32 tensor of at least n entries in order, or None."""
     if t is None:
@@ -504,7 +517,7 @@ def _ints(what, t, n, device):
     if _INT32 is None:
         _load_dtypes()
     if t.dtype is not _INT32 or t.numel() < n or not t.is_contiguous() or t.get_device() != device:
-        raise ValueError(f"{what}: a contiguous int32 tensor of at least {n} entries on the cache's "
+        raise ValueError(f"{what}: a contiguous int32 tensor of at least {n} entries on the handle's "
                          f"device is needed, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
@@ -527,7 +540,7 @@ class Rope:
                              orig_pos, low, high, attn)
         out = P()
         _check("medusa_rope_create", lib().medusa_rope_create(C.byref(self.desc), C.byref(out)))
-        self.handle = out
+        self.handle, self.device = out, _device()
 
     def status(self, stream=None):
         return _status("medusa_rope_get_status", self.handle, stream)
@@ -552,7 +565,8 @@ def rope_apply(rope, pos, parts, inverse=False, stream=None):
     """medusa_rope_apply: `parts` holds (x, y) pairs of [rows][heads][dh] tensors (any strides
     between rows and heads); y may be x."""
     rows, first = pos.numel(), parts[0][0]
-    dh, dtype, t, device = first.shape[-1], _dtype(first), first.dtype, first.get_device()
+    dh, dtype, t, device = first.shape[-1], _dtype(first), first.dtype, rope.device
+    _on(rope, first)
     args = []
     for x, y in parts:
         xs, xt, ys, yt = x.shape, x.stride(), y.shape, y.stride()
@@ -577,7 +591,7 @@ class Cache:
         self.dims = CacheDims(B, Hq, Hkv, dh, format, capacity, page_size, num_pages, max_nodes)
         out = P()
         _check("medusa_cache_create", lib().medusa_cache_create(C.byref(self.dims), C.byref(out)))
-        self.handle = out
+        self.handle, self.device = out, _device()
         self.B, self.Hq, self.Hkv, self.dh, self.format = B, Hq, Hkv, dh, format
         self.pool_bytes = lib().medusa_cache_pool_bytes(out)
         self.workspace_size = lib().medusa_cache_workspace_size(out)
@@ -619,7 +633,8 @@ def kv_append(cache, kv, k, v, start=None, per_seq=None, count=None, index=None,
     """medusa_kv_append: k, v [rows][Hkv][dh] (any strides between rows and heads).  Packed
     batches give `start`, padded ones `per_seq` (default: an equal share of the rows) and
     `count`; with `index` the item places are index's and k, v the rows they name."""
-    device = k.get_device()
+    device = cache.device
+    _on(cache, k)
     n, start, per_seq, count = _items(cache, k.shape[0] if index is None else index.numel(), start,
                                       rows, per_seq, count, device)
     need = n if index is None else cache.B * index_rows
@@ -636,7 +651,8 @@ def kv_append(cache, kv, k, v, start=None, per_seq=None, count=None, index=None,
 def kv_read(cache, kv, k, v, start=None, per_seq=None, count=None, first=None, k_scale=1.0,
             v_scale=1.0, rows=None, stream=None):
     """medusa_kv_read into k, v [rows][Hkv][dh]; batches as in kv_append."""
-    device = k.get_device()
+    device = cache.device
+    _on(cache, k)
     n, start, per_seq, count = _items(cache, k.shape[0], start, rows, per_seq, count, device)
     kr, kh = _rows("k", k, n, cache.Hkv, cache.dh)
     vr, vh = _rows("v", v, n, cache.Hkv, cache.dh)
@@ -661,13 +677,16 @@ def kv4_attention(cache, kv, q, o, ws, tree_k=None, tree_v=None, mask=None, scal
     for s in (qs, os_):
         if s[3] != 1 or (at and B > 1 and s[0] != n1 * s[1]):
             raise ValueError(f"q, o: elements in order and evenly spaced rows are needed, got strides {s}")
+    _on(cache, q, ws)
     _same(q, o, tree_k, tree_v)
+    if not ws.is_contiguous():
+        raise ValueError("ws: a contiguous tensor is needed")
     for t in (tree_k, tree_v):
         if t is not None and (t.shape != (B, n1, cache.Hkv, cache.dh) or not t.is_contiguous()):
             raise ValueError(f"tree_k, tree_v: contiguous [{B}][{n1}][{cache.Hkv}][{cache.dh}] is needed")
     a = KV4Query(q.data_ptr(), o.data_ptr(), _dtype(q), n1, qs[at], qs[2], os_[at], os_[2],
                  None if tree_k is None else tree_k.data_ptr(), None if tree_v is None else tree_v.data_ptr(),
-                 _ints("mask", mask, 8 * n1, q.get_device()), scale, k_scale, v_scale)
+                 _ints("mask", mask, 8 * n1, cache.device), scale, k_scale, v_scale)
     _check("medusa_kv4_attention",
            lib().medusa_kv4_attention(cache.handle, kv, a, ws.data_ptr(), ws.numel() * ws.element_size(),
                                       _stream(stream)))

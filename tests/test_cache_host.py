@@ -121,3 +121,28 @@ def test_rows_that_are_no_equal_shares_are_refused():
             call(per_seq=2)
         with pytest.raises(Bnd.MedusaError):
             call(rows=8)
+
+
+@pytest.mark.parametrize("device,error", [(0, ValueError), (-1, Bnd.MedusaError)])
+def test_tensors_on_another_device_are_refused(device, error):
+    """Their addresses would go to the kernels.  Tensors of the CPU with handles of a GPU, and (which the library
+    alone refuses) with handles whose device is theirs."""
+    x, ints = torch.zeros(4, 2, 32), torch.zeros(64, dtype=torch.int32)
+    q, tree, ws = torch.zeros(2, 2, 2, 32), torch.zeros(2, 2, 2, 32), torch.zeros(256, dtype=torch.uint8)
+    cache, rope = unopened(Bnd.Cache, B=2, Hq=2, Hkv=2, dh=32, format=Bnd.KV4), unopened(Bnd.Rope)
+    cache.device = rope.device = device
+
+    def attend(ws):
+        Bnd.kv4_attention(cache, Bnd.KV(), q, torch.empty_like(q), ws, tree_k=tree, tree_v=tree, mask=ints,
+                          stream=NO_STREAM)
+
+    for call in (lambda: Bnd.rope_apply(rope, ints[:4], [(x, x)], stream=NO_STREAM),
+                 lambda: Bnd.kv_append(cache, Bnd.KV(), x, x, pos=ints[:4], stream=NO_STREAM),
+                 lambda: Bnd.kv_read(cache, Bnd.KV(), x, x, first=ints[:2], stream=NO_STREAM), lambda: attend(ws)):
+        with pytest.raises(error):
+            call()
+    elsewhere = SimpleNamespace(device="elsewhere", get_device=lambda: 7, data_ptr=lambda: 256, numel=lambda: 256,
+                                element_size=lambda: 1, is_contiguous=lambda: True)
+    for bad in (elsewhere, ws[::2]):
+        with pytest.raises(ValueError):
+            attend(bad)
