@@ -633,6 +633,8 @@ def kv_append(cache, kv, k, v, start=None, per_seq=None, count=None, index=None,
     """medusa_kv_append: k, v [rows][Hkv][dh] (any strides between rows and heads).  Packed
     batches give `start`, padded ones `per_seq` (default: an equal share of the rows) and
     `count`; with `index` the item places are index's and k, v the rows they name."""
+    if rope is not None and not rope.handle:
+        raise ValueError("rope: closed")               # (the library turns nothing for NULL)
     device = cache.device
     _on(cache, k)
     n, start, per_seq, count = _items(cache, k.shape[0] if index is None else index.numel(), start,

@@ -146,3 +146,14 @@ def test_tensors_on_another_device_are_refused(device, error):
     for bad in (elsewhere, ws[::2]):
         with pytest.raises(ValueError):
             attend(bad)
+
+
+def test_closed_rotation_is_refused():
+    """Appending with a Rope that has been closed must not leave the keys unturned."""
+    cache, rope = unopened(Bnd.Cache, B=2, Hq=2, Hkv=2, dh=32, format=Bnd.KV4), unopened(Bnd.Rope)
+    rope.close()
+    x = torch.zeros(4, 2, 32)
+    with pytest.raises(ValueError, match="closed"):
+        Bnd.kv_append(cache, Bnd.KV(), x, x, rope=rope, stream=NO_STREAM)
+    with pytest.raises(Bnd.MedusaError):
+        Bnd.rope_apply(rope, torch.zeros(4, dtype=torch.int32), [(x, x)], stream=NO_STREAM)
