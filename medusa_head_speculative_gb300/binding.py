@@ -503,11 +503,10 @@ def _device():
     return torch.cuda.current_device()
 
 
-def _on(handle, *tensors):
-    """The tensors (None: none) are on the handle's device: the kernels take their addresses as they are."""
-    for t in tensors:
-        if t is not None and t.get_device() != handle.device:
-            raise ValueError(f"tensors on cuda:{handle.device}, the handle's device, are needed, got one on {t.device}")
+def _elsewhere(handle, *tensors):
+    """Not all tensors are on the handle's device, and the kernels take their addresses as they are."""
+    raise ValueError(f"tensors on cuda:{handle.device}, the handle's device, are needed, got "
+                     + ", ".join(str(t.device) for t in tensors))
 
 
 def _ints(what, t, n, device):
@@ -566,7 +565,8 @@ def rope_apply(rope, pos, parts, inverse=False, stream=None):
     between rows and heads); y may be x."""
     rows, first = pos.numel(), parts[0][0]
     dh, dtype, t, device = first.shape[-1], _dtype(first), first.dtype, rope.device
-    _on(rope, first)
+    if first.get_device() != device:
+        _elsewhere(rope, first)
     args = []
     for x, y in parts:
         xs, xt, ys, yt = x.shape, x.stride(), y.shape, y.stride()
@@ -636,7 +636,8 @@ def kv_append(cache, kv, k, v, start=None, per_seq=None, count=None, index=None,
     if rope is not None and not rope.handle:
         raise ValueError("rope: closed")               # (the library turns nothing for NULL)
     device = cache.device
-    _on(cache, k)
+    if k.get_device() != device:
+        _elsewhere(cache, k)
     n, start, per_seq, count = _items(cache, k.shape[0] if index is None else index.numel(), start,
                                       rows, per_seq, count, device)
     need = n if index is None else cache.B * index_rows
@@ -654,7 +655,8 @@ def kv_read(cache, kv, k, v, start=None, per_seq=None, count=None, first=None, k
             v_scale=1.0, rows=None, stream=None):
     """medusa_kv_read into k, v [rows][Hkv][dh]; batches as in kv_append."""
     device = cache.device
-    _on(cache, k)
+    if k.get_device() != device:
+        _elsewhere(cache, k)
     n, start, per_seq, count = _items(cache, k.shape[0], start, rows, per_seq, count, device)
     kr, kh = _rows("k", k, n, cache.Hkv, cache.dh)
     vr, vh = _rows("v", v, n, cache.Hkv, cache.dh)
@@ -679,7 +681,9 @@ def kv4_attention(cache, kv, q, o, ws, tree_k=None, tree_v=None, mask=None, scal
     for s in (qs, os_):
         if s[3] != 1 or (at and B > 1 and s[0] != n1 * s[1]):
             raise ValueError(f"q, o: elements in order and evenly spaced rows are needed, got strides {s}")
-    _on(cache, q, ws)
+    device = cache.device
+    if q.get_device() != device or ws.get_device() != device:
+        _elsewhere(cache, q, ws)
     _same(q, o, tree_k, tree_v)
     if not ws.is_contiguous():
         raise ValueError("ws: a contiguous tensor is needed")
@@ -688,7 +692,7 @@ def kv4_attention(cache, kv, q, o, ws, tree_k=None, tree_v=None, mask=None, scal
             raise ValueError(f"tree_k, tree_v: contiguous [{B}][{n1}][{cache.Hkv}][{cache.dh}] is needed")
     a = KV4Query(q.data_ptr(), o.data_ptr(), _dtype(q), n1, qs[at], qs[2], os_[at], os_[2],
                  None if tree_k is None else tree_k.data_ptr(), None if tree_v is None else tree_v.data_ptr(),
-                 _ints("mask", mask, 8 * n1, cache.device), scale, k_scale, v_scale)
+                 _ints("mask", mask, 8 * n1, device), scale, k_scale, v_scale)
     _check("medusa_kv4_attention",
            lib().medusa_kv4_attention(cache.handle, kv, a, ws.data_ptr(), ws.numel() * ws.element_size(),
                                       _stream(stream)))
