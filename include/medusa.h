@@ -445,7 +445,8 @@ void medusa_rope_destroy(medusa_rope* rope);
 /* As medusa_get_status, for the handle's own status word. */
 medusa_status medusa_rope_get_status(const medusa_rope* rope, void* stream, uint32_t* flags);
 /* One set of rows: element e of head h of row r is x[r * x_row + h * x_head + e] (strides in
- * elements), its result y[r * y_row + h * y_head + e].  y == x with equal strides turns the
+ * elements), its result y[r * y_row + h * y_head + e]; no two results may share an element, here and in
+ * the calls below (MEDUSA_ERR_INVALID).  y == x with equal strides turns the
  * rows in place; otherwise x and y must not overlap. */
 typedef struct {
   const void* x;

@@ -38,6 +38,18 @@ bool here(int device) {
   int d = -1;
   return cudaGetDevice(&d) == cudaSuccess && d == device;
 }
+// Whether no two of rows x heads pieces of dh elements, row and head elements apart, share an element: results
+// that lie on one another would be written in any order.
+bool lie_apart(long long rows, long long row, long long heads, long long head, int dh) {
+  if ((rows > 1 && row < dh) || (heads > 1 && head < dh)) return false;
+  if (rows <= 1 || heads <= 1) return true;
+  if (row >= (__int128)(heads - 1) * head + dh || head >= (__int128)(rows - 1) * row + dh) return true;
+  for (long long i = 1; i < heads; ++i) {          // neither within the other's gaps: piece by piece
+    const __int128 at = (__int128)i * head, j = at / row;
+    if ((j < rows && at - j * row < dh) || (j + 1 < rows && (j + 1) * row - at < dh)) return false;
+  }
+  return true;
+}
 medusa_status done(cudaError_t e) { return e == cudaSuccess ? MEDUSA_OK : MEDUSA_ERR_CUDA; }
 
 medusa_status read_status(uint32_t* word, void* stream, uint32_t* flags) {
@@ -236,6 +248,7 @@ medusa_status medusa_rope_apply(const medusa_rope* r, int dtype, int dh, int row
       return MEDUSA_ERR_INVALID;
     if (!aligned(p.x, elem(dtype)) || !aligned(p.y, elem(dtype))) return MEDUSA_ERR_INVALID;
     if (rows > 0 && p.x == p.y && (p.x_row != p.y_row || p.x_head != p.y_head)) return MEDUSA_ERR_INVALID;
+    if (rows > 0 && !lie_apart(rows, p.y_row, p.heads, p.y_head, dh)) return MEDUSA_ERR_INVALID;
     if (p.heads > 65535 || a.heads + p.heads > 65535) return MEDUSA_ERR_UNSUPPORTED;
     a.part[i] = p;
     a.heads += p.heads;
@@ -331,6 +344,9 @@ medusa_status medusa_kv_read(const medusa_cache* c, const medusa_kv* kv, const m
   if (s != MEDUSA_OK) return s;
   if ((s = check_scales(c, k_scale, v_scale)) != MEDUSA_OK) return s;
   if ((s = check_items(c, places, &a.m)) != MEDUSA_OK) return s;
+  if (!lie_apart(places->rows, places->k_row, c->d.Hkv, places->k_head, c->d.dh) ||
+      !lie_apart(places->rows, places->v_row, c->d.Hkv, places->v_head, c->d.dh))
+    return MEDUSA_ERR_INVALID;
   a.c = view_of(c, kv, k_scale, v_scale);
   a.k = places->k;
   a.v = places->v;
@@ -361,6 +377,7 @@ medusa_status medusa_kv4_attention(const medusa_cache* c, const medusa_kv* kv, c
   if (q->q_row < 0 || q->q_head < 0 || q->o_row < 0 || q->o_head < 0 || q->q_row % n || q->q_head % n ||
       q->o_row % n || q->o_head % n)
     return MEDUSA_ERR_INVALID;
+  if (!lie_apart((long long)c->d.B * q->n1, q->o_row, c->d.Hq, q->o_head, c->d.dh)) return MEDUSA_ERR_INVALID;
   if (!ws || ws_bytes < c->ws_bytes || !aligned(ws, 256)) return MEDUSA_ERR_WORKSPACE;
   Kv4AttnArgs a{};
   a.c = view_of(c, kv, q->k_scale, q->v_scale);

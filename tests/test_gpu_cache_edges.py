@@ -227,3 +227,59 @@ def test_rows_that_are_no_equal_shares_are_refused():
     Bnd.kv_append(case.cache, case.kv(length, out), rows[:8], rows[:8])
     Bnd.kv_append(case.cache, case.kv(length, out), rows, rows, per_seq=2)      # the rows behind are the caller's
     assert out.tolist() == [2] * 4
+
+
+# ------------------------------------------------------------------ results that lie on one another
+def strided(shape, strides, dtype=torch.bfloat16):
+    n = 1 + sum((a - 1) * b for a, b in zip(shape, strides))
+    return torch.as_strided(torch.full((n,), 7.0, dtype=dtype, device="cuda"), shape, strides)
+
+
+@pytest.mark.parametrize("rows,heads,row,head,ok", [
+    (6, 2, 0, 64, False), (6, 2, 128, 0, False), (6, 2, 128, 40, False), (6, 2, 64, 64, False),
+    (6, 2, 128, 64, True), (6, 2, 64, 6 * 64, True), (6, 2, 64, 5 * 64, False),
+    (2, 3, 192, 128, True), (3, 4, 192, 128, False), (6, 2, 136, 72, True),
+    (2, 3, 200, 128, False),                   # row 1, head 0 has 200..263, row 0, head 2 256..319
+])
+def test_results_that_share_elements_are_refused(rows, heads, row, head, ok):
+    """Rotated rows, slots read and attention's results written more than once, in any order."""
+    dh = 64
+    shape, strides = (rows, heads, dh), (row, head, 1)
+    refused = pytest.raises(Bnd.MedusaError)
+    rope, x = Bnd.Rope(dh, 16), rnd(1, shape, "bf16").cuda()
+    y, want = strided(shape, strides), torch.empty_like(x)
+    pos = i32(list(range(rows)))
+
+    def attempt(call):
+        if ok:
+            return call()
+        with refused as e:
+            call()
+        assert e.value.code == Bnd.MEDUSA_ERR_INVALID
+
+    attempt(lambda: Bnd.rope_apply(rope, pos, [(x, y)]))
+    Bnd.rope_apply(rope, pos, [(x, want)])
+    assert torch.equal(y, want) or not ok
+    case = Case("kv4", 1, heads, dh, 16, max_nodes=rows)
+    case.fill([rows])
+    kv = case.kv(i32([rows]))
+    k, v, want = strided(shape, strides), torch.empty_like(x), torch.empty_like(x)
+    attempt(lambda: Bnd.kv_read(case.cache, kv, k, v, per_seq=rows))
+    attempt(lambda: Bnd.kv_read(case.cache, kv, v, k, per_seq=rows))
+    Bnd.kv_read(case.cache, kv, v, want, per_seq=rows)
+    assert torch.equal(k, want) or not ok
+    q, o, want = x[None], strided((1,) + shape, (0,) + strides), torch.empty_like(x[None])
+    ws = torch.empty(case.cache.workspace_size, dtype=torch.uint8, device="cuda")
+    attempt(lambda: Bnd.kv4_attention(case.cache, kv, q, o, ws))
+    Bnd.kv4_attention(case.cache, kv, q, want, ws)
+    assert torch.equal(o, want) or not ok
+
+
+def test_rows_turned_in_place_more_than_once_are_refused():
+    rope, x = Bnd.Rope(64, 16), rnd(1, (1, 2, 64), "bf16").cuda()
+    same = x.expand(4, 2, 64)
+    with pytest.raises(Bnd.MedusaError):
+        Bnd.rope_apply(rope, i32([0, 1, 2, 3]), [(same, same)])
+    y = torch.empty(4, 2, 64, dtype=torch.bfloat16, device="cuda")
+    Bnd.rope_apply(rope, i32([0, 1, 2, 3]), [(same, y)])               # read more than once: as often as wanted
+    assert torch.equal(y[0], x[0]) and not torch.equal(y[1], x[0])
