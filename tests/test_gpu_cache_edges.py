@@ -9,7 +9,7 @@ import torch
 import kv4_ref as R
 from harness import ensure_built
 from medusa_head_speculative_gb300 import binding as Bnd
-from test_gpu_cache import DT, U, Case, attn_bound, f64, i32, mask_of, rnd, see_matrix, want_rows
+from test_gpu_cache import DT, H, U, Case, attn_bound, f64, i32, mask_of, rnd, see_matrix, want_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -283,3 +283,119 @@ def test_rows_turned_in_place_more_than_once_are_refused():
     y = torch.empty(4, 2, 64, dtype=torch.bfloat16, device="cuda")
     Bnd.rope_apply(rope, i32([0, 1, 2, 3]), [(same, y)])               # read more than once: as often as wanted
     assert torch.equal(y[0], x[0]) and not torch.equal(y[1], x[0])
+
+
+# ------------------------------------------------------------------ many rows, and rotations of a part
+def held(case, raw, seq, slot):
+    """What pool raw has at (sequence, slot) pairs: [n][Hkv][dh] elements, or 4-bit codes and scales."""
+    per = case.page or case.capacity
+    unit = seq if not case.page else case.pages[seq, slot // per]
+    at = slot % per
+    if case.fmt != "kv4":
+        return raw.reshape(-1, per, case.Hkv, case.dh)[unit, at]
+    n, dh = len(seq), case.dh
+    blocks = raw.reshape(-1, case.Hkv, per // 16, 9 * dh)[unit, :, at // 16]
+    return (blocks[..., :8 * dh].reshape(n, case.Hkv, 16, dh // 2)[np.arange(n), :, at % 16],
+            blocks[..., 8 * dh:].reshape(n, case.Hkv, 16, dh // 16)[np.arange(n), :, at % 16])
+
+
+def rest(case, raw, seq, slot):
+    """The pool with those slots blanked."""
+    raw, per = raw.copy(), case.page or case.capacity
+    unit = seq if not case.page else case.pages[seq, slot // per]
+    at = slot % per
+    if case.fmt != "kv4":
+        raw.reshape(-1, per, case.Hkv, case.dh)[unit, at] = 0
+        return raw
+    dh, blocks = case.dh, raw.reshape(-1, case.Hkv, per // 16, 9 * case.dh)
+    for u, t in zip(unit, at):
+        r = t % 16
+        blocks[u, :, t // 16, r * dh // 2:(r + 1) * dh // 2] = 0
+        blocks[u, :, t // 16, 8 * dh + r * dh // 16:8 * dh + (r + 1) * dh // 16] = 0
+    return raw
+
+
+def check_turned(fmt, got, x, pos, rot, layout, g):
+    """Keys x [n][Hkv][dh] as held after their rotation; bounds as in test_append_packed."""
+    w = R.rope(x, pos, rot, layout)
+    tol = 4 * U * (np.abs(x) + 4 * np.abs(x).max(-1, keepdims=True))
+    tol[..., rot:] = 0                                     # passes through
+    if fmt != "kv4":
+        tol = np.where(tol > 0, tol + H[fmt] * (np.abs(w) + tol), H[fmt] * np.abs(w))
+        assert (np.abs(got - w) <= tol).all()
+        return
+    codes, scales = got
+    near = [R.encode(w * f, g)[1] for f in (1 - 2 ** -20, 1 + 2 ** -20)]
+    assert ((scales == near[0]) | (scales == near[1])).all()
+    s = np.repeat(R.E4M3[scales], 16, -1) * g
+    best = np.abs(R.E2M1[R.e2m1_nearest(np.abs(w) / np.where(s > 0, s, 1))] * s - np.abs(w))
+    assert (np.abs(R.decode(codes, scales, g) - w) <= best + 2 * tol + 4 * U * 6 * s).all()
+
+
+MANY = [
+    # fmt, src, Hkv, dh, rows, page, layout, rot (a warp takes several rows from 7296 on, 8192 elements of them)
+    ("kv4", "bf16", 8, 32, 20001, 16, "half", 32), ("bf16", "bf16", 8, 32, 20001, 0, "half", 32),
+    ("kv4", "f32", 8, 32, 7297, 0, None, 0), ("f32", "bf16", 8, 32, 7301, 5, "interleaved", 16),
+    ("kv4", "bf16", 19, 64, 7301, 48, "interleaved", 48), ("bf16", "f32", 19, 64, 7301, 0, "half", 32),
+    ("kv4", "bf16", 21, 128, 7303, 16, "half", 64), ("f32", "f32", 21, 128, 7296, 0, "interleaved", 48),
+    # part of a head turned, whole units: pairs, then what passes through; a row over several warps
+    ("kv4", "bf16", 2, 128, 37, 0, "half", 32), ("kv4", "f32", 40, 128, 37, 16, "half", 96),
+    ("bf16", "bf16", 3, 128, 41, 5, "half", 64), ("f32", "f32", 2, 64, 37, 0, "half", 32),
+    ("kv4", "bf16", 2, 128, 37, 16, "interleaved", 16), ("kv4", "bf16", 1, 64, 300, 0, "interleaved", 48),
+    ("bf16", "f32", 5, 64, 37, 16, "interleaved", 16), ("f32", "bf16", 2, 128, 41, 0, "interleaved", 112),
+    ("bf16", "bf16", 2, 128, 37, 0, "interleaved", 48),
+]
+
+
+@pytest.mark.parametrize("fmt,src,Hkv,dh,rows,page,layout,rot", MANY)
+@pytest.mark.parametrize("given", [False, True])
+def test_append_and_read_many_rows(fmt, src, Hkv, dh, rows, page, layout, rot, given):
+    """Packed sequences, empty ones among them, and places that belong to none; positions from the slots or given."""
+    lead, tail, B = 5, 9, 7
+    n = rows - lead - tail
+    new = [0, n // 9, 0, 3, n // 2, 0]
+    new.append(n - sum(new))
+    before = [3, 0, 7, 20, 1, 0, 33]
+    unit = page or 16
+    capacity = (max(new) + 40 + unit - 1) // unit * unit
+    case = Case(fmt, B, Hkv, dh, capacity, page)
+    rng = np.random.default_rng(rows)
+    x = rnd(rows, (rows, 2 * Hkv, dh), src).cuda()
+    k, v = x[:, :Hkv], x[:, Hkv:]
+    start = np.concatenate(([0], np.cumsum(new))) + lead
+    seq = np.repeat(np.arange(B), new)
+    slot = np.concatenate([before[b] + np.arange(new[b]) for b in range(B)])
+    rope = Bnd.Rope(rot, capacity, layout=layout) if layout else None
+    pos = rng.integers(0, capacity, rows) if given else None
+    out, old = i32([-1] * B), (case.host(0), case.host(1))
+    Bnd.kv_append(case.cache, case.kv(i32(before), out), k, v, start=i32(start), rope=rope,
+                  pos=None if pos is None else i32(pos), k_scale=case.gk, v_scale=case.gv)
+    lens = [a + b for a, b in zip(before, new)]
+    assert out.tolist() == lens and case.cache.status() == 0
+    raw = case.host(0), case.host(1)
+    for which in (0, 1):
+        np.testing.assert_array_equal(rest(case, old[which], seq, slot).view(np.uint8),
+                                      rest(case, raw[which], seq, slot).view(np.uint8))
+    src_k, src_v = f64(k[lead:lead + n]), f64(v[lead:lead + n])
+    for which, rows_in, g in ((1, src_v, case.gv),) + (() if layout else ((0, src_k, case.gk),)):
+        got = held(case, raw[which], seq, slot)
+        if fmt == "kv4":
+            for a, b in zip(got, R.encode(rows_in, g)):
+                np.testing.assert_array_equal(a, b)
+        else:
+            np.testing.assert_array_equal(got.astype(np.float64), want_rows(case, rows_in, g, fmt))
+    if layout:
+        check_turned(fmt, held(case, raw[0], seq, slot), src_k, slot if pos is None else pos[lead:lead + n], rot, layout,
+                     case.gk)
+    # and back: the same slots, from a place of each sequence on
+    first = [int(b) for b in before]
+    wide = [torch.full((rows, Hkv + 1, dh), 3.0, dtype=DT[src], device="cuda") for _ in "kv"]
+    rk, rv = wide[0][:, 1:], wide[1][:, :Hkv]
+    Bnd.kv_read(case.cache, case.kv(out), rk, rv, start=i32(start), first=i32(first), k_scale=case.gk, v_scale=case.gv)
+    assert case.cache.status() == 0
+    for which, y, g in ((0, rk, case.gk), (1, rv, case.gv)):
+        got = held(case, raw[which], seq, slot)
+        want = R.decode(*got, g) if fmt == "kv4" else got.astype(np.float64)
+        np.testing.assert_array_equal(f64(y[lead:lead + n]), f64(torch.from_numpy(want).float().to(DT[src])))
+        assert (y[:lead] == 3).all() and (y[lead + n:] == 3).all()
+    assert (wide[0][:, 0] == 3).all() and (wide[1][:, Hkv] == 3).all()
