@@ -439,7 +439,9 @@ typedef struct {
   double attn;     /* multiplier of cosine and sine, 0 means 1 */
 } medusa_rope_desc;
 typedef struct medusa_rope medusa_rope;   /* opaque: the table and a status word, on one GPU */
-/* Creates the handle on the current device (allocates, and waits for the table). */
+/* Creates the handle on the current device (allocates, and waits for the table).  Destroying it frees
+ * both, so it comes after every call has ended that was given the handle; a CUDA graph that captured
+ * such calls keeps the addresses, and the handle has to stay until its last replay has ended. */
 medusa_status medusa_rope_create(const medusa_rope_desc* desc, medusa_rope** out);
 void medusa_rope_destroy(medusa_rope* rope);
 /* As medusa_get_status, for the handle's own status word. */
@@ -488,7 +490,9 @@ typedef struct {
   int num_pages;     /* paged: pages in the pool */
   int max_nodes;     /* query rows (tree nodes) per sequence and attention call, 1..MEDUSA_MAX_NODES */
 } medusa_cache_dims;
-typedef struct medusa_cache medusa_cache;   /* opaque: sizes and a status word, on one GPU */
+/* opaque: sizes and a status word, on one GPU.  Calls, and graphs that captured them, keep the status
+ * word's address: destroy the handle after the last of them has ended. */
+typedef struct medusa_cache medusa_cache;
 medusa_status medusa_cache_create(const medusa_cache_dims* dims, medusa_cache** out);
 void medusa_cache_destroy(medusa_cache* cache);
 /* Bytes of the key pool, and of the value pool. */
@@ -557,7 +561,8 @@ typedef struct {
   const int32_t* first;                 /* device [B] or NULL */
 } medusa_kv_places;
 /* Reads slots back (kv->k, v, page_table, len): what the cache holds, rounded once to dtype.
- * Only slots in [0, len[b]) are read; places of other slots are left as they were and set
+ * Only slots in [0, len[b]) are read (a len outside 0..capacity is taken as the nearer end, here and in
+ * medusa_kv4_attention, without a flag); places of other slots are left as they were and set
  * MEDUSA_FLAG_KV_CAPACITY. */
 medusa_status medusa_kv_read(const medusa_cache* cache, const medusa_kv* kv,
                              const medusa_kv_places* places, float k_scale, float v_scale,

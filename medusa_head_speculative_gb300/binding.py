@@ -531,7 +531,8 @@ def _rows(what, x, rows, heads, dh):
 
 
 class Rope:
-    """Owns a medusa_rope: the cosine/sine table of one rotation, on the current device."""
+    """Owns a medusa_rope: the cosine/sine table of one rotation, on the current device.  Keep it as
+    long as CUDA graphs that captured calls with it: they use its memory."""
 
     def __init__(self, rot, max_pos, layout="half", base=10000.0, scaling="plain", factor=1.0,
                  orig_pos=0, low=1.0, high=32.0, attn=1.0):
@@ -585,7 +586,8 @@ def rope_apply(rope, pos, parts, inverse=False, stream=None):
 
 
 class Cache:
-    """Owns a medusa_cache: the sizes and format of a KV cache whose pools the caller holds."""
+    """Owns a medusa_cache: the sizes and format of a KV cache whose pools the caller holds.  Keep it
+    as long as CUDA graphs that captured calls with it: they use its status word."""
 
     def __init__(self, B, Hq, Hkv, dh, format, capacity, page_size=0, num_pages=0, max_nodes=1):
         self.dims = CacheDims(B, Hq, Hkv, dh, format, capacity, page_size, num_pages, max_nodes)

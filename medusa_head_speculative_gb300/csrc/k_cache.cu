@@ -3,11 +3,13 @@
 // section 6: the cache is paged).  Formats and rules: include/medusa.h.
 //
 // Appending: y = rotate(x, position), then y as it is, or of 16 elements s = e4m3(max|y| / (6 g)) and
-// e2m1(y / (g s)) each (kvcache.cuh).  Reading: e2m1 e4m3 g.  A long call is bound by what it moves, a
-// 4-bit append also by some 200 instructions for 16 elements, a short one by the chain of loads that
-// finds a row's place.  Measured: 32,000 rows of 40 heads of 128 bf16 elements, keys (turned) and values,
-// into a 4-bit cache (839 MB, 124 us at copy bandwidth) 214 us, 3.9 TB/s; 98,000 rows of 8 heads read
-// back as bf16 (519 MB, 76 us) 88 us, 5.9 TB/s; one row in each of 16 sequences 3.5 us.
+// e2m1(y / (g s)) each (kvcache.cuh).  Reading: e2m1 e4m3 g.  A long call is bound by what it moves, but
+// for 4-bit appends, which wait for loads: no unit is full (49 % of the issue slots, 27 % of the warps, 53 %
+// of the copy rate), with one task fetched ahead and the angles loaded where they are used.  A short call is
+// bound by the chain of loads that finds a row's place.  Measured: 32,000 rows of 40 heads of 128 bf16
+// elements, keys (turned) and values, into a 4-bit cache (839 MB, 124 us at copy bandwidth) 221 us, 3.8 TB/s;
+// 98,000 rows of 8 heads read back as bf16 (519 MB, 76 us) 89 us, 5.8 TB/s; one row in each of 16 sequences
+// 3.3 us.
 #include "cache.h"
 #include "common.cuh"
 #include "kvcache.cuh"

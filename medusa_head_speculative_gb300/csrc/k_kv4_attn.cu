@@ -137,8 +137,10 @@ template <int N> __device__ __forceinline__ void store_f(bf16* p, const float (&
 }
 
 // One warp finishes a query row: the prefix's (o, reference, sum) from join(m, l, o), the call's own
-// rows the row sees added in float, and the quotient rounded once.  A tree row sees its
-// ancestors only (at most 9), so going through the set bits beats a masked product with all n1.
+// rows the row sees added in float, and the quotient rounded once.  A row of a candidate tree sees its
+// ancestors only (at most 9), so going through the set bits beats a masked product with all n1; a chunk
+// without a mask, whose rows see up to 256, pays for it row by row (8 x 256 rows of 32 heads over 3000
+// slots: 650 us, 133 without the call's own rows).
 // The first four visible rows' keys and values are loaded before join, which waits for loads too.
 template <typename T, int DH, typename Join>
 __device__ __forceinline__ void finish_row(const Kv4Work& w, int b, int node, int hq, Join join) {

@@ -36,7 +36,7 @@
 // before it writes the partial.
 //
 // Measured: 8 sequences x 40 heads x 65 nodes over 2048-4096 slots each (161 MB, 24 us at copy
-// bandwidth) 98 us; 16 x 8 heads x 172 rows over 8192 slots (165 MB; 92 GFLOP, 73 us of tensor time
+// bandwidth) 96 us; 16 x 8 heads x 172 rows over 8192 slots (165 MB; 92 GFLOP, 73 us of tensor time
 // on whole tiles) 139.5 us; 17 us of either for joining.  No single part bounds it: a chunk takes
 // 2000 cycles (two tiles: 3900), with copies and signals alone 1250 (2500), and besides these
 // with only the softmax 1500 (2700), the decoding 1650 (2700) or the MMAs 1650 (3300): the parts

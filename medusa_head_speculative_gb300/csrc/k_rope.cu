@@ -9,7 +9,7 @@
 // Bound by what it moves.  Measured: 16,381 rows of 40 heads of 128 bf16 elements, 64 of them turned
 // (340 MB, 50 us at copy bandwidth) 57 us, 5.9 TB/s; 65 rows of 64 heads 2.1 us (latency).  Units of 16
 // bytes where alignment and rot allow, of 8 for the bf16 rows that allow only these (halves of 36
-// elements, 16,384 rows of 40 heads: 94 us), single elements for the rest (394 us there).
+// elements, 16,384 rows of 40 heads: 98 us), single elements for the rest (394 us there).
 #include "cache.h"
 #include "common.cuh"
 #include "launch.cuh"
