@@ -256,6 +256,9 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
           for (int y = 0; y < PP; ++y)
             if (key0 + (DH == 128 ? 8 * y : 16 * y) >= valid) cw[y][0] = cw[y][1] = cw[y][2] = cw[y][3] = sc[y] = 0u;
         }
+        // the reads above come before the copy engine's next write there: an arrival alone does not order
+        // the two proxies, and now and then a late read found the next chunk's codes
+        fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(TB_LE + st));
         const int NS = part ? SV : SK, stage = i % NS, turn = i / NS;

@@ -399,3 +399,37 @@ def test_append_and_read_many_rows(fmt, src, Hkv, dh, rows, page, layout, rot, g
         np.testing.assert_array_equal(f64(y[lead:lead + n]), f64(torch.from_numpy(want).float().to(DT[src])))
         assert (y[:lead] == 3).all() and (y[lead + n:] == 3).all()
     assert (wide[0][:, 0] == 3).all() and (wide[1][:, Hkv] == 3).all()
+
+
+# ------------------------------------------------------------------ calls at the same time
+@pytest.mark.parametrize("dtype,Hq,Hkv,dh,n1,page", [
+    ("bf16", 8, 8, 128, 20, 0), ("bf16", 8, 8, 128, 43, 256), ("bf16", 8, 8, 128, 100, 0), ("bf16", 8, 8, 64, 65, 0),
+    ("bf16", 32, 8, 128, 43, 0), ("bf16", 8, 8, 64, 150, 48), ("bf16", 32, 8, 128, 1, 0), ("f32", 8, 8, 128, 9, 0),
+])
+def test_series_on_two_streams_repeat_bit_for_bit(dtype, Hq, Hkv, dh, n1, page):
+    """Series of calls on two streams, each with its own workspace and result: blocks of one kernel start where
+    those of another end, and staged codes wait for their readers.  The same bits every time."""
+    B, capacity = 33, 9216
+    rng = np.random.default_rng(1)
+    lens = [int(rng.choice([0, 1, 9000, rng.integers(0, 9000), rng.integers(0, 70) * 128])) for _ in range(B)]
+    case = Case("kv4", B, Hkv, dh, capacity, page, Hq=Hq, max_nodes=n1)
+    for pool in case.pool:                             # any codes, scales from 0.5 to 1.875
+        scales = pool.view(-1, 9 * dh)[:, 8 * dh:]
+        scales.copy_(torch.randint(0x30, 0x40, scales.shape, dtype=torch.uint8, device="cuda"))
+    q = rnd(1, (B, n1, Hq, dh), dtype).cuda()
+    kv = case.kv(i32(lens))
+    calls = 12 if q.numel() * q.element_size() < 1 << 25 else 6
+    ws = [torch.empty(case.cache.workspace_size, dtype=torch.uint8, device="cuda") for _ in range(calls)]
+    o = [torch.empty_like(q) for _ in range(calls)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    want = None
+    for _ in range(300 if dtype == "bf16" else 60):
+        for i in range(calls):
+            Bnd.kv4_attention(case.cache, kv, q, o[i], ws[i], k_scale=case.gk, v_scale=case.gv, stream=streams[i % 2])
+        torch.cuda.synchronize()
+        if want is None:
+            want = o[0].clone()
+            assert torch.isfinite(want.float()).all()
+        assert all(torch.equal(x, want) for x in o)
+    assert case.cache.status() == 0
