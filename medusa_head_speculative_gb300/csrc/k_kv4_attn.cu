@@ -521,7 +521,8 @@ __global__ void __launch_bounds__(KD_WARPS * 32, KD_CTAS<NR>) kv4_rows_kernel(co
           }
         }
       }
-      __syncwarp();                          // every lane has read the stage
+      fence_proxy_async();                   // every lane has read the stage before the copy engine writes there
+      __syncwarp();
       copy_next();
     }
     // ---- join the warps' partials and write the CTA's: everybody on one reference, then the
