@@ -137,6 +137,21 @@ __device__ __forceinline__ void kt_st32(uint32_t taddr, const uint32_t (&v)[32])
       "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
       : "memory");
 }
+// 16 columns of this thread's TMEM lane.  Load and wait are one statement: nothing else keeps the compiler from
+// using a register between them.
+__device__ __forceinline__ void kt_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void kt_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -563,7 +578,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
 #pragma unroll 1
                 for (int x = 0; x < DH; x += 16) {
                   float v[16];
-                  tmem_ld16(ocol + x, v);
+                  kt_ld16(ocol + x, v);
 #pragma unroll
                   for (int e = 0; e < 16; ++e) v[e] *= f;
                   tmem_st16(ocol + x, v);
@@ -606,7 +621,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
 #pragma unroll 2
           for (int x = 0; x < DH; x += 16) {
             float v[16];
-            tmem_ld16(ocol + x, v);
+            kt_ld16(ocol + x, v);
             store_rows(dst - (lane & 3) * DH + x, w.R - (gr - (lane & 3)), v);
           }
           if (row_ok) w.part_ml[prow] = make_float2(m_use, l_acc);
@@ -636,9 +651,9 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_tree_kernel(const __grid_co
 #pragma unroll 2
           for (int x = 0; x < DH; x += 16) {
             float v0[16], v1[16];
-            tmem_ld16(ocol + x, v0);
+            kt_ld16(ocol + x, v0);
             if (nj1 > 0) {
-              tmem_ld16(ocol1 + x, v1);            // written by this block's P V of slot 1
+              kt_ld16(ocol1 + x, v1);            // written by this block's P V of slot 1
             } else {
 #pragma unroll
               for (int e = 0; e < 16; ++e) v1[e] = 0.f;
