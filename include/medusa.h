@@ -591,7 +591,7 @@ typedef struct {
   const void* tree_k;
   const void* tree_v;
   const uint32_t* mask;                 /* device [n1][8] or NULL */
-  float scale;                          /* 0: 1/sqrt(dh) */
+  float scale;                          /* 0: 1/sqrt(dh); at most 1e38 */
   float k_scale, v_scale;
 } medusa_kv4_query;
 medusa_status medusa_kv4_attention(const medusa_cache* cache, const medusa_kv* kv,

@@ -370,7 +370,7 @@ medusa_status medusa_kv4_attention(const medusa_cache* c, const medusa_kv* kv, c
   if ((s = check_scales(c, q->k_scale, q->v_scale)) != MEDUSA_OK) return s;
   if (!q->q || !q->o || !is_dtype(q->dtype) || q->n1 < 1 || q->n1 > c->d.max_nodes) return MEDUSA_ERR_INVALID;
   if (!q->tree_k != !q->tree_v || (q->mask && !q->tree_k)) return MEDUSA_ERR_INVALID;
-  if (!std::isfinite(q->scale) || q->scale < 0) return MEDUSA_ERR_INVALID;
+  if (!(q->scale >= 0 && q->scale <= 1e38f)) return MEDUSA_ERR_INVALID;        // times log2(e) it stays a float
   const long long n = 16 / (long long)elem(q->dtype);
   if (!aligned(q->q, 16) || !aligned(q->o, 16) || !aligned(q->tree_k, 16) || !aligned(q->tree_v, 16))
     return MEDUSA_ERR_INVALID;

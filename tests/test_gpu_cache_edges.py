@@ -97,6 +97,22 @@ def test_attention_factors_outside_a_float(qgain, scale, g, kvgain, kind, n1, dt
         assert (np.abs(got - w) <= attn_bound(dtype, w, spread, reach, dh, n + n1, vmax)).all()
 
 
+def test_attention_scales_at_the_end_of_a_float():
+    """scale * log2(e) past a float's range made scores of 0 NaN: such scales are refused, the largest others work."""
+    case = Case("kv4", 1, 1, 64, 16, max_nodes=1)
+    case.fill([0])
+    q = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    t, o = rnd(1, q.shape, "bf16").cuda(), torch.empty_like(q)
+    ws = torch.empty(case.cache.workspace_size, dtype=torch.uint8, device="cuda")
+    kv = case.kv(i32([0]))
+    for scale in (3e38, -1.0, float("nan"), float("inf")):
+        with pytest.raises(Bnd.MedusaError) as e:
+            Bnd.kv4_attention(case.cache, kv, q, o, ws, tree_k=t, tree_v=t, scale=scale)
+        assert e.value.code == Bnd.MEDUSA_ERR_INVALID
+    Bnd.kv4_attention(case.cache, kv, q, o, ws, tree_k=t, tree_v=t, scale=1e38)
+    assert torch.equal(o, t)                           # one row seen, with a score of 0
+
+
 # ------------------------------------------------------------------ waits that run out
 @pytest.mark.parametrize("dtype,Hq,Hkv,dh,n1,capacity,page", [
     ("bf16", 4, 4, 128, 1, 512, 16), ("f32", 4, 2, 64, 9, 512, 0),         # few rows, short caches
