@@ -598,6 +598,90 @@ medusa_status medusa_kv4_attention(const medusa_cache* cache, const medusa_kv* k
                                    const medusa_kv4_query* query, void* workspace,
                                    size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------ attention over a shared prefix */
+/* Attention for a batch whose B sequences begin with the same tokens (instructions, a document): the
+ * shared keys and values lie once, in a cache of one sequence, and are read once for all queries.  Row n
+ * of sequence b, query head h attends, with key/value head h / (Hq/Hkv), to the slots [0, len[0]) of
+ * `shared`, the slots [0, len[b]) of its own in `own` and, where tree_k is given, to the call's rows j
+ * that n sees: bit j of mask row n (medusa_tree_build's mask), or j <= n without a mask.
+ *   o = sum_j p_j v_j,  p = softmax(scale q . k_j)
+ * Keys are taken as they lie in the caches: a sequence's own tokens follow the prefix, so that rotated keys
+ * have been turned by positions that count from the prefix's first token (medusa_kv_rows.pos).
+ *   own, shared: caches of one format, MEDUSA_F32 or MEDUSA_BF16, and of equal Hq, Hkv, dh on one GPU;
+ *   shared of one sequence, each contiguous or paged; the query's n1 at most own's max_nodes
+ *   q, o, tree_k, tree_v: as in medusa_kv4_query, of the caches' dtype (k_scale and v_scale are not read)
+ * A length outside 0..capacity is taken as the nearer end.  A page outside the pool is read as page 0 and
+ * sets MEDUSA_FLAG_PAGE_RANGE in its cache's status; an expired wait sets MEDUSA_FLAG_TIMEOUT in own's.  A
+ * row that sees nothing gives zeros, one that sees an infinity or a NaN gives infinities or NaN.  Slots from
+ * the lengths on and rows that are not seen may hold anything.  Calls that may run at the same time need
+ * workspaces of their own.
+ * Scores, softmax statistics and sums are 32 bits wide; with MEDUSA_BF16 probabilities keep 8 bits. */
+/* Bytes of device workspace (256-byte aligned) for calls with these caches; 0 where they do not fit. */
+size_t medusa_prefix_workspace_size(const medusa_cache* own, const medusa_cache* shared);
+medusa_status medusa_prefix_attention(const medusa_cache* own, const medusa_kv* own_kv,
+                                      const medusa_cache* shared, const medusa_kv* shared_kv,
+                                      const medusa_kv4_query* query, void* workspace, size_t ws_bytes,
+                                      void* stream);
+
+/* ------------------------------------------------------------------ projections in 8 bits */
+/* Matrix products of rows and weights held in 8 bits, for the projections of a layer and for
+ * feed-forward blocks.  An element is an e4m3 code times a float scale: rows [rows][k] have one scale for
+ * each 128 consecutive elements ([rows][ceil(k/128)]), weights [n][k] one for each 128 x 128 block
+ * ([ceil(n/128)][ceil(k/128)]); the last groups and blocks may be shorter.
+ * Rounding takes s = 2^e with the smallest whole e >= -126 for which max|x| <= 448 * 2^e over the group
+ * or block (s = 1 where all are zero), and the nearest code to x / s, ties to even.  A group or block that
+ * holds an infinity or a NaN becomes NaN with s = 1 and sets MEDUSA_FLAG_NONFINITE. */
+typedef struct {
+  int n, k;       /* weights [n][k]: k inputs (a multiple of 16), n outputs */
+  int max_rows;   /* rows of a call at most */
+  int gated;      /* 1: the handle also takes pairs of weights (medusa_fp8_product.up) */
+} medusa_fp8_dims;
+/* opaque: sizes and a status word, on one GPU; as medusa_cache, destroy it after the last call or replay. */
+typedef struct medusa_fp8 medusa_fp8;
+/* MEDUSA_ERR_UNSUPPORTED past n = 2^24, k = 2^20, max_rows = 2^24 or 2^38 elements a matrix. */
+medusa_status medusa_fp8_create(const medusa_fp8_dims* dims, medusa_fp8** out);
+void medusa_fp8_destroy(medusa_fp8* h);
+/* Bytes of device workspace medusa_fp8_linear needs (256-byte aligned). */
+size_t medusa_fp8_workspace_size(const medusa_fp8* h);
+/* As medusa_get_status, for the handle's own status word. */
+medusa_status medusa_fp8_get_status(const medusa_fp8* h, void* stream, uint32_t* flags);
+/* Rounds x [rows][k] (element e of row r at x[r * x_row + e], dtype MEDUSA_F32 or MEDUSA_BF16) to
+ * codes [rows][k] (4-byte aligned) and scales.  block = 1: rows, 0 <= rows <= max_rows; block = 128: weights, rows = n. */
+medusa_status medusa_fp8_round(const medusa_fp8* h, const void* x, int dtype, int rows, long long x_row,
+                               void* codes, float* scales, int block, void* stream);
+/* Codes and scales back to y [rows][k] (row stride y_row >= k): code * scale, rounded once to dtype. */
+medusa_status medusa_fp8_read(const medusa_fp8* h, const void* codes, const float* scales, int rows, int block,
+                              void* y, int dtype, long long y_row, void* stream);
+enum { MEDUSA_E4M3 = 3 };
+/* y = x w^T (+ add), or with `up` y = silu(x w^T) * (x up^T), silu(a) = a / (1 + e^-a).
+ *   x: [rows][k], row stride x_row; MEDUSA_E4M3 codes with x_scales (16-byte aligned, x_row a multiple of
+ *      16), or MEDUSA_F32 / MEDUSA_BF16 elements, which are rounded as above on the way
+ *   w, up: codes [n][k], 16-byte aligned; w_scales, up_scales: any finite scales whose products with a
+ *      row's are finite
+ *   add: NULL or [rows][n] of y's dtype, row stride add_row; y itself with equal strides, or apart from it
+ *   y: [rows][n], MEDUSA_F32 or MEDUSA_BF16, row stride y_row >= n
+ * The products of 128 elements are summed in float on the tensor cores, scaled, and added up in float;
+ * the result is rounded once.  rows = 0 does nothing.  Calls that may run at the same time need
+ * workspaces of their own. */
+typedef struct {
+  const void* x;
+  int x_dtype;
+  const float* x_scales;
+  long long x_row;
+  int rows;
+  const void* w;
+  const float* w_scales;
+  const void* up;
+  const float* up_scales;
+  const void* add;
+  long long add_row;
+  void* y;
+  int y_dtype;
+  long long y_row;
+} medusa_fp8_product;
+medusa_status medusa_fp8_linear(const medusa_fp8* h, const medusa_fp8_product* p, void* workspace,
+                                size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -17,7 +17,7 @@ LIB_PATH = os.path.join(_HERE, "libmedusa.so")
 
 MEDUSA_OK, MEDUSA_ERR_INVALID, MEDUSA_ERR_UNSUPPORTED = 0, -1, -2
 MEDUSA_ERR_CUDA, MEDUSA_ERR_DEVICE, MEDUSA_ERR_WORKSPACE = -3, -4, -6
-F32, BF16, KV4 = 0, 1, 2
+F32, BF16, KV4, E4M3 = 0, 1, 2, 3
 GREEDY, TYPICAL, REJECT = 0, 1, 2
 MAX_HEADS, MAX_TOPS, MAX_NODES = 8, 16, 256
 FLAG_TOKEN_RANGE, FLAG_KV_CAPACITY, FLAG_PAGE_RANGE, FLAG_NONFINITE, FLAG_TIMEOUT = 1, 2, 4, 8, 16
@@ -104,6 +104,17 @@ class KV4Query(C.Structure):
                 ("v_scale", C.c_float)]
 
 
+class Fp8Dims(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("n", "k", "max_rows", "gated")]
+
+
+class Fp8Product(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("x_dtype", C.c_int), ("x_scales", C.c_void_p), ("x_row", C.c_longlong),
+                ("rows", C.c_int), ("w", C.c_void_p), ("w_scales", C.c_void_p), ("up", C.c_void_p),
+                ("up_scales", C.c_void_p), ("add", C.c_void_p), ("add_row", C.c_longlong),
+                ("y", C.c_void_p), ("y_dtype", C.c_int), ("y_row", C.c_longlong)]
+
+
 _lib = None
 P = C.c_void_p
 SZ = C.c_size_t
@@ -166,6 +177,15 @@ def lib():
         "medusa_kv_append": (I, [P, C.POINTER(KV), C.POINTER(KVRows), P, C.c_float, C.c_float, P]),
         "medusa_kv_read": (I, [P, C.POINTER(KV), C.POINTER(KVPlaces), C.c_float, C.c_float, P]),
         "medusa_kv4_attention": (I, [P, C.POINTER(KV), C.POINTER(KV4Query), P, SZ, P]),
+        "medusa_prefix_workspace_size": (SZ, [P, P]),
+        "medusa_prefix_attention": (I, [P, C.POINTER(KV), P, C.POINTER(KV), C.POINTER(KV4Query), P, SZ, P]),
+        "medusa_fp8_create": (I, [C.POINTER(Fp8Dims), C.POINTER(P)]),
+        "medusa_fp8_destroy": (None, [P]),
+        "medusa_fp8_workspace_size": (SZ, [P]),
+        "medusa_fp8_get_status": (I, [P, P, C.POINTER(C.c_uint32)]),
+        "medusa_fp8_round": (I, [P, P, I, I, C.c_longlong, P, P, I, P]),
+        "medusa_fp8_read": (I, [P, P, P, I, I, P, I, C.c_longlong, P]),
+        "medusa_fp8_linear": (I, [P, C.POINTER(Fp8Product), P, SZ, P]),
     }
     for name, (res, args) in sigs.items():
         f = getattr(L, name)
@@ -669,10 +689,8 @@ def kv_read(cache, kv, k, v, start=None, per_seq=None, count=None, first=None, k
            lib().medusa_kv_read(cache.handle, kv, r, k_scale, v_scale, _stream(stream)))
 
 
-def kv4_attention(cache, kv, q, o, ws, tree_k=None, tree_v=None, mask=None, scale=0.0, k_scale=1.0,
-                  v_scale=1.0, stream=None):
-    """medusa_kv4_attention: q, o [B][n1][Hq][dh] (rows evenly spaced), tree_k, tree_v
-    [B][n1][Hkv][dh] contiguous or None, mask int32 [n1][8] or None."""
+def _query(cache, q, o, ws, tree_k, tree_v, mask, scale, k_scale, v_scale):
+    """The checked medusa_kv4_query of an attention call."""
     shape = q.shape
     if len(shape) != 4 or shape[0] != cache.B or shape[2] != cache.Hq or shape[3] != cache.dh or o.shape != shape:
         raise ValueError(f"q, o: [{cache.B}][n1][{cache.Hq}][{cache.dh}] is needed, got {tuple(shape)}, "
@@ -692,9 +710,142 @@ def kv4_attention(cache, kv, q, o, ws, tree_k=None, tree_v=None, mask=None, scal
     for t in (tree_k, tree_v):
         if t is not None and (t.shape != (B, n1, cache.Hkv, cache.dh) or not t.is_contiguous()):
             raise ValueError(f"tree_k, tree_v: contiguous [{B}][{n1}][{cache.Hkv}][{cache.dh}] is needed")
-    a = KV4Query(q.data_ptr(), o.data_ptr(), _dtype(q), n1, qs[at], qs[2], os_[at], os_[2],
-                 None if tree_k is None else tree_k.data_ptr(), None if tree_v is None else tree_v.data_ptr(),
-                 _ints("mask", mask, 8 * n1, device), scale, k_scale, v_scale)
+    return KV4Query(q.data_ptr(), o.data_ptr(), _dtype(q), n1, qs[at], qs[2], os_[at], os_[2],
+                    None if tree_k is None else tree_k.data_ptr(), None if tree_v is None else tree_v.data_ptr(),
+                    _ints("mask", mask, 8 * n1, device), scale, k_scale, v_scale)
+
+
+def kv4_attention(cache, kv, q, o, ws, tree_k=None, tree_v=None, mask=None, scale=0.0, k_scale=1.0,
+                  v_scale=1.0, stream=None):
+    """medusa_kv4_attention: q, o [B][n1][Hq][dh] (rows evenly spaced), tree_k, tree_v
+    [B][n1][Hkv][dh] contiguous or None, mask int32 [n1][8] or None."""
+    a = _query(cache, q, o, ws, tree_k, tree_v, mask, scale, k_scale, v_scale)
     _check("medusa_kv4_attention",
            lib().medusa_kv4_attention(cache.handle, kv, a, ws.data_ptr(), ws.numel() * ws.element_size(),
                                       _stream(stream)))
+
+
+def prefix_workspace_size(own, shared):
+    """medusa_prefix_workspace_size: bytes for prefix_attention with these caches."""
+    return lib().medusa_prefix_workspace_size(own.handle, shared.handle)
+
+
+def prefix_attention(own, own_kv, shared, shared_kv, q, o, ws, tree_k=None, tree_v=None, mask=None, scale=0.0,
+                     stream=None):
+    """medusa_prefix_attention: `own` and `shared` (one sequence) are Caches of q's dtype, the rest as in
+    kv4_attention."""
+    if shared.device != own.device:
+        raise ValueError(f"caches on one device are needed, got cuda:{own.device}, cuda:{shared.device}")
+    a = _query(own, q, o, ws, tree_k, tree_v, mask, scale, 1.0, 1.0)
+    _check("medusa_prefix_attention",
+           lib().medusa_prefix_attention(own.handle, own_kv, shared.handle, shared_kv, a, ws.data_ptr(),
+                                         ws.numel() * ws.element_size(), _stream(stream)))
+
+
+# ------------------------------------------------------------------ projections in 8 bits
+class Fp8:
+    """Owns a medusa_fp8: the sizes of weights [n][k] held in 8 bits and of the rows they are multiplied
+    with.  Keep it as long as CUDA graphs that captured calls with it: they use its status word."""
+
+    def __init__(self, n, k, max_rows, gated=False):
+        self.dims = Fp8Dims(n, k, max_rows, 1 if gated else 0)
+        out = P()
+        _check("medusa_fp8_create", lib().medusa_fp8_create(C.byref(self.dims), C.byref(out)))
+        self.handle, self.device = out, _device()
+        self.n, self.k, self.kb, self.nb = n, k, (k + 127) // 128, (n + 127) // 128
+        self.workspace_size = lib().medusa_fp8_workspace_size(out)
+
+    def status(self, stream=None):
+        return _status("medusa_fp8_get_status", self.handle, stream)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            lib().medusa_fp8_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+_CODES = _FLOAT = None
+
+
+def _codes(what, h, t, s, rows, block, strides=False):
+    """Checks codes t [rows][k] and their scales s on the handle's device; the codes' row stride."""
+    global _CODES, _FLOAT
+    if _CODES is None:
+        import torch
+        _CODES, _FLOAT = (torch.float8_e4m3fn, torch.uint8), torch.float32
+    if t.dtype not in _CODES or s.dtype is not _FLOAT:
+        raise TypeError(f"{what}: float8_e4m3fn (or uint8) codes and float32 scales are needed, got {t.dtype}, {s.dtype}")
+    shape = (rows, h.k)
+    if t.shape != shape or not (t.is_contiguous() or (strides and t.stride(1) == 1)):
+        raise ValueError(f"{what}: codes [{rows}][{h.k}] in order are needed, got {tuple(t.shape)}, strides {t.stride()}")
+    if s.shape != (-(-rows // block), h.kb) or not s.is_contiguous():
+        raise ValueError(f"{what}: contiguous scales [{-(-rows // block)}][{h.kb}] are needed, got {tuple(s.shape)}")
+    if t.get_device() != h.device or s.get_device() != h.device:
+        _elsewhere(h, t, s)
+    return t.stride(0)
+
+
+def _matrix(what, h, t, cols):
+    """Checks t [rows][cols] with elements in order on the handle's device; its row stride."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or shape[1] != cols or (strides[1] != 1 and cols > 1):
+        raise ValueError(f"{what}: [rows][{cols}] with elements in order is needed, got {tuple(shape)}, strides {strides}")
+    if t.get_device() != h.device:
+        _elsewhere(h, t)
+    return strides[0]
+
+
+def fp8_round(h, x, codes, scales, block=1, stream=None):
+    """medusa_fp8_round: x [rows][k] (any row stride) to contiguous codes [rows][k] and scales
+    [ceil(rows / block)][ceil(k / 128)]; block 1 (rows) or 128 (weights)."""
+    row = _matrix("x", h, x, h.k)
+    rows = x.shape[0]
+    _codes("codes", h, codes, scales, rows, block)
+    _check("medusa_fp8_round",
+           lib().medusa_fp8_round(h.handle, x.data_ptr(), _dtype(x), rows, row, codes.data_ptr(), scales.data_ptr(),
+                                  block, _stream(stream)))
+
+
+def fp8_read(h, codes, scales, y, block=1, stream=None):
+    """medusa_fp8_read: codes and scales, as fp8_round leaves them, to y [rows][k] (any row stride)."""
+    row = _matrix("y", h, y, h.k)
+    rows = y.shape[0]
+    _codes("codes", h, codes, scales, rows, block)
+    _check("medusa_fp8_read",
+           lib().medusa_fp8_read(h.handle, codes.data_ptr(), scales.data_ptr(), rows, block, y.data_ptr(), _dtype(y),
+                                 row, _stream(stream)))
+
+
+def fp8_linear(h, x, w, w_scales, y, ws, x_scales=None, up=None, up_scales=None, add=None, stream=None):
+    """medusa_fp8_linear: y = x w^T (+ add), or with `up` silu(x w^T) * (x up^T).  x [rows][k] is float32,
+    bfloat16, or codes with x_scales; w, up contiguous codes [n][k]; y, add [rows][n] of one dtype."""
+    rows = x.shape[0]
+    if x_scales is None:
+        x_dtype, x_row = _dtype(x), _matrix("x", h, x, h.k)
+    else:
+        x_dtype, x_row = E4M3, _codes("x", h, x, x_scales, rows, 1, strides=True)
+    _codes("w", h, w, w_scales, h.n, 128)
+    if (up is None) != (up_scales is None):
+        raise ValueError("up and up_scales go together")
+    if up is not None:
+        _codes("up", h, up, up_scales, h.n, 128)
+    y_row, add_row = _matrix("y", h, y, h.n), 0
+    if y.shape[0] != rows:
+        raise ValueError(f"y: {rows} rows are needed, got {y.shape[0]}")
+    if add is not None:
+        _same(y, add)
+        add_row = _matrix("add", h, add, h.n)
+        if add.shape[0] != rows:
+            raise ValueError(f"add: {rows} rows are needed, got {add.shape[0]}")
+    if ws.get_device() != h.device or not ws.is_contiguous():
+        raise ValueError("ws: a contiguous tensor on the handle's device is needed")
+    p = Fp8Product(x.data_ptr(), x_dtype, ptr(x_scales), x_row, rows, w.data_ptr(), w_scales.data_ptr(), ptr(up),
+                   ptr(up_scales), ptr(add), add_row, y.data_ptr(), _dtype(y), y_row)
+    _check("medusa_fp8_linear",
+           lib().medusa_fp8_linear(h.handle, p, ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)))

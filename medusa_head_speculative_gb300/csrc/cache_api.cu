@@ -6,9 +6,11 @@
 #include <cmath>
 #include <new>
 
+#include "api.h"
 #include "cache.h"
 #include "common.cuh"
 #include "launch.cuh"
+#include "prefix.h"
 
 using namespace medusa;
 
@@ -28,38 +30,6 @@ struct medusa_cache {
 };
 
 namespace {
-
-inline cudaStream_t S(void* s) { return reinterpret_cast<cudaStream_t>(s); }
-bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
-size_t elem(int dtype) { return dtype == MEDUSA_F32 ? 4 : 2; }
-bool is_dtype(int t) { return t == MEDUSA_F32 || t == MEDUSA_BF16; }
-// A handle's memory lives on the device that was current when it was made.
-bool here(int device) {
-  int d = -1;
-  return cudaGetDevice(&d) == cudaSuccess && d == device;
-}
-// Whether no two of rows x heads pieces of dh elements, row and head elements apart, share an element: results
-// that lie on one another would be written in any order.
-bool lie_apart(long long rows, long long row, long long heads, long long head, int dh) {
-  if ((rows > 1 && row < dh) || (heads > 1 && head < dh)) return false;
-  if (rows <= 1 || heads <= 1) return true;
-  if (row >= (__int128)(heads - 1) * head + dh || head >= (__int128)(rows - 1) * row + dh) return true;
-  for (long long i = 1; i < heads; ++i) {          // neither within the other's gaps: piece by piece
-    const __int128 at = (__int128)i * head, j = at / row;
-    if ((j < rows && at - j * row < dh) || (j + 1 < rows && (j + 1) * row - at < dh)) return false;
-  }
-  return true;
-}
-medusa_status done(cudaError_t e) { return e == cudaSuccess ? MEDUSA_OK : MEDUSA_ERR_CUDA; }
-
-medusa_status read_status(uint32_t* word, void* stream, uint32_t* flags) {
-  uint32_t v = 0;
-  if (cudaMemcpyAsync(&v, word, sizeof(v), cudaMemcpyDeviceToHost, S(stream)) != cudaSuccess ||
-      cudaMemsetAsync(word, 0, sizeof(v), S(stream)) != cudaSuccess || cudaStreamSynchronize(S(stream)) != cudaSuccess)
-    return MEDUSA_ERR_CUDA;
-  *flags = v;
-  return v ? MEDUSA_ERR_DEVICE : MEDUSA_OK;
-}
 
 bool finite_pos(double x) { return x > 0 && std::isfinite(x); }
 
@@ -153,6 +123,21 @@ CacheView view_of(const medusa_cache* c, const medusa_kv* kv, float gk, float gv
   v.gv = gv;
   v.status = c->status;
   return v;
+}
+
+// what both attentions ask of a query
+medusa_status check_query(const medusa_cache* c, const medusa_kv4_query* q) {
+  if (!q->q || !q->o || !is_dtype(q->dtype) || q->n1 < 1 || q->n1 > c->d.max_nodes) return MEDUSA_ERR_INVALID;
+  if (!q->tree_k != !q->tree_v || (q->mask && !q->tree_k)) return MEDUSA_ERR_INVALID;
+  if (!(q->scale >= 0 && q->scale <= 1e38f)) return MEDUSA_ERR_INVALID;        // times log2(e) it stays a float
+  const long long n = 16 / (long long)elem(q->dtype);
+  if (!aligned(q->q, 16) || !aligned(q->o, 16) || !aligned(q->tree_k, 16) || !aligned(q->tree_v, 16))
+    return MEDUSA_ERR_INVALID;
+  if (q->q_row < 0 || q->q_head < 0 || q->o_row < 0 || q->o_head < 0 || q->q_row % n || q->q_head % n ||
+      q->o_row % n || q->o_head % n)
+    return MEDUSA_ERR_INVALID;
+  if (!lie_apart((long long)c->d.B * q->n1, q->o_row, c->d.Hq, q->o_head, c->d.dh)) return MEDUSA_ERR_INVALID;
+  return MEDUSA_OK;
 }
 
 // rows, start, per_seq, count of medusa_kv_rows and medusa_kv_places
@@ -368,16 +353,7 @@ medusa_status medusa_kv4_attention(const medusa_cache* c, const medusa_kv* kv, c
   medusa_status s = check_kv(c, kv, false);
   if (s != MEDUSA_OK) return s;
   if ((s = check_scales(c, q->k_scale, q->v_scale)) != MEDUSA_OK) return s;
-  if (!q->q || !q->o || !is_dtype(q->dtype) || q->n1 < 1 || q->n1 > c->d.max_nodes) return MEDUSA_ERR_INVALID;
-  if (!q->tree_k != !q->tree_v || (q->mask && !q->tree_k)) return MEDUSA_ERR_INVALID;
-  if (!(q->scale >= 0 && q->scale <= 1e38f)) return MEDUSA_ERR_INVALID;        // times log2(e) it stays a float
-  const long long n = 16 / (long long)elem(q->dtype);
-  if (!aligned(q->q, 16) || !aligned(q->o, 16) || !aligned(q->tree_k, 16) || !aligned(q->tree_v, 16))
-    return MEDUSA_ERR_INVALID;
-  if (q->q_row < 0 || q->q_head < 0 || q->o_row < 0 || q->o_head < 0 || q->q_row % n || q->q_head % n ||
-      q->o_row % n || q->o_head % n)
-    return MEDUSA_ERR_INVALID;
-  if (!lie_apart((long long)c->d.B * q->n1, q->o_row, c->d.Hq, q->o_head, c->d.dh)) return MEDUSA_ERR_INVALID;
+  if ((s = check_query(c, q)) != MEDUSA_OK) return s;
   if (!ws || ws_bytes < c->ws_bytes || !aligned(ws, 256)) return MEDUSA_ERR_WORKSPACE;
   Kv4AttnArgs a{};
   a.c = view_of(c, kv, q->k_scale, q->v_scale);
@@ -402,6 +378,53 @@ medusa_status medusa_kv4_attention(const medusa_cache* c, const medusa_kv* kv, c
   }
   if (c->test_wait_ns.load(std::memory_order_relaxed)) a.test_wait_ns = c->test_wait_ns.exchange(0);
   return done(launch_kv4_attention(a, q->dtype, ws, c->num_sms, S(stream)));
+}
+
+// Whether a call may join the two caches.
+static bool caches_fit(const medusa_cache* own, const medusa_cache* shared) {
+  return own && shared && own->device == shared->device && own->d.format == shared->d.format && shared->d.B == 1 &&
+         own->d.Hq == shared->d.Hq && own->d.Hkv == shared->d.Hkv && own->d.dh == shared->d.dh;
+}
+// Rows of all sequences together stay below 2^31, as do the joining kernel's blocks.
+static bool prefix_rows_fit(const medusa_cache* own) {
+  return (double)own->d.B * own->d.Hq * own->d.max_nodes < 2147483648.0;
+}
+
+size_t medusa_prefix_workspace_size(const medusa_cache* own, const medusa_cache* shared) {
+  if (!caches_fit(own, shared) || !is_dtype(own->d.format) || !prefix_rows_fit(own)) return 0;
+  return prefix_workspace(own->d.B, own->d.Hq, own->d.Hkv, own->d.dh, own->d.max_nodes, own->num_sms);
+}
+
+medusa_status medusa_prefix_attention(const medusa_cache* own, const medusa_kv* own_kv, const medusa_cache* shared,
+                                      const medusa_kv* shared_kv, const medusa_kv4_query* q, void* ws, size_t ws_bytes,
+                                      void* stream) {
+  EntryScope scope("medusa_prefix_attention");
+  if (!own || !shared || !q || !caches_fit(own, shared) || !here(own->device)) return MEDUSA_ERR_INVALID;
+  if (!is_dtype(own->d.format) || !prefix_rows_fit(own)) return MEDUSA_ERR_UNSUPPORTED;
+  medusa_status s = check_kv(own, own_kv, false);
+  if (s != MEDUSA_OK) return s;
+  if ((s = check_kv(shared, shared_kv, false)) != MEDUSA_OK) return s;
+  if ((s = check_query(own, q)) != MEDUSA_OK) return s;
+  if (q->dtype != own->d.format) return MEDUSA_ERR_INVALID;
+  if (!ws || ws_bytes < medusa_prefix_workspace_size(own, shared) || !aligned(ws, 256)) return MEDUSA_ERR_WORKSPACE;
+  PrefixArgs a{};
+  a.own = view_of(own, own_kv, 1.f, 1.f);
+  a.shared = view_of(shared, shared_kv, 1.f, 1.f);
+  a.q = q->q;
+  a.o = q->o;
+  a.q_row = q->q_row;
+  a.q_head = q->q_head;
+  a.o_row = q->o_row;
+  a.o_head = q->o_head;
+  a.tk = q->tree_k;
+  a.tv = q->tree_v;
+  a.mask = q->mask;
+  a.n1 = q->n1;
+  a.Hq = own->d.Hq;
+  a.G = own->d.Hq / own->d.Hkv;
+  a.scale2 = (q->scale > 0 ? q->scale : 1.0f / std::sqrt((float)own->d.dh)) * 1.4426950408889634f;
+  a.status = own->status;
+  return done(launch_prefix_attention(a, q->dtype, ws, own->num_sms, S(stream)));
 }
 
 }  // extern "C"

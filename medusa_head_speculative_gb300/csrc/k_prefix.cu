@@ -1,0 +1,338 @@
+// Attention of a batch whose sequences share a prefix ("Medusa: Simple LLM Inference Acceleration Framework
+// with Multiple Decoding Heads" §3.4 Tree Attention, Steps 3 and 5, with the common part of the prefixes
+// held once): the kernel for float rows and small heads, on the CUDA cores, and the joining kernel.
+//
+// A CTA has 64 query rows; of a chunk of 128 keys it takes two halves of 64 through shared memory in float.
+// A thread has 4 rows x 4 keys of the scores and 4 rows x dh/16 columns of o; a row's 64 scores lie in 16
+// lanes, which share its running maximum m and sum l: o = sum 2^(s - m) v, l = sum 2^(s - m), s in base-2
+// units.
+#include <algorithm>
+
+#include "launch.cuh"
+#include "prefix.cuh"
+#include "tc_ptx.cuh"
+
+namespace medusa {
+
+constexpr int PS_ROWS = 64, PS_KEYS = 64;
+
+__device__ __forceinline__ bool nonfinite(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
+
+template <typename T, int DH>
+__global__ void __launch_bounds__(256) prefix_simt_kernel(PxWork w) {
+  constexpr int P = DH + 4, C = DH / 16;
+  extern __shared__ float sm[];
+  float* Qs = sm;                                 // [64][DH + 4]
+  float* Ks = Qs + PS_ROWS * P;                   // [64][DH + 4]
+  float* Vs = Ks + PS_KEYS * P;                   // [64][DH]
+  float* Ps = Vs + PS_KEYS * DH;                  // [64][64 + 4]
+  __shared__ uint32_t s_bad[2];                   // keys whose value holds an infinity or a NaN
+  pdl_trigger();
+  pdl_wait();
+  const PrefixArgs& a = w.a;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const PxPlan plan = px_plan(w, blockIdx.x == 0 && tid < 32);
+  PxWalk walk = px_start(w, plan, blockIdx.x);
+  const bool shared = walk.shared;
+  const CacheView& c = shared ? a.shared : a.own;
+  PxSeg s;
+  while (px_next(w, walk, s)) {
+    const int b = shared ? 0 : s.b, len = clamp_len(c, c.len[b]), prefix_chunks = (len + PX_KEYS - 1) / PX_KEYS;
+    __syncthreads();
+    for (int e = tid; e < PS_ROWS * DH; e += 256) {
+      const PxRow x = px_row(w, shared, s, e / DH);
+      Qs[e / DH * P + e % DH] = x.ok ? to_f32(static_cast<const T*>(a.q)[x.node_row * a.q_row + x.head * a.q_head + e % DH]) : 0.f;
+    }
+    float o[4][C] = {}, m[4], l[4] = {};
+    PxRow row[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = -INFINITY;
+      row[i] = px_row(w, shared, s, ty + 16 * i);
+    }
+    for (int jj = 2 * s.j; jj < 2 * (s.j + s.n); ++jj) {
+      const bool tree = jj / 2 >= prefix_chunks;
+      const int t0 = tree ? jj * PS_KEYS - prefix_chunks * PX_KEYS : jj * PS_KEYS, end = tree ? a.n1 : len;
+      if (t0 >= end) continue;
+      __syncthreads();
+      if (tid < 2) s_bad[tid] = 0;
+      __syncthreads();
+      for (int e = tid; e < PS_KEYS * DH; e += 256) {
+        const int j = e / DH, i = e - j * DH, t = t0 + j;
+        float kx = 0.f, vx = 0.f;
+        if (t < end) {
+          if (tree) {
+            const long at = (((long)b * a.n1 + t) * c.Hkv + s.g) * DH + i;
+            kx = to_f32(static_cast<const T*>(a.tk)[at]);
+            vx = to_f32(static_cast<const T*>(a.tv)[at]);
+            if (nonfinite(vx)) {                  // not every row sees it: 0, and a NaN sum for those that do
+              vx = 0.f;
+              atomicOr(&s_bad[j >> 5], 1u << (j & 31));
+            }
+          } else {
+            long unit;
+            int in;
+            if (!unit_of(c, b, t, unit, in)) {
+              set_flag(c.status, MEDUSA_FLAG_PAGE_RANGE);
+              unit = 0;
+            }
+            const long at = plain_offset(c, unit, in, s.g) + i;
+            kx = to_f32(static_cast<const T*>(c.k)[at]);
+            vx = to_f32(static_cast<const T*>(c.v)[at]);
+          }
+        }
+        Ks[j * P + i] = kx;
+        Vs[j * DH + i] = vx;
+      }
+      __syncthreads();
+      float p[4][4] = {};
+#pragma unroll 4
+      for (int i = 0; i < DH; i += 4) {
+        float4 q[4], k[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          q[u] = *reinterpret_cast<const float4*>(Qs + (ty + 16 * u) * P + i);
+          k[u] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * u) * P + i);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            p[u][v] = fmaf(q[u].x, k[v].x, fmaf(q[u].y, k[v].y, fmaf(q[u].z, k[v].z, fmaf(q[u].w, k[v].w, p[u][v]))));
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        uint32_t see[2] = {0xffffffffu, 0xffffffffu};
+        if (tree && row[u].ok)
+          for (int i = 0; i < 2; ++i) see[i] = px_sees(a, row[u].n, (t0 >> 5) + i);
+        float mx = -INFINITY;
+        bool bad = false;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int j = tx + 16 * v;
+          const bool seen = row[u].ok && t0 + j < end && ((see[j >> 5] >> (j & 31)) & 1u);
+          p[u][v] = seen ? p[u][v] * a.scale2 : -INFINITY;
+          bad |= seen && ((s_bad[j >> 5] >> (j & 31)) & 1u);
+          mx = fmaxf(mx, p[u][v]);
+        }
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        const float top = fmaxf(m[u], mx), ref = top == -INFINITY ? 0.f : top;
+        const float f = m[u] == -INFINITY ? 0.f : exp2f(m[u] - ref);
+        float sum = bad ? NAN : 0.f;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float x = exp2f(p[u][v] - ref);
+          sum += x;
+          Ps[(ty + 16 * u) * 68 + tx + 16 * v] = x;
+        }
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        l[u] = l[u] * f + sum;
+        m[u] = top;
+#pragma unroll
+        for (int i = 0; i < C; ++i) o[u][i] *= f;
+      }
+      __syncwarp();                               // a row's probabilities are read by its own 16 lanes
+      for (int j = 0; j < PS_KEYS; j += 4) {
+        float pr[4][4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float4 x = *reinterpret_cast<const float4*>(Ps + (ty + 16 * u) * 68 + j);
+          pr[u][0] = x.x;
+          pr[u][1] = x.y;
+          pr[u][2] = x.z;
+          pr[u][3] = x.w;
+        }
+#pragma unroll
+        for (int jj2 = 0; jj2 < 4; ++jj2) {
+          float v[C];
+#pragma unroll
+          for (int i = 0; i < C; i += 2) {
+            const float2 x = *reinterpret_cast<const float2*>(Vs + (j + jj2) * DH + tx * 2 + 16 * i);
+            v[i] = x.x;
+            v[i + 1] = x.y;
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int i = 0; i < C; ++i) o[u][i] = fmaf(pr[u][jj2], v[i], o[u][i]);
+        }
+      }
+    }
+    const int rb = shared ? w.rbs : w.rbo;
+    float* po = shared ? w.o_s : w.o_o;
+    float2* pml = shared ? w.ml_s : w.ml_o;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = ty + 16 * u;
+      if (!row[u].ok) continue;
+      const long at = s.slot * rb + r;
+#pragma unroll
+      for (int i = 0; i < C; i += 2)
+        *reinterpret_cast<float2*>(po + at * DH + tx * 2 + 16 * i) = make_float2(o[u][i], o[u][i + 1]);
+      if (tx == 0) pml[at] = make_float2(l[u] != l[u] && m[u] == -INFINITY ? 0.f : m[u], l[u]);
+    }
+  }
+}
+
+// One warp per (sequence, node, query head): o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the row's
+// partials, M the largest m_s; a lane has VPL columns.  A row's partials are those of the CTAs that its
+// item's chunks lie in: with W chunks over C CTAs chunk x is CTA ceil((x + 1) C / W) - 1's.
+template <typename T, int VPL>
+__global__ void __launch_bounds__(256) prefix_join_kernel(PxWork w) {
+  constexpr int SB = 4;
+  pdl_trigger();
+  pdl_wait();
+  const PrefixArgs& a = w.a;
+  const long i = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (i >= (long)w.rows * a.own.Hkv) return;
+  const int lane = threadIdx.x & 31;
+  const int gr = (int)(i / a.own.Hkv), g = (int)(i - (long)gr * a.own.Hkv);       // row of head g over all sequences
+  const int b = gr / w.R, r = gr - b * w.R, node = gr / a.G, head = g * a.G + gr - node * a.G;
+  const PxPlan p = *w.plan;
+  auto cta = [](long x, long n, long total) { return (((x + 1) * n + total - 1) / total) - 1; };
+  float M = -INFINITY, L = 0.f, acc[VPL] = {};
+  for (int kind = 0; kind < 2; ++kind) {
+    long slot, rb, row;
+    int n;
+    if (kind == 0) {
+      if (p.ns == 0) continue;
+      const int rbi = gr / w.rbs, item = g * w.nrbs + rbi;
+      const long x = (long)item * p.ns, c0 = cta(x, p.cs, p.ws);
+      n = (int)(cta(x + p.ns - 1, p.cs, p.ws) - c0) + 1;
+      slot = c0 + item;
+      rb = w.rbs;
+      row = gr - rbi * w.rbs;
+    } else {
+      const int nb = px_chunks(w, b);
+      if (nb == 0) continue;
+      const int rbi = r / w.rbo, per = a.own.Hkv * w.nrbo, item = g * w.nrbo + rbi;
+      const long x = w.first[b] * per + (long)item * nb, c0 = cta(x, p.co, p.wo);
+      n = (int)(cta(x + nb - 1, p.co, p.wo) - c0) + 1;
+      slot = c0 + (long)b * per + item;
+      rb = w.rbo;
+      row = r - rbi * w.rbo;
+    }
+    const float* po = kind == 0 ? w.o_s : w.o_o;
+    const float2* pml = kind == 0 ? w.ml_s : w.ml_o;
+    for (int s0 = 0; s0 < n; s0 += SB) {
+      float2 ml[SB];
+      float v[SB][VPL];
+#pragma unroll
+      for (int u = 0; u < SB; ++u) {
+        ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int e = 0; e < VPL; ++e) v[u][e] = 0.f;
+        if (s0 + u < n) {
+          const long at = (slot + s0 + u) * rb + row;
+          ml[u] = pml[at];
+          const float* src = po + at * (32 * VPL) + lane * VPL;
+          if constexpr (VPL == 4) {
+            const float4 t = *reinterpret_cast<const float4*>(src);
+            v[u][0] = t.x;
+            v[u][1] = t.y;
+            v[u][2] = t.z;
+            v[u][3] = t.w;
+          } else if constexpr (VPL == 2) {
+            const float2 t = *reinterpret_cast<const float2*>(src);
+            v[u][0] = t.x;
+            v[u][1] = t.y;
+          } else {
+            v[u][0] = src[0];
+          }
+        }
+      }
+      float top = M;
+#pragma unroll
+      for (int u = 0; u < SB; ++u) top = fmaxf(top, ml[u].x);
+      if (top == -INFINITY) continue;             // nothing seen so far
+      const float f = M == -INFINITY ? 0.f : exp2f(M - top);
+      L *= f;
+#pragma unroll
+      for (int e = 0; e < VPL; ++e) acc[e] *= f;
+      M = top;
+#pragma unroll
+      for (int u = 0; u < SB; ++u) {
+        if (ml[u].x == -INFINITY) continue;
+        const float x = exp2f(ml[u].x - M);
+        L += x * ml[u].y;
+#pragma unroll
+        for (int e = 0; e < VPL; ++e) acc[e] += x * v[u][e];
+      }
+    }
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;     // (a NaN sum stays one)
+  T* dst = static_cast<T*>(a.o) + (long)node * a.o_row + (long)head * a.o_head + lane * VPL;
+#pragma unroll
+  for (int e = 0; e < VPL; ++e) dst[e] = from_f32<T>(L == 0.f ? 0.f : acc[e] * inv);
+}
+
+// ------------------------------------------------------------------ host side
+// Rows of a block: 64 here, on the tensor cores a tile of 128 rows or two.
+static void row_blocks(bool tc, int R, int* rb, int* nrb) {
+  const int most = !tc ? PS_ROWS : R > 128 ? 256 : 128;
+  *rb = std::min(R, most);
+  *nrb = (R + most - 1) / most;
+}
+static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+static int max_ctas(int num_sms) { return std::max(2, num_sms); }
+
+size_t prefix_workspace(int B, int Hq, int Hkv, int dh, int max_nodes, int num_sms) {
+  // slots of a kind: its items and a CTA's each; items' blocks together: their rows, and a block over
+  const size_t G = Hq / Hkv, R = (size_t)max_nodes * G, C = max_ctas(num_sms);
+  const size_t rbo = std::min<size_t>(R, 256), rbs = std::min<size_t>((size_t)B * R, 256);
+  const size_t own = (size_t)B * Hkv * (R + rbo) + C * rbo, shared = Hkv * ((size_t)B * R + rbs) + C * rbs;
+  return up256(sizeof(PxPlan)) + up256(B * sizeof(long)) + up256(own * dh * 4) + up256(own * 8) +
+         up256(shared * dh * 4) + up256(shared * 8);
+}
+
+template <typename T, int DH> static cudaError_t simt_go(const PxWork& w, cudaStream_t st) {
+  const size_t smem = (size_t)(2 * PS_ROWS * (DH + 4) + PS_KEYS * DH + PS_ROWS * 68) * sizeof(float);
+  const cudaError_t e = cudaFuncSetAttribute(prefix_simt_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(prefix_simt_kernel<T, DH>, dim3(w.ctas), dim3(256), smem, st, 1, w);
+}
+template <typename T> static cudaError_t prefix_go(const PxWork& w, bool tc, int num_sms, cudaStream_t st) {
+  cudaError_t e;
+  const int dh = w.a.own.dh;
+  if (tc) e = launch_prefix_tc(w, num_sms, st);
+  else if (dh == 32) e = simt_go<T, 32>(w, st);
+  else if (dh == 64) e = simt_go<T, 64>(w, st);
+  else e = simt_go<T, 128>(w, st);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)(((long)w.rows * w.a.own.Hkv + 7) / 8));
+  if (dh == 32) return launch_kernel(prefix_join_kernel<T, 1>, grid, dim3(256), 0, st, 1, w);
+  if (dh == 64) return launch_kernel(prefix_join_kernel<T, 2>, grid, dim3(256), 0, st, 1, w);
+  return launch_kernel(prefix_join_kernel<T, 4>, grid, dim3(256), 0, st, 1, w);
+}
+
+cudaError_t launch_prefix_attention(const PrefixArgs& a, int dtype, void* ws, int num_sms, cudaStream_t st) {
+  const bool tc = prefix_tc_takes(dtype, a.own.dh);
+  PxWork w{};
+  w.a = a;
+  w.R = a.n1 * a.G;
+  w.rows = a.own.B * w.R;
+  row_blocks(tc, w.rows, &w.rbs, &w.nrbs);
+  row_blocks(tc, w.R, &w.rbo, &w.nrbo);
+  w.cost_s = w.cost_o = 1;
+  w.tree = a.tk ? (a.n1 + PX_KEYS - 1) / PX_KEYS : 0;
+  w.ctas = max_ctas(num_sms);
+  char* p = static_cast<char*>(ws);
+  auto take = [&](size_t bytes) {
+    char* at = p;
+    p += up256(bytes);
+    return at;
+  };
+  w.plan = reinterpret_cast<PxPlan*>(take(sizeof(PxPlan)));
+  w.first = reinterpret_cast<long*>(take(a.own.B * sizeof(long)));
+  const size_t so = ((size_t)a.own.B * a.own.Hkv * w.nrbo + w.ctas) * w.rbo;
+  const size_t ss = ((size_t)a.own.Hkv * w.nrbs + w.ctas) * w.rbs;
+  w.o_o = reinterpret_cast<float*>(take(so * a.own.dh * 4));
+  w.ml_o = reinterpret_cast<float2*>(take(so * 8));
+  w.o_s = reinterpret_cast<float*>(take(ss * a.own.dh * 4));
+  w.ml_s = reinterpret_cast<float2*>(take(ss * 8));
+  return dtype == MEDUSA_F32 ? prefix_go<float>(w, tc, num_sms, st) : prefix_go<bf16>(w, tc, num_sms, st);
+}
+
+}  // namespace medusa
