@@ -1,84 +1,442 @@
-// Products of rows and weights in 8 bits (the format of include/medusa.h):
-//   y[r][n] = sum_j xs[r][j] ws[n / 128][j] sum_{k in group j} x[r][k] w[n][k]   (+ add), or the gated pair.
-// Codes are decoded to shared memory; a thread has 4 x 4 results of a 64 x 64 tile.
+// Products of rows and weights in 8 bits (the format of include/medusa.h) on the tcgen05 tensor cores:
+//   y[r][n] = sum_j xs[r][j] ws[n / 128][j] sum_{k in group j} x[r][k] w[n][k]   (+ add), or the gated pair
+// silu(x w^T) (x up^T).
+//
+// A group's scales differ from the next one's, so tensor memory can hold the sum of one group only: the sums
+// of a group of 128 (4 MMAs of 32, kind::f8f6f4, float) go to one of two accumulators, and while the next
+// group is multiplied, promoting warps read it and add scale times sum to their registers.  Rows are the
+// MMA's M (128, a thread's row is its TMEM lane, so that a scale is one number a thread), weight rows its N:
+// BN = 256 or 128 columns; a gated tile has 128 columns of either matrix.
+//
+//   warp 0 (one lane)  copies: rows and weights of a group, 128 bytes a row, through a ring of stages
+//   warp 1 (one lane)  MMAs
+//   warps 4-7, 8-11    promote half the columns each, then write y (or a partial)
+//
+// One CTA per SM.  The work is dealt out by groups: whole tiles while there is one for every CTA, the tiles
+// that are left (with few rows: all) as an even share of their groups in one line, so that weights stream
+// evenly over the SMs; a CTA that has a part of a tile's groups writes a partial of its own, and a second
+// kernel adds a tile's partials up in order and finishes it.
+//
+// Every wait is bounded; on expiry MEDUSA_FLAG_TIMEOUT is set, the CTA stops taking work, drains the copies
+// it issued and frees its tensor memory.
+#include <algorithm>
+
 #include "fp8.cuh"
 #include "launch.cuh"
+#include "tc_ptx.cuh"
+#include "tma_host.h"
 
 namespace medusa {
 
-constexpr int LT = 64, LP = kFp8Group + 4;
+constexpr int FL_THREADS = 384, FL_MAXST = 8;
+constexpr uint32_t FL_ROW = 128;                    // bytes of a row in a stage
+// Registers a thread: 168 at launch (384 x 168 = 64512), then 56 for copies and MMAs and 216 to promote:
+// 56 + 2 x 216 = 488 <= 3 x 168.
+constexpr int FL_REG_ISSUE = 56, FL_REG_PROMOTE = 216;
 
-template <typename T, int NW>
-__global__ void __launch_bounds__(256) fp8_linear_kernel(Fp8LinearArgs a) {
-  extern __shared__ float sm[];
-  float* xs = sm;                                  // [64][132]
-  float* wt = sm + LT * LP;
-  pdl_trigger();
-  pdl_wait();
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int n0 = blockIdx.x * LT;
-  const long r0 = (long)blockIdx.y * LT;
-  float acc[NW][4][4] = {};
-  for (int j = 0; j < a.kb; ++j) {
-    const int kn = min(kFp8Group, a.k - j * kFp8Group);
-    for (int h = 0; h < NW; ++h) {
-      __syncthreads();
-      for (int e = tid; e < LT * 32; e += 256) {
-        const int r = e / 32, c = e % 32 * 4;
-        float v[4] = {};
-        if (h == 0) {
-          if (r0 + r < a.rows && c < kn) fp8_values(*reinterpret_cast<const uint32_t*>(a.x + (r0 + r) * a.x_row + j * kFp8Group + c), v);
-          *reinterpret_cast<float4*>(xs + r * LP + c) = make_float4(v[0], v[1], v[2], v[3]);
+struct FlArgs {
+  CUtensorMap tx, tw[2];                            // rows: box {128, abox}; weights: box {128, 128}
+  Fp8LinearArgs a;
+  int abox, stages;                                 // rows of a copy (a multiple of 8), ring depth
+  int mt, nt;                                       // tiles
+  int whole, ctas;                                  // tiles taken whole, CTAs
+  int shares;                                       // CTAs that share the groups of the other tiles
+  float* part;                                      // [slot][128][BN]
+  int rows_last;                                    // weights are read once (mt == 1)
+};
+
+enum { FB_FULL = 0, FB_EMPTY = FL_MAXST, FB_TF = 2 * FL_MAXST, FB_TE = FB_TF + 2, FB_END = FB_TE + 2, FB_COUNT = FB_END + 1 };
+
+__device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor, kind::f8f6f4: fp32 D, e4m3 A and B, both K-major, M x N.
+constexpr uint32_t idesc_e4m3(int M, int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24); }
+
+// One stretch of a tile's groups: j .. j + n - 1.
+struct FlSeg {
+  int m, n0, j, n;                                  // tile row, first weight row
+  long slot;                                        // partial; < 0: the whole tile
+};
+struct FlWalk {
+  int tile;                                         // of the whole ones
+  long w, w1;                                       // groups of the others
+};
+template <int OC> __device__ __forceinline__ FlWalk fl_start(const FlArgs& g) {
+  const long total = (long)(g.mt * g.nt - g.whole) * g.a.kb;
+  if ((int)blockIdx.x >= g.shares) return {(int)blockIdx.x, 0, 0};
+  return {(int)blockIdx.x, total * blockIdx.x / g.shares, total * (blockIdx.x + 1) / g.shares};
+}
+template <int OC> __device__ __forceinline__ bool fl_next(const FlArgs& g, FlWalk& k, FlSeg& s) {
+  int t;
+  if (k.tile < g.whole) {
+    t = k.tile;
+    k.tile += g.ctas;
+    s.j = 0;
+    s.n = g.a.kb;
+    s.slot = -1;
+  } else {
+    if (k.w >= k.w1) return false;
+    const int i = (int)(k.w / g.a.kb);
+    t = g.whole + i;
+    s.j = (int)(k.w - (long)i * g.a.kb);
+    s.n = (int)min((long)(g.a.kb - s.j), k.w1 - k.w);
+    s.slot = s.n == g.a.kb ? -1 : (long)blockIdx.x + i;
+    k.w += s.n;
+  }
+  s.m = t % g.mt;                                   // neighbours share weights
+  s.n0 = t / g.mt * OC;
+  return true;
+}
+
+__device__ __forceinline__ float2 fma2(float2 v, float2 s, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&v)), "l"(*reinterpret_cast<uint64_t*>(&s)), "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&r);
+}
+
+// Four results (columns n .. n + 3 of row r): the gated product or the residual, and the store.
+template <typename T, bool GATED>
+__device__ __forceinline__ void fl_finish4(const Fp8LinearArgs& a, long r, int n, float (&y)[4], const float (&u)[4], bool vec) {
+  if (n >= a.n) return;
+  const int there = min(4, a.n - n);
+  T* dst = static_cast<T*>(a.y) + r * a.y_row + n;
+  if (GATED) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = y[e] / (1.f + expf(-y[e])) * u[e];
+  } else if (a.add) {
+    const T* src = static_cast<const T*>(a.add) + r * a.add_row + n;
+    float x[4] = {};
+    if (there == 4) load4(src, vec, x);
+    else
+      for (int e = 0; e < there; ++e) x[e] = to_f32(src[e]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] += x[e];
+  }
+  if (there == 4) save4(dst, vec, y);
+  else
+    for (int e = 0; e < there; ++e) dst[e] = from_f32<T>(y[e]);
+}
+template <typename T> __device__ __forceinline__ bool fl_vec(const Fp8LinearArgs& a) {
+  const uintptr_t n = 4 * sizeof(T);
+  return (uintptr_t)a.y % n == 0 && a.y_row % 4 == 0 && (uintptr_t)a.add % n == 0 && a.add_row % 4 == 0;
+}
+
+template <typename T, int BN, bool GATED>
+__global__ void __launch_bounds__(FL_THREADS, 1) fp8_linear_kernel(const __grid_constant__ FlArgs g) {
+  constexpr int OC = GATED ? BN / 2 : BN;            // results of a tile's row
+  constexpr int HC = BN / 2;                         // columns a promoting thread adds up
+  constexpr uint32_t WB = BN * FL_ROW;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t bars[FB_COUNT];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int s_issued, s_waited, s_abort;
+  const Fp8LinearArgs& a = g.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, ST = g.stages;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t ws = base, xs = base + ST * WB;     // the rows' ring comes last: an MMA reads 128 rows from a stage
+  const uint32_t xb = g.abox * FL_ROW;               // of abox, and what lies behind goes to lanes that no row has
+  const uint32_t bar0 = smem_u32(bars);
+  auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(bar(FB_FULL + i), 1);
+      mbar_init(bar(FB_EMPTY + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(FB_TF + i), 1);
+      mbar_init(bar(FB_TE + i), 8);
+    }
+    mbar_init(bar(FB_END), 1);
+    s_issued = s_waited = s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc(smem_u32(&tmem_slot), 2 * BN);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_trigger();                          // only once this CTA holds its TMEM
+  const uint32_t tmem = tmem_slot;
+  bool timed_out = false;
+  auto aborted = [&]() { return *(volatile int*)&s_abort != 0; };
+  FlWalk walk = fl_start<OC>(g);
+  FlSeg s;
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FL_REG_ISSUE));
+    if (warp == 0 && lane == 0) {
+      // ------------------------------------------------------------ copies
+      const uint64_t pol_w = g.rows_last ? policy_evict_first() : policy_evict_last(), pol_x = policy_evict_last();
+      // weights are written by no kernel of this call: the first stages' go out before the wait for the rows
+      FlWalk ahead = walk;
+      int pre = 0, c = 0;
+      auto load_w = [&](const FlSeg& q, int j, int st) {
+        mbar_expect_tx(bar(FB_FULL + st), WB + xb);
+#pragma unroll
+        for (int h = 0; h < BN / 128; ++h)
+          tma_load_2d(ws + st * WB + h * 128 * FL_ROW, GATED ? &g.tw[h] : &g.tw[0], j * 128, GATED ? q.n0 : q.n0 + 128 * h,
+                      bar(FB_FULL + st), pol_w);
+      };
+      while (pre < ST && fl_next<OC>(g, ahead, s))
+        for (int i = 0; i < s.n && pre < ST; ++i) load_w(s, s.j + i, pre++);
+      s_issued = pre;
+      pdl_wait();
+      while (!timed_out && fl_next<OC>(g, walk, s)) {
+        for (int i = 0; i < s.n; ++i, ++c) {
+          const int st = c % ST;
+          if (c >= pre) {
+            if (!mbar_wait(bar(FB_EMPTY + st), ((c / ST) & 1) ^ 1, TC_TIMEOUT_NS)) { timed_out = true; break; }
+            load_w(s, s.j + i, st);
+            s_issued = c + 1;
+          }
+          tma_load_2d(xs + st * xb, &g.tx, (s.j + i) * 128, s.m * 128, bar(FB_FULL + st), pol_x);
         }
-        float u[4] = {};
-        if (n0 + r < a.n && c < kn) fp8_values(*reinterpret_cast<const uint32_t*>(a.w[h] + (long)(n0 + r) * a.k + j * kFp8Group + c), u);
-        *reinterpret_cast<float4*>(wt + r * LP + c) = make_float4(u[0], u[1], u[2], u[3]);
+        if (aborted()) break;
       }
-      __syncthreads();
-      float p[4][4] = {};
-      for (int c = 0; c < kn; c += 4)
+      for (; c < pre; ++c)                           // (left early) a stage's weights are in flight: let it fill
+        tma_load_2d(xs + (c % ST) * xb, &g.tx, 0, 0, bar(FB_FULL + c % ST), pol_x);
+    } else if (warp == 1 && lane == 0) {
+      // ------------------------------------------------------------ MMAs
+      const uint32_t idesc = idesc_e4m3(128, BN);
+      int c = 0;
+      while (!timed_out && fl_next<OC>(g, walk, s)) {
+        for (int i = 0; i < s.n; ++i, ++c) {
+          const int st = c % ST, buf = c & 1;
+          if (!mbar_wait(bar(FB_FULL + st), (c / ST) & 1, TC_TIMEOUT_NS)) { timed_out = true; break; }
+          s_waited = c + 1;
+          if (!mbar_wait(bar(FB_TE + buf), ((c >> 1) & 1) ^ 1, TC_TIMEOUT_NS)) { timed_out = true; break; }
+          tc_fence_after();
+          const uint64_t da = sw128_desc(xs + st * xb), db = sw128_desc(ws + st * WB);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 x = *reinterpret_cast<const float4*>(xs + (ty + 16 * i) * LP + c);
+          for (int q = 0; q < 4; ++q) umma_e4m3(tmem + buf * BN, da + 2 * q, db + 2 * q, idesc, q > 0);
+          umma_commit(bar(FB_EMPTY + st));
+          umma_commit(bar(FB_TF + buf));
+        }
+        if (aborted()) break;
+      }
+      umma_commit(bar(FB_END));                      // arrives once every MMA issued above is done
+    }
+  } else {
+    // -------------------------------------------------------------- promote
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FL_REG_PROMOTE));
+    const int half = (warp >> 2) - 1, wl = warp & 3;
+    // columns of this thread: HC from half * HC on, or (gated) HC / 2 of either matrix
+    const uint32_t lanes = tmem + ((uint32_t)(wl * 32) << 16);
+    pdl_wait();
+    int c = 0;
+    while (!timed_out && fl_next<OC>(g, walk, s)) {
+      const long r = (long)s.m * 128 + wl * 32 + lane;
+      const bool live = (long)s.m * 128 + wl * 32 < a.rows, ok = r < a.rows;
+      const int nb0 = GATED || BN == 128 ? s.n0 / 128 : min(s.n0 / 128 + half, (a.n - 1) / 128);
+      const float* px = a.xs + min(r, (long)a.rows - 1) * a.kb + s.j;
+      const float* pw = a.ws[0] + (long)nb0 * a.kb + s.j;
+      const float* pu = GATED ? a.ws[1] + (long)nb0 * a.kb + s.j : pw;
+      float2 acc[HC / 2];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float4 w = *reinterpret_cast<const float4*>(wt + (tx + 16 * q) * LP + c);
-            p[i][q] = fmaf(x.x, w.x, fmaf(x.y, w.y, fmaf(x.z, w.z, fmaf(x.w, w.w, p[i][q]))));
+      for (int i = 0; i < HC / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+      constexpr int AHEAD = 3;                       // groups whose scales are in flight
+      float fx[AHEAD], fw[AHEAD], fu[AHEAD];
+      if (live) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+          const int j = min(i, s.n - 1);
+          fx[i] = px[j];
+          fw[i] = pw[j];
+          fu[i] = GATED ? pu[j] : 0.f;
+        }
+      }
+      for (int i = 0; i < s.n; ++i, ++c) {
+        const int buf = c & 1;
+        const bool got = __all_sync(0xffffffffu, mbar_wait(bar(FB_TF + buf), (c >> 1) & 1, TC_TIMEOUT_NS));
+        if (!got) { timed_out = true; break; }
+        tc_fence_after();
+        if (live) {
+          const float s0 = fx[0] * fw[0], s1 = GATED ? fx[0] * fu[0] : s0;
+#pragma unroll
+          for (int q = 0; q + 1 < AHEAD; ++q) {
+            fx[q] = fx[q + 1];
+            fw[q] = fw[q + 1];
+            fu[q] = fu[q + 1];
+          }
+          const int j = min(i + AHEAD, s.n - 1);
+          fx[AHEAD - 1] = px[j];
+          fw[AHEAD - 1] = pw[j];
+          if (GATED) fu[AHEAD - 1] = pu[j];
+#pragma unroll
+          for (int q = 0; q < HC / 64; ++q) {
+            // gated: 64 columns of the first matrix, then 64 of the second
+            const uint32_t col = buf * BN + (GATED ? q * 128 + half * 64 : half * HC + q * 64);
+            float v[64];
+            tmem_ld64(lanes + col, v);
+            const float sc = GATED && q == 1 ? s1 : s0;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              acc[q * 32 + e] = fma2(make_float2(v[2 * e], v[2 * e + 1]), make_float2(sc, sc), acc[q * 32 + e]);
           }
         }
-      const float sw = a.ws[h][(long)(n0 / kFp8Group) * a.kb + j];
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(FB_TE + buf));
+      }
+      if (timed_out || !live) continue;
+      if (s.slot >= 0) {
+        if (ok) {
+          float* dst = g.part + (s.slot * 128 + wl * 32 + lane) * BN;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const long r = r0 + ty + 16 * i;
-        const float s = r < a.rows ? a.xs[r * a.kb + j] * sw : 0.f;
+          for (int q = 0; q < HC / 64; ++q)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[h][i][q] = fmaf(p[i][q], s, acc[h][i][q]);
+            for (int e = 0; e < 64; e += 4)
+              *reinterpret_cast<float4*>(dst + (GATED ? q * 128 + half * 64 : half * HC + q * 64) + e) =
+                  make_float4(acc[q * 32 + e / 2].x, acc[q * 32 + e / 2].y, acc[q * 32 + e / 2 + 1].x, acc[q * 32 + e / 2 + 1].y);
+        }
+      } else if (ok) {
+        const bool vec = fl_vec<T>(a);
+        constexpr int N = GATED ? 64 : HC;
+#pragma unroll
+        for (int e = 0; e < N; e += 4) {
+          float y[4] = {acc[e / 2].x, acc[e / 2].y, acc[e / 2 + 1].x, acc[e / 2 + 1].y}, u[4] = {};
+          if (GATED) {
+            u[0] = acc[32 + e / 2].x;
+            u[1] = acc[32 + e / 2].y;
+            u[2] = acc[32 + e / 2 + 1].x;
+            u[3] = acc[32 + e / 2 + 1].y;
+          }
+          fl_finish4<T, GATED>(a, r, s.n0 + half * N + e, y, u, vec);
+        }
       }
     }
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const long r = r0 + ty + 16 * i;
-      const int n = n0 + tx + 16 * q;
-      if (r >= a.rows || n >= a.n) continue;
-      float y = acc[0][i][q];
-      if (NW == 2) y = y / (1.f + expf(-y)) * acc[NW - 1][i][q];
-      if (a.add) y += to_f32(static_cast<const T*>(a.add)[r * a.add_row + n]);
-      static_cast<T*>(a.y)[r * a.y_row + n] = from_f32<T>(y);
-    }
+  if (timed_out) {
+    set_flag(a.status, MEDUSA_FLAG_TIMEOUT);
+    *(volatile int*)&s_abort = 1;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0) {
+    // every MMA done, then the copies issued but never waited for (bounded)
+    mbar_wait(bar(FB_END), 0, TC_TIMEOUT_NS);
+    for (int c = s_waited; c < s_issued; ++c) mbar_wait(bar(FB_FULL + c % ST), (c / ST) & 1, TC_TIMEOUT_NS / 16);
+  }
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, 2 * BN);
 }
 
-template <typename T, int NW> static cudaError_t linear_go(const Fp8LinearArgs& a, cudaStream_t st) {
-  const size_t smem = 2 * LT * LP * sizeof(float);
-  const cudaError_t e = cudaFuncSetAttribute(fp8_linear_kernel<T, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  return launch_kernel(fp8_linear_kernel<T, NW>, dim3((a.n + LT - 1) / LT, (a.rows + LT - 1) / LT), dim3(256), smem, st, 1, a);
+// Adds up the partials of the tiles that several CTAs had a part of: with W groups over C CTAs group x is
+// CTA ceil((x + 1) C / W) - 1's.  A thread has four results of a row.
+template <typename T, int BN, bool GATED>
+__global__ void __launch_bounds__(256) fp8_join_kernel(const __grid_constant__ FlArgs g) {
+  constexpr int OC = GATED ? BN / 2 : BN, Q = OC / 4, SB = 4;
+  pdl_trigger();
+  const Fp8LinearArgs& a = g.a;
+  const int i = blockIdx.x, t = g.whole + i, m = t % g.mt, n0 = t / g.mt * OC;
+  const long total = (long)(g.mt * g.nt - g.whole) * a.kb, x = (long)i * a.kb;
+  auto cta = [&](long w) { return ((w + 1) * g.shares + total - 1) / total - 1; };
+  const long c0 = cta(x), c1 = cta(x + a.kb - 1);
+  const int e = blockIdx.y * 256 + threadIdx.x, row = e / Q, col = (e - row * Q) * 4;
+  const long r = (long)m * 128 + row;
+  pdl_wait();
+  if (c0 == c1 || row >= 128 || r >= a.rows) return;
+  const float* src = g.part + ((c0 + i) * 128 + row) * BN + col;
+  float y[4] = {}, u[4] = {};
+  for (long c = c0; c <= c1; c += SB) {
+    float4 p[SB], q[SB];
+#pragma unroll
+    for (int b = 0; b < SB; ++b) {
+      p[b] = q[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c + b <= c1) {
+        p[b] = *reinterpret_cast<const float4*>(src + (c + b - c0) * 128 * BN);
+        if (GATED) q[b] = *reinterpret_cast<const float4*>(src + (c + b - c0) * 128 * BN + 128);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < SB; ++b) {
+      y[0] += p[b].x;
+      y[1] += p[b].y;
+      y[2] += p[b].z;
+      y[3] += p[b].w;
+      u[0] += q[b].x;
+      u[1] += q[b].y;
+      u[2] += q[b].z;
+      u[3] += q[b].w;
+    }
+  }
+  fl_finish4<T, GATED>(a, r, n0 + col, y, u, fl_vec<T>(a));
 }
+
+// ------------------------------------------------------------------ host side
+static bool make_map(CUtensorMap* map, const void* p, long k, long rows, long row, int box) {
+  auto fn = tma_encode();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)row};
+  const cuuint32_t boxes[2] = {128, (cuuint32_t)box}, step[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, strides, boxes, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How a call of `rows` rows is cut up.
+struct FlPlan {
+  int bn, mt, nt, whole, ctas, shares;
+};
+static FlPlan fl_plan(int rows, int n, int kb, bool gated, int num_sms) {
+  FlPlan p;
+  p.mt = (rows + 127) / 128;
+  p.bn = gated || p.mt > 1 ? 256 : 128;
+  const int oc = gated ? 128 : p.bn;
+  p.nt = (n + oc - 1) / oc;
+  const long tiles = (long)p.mt * p.nt;
+  p.whole = (int)(tiles / num_sms * num_sms);
+  const long left = tiles - p.whole;
+  p.shares = (int)std::min<long>(num_sms, left * kb);
+  p.ctas = p.whole ? num_sms : p.shares;
+  return p;
+}
+
+size_t fp8_linear_partials(int max_rows, int n, int kb, bool gated, int num_sms) {
+  // tiles that are left are fewer than CTAs, so that a call has at most twice the CTAs' slots
+  return (size_t)2 * num_sms * 128 * 256 * sizeof(float);
+}
+
+template <typename T, int BN, bool GATED> static cudaError_t linear_go(FlArgs& g, int num_sms, cudaStream_t st) {
+  static unsigned long long allowed = 0;
+  constexpr size_t limit = 225 * 1024;
+  const size_t stage = BN * FL_ROW + g.abox * FL_ROW, fixed = 1024 + (128 - g.abox) * FL_ROW;
+  g.stages = (int)std::min<size_t>(FL_MAXST, (limit - fixed) / stage);
+  cudaError_t e = allow_smem(fp8_linear_kernel<T, BN, GATED>, limit, &allowed);
+  if (e != cudaSuccess) return e;
+  e = launch_kernel(fp8_linear_kernel<T, BN, GATED>, dim3(g.ctas), dim3(FL_THREADS), fixed + g.stages * stage, st, 1, g);
+  const int left = g.mt * g.nt - g.whole;
+  if (e != cudaSuccess || left == 0 || g.shares == left) return e;      // (every CTA has one tile: no partials)
+  const int rows = std::min(g.a.rows, 128);
+  return launch_kernel(fp8_join_kernel<T, BN, GATED>, dim3(left, (rows * (GATED ? BN / 8 : BN / 4) + 255) / 256), dim3(256), 0, st, 1, g);
+}
+
+template <typename T> static cudaError_t linear_type(FlArgs& g, int bn, int num_sms, cudaStream_t st) {
+  if (g.a.w[1]) return linear_go<T, 256, true>(g, num_sms, st);
+  return bn == 128 ? linear_go<T, 128, false>(g, num_sms, st) : linear_go<T, 256, false>(g, num_sms, st);
+}
+
 cudaError_t launch_fp8_linear(const Fp8LinearArgs& a, int dtype, void* part, int num_sms, cudaStream_t st) {
-  if (dtype == MEDUSA_F32) return a.w[1] ? linear_go<float, 2>(a, st) : linear_go<float, 1>(a, st);
-  return a.w[1] ? linear_go<bf16, 2>(a, st) : linear_go<bf16, 1>(a, st);
+  const bool gated = a.w[1] != nullptr;
+  const FlPlan p = fl_plan(a.rows, a.n, a.kb, gated, num_sms);
+  FlArgs g{};
+  g.a = a;
+  g.abox = std::min(128, (a.rows + 7) / 8 * 8);
+  g.mt = p.mt;
+  g.nt = p.nt;
+  g.whole = p.whole;
+  g.ctas = p.ctas;
+  g.shares = p.shares;
+  g.part = static_cast<float*>(part);
+  g.rows_last = p.mt == 1;
+  if (!make_map(&g.tx, a.x, a.k, a.rows, a.x_row, g.abox) || !make_map(&g.tw[0], a.w[0], a.k, a.n, a.k, 128) ||
+      (gated && !make_map(&g.tw[1], a.w[1], a.k, a.n, a.k, 128)))
+    return cudaErrorInvalidValue;
+  return dtype == MEDUSA_F32 ? linear_type<float>(g, p.bn, num_sms, st) : linear_type<bf16>(g, p.bn, num_sms, st);
 }
 
 }  // namespace medusa

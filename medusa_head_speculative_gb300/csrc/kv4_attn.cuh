@@ -6,6 +6,7 @@
 #include "cache.h"
 #include "common.cuh"
 #include "kvcache.cuh"
+#include "launch.cuh"
 
 namespace medusa {
 
@@ -101,18 +102,6 @@ __device__ __forceinline__ void kd_next(const CacheView& c, int per, KdCursor& k
     ++k.b;
     k.nb = k.b < c.B ? kd_chunks(c, k.b) : 1;
   } while (k.nb == 0);
-}
-
-// Once per kernel and device: its dynamic shared memory limit (the call takes longer than a launch).
-template <typename K> cudaError_t allow_smem(K kern, size_t smem, unsigned long long* done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = 1ull << (dev & 63);
-  if (__atomic_load_n(done, __ATOMIC_ACQUIRE) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e == cudaSuccess) __atomic_fetch_or(done, bit, __ATOMIC_RELEASE);
-  return e;
 }
 
 // Many rows a head on the tensor cores (k_kv4_tree.cu): bf16, dh 64 or 128.
