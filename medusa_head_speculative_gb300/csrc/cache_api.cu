@@ -423,6 +423,7 @@ medusa_status medusa_prefix_attention(const medusa_cache* own, const medusa_kv* 
   a.Hq = own->d.Hq;
   a.G = own->d.Hq / own->d.Hkv;
   a.scale2 = (q->scale > 0 ? q->scale : 1.0f / std::sqrt((float)own->d.dh)) * 1.4426950408889634f;
+  if (!(a.scale2 >= 1.2e-38f)) a.scale2 = 1.2e-38f;       // not 0: a masked score's -infinity stays one
   a.status = own->status;
   return done(launch_prefix_attention(a, q->dtype, ws, own->num_sms, S(stream)));
 }

@@ -315,7 +315,9 @@ cudaError_t launch_prefix_attention(const PrefixArgs& a, int dtype, void* ws, in
   w.rows = a.own.B * w.R;
   row_blocks(tc, w.rows, &w.rbs, &w.nrbs);
   row_blocks(tc, w.R, &w.rbo, &w.nrbo);
-  w.cost_s = w.cost_o = 1;
+  // a chunk against two tiles of rows takes longer than against one
+  w.cost_s = tc && w.rbs > 128 ? 2 : 1;
+  w.cost_o = tc && w.rbo > 128 ? 2 : 1;
   w.tree = a.tk ? (a.n1 + PX_KEYS - 1) / PX_KEYS : 0;
   w.ctas = max_ctas(num_sms);
   char* p = static_cast<char*>(ws);
