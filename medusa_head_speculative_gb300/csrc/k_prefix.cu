@@ -176,39 +176,42 @@ __global__ void __launch_bounds__(256) prefix_simt_kernel(PxWork w) {
   }
 }
 
-// One warp per (sequence, node, query head): o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the row's
-// partials, M the largest m_s; a lane has VPL columns.  A row's partials are those of the CTAs that its
-// item's chunks lie in: with W chunks over C CTAs chunk x is CTA ceil((x + 1) C / W) - 1's.
-template <typename T, int VPL>
+// o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over a row's partials, M the largest m_s.  Eight lanes have
+// a row (dh/8 columns each), so that four rows' loads are in flight a warp: a row's time is a chain of loads (its
+// length, its references, its sums).  A row's partials are those of the CTAs that its item's chunks lie in:
+// with W units over C CTAs unit x is CTA ceil((x + 1) C / W) - 1's.
+template <typename T, int DH>
 __global__ void __launch_bounds__(256) prefix_join_kernel(PxWork w) {
-  constexpr int SB = 4;
+  constexpr int SB = 2, U = DH / 32;              // partials a round, 16-byte units a lane
   pdl_trigger();
   pdl_wait();
   const PrefixArgs& a = w.a;
-  const long i = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const long i = (long)blockIdx.x * 32 + (threadIdx.x >> 3);
   if (i >= (long)w.rows * a.own.Hkv) return;
-  const int lane = threadIdx.x & 31;
-  const int gr = (int)(i / a.own.Hkv), g = (int)(i - (long)gr * a.own.Hkv);       // row of head g over all sequences
+  const int lane = threadIdx.x & 7;
+  const int g = (int)(i / w.rows), gr = (int)(i - (long)g * w.rows);       // row of head g over all sequences
   const int b = gr / w.R, r = gr - b * w.R, node = gr / a.G, head = g * a.G + gr - node * a.G;
   const PxPlan p = *w.plan;
+  const int nb = px_chunks(w, b);
+  const long first = w.first[b];
   auto cta = [](long x, long n, long total) { return (((x + 1) * n + total - 1) / total) - 1; };
-  float M = -INFINITY, L = 0.f, acc[VPL] = {};
+  float M = -INFINITY, L = 0.f, acc[U][4] = {};
+#pragma unroll 1
   for (int kind = 0; kind < 2; ++kind) {
     long slot, rb, row;
     int n;
     if (kind == 0) {
       if (p.ns == 0) continue;
       const int rbi = gr / w.rbs, item = g * w.nrbs + rbi;
-      const long x = (long)item * p.ns, c0 = cta(x, p.cs, p.ws);
+      const long x = (long)item * px_units(p.ns) + PX_ITEM, c0 = cta(x, p.cs, p.ws);
       n = (int)(cta(x + p.ns - 1, p.cs, p.ws) - c0) + 1;
       slot = c0 + item;
       rb = w.rbs;
       row = gr - rbi * w.rbs;
     } else {
-      const int nb = px_chunks(w, b);
       if (nb == 0) continue;
       const int rbi = r / w.rbo, per = a.own.Hkv * w.nrbo, item = g * w.nrbo + rbi;
-      const long x = w.first[b] * per + (long)item * nb, c0 = cta(x, p.co, p.wo);
+      const long x = first * per + (long)item * px_units(nb) + PX_ITEM, c0 = cta(x, p.co, p.wo);
       n = (int)(cta(x + nb - 1, p.co, p.wo) - c0) + 1;
       slot = c0 + (long)b * per + item;
       rb = w.rbo;
@@ -218,29 +221,17 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(PxWork w) {
     const float2* pml = kind == 0 ? w.ml_s : w.ml_o;
     for (int s0 = 0; s0 < n; s0 += SB) {
       float2 ml[SB];
-      float v[SB][VPL];
+      float4 v[SB][U];
 #pragma unroll
       for (int u = 0; u < SB; ++u) {
         ml[u] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-        for (int e = 0; e < VPL; ++e) v[u][e] = 0.f;
+        for (int e = 0; e < U; ++e) v[u][e] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (s0 + u < n) {
           const long at = (slot + s0 + u) * rb + row;
           ml[u] = pml[at];
-          const float* src = po + at * (32 * VPL) + lane * VPL;
-          if constexpr (VPL == 4) {
-            const float4 t = *reinterpret_cast<const float4*>(src);
-            v[u][0] = t.x;
-            v[u][1] = t.y;
-            v[u][2] = t.z;
-            v[u][3] = t.w;
-          } else if constexpr (VPL == 2) {
-            const float2 t = *reinterpret_cast<const float2*>(src);
-            v[u][0] = t.x;
-            v[u][1] = t.y;
-          } else {
-            v[u][0] = src[0];
-          }
+#pragma unroll
+          for (int e = 0; e < U; ++e) v[u][e] = *reinterpret_cast<const float4*>(po + at * DH + e * 32 + lane * 4);
         }
       }
       float top = M;
@@ -250,7 +241,9 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(PxWork w) {
       const float f = M == -INFINITY ? 0.f : exp2f(M - top);
       L *= f;
 #pragma unroll
-      for (int e = 0; e < VPL; ++e) acc[e] *= f;
+      for (int e = 0; e < U; ++e)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[e][q] *= f;
       M = top;
 #pragma unroll
       for (int u = 0; u < SB; ++u) {
@@ -258,14 +251,28 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(PxWork w) {
         const float x = exp2f(ml[u].x - M);
         L += x * ml[u].y;
 #pragma unroll
-        for (int e = 0; e < VPL; ++e) acc[e] += x * v[u][e];
+        for (int e = 0; e < U; ++e) {
+          acc[e][0] += x * v[u][e].x;
+          acc[e][1] += x * v[u][e].y;
+          acc[e][2] += x * v[u][e].z;
+          acc[e][3] += x * v[u][e].w;
+        }
       }
     }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;     // (a NaN sum stays one)
-  T* dst = static_cast<T*>(a.o) + (long)node * a.o_row + (long)head * a.o_head + lane * VPL;
+  T* dst = static_cast<T*>(a.o) + (long)node * a.o_row + (long)head * a.o_head + lane * 4;
 #pragma unroll
-  for (int e = 0; e < VPL; ++e) dst[e] = from_f32<T>(L == 0.f ? 0.f : acc[e] * inv);
+  for (int e = 0; e < U; ++e) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[e][q] = L == 0.f ? 0.f : acc[e][q] * inv;
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(dst + e * 32) = make_float4(acc[e][0], acc[e][1], acc[e][2], acc[e][3]);
+    } else {
+      __nv_bfloat162 lo = __floats2bfloat162_rn(acc[e][0], acc[e][1]), hi = __floats2bfloat162_rn(acc[e][2], acc[e][3]);
+      *reinterpret_cast<uint2*>(dst + e * 32) = make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+    }
+  }
 }
 
 // ------------------------------------------------------------------ host side
@@ -301,10 +308,10 @@ template <typename T> static cudaError_t prefix_go(const PxWork& w, bool tc, int
   else if (dh == 64) e = simt_go<T, 64>(w, st);
   else e = simt_go<T, 128>(w, st);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)(((long)w.rows * w.a.own.Hkv + 7) / 8));
-  if (dh == 32) return launch_kernel(prefix_join_kernel<T, 1>, grid, dim3(256), 0, st, 1, w);
-  if (dh == 64) return launch_kernel(prefix_join_kernel<T, 2>, grid, dim3(256), 0, st, 1, w);
-  return launch_kernel(prefix_join_kernel<T, 4>, grid, dim3(256), 0, st, 1, w);
+  const dim3 grid((unsigned)(((long)w.rows * w.a.own.Hkv + 31) / 32));
+  if (dh == 32) return launch_kernel(prefix_join_kernel<T, 32>, grid, dim3(256), 0, st, 1, w);
+  if (dh == 64) return launch_kernel(prefix_join_kernel<T, 64>, grid, dim3(256), 0, st, 1, w);
+  return launch_kernel(prefix_join_kernel<T, 128>, grid, dim3(256), 0, st, 1, w);
 }
 
 cudaError_t launch_prefix_attention(const PrefixArgs& a, int dtype, void* ws, int num_sms, cudaStream_t st) {

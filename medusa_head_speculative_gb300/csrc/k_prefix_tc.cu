@@ -15,15 +15,15 @@
 //                a row's infinities and NaN become 0 there and the key is noted, since rows that do not
 //                see it multiply it by 0; a row that does gets a NaN sum
 //   warps 8, 9   MMAs of a "slot" each, with S (128 columns) and O (dh columns) in tensor memory: S = Q K^T,
-//                then O += P V with P read from tensor memory and V from shared memory (MN-major), in
-//                halves of 64 keys: while the softmax has one half, the other half's P is multiplied with
-//                V and the next chunk's scores take its place
-//   warps 0-3,   two softmax warpgroups, one per slot, one query row per thread: they load the block's
-//   4-7          queries, read a half of S, exponentiate and write P over it
+//                then O += P V with P read from tensor memory and V from shared memory (MN-major)
+//   warps 10, 11 copies of the queries; with one tile a block ahead
+//   warps 0-3,   two softmax warpgroups, one per slot, one query row per thread: they read S,
+//   4-7          exponentiate and write P over it, 32 keys at a time (all 64 of a half unrolled made the
+//                warps of a CTA wait for instructions)
 //
 // With two tiles the slots are the tiles and share every chunk; with one both slots work on it and take
 // alternate chunks, and the first warpgroup merges the second's (O, reference, sum) before it writes the
-// partial.
+// partial (of an item's only chunk its slot writes it).
 //
 // A wait names a phase by its parity: a waiter has to have seen the phase before.  With one tile a slot
 // sees every other chunk of the CTA, odd or even ones over all its items, and the rings are of two or four
@@ -39,9 +39,9 @@
 
 namespace medusa {
 
-constexpr int PT_ROWS = 128, PT_MAXST = 4, PT_MMA_WARP = 8, PT_COPY_WARP = 12, PT_THREADS = 512;
-// Registers a thread: 128 at launch (512 x 128 = 65536), then 2 x 176 + 2 x 80 = 4 x 128.
-constexpr int PT_REG_SOFTMAX = 176, PT_REG_REST = 80;
+constexpr int PT_ROWS = 128, PT_MAXST = 4, PT_MMA_WARP = 8, PT_QUERY_WARP = 10, PT_COPY_WARP = 12, PT_THREADS = 512;
+// Registers a thread: 128 at launch (512 x 128 = 65536), then 2 x 160 + 2 x 96 = 4 x 128.
+constexpr int PT_REG_SOFTMAX = 160, PT_REG_REST = 96;
 static_assert(2 * PT_REG_SOFTMAX + 2 * PT_REG_REST == 4 * 128, "what the launch holds");
 constexpr uint32_t PT_SLOT_COLS = 256;              // per slot: S / P [0, 128), O [128, 128 + dh)
 constexpr float PT_LAZY = 8.f;
@@ -53,14 +53,43 @@ struct PtArgs {
   int nt[2], sk[2], sv[2];                          // shared, own: tiles of a block, stages of the rings
 };
 
-// QF / QE: query tiles written / no longer read.  KF / KE and VF / VE: stages full / free.  Per slot and half:
-// SF (S written), PR (P written), OF (P V done).  MRG / MFR: the second slot's (reference, sum) are in shared
+// QF / QE: query tiles (with one tile: two in turn) written / no longer read.  KF and VF: stages full.  Per slot
+// and stage: SF (S written, so that the keys' stage is free as far as the slot goes), OF (P V done, the values'
+// stage).  Per slot: P1 and P2 (P of the first 64 keys, of all written), O1 (P V of the first done).  One barrier for
+// both who wait: each commit costs the tensor cores 50 to 75 cycles (QK and PV of a chunk take 1025 cycles
+// without, 1390 with four).  MRG / MFR: the second slot's (reference, sum) are in shared
 // memory / consumed.  END: every MMA issued has completed.
 enum {
-  XB_QF = 0, XB_QE = 1, XB_KF = 2, XB_KE = XB_KF + PT_MAXST, XB_VF = XB_KE + PT_MAXST, XB_VE = XB_VF + PT_MAXST,
-  XB_SF = XB_VE + PT_MAXST, XB_PR = XB_SF + 4, XB_OF = XB_PR + 4, XB_MRG = XB_OF + 4, XB_MFR = XB_MRG + 1,
+  XB_QF = 0, XB_QE = 2, XB_KF = 4, XB_VF = XB_KF + PT_MAXST, XB_SF = XB_VF + PT_MAXST, XB_OF = XB_SF + 2 * PT_MAXST,
+  XB_P1 = XB_OF + 2 * PT_MAXST, XB_P2 = XB_P1 + 2, XB_O1 = XB_P2 + 2, XB_MRG = XB_O1 + 2, XB_MFR = XB_MRG + 1,
   XB_END = XB_MFR + 1, XB_COUNT = XB_END + 1
 };
+
+// Of chunk j (pc: chunks of cached slots, len of them): whether it is of the call's own rows, its keys, and
+// whether the copy engine brings it.
+__device__ __forceinline__ int pt_keys(const PrefixArgs& a, int j, int pc, int len) {
+  return min((j < pc ? len : a.n1) - (j < pc ? j : j - pc) * PX_KEYS, PX_KEYS);
+}
+__device__ __forceinline__ bool pt_engine(const PtArgs& g, int kind, int j, int len) {
+  return g.tma[kind] && (long)(j + 1) * PX_KEYS <= len;
+}
+
+// A place in a ring of stages that is walked through in steps (a division by its depth, which is no constant,
+// would take longer than what it is needed for).
+struct PtRing {
+  int st, ph;
+  __device__ __forceinline__ void next(int by, int depth) {
+    st += by;
+    if (st >= depth) {
+      st -= depth;
+      ph ^= 1;
+    }
+  }
+};
+
+// A value that all lanes have, as the compiler can tell: what an MMA takes comes from uniform registers, and moving
+// an operand there costs as much as half an MMA (16 MMAs of a job 1800 cycles to issue, 1025 to run).
+__device__ __forceinline__ int uni(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
@@ -79,34 +108,38 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
   __shared__ float2 s_ml[PT_ROWS];                   // second slot's (reference, sum) per row
   const PxWork& w = g.w;
   const PrefixArgs& a = w.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uni(tid >> 5), lane = tid & 31;
   pdl_wait();
-  const PxPlan plan = px_plan(w, blockIdx.x == 0 && warp == PT_MMA_WARP + 2);
+  const PxPlan plan = px_plan(w, blockIdx.x == 0 && warp == PT_QUERY_WARP);
   if ((int)blockIdx.x >= plan.cs + plan.co) {
     pdl_trigger();
     return;
   }
   PxWalk walk = px_start(w, plan, blockIdx.x);
-  const bool shared = walk.shared;
+  const bool shared = uni(walk.shared);
   const int kind = shared ? 0 : 1, nt = g.nt[kind], SK = g.sk[kind], SV = g.sv[kind];
   const CacheView& c = shared ? a.shared : a.own;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t qs = base, k0s = base + nt * CHUNK, v0s = k0s + SK * CHUNK;
+  const uint32_t qs = base, k0s = base + 2 * CHUNK, v0s = k0s + SK * CHUNK;
   const uint32_t bar0 = smem_u32(bars);
   auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   if (tid == 0) {
-    mbar_init(bar(XB_QF), nt * PT_ROWS);
-    mbar_init(bar(XB_QE), 2);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(XB_QF + i), 64);
+      mbar_init(bar(XB_QE + i), 2);
+    }
     for (int i = 0; i < PT_MAXST; ++i) {
       mbar_init(bar(XB_KF + i), 128);
-      mbar_init(bar(XB_KE + i), nt);
       mbar_init(bar(XB_VF + i), 128);
-      mbar_init(bar(XB_VE + i), nt);
     }
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < 2 * PT_MAXST; ++s) {
       mbar_init(bar(XB_SF + s), 1);
-      mbar_init(bar(XB_PR + s), PT_ROWS);
       mbar_init(bar(XB_OF + s), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(XB_P1 + s), PT_ROWS);
+      mbar_init(bar(XB_P2 + s), PT_ROWS);
+      mbar_init(bar(XB_O1 + s), 1);
     }
     mbar_init(bar(XB_MRG), PT_ROWS);
     mbar_init(bar(XB_MFR), PT_ROWS);
@@ -119,7 +152,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
   __syncthreads();
   tc_fence_after();
   pdl_trigger();                          // only once this CTA holds its TMEM
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = (uint32_t)uni((int)tmem_slot);
   bool timed_out = false;
   auto aborted = [&]() { return *(volatile int*)&s_abort != 0; };
   PxSeg s;
@@ -132,6 +165,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
     const uint64_t pol = shared ? policy_evict_last() : policy_evict_first();
     const bool boss = pw == 0 && lane == 0;
     int x = 0, trees = 0;                            // chunks, chunks of the call's own rows so far
+    PtRing ring[2] = {{0, 0}, {0, 0}};
     auto abandon = [&](bool got) { timed_out = !got; return !got; };
     while (!timed_out && px_next(w, walk, s)) {
       const int b = shared ? 0 : s.b, len = clamp_len(c, c.len[b]), pc = (len + PX_KEYS - 1) / PX_KEYS;
@@ -151,14 +185,21 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
       long next = offset(s.j);
       for (int i = 0; i < s.n; ++i, ++x) {
         const int j = s.j + i;
-        const bool tree = j >= pc, engine = !tree && g.tma[kind] && (j + 1) * PX_KEYS <= len;
+        const bool tree = j >= pc, engine = pt_engine(g, kind, j, len);
         const long at = next;
         if (i + 1 < s.n) next = offset(j + 1);
 #pragma unroll 1
         for (int part = 0; part < 2; ++part) {
-          const int n = part ? SV : SK, st = x % n;
+          const int n = part ? SV : SK, st = part ? ring[1].st : ring[0].st;
           const uint32_t full = bar((part ? XB_VF : XB_KF) + st), dst = (part ? v0s : k0s) + st * CHUNK;
-          if (abandon(kt_warp_wait(bar((part ? XB_VE : XB_KE) + st), ((x / n) & 1) ^ 1))) break;
+          // the stage's last chunk has been multiplied by the slots that took it
+          if (x >= n) {
+            const int done = (part ? XB_OF : XB_SF) + st, ph = part ? ring[1].ph : ring[0].ph;
+            bool got = true;
+            if (nt == 2 || !(st & 1)) got = kt_warp_wait(bar(done), ph ^ 1);
+            if (got && (nt == 2 || (st & 1))) got = kt_warp_wait(bar(done + PT_MAXST), ph ^ 1);
+            if (abandon(got)) break;
+          }
           if (engine) {
             if (boss) {
               mbar_expect_tx(full, CHUNK);
@@ -174,24 +215,31 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
           const uint32_t to = dst + (unit >> 3) * TILE;
           if (tree && part) {
             uint32_t bad = 0;
-#pragma unroll 4
-            for (int y = 0; y < UPR; ++y) {
-              const int row = y * RPI + sub;
-              const long o = __shfl_sync(0xffffffffu, at, row);
-              uint4 v = make_uint4(0u, 0u, 0u, 0u);
-              if (o >= 0) v = *reinterpret_cast<const uint4*>(src + o + unit * 8);
-              const uint32_t words[4] = {v.x, v.y, v.z, v.w};
-              bool no = false;
+            constexpr int FLY = 8;                       // loads in flight a lane
+#pragma unroll 1
+            for (int y0 = 0; y0 < UPR; y0 += FLY) {
+              uint4 v[FLY];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                no |= (words[e] & 0x7f80u) == 0x7f80u || (words[e] & 0x7f800000u) == 0x7f800000u;
-              if (no) v = make_uint4(0u, 0u, 0u, 0u);
-              const uint32_t hit = __ballot_sync(0xffffffffu, no);
+              for (int y = 0; y < FLY; ++y) {
+                const long o = __shfl_sync(0xffffffffu, at, (y0 + y) * RPI + sub);
+                v[y] = make_uint4(0u, 0u, 0u, 0u);
+                if (o >= 0) v[y] = *reinterpret_cast<const uint4*>(src + o + unit * 8);
+              }
 #pragma unroll
-              for (int e = 0; e < RPI; ++e)
-                if ((hit >> (e * UPR)) & ((1u << UPR) - 1u)) bad |= 1u << (y * RPI + e);
-              const int r = 32 * pw + row;
-              st_shared16(to + r * 128 + (((unit & 7) ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
+              for (int y = 0; y < FLY; ++y) {
+                const uint32_t words[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
+                bool no = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  no |= (words[e] & 0x7f80u) == 0x7f80u || (words[e] & 0x7f800000u) == 0x7f800000u;
+                if (no) v[y] = make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t hit = __ballot_sync(0xffffffffu, no);
+#pragma unroll
+                for (int e = 0; e < RPI; ++e)
+                  if ((hit >> (e * UPR)) & ((1u << UPR) - 1u)) bad |= 1u << ((y0 + y) * RPI + e);
+                const int r = 32 * pw + (y0 + y) * RPI + sub;
+                st_shared16(to + r * 128 + (((unit & 7) ^ (r & 7)) << 4), v[y].x, v[y].y, v[y].z, v[y].w);
+              }
             }
             if (lane == 0) s_bad[trees & 7][pw] = bad;
             fence_proxy_async();
@@ -207,6 +255,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
           }
         }
         if (timed_out) break;
+        ring[0].next(1, SK);
+        ring[1].next(1, SV);
         trees += tree;
       }
       if (aborted()) break;
@@ -221,92 +271,123 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
   } else if (warp >= PT_MMA_WARP) {
     // ------------------------------------------------------------ MMAs of one slot
     reg_fewer<PT_REG_REST>();
-    if (warp < PT_MMA_WARP + 2) {
+    if (warp < PT_QUERY_WARP) {
       const int slot = warp - PT_MMA_WARP;
       const uint32_t lead = lane == 0;
-      const uint32_t id_qk = idesc_bf16(PT_ROWS, PX_KEYS / 2);
+      const uint32_t id_qk = idesc_bf16(PT_ROWS, PX_KEYS), id_half = idesc_bf16(PT_ROWS, PX_KEYS / 2);
       const uint32_t id_pv = idesc_bf16(PT_ROWS, DH) | IDESC_B_MN_MAJOR;
       // descriptors hold addresses in 16-byte units: an offset is added to them
       const uint64_t dq = sw128_desc(qs + (nt == 2 ? slot : 0) * CHUNK), dk = sw128_desc(k0s), dv = sw128_desc_mn(v0s, TILE);
       const uint32_t sp = tmem + slot * PT_SLOT_COLS, od = sp + PX_KEYS;
       const int step = nt == 2 ? 1 : 2;                  // two tiles: every chunk; one: alternate ones
-      int gc = 0, qn = 0, js = 0;         // chunks, blocks and this slot's jobs so far
+      int gc = 0, qn = 0, mc = 0;         // chunks, blocks and merged blocks so far
+      int done = 0, halves = 0;           // this slot's chunks with rows so far, and those of more than 64 keys
       bool dead = false;
-      // stages may have been written by 16-byte copies (the generic proxy): make them visible to the MMAs
-      auto wait_k = [&](int x) {
-        const bool got = kt_warp_wait(bar(XB_KF + x % SK), (x / SK) & 1);
-        fence_proxy_async();
+      int pc = 0, len = 0;                // of the item's cache
+      PtRing kr = {nt == 2 ? 0 : slot, 0}, vr = kr;  // (rings have two stages at least)
+      // a stage written by 16-byte copies (the generic proxy) is made visible to the MMAs
+      auto wait_k = [&](int j) {
+        const bool got = kt_warp_wait(bar(XB_KF + kr.st), kr.ph);
+        if (!pt_engine(g, kind, j, len)) fence_proxy_async();
         return got;
       };
-      auto wait_v = [&](int x) {
-        const bool got = kt_warp_wait(bar(XB_VF + x % SV), (x / SV) & 1);
-        fence_proxy_async();
+      auto wait_v = [&](int j) {
+        const bool got = kt_warp_wait(bar(XB_VF + vr.st), vr.ph);
+        if (!pt_engine(g, kind, j, len)) fence_proxy_async();
         return got;
       };
-      auto scores = [&](int x, int hf) {
-        kt_qk<H>(sp + 64 * hf, dq, dk + (x % SK) * (CHUNK >> 4) + 512 * hf, id_qk, lead);
-        kt_commit(bar(XB_SF + 2 * slot + hf), lead);
+      uint64_t q = dq;                    // the block's queries
+      auto two = [&](int j) { return pt_keys(a, j, pc, len) > PX_KEYS / 2; };   // whether a chunk has a second half
+      auto scores = [&](int j) {
+        kt_qk<H>(sp, q, dk + kr.st * (CHUNK >> 4), two(j) ? id_qk : id_half, lead);
+        kt_commit(bar(XB_SF + slot * PT_MAXST + kr.st), lead);
+        kr.next(step, SK);
       };
       while (!dead && px_next(w, walk, s)) {
-        const int n = s.n;
-        const bool idle = nt == 2 && s.rb * 2 * PT_ROWS + slot * PT_ROWS >= (shared ? w.rows : w.R);
+        const int n = uni(s.n), j0 = uni(s.j);
+        const bool idle = uni(nt == 2 && s.rb * 2 * PT_ROWS + slot * PT_ROWS >= (shared ? w.rows : w.R));
         const int i0 = nt == 2 ? 0 : (slot - gc) & 1;    // this slot's first chunk
-        if (!kt_warp_wait(bar(XB_QF), qn & 1)) { dead = true; break; }
+        len = uni(clamp_len(c, c.len[shared ? 0 : s.b]));
+        pc = (len + PX_KEYS - 1) / PX_KEYS;
+        const int qb = nt == 2 ? 0 : qn & 1;
+        if (!kt_warp_wait(bar(XB_QF + qb), (nt == 2 ? qn : qn >> 1) & 1)) { dead = true; break; }
+        fence_proxy_async();
         tc_fence_after();
+        q = dq + qb * (CHUNK >> 4);
         if (idle) {                                      // no rows: only let the stages go
           for (int i = 0; i < n; ++i) {
-            if (!wait_k(gc + i) || !wait_v(gc + i)) { dead = true; break; }
-            kt_commit(bar(XB_KE + (gc + i) % SK), lead);
-            kt_commit(bar(XB_VE + (gc + i) % SV), lead);
+            if (!wait_k(j0 + i) || !wait_v(j0 + i)) { dead = true; break; }
+            kt_commit(bar(XB_SF + slot * PT_MAXST + kr.st), lead);
+            kt_commit(bar(XB_OF + slot * PT_MAXST + vr.st), lead);
+            kr.next(1, SK);
+            vr.next(1, SV);
           }
         } else if (i0 < n) {
-          if (!wait_k(gc + i0)) { dead = true; break; }
-          scores(gc + i0, 0);
-          scores(gc + i0, 1);
-          kt_commit(bar(XB_KE + (gc + i0) % SK), lead);
-          if (i0 + step >= n) kt_commit(bar(XB_QE), lead);
+          if (!wait_k(j0 + i0)) { dead = true; break; }
+          scores(j0 + i0);
+          if (i0 + step >= n) kt_commit(bar(XB_QE + qb), lead);
 #pragma unroll 1
           for (int i = i0; i < n && !dead; i += step) {
-            const int x = gc + i, xn = x + step;
+            const int j = j0 + i;
+            const uint64_t v = dv + vr.st * (CHUNK >> 4);
             // one tile: slot 1's O may be overwritten only after the first warpgroup has merged it into the
             // previous block's partial
-            if (nt == 1 && slot == 1 && i == i0 && qn > 0 && !kt_warp_wait(bar(XB_MFR), (qn - 1) & 1)) { dead = true; break; }
-            if (!wait_v(x)) { dead = true; break; }
-            // each half of P as it comes, and in its place the next chunk's scores
-            int next = i + step < n ? 0 : 2;             // halves of the next chunk's scores issued
-#pragma unroll 1
-            for (int hf = 0; hf < 2; ++hf) {
-              if (!kt_warp_wait(bar(XB_PR + 2 * slot + hf), js & 1)) { dead = true; break; }
+            if (nt == 1 && slot == 1 && i == i0 && mc > 0 && !kt_warp_wait(bar(XB_MFR), (mc - 1) & 1)) { dead = true; break; }
+            if (!wait_v(j)) { dead = true; break; }
+            const bool both = two(j), more = i + step < n;
+            if (both) {
+              if (!kt_warp_wait(bar(XB_P1 + slot), halves & 1)) { dead = true; break; }
+              ++halves;
               tc_fence_after();
-              kt_pv(od, sp + 64 * hf, dv + (x % SV) * (CHUNK >> 4) + 512 * hf, id_pv, i != i0 || hf, lead);
-              kt_commit(bar(XB_OF + 2 * slot + hf), lead);
-              if (hf == 1) kt_commit(bar(XB_VE + x % SV), lead);
-              if (next == 0) {
-                // the first half's scores wait for P's second half where their keys are not there yet
-                const bool now = hf == 1 ? wait_k(xn) : __all_sync(0xffffffffu, mbar_test(bar(XB_KF + xn % SK), (xn / SK) & 1));
-                if (hf == 1 && !now) { dead = true; break; }
-                if (now) {
-                  fence_proxy_async();
-                  scores(xn, 0);
-                  next = 1;
-                }
-              }
-              if (hf == 1 && next == 1) {
-                scores(xn, 1);
-                kt_commit(bar(XB_KE + xn % SK), lead);
-                if (i + 2 * step >= n) kt_commit(bar(XB_QE), lead);
-              }
+              kt_pv(od, sp, v, id_pv, i != i0, lead);
+              kt_commit(bar(XB_O1 + slot), lead);
             }
-            ++js;
+            if (!kt_warp_wait(bar(XB_P2 + slot), done & 1)) { dead = true; break; }
+            ++done;
+            tc_fence_after();
+            if (both) kt_pv(od, sp + 32, v + 512, id_pv, 1, lead);
+            else kt_pv(od, sp, v, id_pv, i != i0, lead);
+            kt_commit(bar(XB_OF + slot * PT_MAXST + vr.st), lead);
+            vr.next(step, SV);
+            if (more) {
+              if (!wait_k(j + step)) { dead = true; break; }
+              scores(j + step);
+              if (i + 2 * step >= n) kt_commit(bar(XB_QE + qb), lead);
+            }
           }
         }
-        if (idle || i0 >= n) kt_commit(bar(XB_QE), lead);
+        if (idle || i0 >= n) kt_commit(bar(XB_QE + qb), lead);
         ++qn;
+        mc += nt == 1 && n > 1;
         gc += n;
         if (aborted()) break;
       }
       timed_out = dead;
       kt_commit(bar(XB_END), lead);                      // arrives once this warp's MMAs are done
+    } else {
+      // ---------------------------------------------------------- copies of queries
+      constexpr int UPR = DH / 8, RPI = 32 / UPR;        // 16-byte units of a row, rows a step of the warp
+      const int unit = lane % UPR, sub = lane / UPR;
+      const bf16* src = static_cast<const bf16*>(a.q);
+      for (int qn = 0; px_next(w, walk, s); ++qn) {
+        const int qb = nt == 2 ? 0 : qn & 1, turn = nt == 2 ? qn : qn >> 1;
+        const uint32_t to = qs + qb * CHUNK + (unit >> 3) * TILE;
+        for (int r0 = 32 * (warp - PT_QUERY_WARP); r0 < nt * PT_ROWS; r0 += 64) {
+          const PxRow row = px_row(w, shared, s, r0 + lane);
+          const long at = row.ok ? row.node_row * a.q_row + row.head * a.q_head : -1;
+          if (r0 < 64 && !kt_warp_wait(bar(XB_QE + qb), (turn & 1) ^ 1)) { timed_out = true; break; }
+#pragma unroll 4
+          for (int y = 0; y < UPR; ++y) {
+            const long o = __shfl_sync(0xffffffffu, at, y * RPI + sub);
+            const int r = r0 + y * RPI + sub;
+            cp_async16(to + (r >> 7) * CHUNK + (r & 127) * 128 + (((unit & 7) ^ (r & 7)) << 4), o >= 0 ? src + o + unit * 8 : src, o >= 0 ? 16 : 0);
+          }
+        }
+        if (timed_out) break;
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(XB_QF + qb)) : "memory");
+        if (aborted()) break;
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
     // ------------------------------------------------------------ softmax warpgroups
@@ -320,108 +401,127 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
     const int rbrows = shared ? w.rbs : w.rbo;
     float* part_o = shared ? w.o_s : w.o_o;
     float2* part_ml = shared ? w.ml_s : w.ml_o;
-    int js = 0, mc = 0, qn = 0, trees = 0, gc = 0;
-    int js1 = 0;                                     // slot 1's jobs (merging warpgroup)
+    int mc = 0, trees = 0, gc = 0;
+    // places of this slot's next chunk in the rings, of its last one (values), and of slot 1's (merging warpgroup)
+    PtRing kr = {nt == 2 ? 0 : slot, 0}, vr = kr, last = kr, other = {1, 0}, last1 = other;
+    const int step = nt == 2 ? 1 : 2;
+    int parts = 0;                                   // this slot's chunks of more than 64 keys so far
     while (px_next(w, walk, s)) {
       const int n = s.n, b = shared ? 0 : s.b, len = clamp_len(c, c.len[b]), pc = (len + PX_KEYS - 1) / PX_KEYS;
       const int tile = nt == 2 ? slot : 0;
       const int br = tile * PT_ROWS + r;             // row of the block
       const PxRow row = px_row(w, shared, s, br);
       const bool live = __any_sync(0xffffffffu, row.ok);
-      // ---- the block's queries.  Two tiles: each slot its own; one: the second slot, which is done with the
-      // block before sooner, while the first one writes that block's partial
-      if (nt == 2 || slot == 1) {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.q) + row.node_row * a.q_row + row.head * a.q_head);
-        uint4 raw[DH / 8];
-#pragma unroll
-        for (int u = 0; u < DH / 8; ++u) raw[u] = row.ok ? src[u] : make_uint4(0u, 0u, 0u, 0u);
-        if (qn > 0 && !kt_warp_wait(bar(XB_QE), (qn - 1) & 1)) { timed_out = true; break; }
-        const uint32_t to = qs + tile * CHUNK + r * 128;
-#pragma unroll
-        for (int u = 0; u < DH / 8; ++u)
-          st_shared16(to + (u >> 3) * TILE + (((u & 7) ^ (r & 7)) << 4), raw[u].x, raw[u].y, raw[u].z, raw[u].w);
-        fence_proxy_async();
-        mbar_arrive(bar(XB_QF));
-      }
       const bool idle = nt == 2 && s.rb * 2 * PT_ROWS + slot * PT_ROWS >= (shared ? w.rows : w.R);
       const int i0 = nt == 2 ? 0 : (slot - gc) & 1;
       const int njobs = idle ? 0 : nt == 2 ? n : (n + 1 - i0) / 2;
       float m_use = -INFINITY, l_acc = 0.f;
+      for (int i = 0; idle && i < n && !timed_out; ++i) {            // (phases have to be seen one by one)
+        timed_out = !kt_warp_wait(bar(XB_SF + slot * PT_MAXST + kr.st), kr.ph);
+        kr.next(1, SK);
+        vr.next(1, SV);
+      }
       for (int jj = 0; jj < njobs; ++jj) {
         const int j = s.j + i0 + (nt == 2 ? jj : 2 * jj);
         const bool tree = j >= pc;
-        const int t0 = (tree ? j - pc : j) * PX_KEYS;
+        const int keys = pt_keys(a, j, pc, len);
+        if (!kt_warp_wait(bar(XB_SF + slot * PT_MAXST + kr.st), kr.ph)) { timed_out = true; break; }
+        tc_fence_after();
 #pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf) {
-          if (!kt_warp_wait(bar(XB_SF + 2 * slot + hf), js & 1)) { timed_out = true; break; }
-          tc_fence_after();
+        for (int q = 0; q < (keys > PX_KEYS / 2 ? 4 : 2); ++q) {
           if (live) {
-            float v[64];
-            tmem_ld64(scol + 64 * hf, v);
-            const int valid = len - t0 - 64 * hf;    // cached keys of this half there are
-            if (tree) {
-              const uint32_t see[2] = {row.ok ? px_sees(a, row.n, (t0 >> 5) + 2 * hf) : 0u,
-                                       row.ok ? px_sees(a, row.n, (t0 >> 5) + 2 * hf + 1) : 0u};
+            float v[32];
+            kt_ld32(scol + 32 * q, v);
+            const int valid = keys - 32 * q;
+            const uint32_t see = tree ? (row.ok ? px_sees(a, row.n, (j - pc) * 4 + q) : 0u)
+                                      : valid >= 32 ? 0xffffffffu : valid <= 0 ? 0u : (1u << valid) - 1u;
+            if (__any_sync(0xffffffffu, see != 0xffffffffu)) {
 #pragma unroll
-              for (int e = 0; e < 64; ++e)
-                if (!((see[e >> 5] >> (e & 31)) & 1u)) v[e] = -INFINITY;
-            } else if (valid < 64) {
-#pragma unroll
-              for (int e = 0; e < 64; ++e)
-                if (e >= valid) v[e] = -INFINITY;
+              for (int e = 0; e < 32; ++e)
+                if (!((see >> e) & 1u)) v[e] = -INFINITY;
             }
-            float x0 = fmaxf(v[0], v[1]), x1 = fmaxf(v[2], v[3]);
+            // Against the reference as it is, the largest score found on the way; where it passes the reference
+            // by PT_LAZY (a row's first keys, and hardly ever later) the reference is raised and all is done again.
+            uint32_t pk[16];
+            float sum;
+#pragma unroll 1
+            for (;;) {
+              const float nm = m_use == -INFINITY ? 0.f : -m_use;   // (nothing seen yet: every score is -infinity)
+              F2 l0 = f2(0.f, 0.f), l1 = l0;
+              float x0 = v[0], x1 = v[1];
 #pragma unroll
-            for (int e = 4; e < 64; e += 4) {
-              x0 = max3(x0, v[e], v[e + 1]);
-              x1 = max3(x1, v[e + 2], v[e + 3]);
-            }
-            const float mx = fmaxf(x0, x1) * sl2;
-            const bool raise = mx > m_use + PT_LAZY;     // (from -infinity: any score)
-            if (__any_sync(0xffffffffu, raise)) {
+              for (int e = 0; e < 32; e += 4) {
+                float p0, p1, p2, p3;
+                unf2(fma2(f2(v[e], v[e + 1]), f2(sl2, sl2), f2(nm, nm)), p0, p1);
+                unf2(fma2(f2(v[e + 2], v[e + 3]), f2(sl2, sl2), f2(nm, nm)), p2, p3);
+                p0 = ex2_approx(p0);
+                p1 = ex2_approx(p1);
+                p2 = ex2_approx(p2);
+                p3 = ex2_approx(p3);
+                l0 = add2(l0, f2(p0, p1));
+                l1 = add2(l1, f2(p2, p3));
+                pk[e / 2] = bf16x2(p0, p1);
+                pk[e / 2 + 1] = bf16x2(p2, p3);
+                x0 = max3(x0, v[e], v[e + 1]);
+                x1 = max3(x1, v[e + 2], v[e + 3]);
+              }
+              float a0, a1;
+              unf2(add2(l0, l1), a0, a1);
+              sum = a0 + a1;
+              const float mx = fmaxf(x0, x1) * sl2;
+              const bool raise = mx > m_use + PT_LAZY;   // (from -infinity: any score)
+              if (!__any_sync(0xffffffffu, raise)) break;
               const float f = !raise ? 1.f : m_use == -INFINITY ? 0.f : ex2_approx(m_use - mx);
-              // O is rescaled once the half before has been added to it; a block's first half finds none
-              if (jj > 0 || hf == 1) {
-                if (!kt_warp_wait(bar(XB_OF + 2 * slot + (hf ^ 1)), (hf ? js : js - 1) & 1)) { timed_out = true; break; }
-                tc_fence_after();
+              // O may be rescaled: the products of the chunks before are done (this S came after them), those of
+              // this chunk's first half are waited for
+              const bool mixed = q > 1;
+              if (mixed && !kt_warp_wait(bar(XB_O1 + slot), (parts - 1) & 1)) { timed_out = true; break; }
+              tc_fence_after();
+              if (jj > 0 || mixed) {
 #pragma unroll 1
                 for (int e = 0; e < DH; e += 16) {
                   float u[16];
                   kt_ld16(ocol + e, u);
 #pragma unroll
-                  for (int q = 0; q < 16; ++q) u[q] *= f;
+                  for (int y = 0; y < 16; ++y) u[y] *= f;
                   tmem_st16(ocol + e, u);
                 }
+              }
+              kt_st_wait();
+#pragma unroll 1
+              for (int e = q & 2; e < q; ++e) {          // and so is P that has not been multiplied
+                float u[16];
+                uint32_t scaled[16];
+                kt_ld16(scol + 16 * e, u);
+#pragma unroll
+                for (int y = 0; y < 16; ++y)
+                  scaled[y] = bf16x2(__uint_as_float(__float_as_uint(u[y]) << 16) * f,
+                                     __uint_as_float(__float_as_uint(u[y]) & 0xffff0000u) * f);
+                kt_st16(scol + 16 * e, scaled);
               }
               l_acc *= f;
               if (raise) m_use = mx;
             }
-            F2 ls = f2(0.f, 0.f);
-            uint32_t pk[32];
-            const float nm = m_use == -INFINITY ? 0.f : -m_use;     // (nothing seen yet: every score is -infinity)
-#pragma unroll
-            for (int e = 0; e < 64; e += 2) {
-              float p0, p1;
-              unf2(fma2(f2(v[e], v[e + 1]), f2(sl2, sl2), f2(nm, nm)), p0, p1);
-              p0 = ex2_approx(p0);
-              p1 = ex2_approx(p1);
-              ls = add2(ls, f2(p0, p1));
-              pk[e / 2] = bf16x2(p0, p1);
-            }
-            kt_st32(scol + 64 * hf, pk);
-            kt_st_wait();
-            float l0, l1;
-            unf2(ls, l0, l1);
-            l_acc += l0 + l1;
+            if (timed_out) break;
+            l_acc += sum;
+            kt_st16(scol + 16 * q, pk);
           }
-          tc_fence_before();
-          mbar_arrive(bar(XB_PR + 2 * slot + hf));
+          if (q == 1 && keys > PX_KEYS / 2) {
+            kt_st_wait();
+            tc_fence_before();
+            mbar_arrive(bar(XB_P1 + slot));
+            ++parts;
+          }
         }
         if (timed_out) break;
-        ++js;
+        kt_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar(XB_P2 + slot));
+        last = vr;
+        kr.next(step, SK);
+        vr.next(step, SV);
       }
       if (timed_out) break;
-      ++qn;
       // ---- the block's partial
       const long prow = s.slot * rbrows + br;
       float* dst = part_o + prow * DH;
@@ -435,9 +535,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
             bad |= row.ok && (px_sees(a, row.n, (first_tree - pc + q) * 4 + u) & *(volatile uint32_t*)&s_bad[(trees + q) & 7][u]) != 0u;
         return bad;
       };
-      if (nt == 2) {
+      if (nt == 2 || n == 1) {
+        if (nt == 1 && njobs == 0) other.next(2, SV);     // (the merging warpgroup follows the other's chunks)
         if (njobs > 0 && live) {
-          if (!kt_warp_wait(bar(XB_OF + 2 * slot + 1), (js - 1) & 1)) { timed_out = true; break; }
+          if (!kt_warp_wait(bar(XB_OF + slot * PT_MAXST + last.st), last.ph)) { timed_out = true; break; }
           tc_fence_after();
           if (n_trees > 0 && noted()) l_acc = NAN;
           if (l_acc != l_acc && m_use == -INFINITY) m_use = 0.f;
@@ -459,11 +560,14 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
         ++mc;
       } else {
         const int nj1 = n - njobs;                   // slot 1's chunks in this block (either may have none)
-        js1 += nj1;
-        bool ok = njobs == 0 || kt_warp_wait(bar(XB_OF + 1), (js - 1) & 1);
+        for (int i = 0; i < nj1; ++i) {
+          last1 = other;
+          other.next(2, SV);
+        }
+        bool ok = njobs == 0 || kt_warp_wait(bar(XB_OF + last.st), last.ph);
         // the second slot's softmax first: it ends once all of its products but the last are done
         if (ok) ok = kt_warp_wait(bar(XB_MRG), mc & 1);
-        if (ok && nj1 > 0) ok = kt_warp_wait(bar(XB_OF + 3), (js1 - 1) & 1);
+        if (ok && nj1 > 0) ok = kt_warp_wait(bar(XB_OF + PT_MAXST + last1.st), last1.ph);
         if (!ok) { timed_out = true; break; }
         tc_fence_after();
         const float2 ml1 = s_ml[r];
@@ -528,7 +632,7 @@ template <int DH> static cudaError_t tc_go(PtArgs& g, cudaStream_t st) {
   constexpr size_t CHUNK = DH / 64 * 128 * 128, limit = 225 * 1024;
   static unsigned long long done = 0;
   for (int kind = 0; kind < 2; ++kind) {
-    const int stages = (int)((limit - 1024) / CHUNK) - g.nt[kind];
+    const int stages = (int)((limit - 1024) / CHUNK) - 2;   // (two tiles of queries)
     if (g.nt[kind] == 1) {                           // even depths: see above
       g.sk[kind] = stages >= 6 ? 4 : 2;
       g.sv[kind] = stages - g.sk[kind] >= 4 ? 4 : 2;

@@ -42,12 +42,27 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Wait for the phase of `parity` to complete; false after the time limit.
+// The same, and the hardware may let the thread sleep for so many nanoseconds until then.
+__device__ __forceinline__ bool mbar_try_for(uint32_t bar, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(ns)
+      : "memory");
+  return ok != 0;
+}
+// Wait for the phase of `parity` to complete; false after the time limit.  A waiting thread sleeps: one that
+// tries and reads the timer (500 cycles) in turn takes issue slots and notices late.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-  if (mbar_try(bar, parity)) return true;
-  const uint64_t t0 = gtimer();
-  while (!mbar_try(bar, parity))
-    if (gtimer() - t0 > limit_ns) return false;
+  uint64_t t0 = 0;
+  while (!mbar_try_for(bar, parity, 100000)) {
+    const uint64_t t = gtimer();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > limit_ns) return false;
+  }
   return true;
 }
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y,
