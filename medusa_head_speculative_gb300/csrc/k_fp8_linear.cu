@@ -58,6 +58,31 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, ui
 // Instruction descriptor, kind::f8f6f4: fp32 D, e4m3 A and B, both K-major, M x N.
 constexpr uint32_t idesc_e4m3(int M, int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24); }
 
+// 32 columns of this thread's TMEM lane.  Until the wait the registers are not there yet: the wait takes them as
+// its operands too, so that nothing that reads them can come before it.
+__device__ __forceinline__ void fl_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,"
+      "%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+        "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void fl_ld_wait(uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+        "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+        "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]),
+        "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+      :
+      : "memory");
+}
+
 // One stretch of a tile's groups: j .. j + n - 1.
 struct FlSeg {
   int m, n0, j, n;                                  // tile row, first weight row
@@ -101,27 +126,28 @@ __device__ __forceinline__ float2 fma2(float2 v, float2 s, float2 c) {
   return *reinterpret_cast<float2*>(&r);
 }
 
-// Four results (columns n .. n + 3 of row r): the gated product or the residual, and the store.
-template <typename T, bool GATED>
-__device__ __forceinline__ void fl_finish4(const Fp8LinearArgs& a, long r, int n, float (&y)[4], const float (&u)[4], bool vec) {
-  if (n >= a.n) return;
-  const int there = min(4, a.n - n);
-  T* dst = static_cast<T*>(a.y) + r * a.y_row + n;
-  if (GATED) {
+// silu(x) u.  (__fdividef gives 0 where 1 + e^-x passes 2^126; the quotient is below 10^-35 there.)
+__device__ __forceinline__ float gate(float x, float u) { return __fdividef(x, 1.f + expf(-x)) * u; }
+
+// Four residuals (columns n .. n + 3 of row r), and four results; vec: aligned, and all four exist.
+template <typename T> __device__ __forceinline__ void fl_add4(const Fp8LinearArgs& a, long r, int n, bool vec, float (&x)[4]) {
+  const T* src = static_cast<const T*>(a.add) + r * a.add_row + n;
+  if (vec) {
+    load4(src, true, x);
+  } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = y[e] / (1.f + expf(-y[e])) * u[e];
-  } else if (a.add) {
-    const T* src = static_cast<const T*>(a.add) + r * a.add_row + n;
-    float x[4] = {};
-    if (there == 4) load4(src, vec, x);
-    else
-      for (int e = 0; e < there; ++e) x[e] = to_f32(src[e]);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] += x[e];
+    for (int e = 0; e < 4; ++e) x[e] = n + e < a.n ? to_f32(src[e]) : 0.f;
   }
-  if (there == 4) save4(dst, vec, y);
-  else
-    for (int e = 0; e < there; ++e) dst[e] = from_f32<T>(y[e]);
+}
+template <typename T> __device__ __forceinline__ void fl_save4(const Fp8LinearArgs& a, long r, int n, bool vec, const float (&y)[4]) {
+  T* dst = static_cast<T*>(a.y) + r * a.y_row + n;
+  if (vec) {
+    save4(dst, true, y);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < a.n) dst[e] = from_f32<T>(y[e]);
+  }
 }
 template <typename T> __device__ __forceinline__ bool fl_vec(const Fp8LinearArgs& a) {
   const uintptr_t n = 4 * sizeof(T);
@@ -239,7 +265,7 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_linear_kernel(const __grid_
       float2 acc[HC / 2];
 #pragma unroll
       for (int i = 0; i < HC / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-      constexpr int AHEAD = 3;                       // groups whose scales are in flight
+      constexpr int AHEAD = 4;                       // groups whose scales are in flight, each in registers of its own
       float fx[AHEAD], fw[AHEAD], fu[AHEAD];
       if (live) {
 #pragma unroll
@@ -250,38 +276,42 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_linear_kernel(const __grid_
           fu[i] = GATED ? pu[j] : 0.f;
         }
       }
-      for (int i = 0; i < s.n; ++i, ++c) {
-        const int buf = c & 1;
-        const bool got = __all_sync(0xffffffffu, mbar_wait(bar(FB_TF + buf), (c >> 1) & 1, TC_TIMEOUT_NS));
-        if (!got) { timed_out = true; break; }
-        tc_fence_after();
-        if (live) {
-          const float s0 = fx[0] * fw[0], s1 = GATED ? fx[0] * fu[0] : s0;
+      for (int i0 = 0; i0 < s.n && !timed_out; i0 += AHEAD) {
 #pragma unroll
-          for (int q = 0; q + 1 < AHEAD; ++q) {
-            fx[q] = fx[q + 1];
-            fw[q] = fw[q + 1];
-            fu[q] = fu[q + 1];
+        for (int u = 0; u < AHEAD; ++u) {
+          if (i0 + u >= s.n || timed_out) continue;
+          const int buf = c & 1;
+          if (!__all_sync(0xffffffffu, mbar_wait(bar(FB_TF + buf), (c >> 1) & 1, TC_TIMEOUT_NS))) {
+            timed_out = true;
+            continue;
           }
-          const int j = min(i + AHEAD, s.n - 1);
-          fx[AHEAD - 1] = px[j];
-          fw[AHEAD - 1] = pw[j];
-          if (GATED) fu[AHEAD - 1] = pu[j];
+          tc_fence_after();
+          if (live) {
+            const float s0 = fx[u] * fw[u], s1 = GATED ? fx[u] * fu[u] : s0;
+            const int j = min(i0 + u + AHEAD, s.n - 1);
+            fx[u] = px[j];
+            fw[u] = pw[j];
+            if (GATED) fu[u] = pu[j];
+            // 32 columns on their way while 32 are added up (gated: 64 columns of the first matrix, then of the second)
+            auto col = [&](int q) { return lanes + buf * BN + (GATED ? (q >> 1) * 128 + half * 64 + (q & 1) * 32 : half * HC + q * 32); };
+            uint32_t v[2][32];
+            fl_ld32(col(0), v[0]);
 #pragma unroll
-          for (int q = 0; q < HC / 64; ++q) {
-            // gated: 64 columns of the first matrix, then 64 of the second
-            const uint32_t col = buf * BN + (GATED ? q * 128 + half * 64 : half * HC + q * 64);
-            float v[64];
-            tmem_ld64(lanes + col, v);
-            const float sc = GATED && q == 1 ? s1 : s0;
+            for (int q = 0; q < HC / 32; ++q) {
+              fl_ld_wait(v[q & 1]);
+              if (q + 1 < HC / 32) fl_ld32(col(q + 1), v[(q + 1) & 1]);
+              const float sc = GATED && q >= 2 ? s1 : s0;
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              acc[q * 32 + e] = fma2(make_float2(v[2 * e], v[2 * e + 1]), make_float2(sc, sc), acc[q * 32 + e]);
+              for (int e = 0; e < 16; ++e)
+                acc[q * 16 + e] = fma2(make_float2(__uint_as_float(v[q & 1][2 * e]), __uint_as_float(v[q & 1][2 * e + 1])),
+                                       make_float2(sc, sc), acc[q * 16 + e]);
+            }
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(FB_TE + buf));
+          ++c;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(FB_TE + buf));
       }
       if (timed_out || !live) continue;
       if (s.slot >= 0) {
@@ -295,18 +325,33 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_linear_kernel(const __grid_
                   make_float4(acc[q * 32 + e / 2].x, acc[q * 32 + e / 2].y, acc[q * 32 + e / 2 + 1].x, acc[q * 32 + e / 2 + 1].y);
         }
       } else if (ok) {
-        const bool vec = fl_vec<T>(a);
+        // 32 columns at a time: their residuals are all asked for before the first store (one after the
+        // other each would wait for memory: 31,000 cycles a tile of 8192 x 5120 x 13824, of 145,000)
         constexpr int N = GATED ? 64 : HC;
+        const int c0 = s.n0 + half * N;
+        const bool vec = fl_vec<T>(a) && c0 + N <= a.n;
 #pragma unroll
-        for (int e = 0; e < N; e += 4) {
-          float y[4] = {acc[e / 2].x, acc[e / 2].y, acc[e / 2 + 1].x, acc[e / 2 + 1].y}, u[4] = {};
-          if (GATED) {
-            u[0] = acc[32 + e / 2].x;
-            u[1] = acc[32 + e / 2].y;
-            u[2] = acc[32 + e / 2 + 1].x;
-            u[3] = acc[32 + e / 2 + 1].y;
+        for (int e0 = 0; e0 < N; e0 += 32) {
+          float add[8][4] = {};
+          if (!GATED && a.add) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) fl_add4<T>(a, r, c0 + e0 + 4 * e, vec, add[e]);
           }
-          fl_finish4<T, GATED>(a, r, s.n0 + half * N + e, y, u, vec);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int i = (e0 + 4 * e) / 2;
+            float y[4] = {acc[i].x, acc[i].y, acc[i + 1].x, acc[i + 1].y};
+            if (GATED) {
+              y[0] = gate(y[0], acc[32 + i].x);
+              y[1] = gate(y[1], acc[32 + i].y);
+              y[2] = gate(y[2], acc[32 + i + 1].x);
+              y[3] = gate(y[3], acc[32 + i + 1].y);
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) y[q] += add[e][q];
+            }
+            fl_save4<T>(a, r, c0 + e0 + 4 * e, vec, y);
+          }
         }
       }
     }
@@ -365,7 +410,17 @@ __global__ void __launch_bounds__(256) fp8_join_kernel(const __grid_constant__ F
       u[3] += q[b].w;
     }
   }
-  fl_finish4<T, GATED>(a, r, n0 + col, y, u, fl_vec<T>(a));
+  const bool vec = fl_vec<T>(a) && n0 + col + 4 <= a.n;
+  if (GATED) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) y[q] = gate(y[q], u[q]);
+  } else if (a.add) {
+    float add[4];
+    fl_add4<T>(a, r, n0 + col, vec, add);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) y[q] += add[q];
+  }
+  fl_save4<T>(a, r, n0 + col, vec, y);
 }
 
 // ------------------------------------------------------------------ host side
@@ -390,9 +445,18 @@ static FlPlan fl_plan(int rows, int n, int kb, bool gated, int num_sms) {
   p.nt = (n + oc - 1) / oc;
   const long tiles = (long)p.mt * p.nt;
   p.whole = (int)(tiles / num_sms * num_sms);
+  // The last tiles whole, too, or in shares: shares save the time in which CTAs without a tile would wait, and cost
+  // partials that go through memory and a kernel that joins them.  In microseconds: a group of a tile takes 0.35,
+  // or with one row of tiles, where weights are waited for, 0.36 a 16 KB of them; partials 1.5 and what their bytes
+  // take at 4 TB/s.
+  const long over = tiles - p.whole;
+  const double group = p.mt > 1 ? 0.35 : 0.36 * p.bn / 128, rows1 = rows < 128 ? rows : 128;
+  const double saved = kb * group * (1.0 - (double)over / num_sms);
+  const double cost = 1.5 + 2.0 * (over + num_sms) * rows1 * p.bn * 4 / 4e6;
+  if (over > 0 && saved < cost) p.whole = (int)tiles;
   const long left = tiles - p.whole;
   p.shares = (int)std::min<long>(num_sms, left * kb);
-  p.ctas = p.whole ? num_sms : p.shares;
+  p.ctas = p.whole ? (int)std::min<long>(num_sms, tiles) : p.shares;
   return p;
 }
 
