@@ -38,6 +38,7 @@ struct FlArgs {
   CUtensorMap tx, tw[2];                            // rows: box {128, abox}; weights: box {128, 128}
   Fp8LinearArgs a;
   int abox, stages;                                 // rows of a copy (a multiple of 8), ring depth
+  uint32_t ring;                                    // bytes of the rings
   int mt, nt;                                       // tiles
   int whole, ctas;                                  // tiles taken whole, CTAs
   int shares;                                       // CTAs that share the groups of the other tiles
@@ -58,27 +59,21 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, ui
 // Instruction descriptor, kind::f8f6f4: fp32 D, e4m3 A and B, both K-major, M x N.
 constexpr uint32_t idesc_e4m3(int M, int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24); }
 
-// 32 columns of this thread's TMEM lane.  Until the wait the registers are not there yet: the wait takes them as
+// 16 columns of this thread's TMEM lane.  Until the wait the registers are not there yet: the wait takes them as
 // its operands too, so that nothing that reads them can come before it.
-__device__ __forceinline__ void fl_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void fl_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,"
-      "%31}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
-        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
-        "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void fl_ld_wait(uint32_t (&r)[32]) {
+__device__ __forceinline__ void fl_ld_wait(uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.wait::ld.sync.aligned;"
       : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-        "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
-        "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]),
-        "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+        "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
       :
       : "memory");
 }
@@ -147,6 +142,25 @@ template <typename T> __device__ __forceinline__ void fl_save4(const Fp8LinearAr
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       if (n + e < a.n) dst[e] = from_f32<T>(y[e]);
+  }
+}
+
+// A warp's 32 rows x 32 columns, a row a lane (v), turned in shared memory (`turn`, 32 x 33 floats of the warp)
+// so that eight lanes have a row's 32 columns, four each, and a store writes whole sectors (a row a lane: 32
+// sectors a store, 8 bytes of each; 27,000 cycles a tile of 128 x 256).  f(row, column, four values) for each.
+template <typename F> __device__ __forceinline__ void fl_turn(float* turn, int lane, const float (&v)[32], F f) {
+  __syncwarp();
+#pragma unroll
+  for (int e = 0; e < 32; ++e) turn[lane * 33 + e] = v[e];
+  __syncwarp();
+  const int c = (lane & 7) * 4;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const int row = q * 4 + (lane >> 3);
+    float y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = turn[row * 33 + c + e];
+    f(q, row, c, y);
   }
 }
 template <typename T> __device__ __forceinline__ bool fl_vec(const Fp8LinearArgs& a) {
@@ -257,7 +271,7 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_linear_kernel(const __grid_
     int c = 0;
     while (!timed_out && fl_next<OC>(g, walk, s)) {
       const long r = (long)s.m * 128 + wl * 32 + lane;
-      const bool live = (long)s.m * 128 + wl * 32 < a.rows, ok = r < a.rows;
+      const bool live = (long)s.m * 128 + wl * 32 < a.rows;
       const int nb0 = GATED || BN == 128 ? s.n0 / 128 : min(s.n0 / 128 + half, (a.n - 1) / 128);
       const float* px = a.xs + min(r, (long)a.rows - 1) * a.kb + s.j;
       const float* pw = a.ws[0] + (long)nb0 * a.kb + s.j;
@@ -292,19 +306,19 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_linear_kernel(const __grid_
             fx[u] = px[j];
             fw[u] = pw[j];
             if (GATED) fu[u] = pu[j];
-            // 32 columns on their way while 32 are added up (gated: 64 columns of the first matrix, then of the second)
-            auto col = [&](int q) { return lanes + buf * BN + (GATED ? (q >> 1) * 128 + half * 64 + (q & 1) * 32 : half * HC + q * 32); };
-            uint32_t v[2][32];
-            fl_ld32(col(0), v[0]);
+            // 16 columns on their way while 16 are added up (gated: 64 columns of the first matrix, then of the second)
+            auto col = [&](int q) { return lanes + buf * BN + (GATED ? (q >> 2) * 128 + half * 64 + (q & 3) * 16 : half * HC + q * 16); };
+            uint32_t v[2][16];
+            fl_ld16(col(0), v[0]);
 #pragma unroll
-            for (int q = 0; q < HC / 32; ++q) {
+            for (int q = 0; q < HC / 16; ++q) {
               fl_ld_wait(v[q & 1]);
-              if (q + 1 < HC / 32) fl_ld32(col(q + 1), v[(q + 1) & 1]);
-              const float sc = GATED && q >= 2 ? s1 : s0;
+              if (q + 1 < HC / 16) fl_ld16(col(q + 1), v[(q + 1) & 1]);
+              const float sc = GATED && q >= 4 ? s1 : s0;
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                acc[q * 16 + e] = fma2(make_float2(__uint_as_float(v[q & 1][2 * e]), __uint_as_float(v[q & 1][2 * e + 1])),
-                                       make_float2(sc, sc), acc[q * 16 + e]);
+              for (int e = 0; e < 8; ++e)
+                acc[q * 8 + e] = fma2(make_float2(__uint_as_float(v[q & 1][2 * e]), __uint_as_float(v[q & 1][2 * e + 1])),
+                                      make_float2(sc, sc), acc[q * 8 + e]);
             }
           }
           tc_fence_before();
@@ -314,44 +328,54 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_linear_kernel(const __grid_
         }
       }
       if (timed_out || !live) continue;
+      float* turn = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)) + g.ring) + (warp - 4) * 32 * 33;
+      const int r0 = s.m * 128 + wl * 32, rows = min(32, a.rows - r0);      // (rows < 2^24)
       if (s.slot >= 0) {
-        if (ok) {
-          float* dst = g.part + (s.slot * 128 + wl * 32 + lane) * BN;
 #pragma unroll
-          for (int q = 0; q < HC / 64; ++q)
+        for (int q = 0; q < HC / 32; ++q) {
+          float v[32];
 #pragma unroll
-            for (int e = 0; e < 64; e += 4)
-              *reinterpret_cast<float4*>(dst + (GATED ? q * 128 + half * 64 : half * HC + q * 64) + e) =
-                  make_float4(acc[q * 32 + e / 2].x, acc[q * 32 + e / 2].y, acc[q * 32 + e / 2 + 1].x, acc[q * 32 + e / 2 + 1].y);
+          for (int e = 0; e < 16; ++e) {
+            v[2 * e] = acc[q * 16 + e].x;
+            v[2 * e + 1] = acc[q * 16 + e].y;
+          }
+          float* dst = g.part + (s.slot * 128 + wl * 32) * BN + (GATED ? (q >> 1) * 128 + half * 64 + (q & 1) * 32 : half * HC + q * 32);
+          fl_turn(turn, lane, v, [&](int, int row, int c, float (&y)[4]) {
+            if (row < rows) *reinterpret_cast<float4*>(dst + row * BN + c) = make_float4(y[0], y[1], y[2], y[3]);
+          });
         }
-      } else if (ok) {
-        // 32 columns at a time: their residuals are all asked for before the first store (one after the
-        // other each would wait for memory: 31,000 cycles a tile of 8192 x 5120 x 13824, of 145,000)
+      } else {
         constexpr int N = GATED ? 64 : HC;
-        const int c0 = s.n0 + half * N;
-        const bool vec = fl_vec<T>(a) && c0 + N <= a.n;
+        const bool al = fl_vec<T>(a);
 #pragma unroll
-        for (int e0 = 0; e0 < N; e0 += 32) {
-          float add[8][4] = {};
+        for (int q = 0; q < N / 32; ++q) {
+          const int n0 = s.n0 + half * N + q * 32, n = n0 + (lane & 7) * 4;
+          const bool vec = al && n + 4 <= a.n;
+          float v[32];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            v[2 * e] = acc[q * 16 + e].x;
+            v[2 * e + 1] = acc[q * 16 + e].y;
+            if (GATED) {
+              v[2 * e] = gate(v[2 * e], acc[32 + q * 16 + e].x);
+              v[2 * e + 1] = gate(v[2 * e + 1], acc[32 + q * 16 + e].y);
+            }
+          }
+          float add[8][4] = {};                        // all asked for before the first store
           if (!GATED && a.add) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) fl_add4<T>(a, r, c0 + e0 + 4 * e, vec, add[e]);
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int i = (e0 + 4 * e) / 2;
-            float y[4] = {acc[i].x, acc[i].y, acc[i + 1].x, acc[i + 1].y};
-            if (GATED) {
-              y[0] = gate(y[0], acc[32 + i].x);
-              y[1] = gate(y[1], acc[32 + i].y);
-              y[2] = gate(y[2], acc[32 + i + 1].x);
-              y[3] = gate(y[3], acc[32 + i + 1].y);
-            } else {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) y[q] += add[e][q];
+            for (int i = 0; i < 8; ++i) {
+              const int row = i * 4 + (lane >> 3);
+              if (row < rows && n < a.n) fl_add4<T>(a, r0 + row, n, vec, add[i]);
             }
-            fl_save4<T>(a, r, c0 + e0 + 4 * e, vec, y);
           }
+          fl_turn(turn, lane, v, [&](int i, int row, int c, float (&y)[4]) {
+            if (row < rows && n < a.n) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) y[e] += add[i][e];
+              fl_save4<T>(a, r0 + row, n, vec, y);
+            }
+          });
         }
       }
     }
@@ -467,12 +491,13 @@ size_t fp8_linear_partials(int max_rows, int n, int kb, bool gated, int num_sms)
 
 template <typename T, int BN, bool GATED> static cudaError_t linear_go(FlArgs& g, int num_sms, cudaStream_t st) {
   static unsigned long long allowed = 0;
-  constexpr size_t limit = 225 * 1024;
+  constexpr size_t turn = 8 * 32 * 33 * sizeof(float), limit = 226 * 1024;
   const size_t stage = BN * FL_ROW + g.abox * FL_ROW, fixed = 1024 + (128 - g.abox) * FL_ROW;
-  g.stages = (int)std::min<size_t>(FL_MAXST, (limit - fixed) / stage);
+  g.stages = (int)std::min<size_t>(FL_MAXST, (limit - fixed - turn) / stage);
+  g.ring = (uint32_t)(fixed - 1024 + g.stages * stage);
   cudaError_t e = allow_smem(fp8_linear_kernel<T, BN, GATED>, limit, &allowed);
   if (e != cudaSuccess) return e;
-  e = launch_kernel(fp8_linear_kernel<T, BN, GATED>, dim3(g.ctas), dim3(FL_THREADS), fixed + g.stages * stage, st, 1, g);
+  e = launch_kernel(fp8_linear_kernel<T, BN, GATED>, dim3(g.ctas), dim3(FL_THREADS), fixed + g.stages * stage + turn, st, 1, g);
   const int left = g.mt * g.nt - g.whole;
   if (e != cudaSuccess || left == 0 || g.shares == left) return e;      // (every CTA has one tile: no partials)
   const int rows = std::min(g.a.rows, 128);
