@@ -10,7 +10,10 @@
 //
 //   warp 0 (one lane)  copies: rows and weights of a group, 128 bytes a row, through a ring of stages
 //   warp 1 (one lane)  MMAs
-//   warps 4-7, 8-11    promote half the columns each, then write y (or a partial)
+//   warps 2, 3         scales of the tile's rows and weights, for each group, into a ring in shared memory (read
+//                      by the promoting threads themselves, a row each, they took 256 cycles of the L1 a group)
+//   warps 4-7, 8-11    promote half the columns each, then write y (or a partial); four warpgroups with a quarter
+//                      each are no faster
 //
 // One CTA per SM.  The work is dealt out by groups: whole tiles while there is one for every CTA, the tiles
 // that are left (with few rows: all) as an even share of their groups in one line, so that weights stream
@@ -28,11 +31,12 @@
 
 namespace medusa {
 
-constexpr int FL_THREADS = 384, FL_MAXST = 8;
+constexpr int FL_PROMOTE = 2, FL_THREADS = 128 * (1 + FL_PROMOTE), FL_MAXST = 8;
 constexpr uint32_t FL_ROW = 128;                    // bytes of a row in a stage
-// Registers a thread: 168 at launch (384 x 168 = 64512), then 56 for copies and MMAs and 216 to promote:
-// 56 + 2 x 216 = 488 <= 3 x 168.
-constexpr int FL_REG_ISSUE = 56, FL_REG_PROMOTE = 216;
+constexpr int FL_SC = 8;                            // groups in the ring of scales: 128 rows' and two of weights each
+// Registers a thread: 168 at launch (384 x 168 = 64512), then 72 for copies and MMAs and 208 to promote:
+// 72 + 2 x 208 = 488 <= 3 x 168.
+constexpr int FL_REG_ISSUE = 72, FL_REG_PROMOTE = 208;
 
 struct FlArgs {
   CUtensorMap tx, tw[2];                            // rows: box {128, abox}; weights: box {128, 128}
@@ -46,7 +50,20 @@ struct FlArgs {
   int rows_last;                                    // weights are read once (mt == 1)
 };
 
-enum { FB_FULL = 0, FB_EMPTY = FL_MAXST, FB_TF = 2 * FL_MAXST, FB_TE = FB_TF + 2, FB_END = FB_TE + 2, FB_COUNT = FB_END + 1 };
+// FULL: a stage has landed.  DONE: its products are in an accumulator, and the stage is free (one barrier for both: a
+// commit costs the tensor cores 50 to 75 cycles).  TE: an accumulator has been read.  SF, SE: scales have been written, read.  END: every MMA is done.
+enum { FB_FULL = 0, FB_DONE = FL_MAXST, FB_TE = 2 * FL_MAXST, FB_SF = FB_TE + 2, FB_SE = FB_SF + FL_SC,
+       FB_END = FB_SE + FL_SC, FB_COUNT = FB_END + 1 };
+// A place in the ring of stages (a division by its depth would take longer than what it is needed for).
+struct FlRing {
+  int st, ph;
+  __device__ __forceinline__ void next(int depth) {
+    if (++st == depth) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+};
 
 __device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -145,22 +162,22 @@ template <typename T> __device__ __forceinline__ void fl_save4(const Fp8LinearAr
   }
 }
 
-// A warp's 32 rows x 32 columns, a row a lane (v), turned in shared memory (`turn`, 32 x 33 floats of the warp)
-// so that eight lanes have a row's 32 columns, four each, and a store writes whole sectors (a row a lane: 32
-// sectors a store, 8 bytes of each; 27,000 cycles a tile of 128 x 256).  f(row, column, four values) for each.
-template <typename F> __device__ __forceinline__ void fl_turn(float* turn, int lane, const float (&v)[32], F f) {
+// A warp's 32 rows x 16 columns, a row a lane (v), turned in shared memory (`turn`, 2 KB of the warp) so that four
+// lanes have a row's 16 columns, four each, and a store writes whole sectors (a row a lane: 32 sectors a store, 8 bytes
+// of each; 27,000 cycles a tile of 128 x 256).  The 16-byte units of a row change places by its number, so that
+// neither way meets a bank twice.  f(step, row, column, four values) for each.
+template <typename F> __device__ __forceinline__ void fl_turn(float4* turn, int lane, const float2 (&v)[8], F f) {
   __syncwarp();
 #pragma unroll
-  for (int e = 0; e < 32; ++e) turn[lane * 33 + e] = v[e];
+  for (int u = 0; u < 4; ++u)
+    turn[lane * 4 + (u ^ ((lane >> 1) & 3))] = make_float4(v[2 * u].x, v[2 * u].y, v[2 * u + 1].x, v[2 * u + 1].y);
   __syncwarp();
-  const int c = (lane & 7) * 4;
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const int row = q * 4 + (lane >> 3);
-    float y[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = turn[row * 33 + c + e];
-    f(q, row, c, y);
+  for (int i = 0; i < 4; ++i) {
+    const int row = i * 8 + (lane >> 2);
+    const float4 x = turn[row * 4 + ((lane & 3) ^ ((row >> 1) & 3))];
+    float y[4] = {x.x, x.y, x.z, x.w};
+    f(i, row, (lane & 3) * 4, y);
   }
 }
 template <typename T> __device__ __forceinline__ bool fl_vec(const Fp8LinearArgs& a) {
@@ -171,11 +188,13 @@ template <typename T> __device__ __forceinline__ bool fl_vec(const Fp8LinearArgs
 template <typename T, int BN, bool GATED>
 __global__ void __launch_bounds__(FL_THREADS, 1) fp8_linear_kernel(const __grid_constant__ FlArgs g) {
   constexpr int OC = GATED ? BN / 2 : BN;            // results of a tile's row
-  constexpr int HC = BN / 2;                         // columns a promoting thread adds up
+  constexpr int HC = BN / FL_PROMOTE;                // columns a promoting thread adds up
+  constexpr int GQ = HC / 32;                        // gated: 16 columns' steps of either matrix
   constexpr uint32_t WB = BN * FL_ROW;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t bars[FB_COUNT];
   __shared__ uint32_t tmem_slot;
+  __shared__ float s_x[FL_SC][128], s_w[FL_SC][2];   // scales
   __shared__ int s_issued, s_waited, s_abort;
   const Fp8LinearArgs& a = g.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, ST = g.stages;
@@ -187,11 +206,14 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_linear_kernel(const __grid_
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(bar(FB_FULL + i), 1);
-      mbar_init(bar(FB_EMPTY + i), 1);
+      mbar_init(bar(FB_DONE + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(FB_TF + i), 1);
-      mbar_init(bar(FB_TE + i), 8);
+      mbar_init(bar(FB_TE + i), 4 * FL_PROMOTE);
+    }
+    for (int i = 0; i < FL_SC; ++i) {
+      mbar_init(bar(FB_SF + i), 64);
+      mbar_init(bar(FB_SE + i), 4 * FL_PROMOTE);
     }
     mbar_init(bar(FB_END), 1);
     s_issued = s_waited = s_abort = 0;
@@ -207,6 +229,7 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_linear_kernel(const __grid_
   auto aborted = [&]() { return *(volatile int*)&s_abort != 0; };
   FlWalk walk = fl_start<OC>(g);
   FlSeg s;
+  FlRing k = {0, 0};
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FL_REG_ISSUE));
     if (warp == 0 && lane == 0) {
@@ -228,148 +251,170 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_linear_kernel(const __grid_
       pdl_wait();
       while (!timed_out && fl_next<OC>(g, walk, s)) {
         for (int i = 0; i < s.n; ++i, ++c) {
-          const int st = c % ST;
           if (c >= pre) {
-            if (!mbar_wait(bar(FB_EMPTY + st), ((c / ST) & 1) ^ 1, TC_TIMEOUT_NS)) { timed_out = true; break; }
-            load_w(s, s.j + i, st);
+            if (c >= ST && !mbar_wait(bar(FB_DONE + k.st), k.ph ^ 1, TC_TIMEOUT_NS)) { timed_out = true; break; }
+            load_w(s, s.j + i, k.st);
             s_issued = c + 1;
           }
-          tma_load_2d(xs + st * xb, &g.tx, (s.j + i) * 128, s.m * 128, bar(FB_FULL + st), pol_x);
+          tma_load_2d(xs + k.st * xb, &g.tx, (s.j + i) * 128, s.m * 128, bar(FB_FULL + k.st), pol_x);
+          k.next(ST);
         }
         if (aborted()) break;
       }
       for (; c < pre; ++c)                           // (left early) a stage's weights are in flight: let it fill
-        tma_load_2d(xs + (c % ST) * xb, &g.tx, 0, 0, bar(FB_FULL + c % ST), pol_x);
+        tma_load_2d(xs + c * xb, &g.tx, 0, 0, bar(FB_FULL + c), pol_x);
     } else if (warp == 1 && lane == 0) {
       // ------------------------------------------------------------ MMAs
       const uint32_t idesc = idesc_e4m3(128, BN);
       int c = 0;
       while (!timed_out && fl_next<OC>(g, walk, s)) {
         for (int i = 0; i < s.n; ++i, ++c) {
-          const int st = c % ST, buf = c & 1;
-          if (!mbar_wait(bar(FB_FULL + st), (c / ST) & 1, TC_TIMEOUT_NS)) { timed_out = true; break; }
+          const int buf = c & 1;
+          if (!mbar_wait(bar(FB_FULL + k.st), k.ph, TC_TIMEOUT_NS)) { timed_out = true; break; }
           s_waited = c + 1;
           if (!mbar_wait(bar(FB_TE + buf), ((c >> 1) & 1) ^ 1, TC_TIMEOUT_NS)) { timed_out = true; break; }
           tc_fence_after();
-          const uint64_t da = sw128_desc(xs + st * xb), db = sw128_desc(ws + st * WB);
+          const uint64_t da = sw128_desc(xs + k.st * xb), db = sw128_desc(ws + k.st * WB);
 #pragma unroll
           for (int q = 0; q < 4; ++q) umma_e4m3(tmem + buf * BN, da + 2 * q, db + 2 * q, idesc, q > 0);
-          umma_commit(bar(FB_EMPTY + st));
-          umma_commit(bar(FB_TF + buf));
+          umma_commit(bar(FB_DONE + k.st));
+          k.next(ST);
         }
         if (aborted()) break;
       }
       umma_commit(bar(FB_END));                      // arrives once every MMA issued above is done
+    } else if (warp >= 2) {
+      // ------------------------------------------------------------ scales: rows t and t + 64 of a tile a thread
+      const int t = tid - 64;
+      const bool quads = a.kb % 4 == 0 && ((uintptr_t)a.xs & 15) == 0;
+      pdl_wait();
+      int c = 0;
+      while (!timed_out && fl_next<OC>(g, walk, s)) {
+        const float* x[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) x[h] = a.xs + min((long)s.m * 128 + t + 64 * h, (long)a.rows - 1) * a.kb;
+        // the weights' scales: of the two blocks of columns, or of the two matrices (one thread each)
+        const int last = (a.n - 1) / 128;
+        const float* w = a.ws[GATED ? t & 1 : 0] + (long)min(s.n0 / 128 + (GATED ? 0 : t & 1), last) * a.kb;
+        for (int i = s.j & ~3; i < s.j + s.n && !timed_out; i += 4) {      // four groups' loads at a time
+          float f[2][4], u[4] = {};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (quads) {
+              const float4 v = *reinterpret_cast<const float4*>(x[h] + i);
+              f[h][0] = v.x;
+              f[h][1] = v.y;
+              f[h][2] = v.z;
+              f[h][3] = v.w;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) f[h][e] = x[h][min(i + e, a.kb - 1)];
+            }
+          }
+          if (t < 2) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[e] = w[min(i + e, a.kb - 1)];
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (i + e < s.j || i + e >= s.j + s.n || timed_out) continue;
+            const int at = c % FL_SC;
+            if (!__all_sync(0xffffffffu, mbar_wait(bar(FB_SE + at), ((c / FL_SC) & 1) ^ 1, TC_TIMEOUT_NS))) {
+              timed_out = true;
+              continue;
+            }
+            s_x[at][t] = f[0][e];
+            s_x[at][t + 64] = f[1][e];
+            if (t < 2) s_w[at][t] = u[e];
+            mbar_arrive(bar(FB_SF + at));
+            ++c;
+          }
+        }
+        if (aborted()) break;
+      }
     }
   } else {
     // -------------------------------------------------------------- promote
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FL_REG_PROMOTE));
-    const int half = (warp >> 2) - 1, wl = warp & 3;
-    // columns of this thread: HC from half * HC on, or (gated) HC / 2 of either matrix
+    const int part = (warp >> 2) - 1, wl = warp & 3;
+    // columns of this thread: HC from part * HC on, or (gated) HC / 2 of either matrix
     const uint32_t lanes = tmem + ((uint32_t)(wl * 32) << 16);
     pdl_wait();
     int c = 0;
     while (!timed_out && fl_next<OC>(g, walk, s)) {
-      const long r = (long)s.m * 128 + wl * 32 + lane;
       const bool live = (long)s.m * 128 + wl * 32 < a.rows;
-      const int nb0 = GATED || BN == 128 ? s.n0 / 128 : min(s.n0 / 128 + half, (a.n - 1) / 128);
-      const float* px = a.xs + min(r, (long)a.rows - 1) * a.kb + s.j;
-      const float* pw = a.ws[0] + (long)nb0 * a.kb + s.j;
-      const float* pu = GATED ? a.ws[1] + (long)nb0 * a.kb + s.j : pw;
       float2 acc[HC / 2];
 #pragma unroll
       for (int i = 0; i < HC / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-      constexpr int AHEAD = 4;                       // groups whose scales are in flight, each in registers of its own
-      float fx[AHEAD], fw[AHEAD], fu[AHEAD];
-      if (live) {
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-          const int j = min(i, s.n - 1);
-          fx[i] = px[j];
-          fw[i] = pw[j];
-          fu[i] = GATED ? pu[j] : 0.f;
+      for (int i = 0; i < s.n; ++i, ++c) {
+        const int buf = c & 1, at = c % FL_SC;
+        const bool got = mbar_wait(bar(FB_SF + at), (c / FL_SC) & 1, TC_TIMEOUT_NS) && mbar_wait(bar(FB_DONE + k.st), k.ph, TC_TIMEOUT_NS);
+        if (!__all_sync(0xffffffffu, got)) {
+          timed_out = true;
+          break;
         }
-      }
-      for (int i0 = 0; i0 < s.n && !timed_out; i0 += AHEAD) {
+        k.next(ST);
+        tc_fence_after();
+        if (live) {
+          const float x = s_x[at][wl * 32 + lane], s0 = x * s_w[at][GATED || BN == 128 ? 0 : part], s1 = GATED ? x * s_w[at][1] : s0;
+          // 16 columns on their way while 16 are added up (gated: of the first matrix, then of the second)
+          auto col = [&](int q) { return lanes + buf * BN + (GATED ? (q / GQ) * 128 + part * (HC / 2) + (q % GQ) * 16 : part * HC + q * 16); };
+          uint32_t v[2][16];
+          fl_ld16(col(0), v[0]);
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
-          if (i0 + u >= s.n || timed_out) continue;
-          const int buf = c & 1;
-          if (!__all_sync(0xffffffffu, mbar_wait(bar(FB_TF + buf), (c >> 1) & 1, TC_TIMEOUT_NS))) {
-            timed_out = true;
-            continue;
+          for (int q = 0; q < HC / 16; ++q) {
+            fl_ld_wait(v[q & 1]);
+            if (q + 1 < HC / 16) fl_ld16(col(q + 1), v[(q + 1) & 1]);
+            const float sc = GATED && q >= GQ ? s1 : s0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              acc[q * 8 + e] = fma2(make_float2(__uint_as_float(v[q & 1][2 * e]), __uint_as_float(v[q & 1][2 * e + 1])),
+                                    make_float2(sc, sc), acc[q * 8 + e]);
           }
-          tc_fence_after();
-          if (live) {
-            const float s0 = fx[u] * fw[u], s1 = GATED ? fx[u] * fu[u] : s0;
-            const int j = min(i0 + u + AHEAD, s.n - 1);
-            fx[u] = px[j];
-            fw[u] = pw[j];
-            if (GATED) fu[u] = pu[j];
-            // 16 columns on their way while 16 are added up (gated: 64 columns of the first matrix, then of the second)
-            auto col = [&](int q) { return lanes + buf * BN + (GATED ? (q >> 2) * 128 + half * 64 + (q & 3) * 16 : half * HC + q * 16); };
-            uint32_t v[2][16];
-            fl_ld16(col(0), v[0]);
-#pragma unroll
-            for (int q = 0; q < HC / 16; ++q) {
-              fl_ld_wait(v[q & 1]);
-              if (q + 1 < HC / 16) fl_ld16(col(q + 1), v[(q + 1) & 1]);
-              const float sc = GATED && q >= 4 ? s1 : s0;
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                acc[q * 8 + e] = fma2(make_float2(__uint_as_float(v[q & 1][2 * e]), __uint_as_float(v[q & 1][2 * e + 1])),
-                                      make_float2(sc, sc), acc[q * 8 + e]);
-            }
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(FB_TE + buf));
-          ++c;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(FB_TE + buf));
+          mbar_arrive(bar(FB_SE + at));
         }
       }
       if (timed_out || !live) continue;
-      float* turn = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)) + g.ring) + (warp - 4) * 32 * 33;
+      float4* turn = reinterpret_cast<float4*>(smem_raw + (base - smem_u32(smem_raw)) + g.ring) + (warp - 4) * 128;
       const int r0 = s.m * 128 + wl * 32, rows = min(32, a.rows - r0);      // (rows < 2^24)
       if (s.slot >= 0) {
 #pragma unroll
-        for (int q = 0; q < HC / 32; ++q) {
-          float v[32];
+        for (int q = 0; q < HC / 16; ++q) {
+          float2 v[8];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            v[2 * e] = acc[q * 16 + e].x;
-            v[2 * e + 1] = acc[q * 16 + e].y;
-          }
-          float* dst = g.part + (s.slot * 128 + wl * 32) * BN + (GATED ? (q >> 1) * 128 + half * 64 + (q & 1) * 32 : half * HC + q * 32);
-          fl_turn(turn, lane, v, [&](int, int row, int c, float (&y)[4]) {
-            if (row < rows) *reinterpret_cast<float4*>(dst + row * BN + c) = make_float4(y[0], y[1], y[2], y[3]);
+          for (int e = 0; e < 8; ++e) v[e] = acc[q * 8 + e];
+          float* dst = g.part + (s.slot * 128 + wl * 32) * BN + (GATED ? (q / GQ) * 128 + part * (HC / 2) + (q % GQ) * 16 : part * HC + q * 16);
+          fl_turn(turn, lane, v, [&](int, int row, int c4, float (&y)[4]) {
+            if (row < rows) *reinterpret_cast<float4*>(dst + row * BN + c4) = make_float4(y[0], y[1], y[2], y[3]);
           });
         }
       } else {
-        constexpr int N = GATED ? 64 : HC;
+        constexpr int N = GATED ? HC / 2 : HC;
         const bool al = fl_vec<T>(a);
 #pragma unroll
-        for (int q = 0; q < N / 32; ++q) {
-          const int n0 = s.n0 + half * N + q * 32, n = n0 + (lane & 7) * 4;
+        for (int q = 0; q < N / 16; ++q) {
+          const int n = s.n0 + part * N + q * 16 + (lane & 3) * 4;
           const bool vec = al && n + 4 <= a.n;
-          float v[32];
+          float2 v[8];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            v[2 * e] = acc[q * 16 + e].x;
-            v[2 * e + 1] = acc[q * 16 + e].y;
-            if (GATED) {
-              v[2 * e] = gate(v[2 * e], acc[32 + q * 16 + e].x);
-              v[2 * e + 1] = gate(v[2 * e + 1], acc[32 + q * 16 + e].y);
-            }
+          for (int e = 0; e < 8; ++e) {
+            v[e] = acc[q * 8 + e];
+            if (GATED) v[e] = make_float2(gate(v[e].x, acc[HC / 4 + q * 8 + e].x), gate(v[e].y, acc[HC / 4 + q * 8 + e].y));
           }
-          float add[8][4] = {};                        // all asked for before the first store
+          float add[4][4] = {};                        // all asked for before the first store
           if (!GATED && a.add) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int row = i * 4 + (lane >> 3);
+            for (int i = 0; i < 4; ++i) {
+              const int row = i * 8 + (lane >> 2);
               if (row < rows && n < a.n) fl_add4<T>(a, r0 + row, n, vec, add[i]);
             }
           }
-          fl_turn(turn, lane, v, [&](int i, int row, int c, float (&y)[4]) {
+          fl_turn(turn, lane, v, [&](int i, int row, int, float (&y)[4]) {
             if (row < rows && n < a.n) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) y[e] += add[i][e];
@@ -491,7 +536,7 @@ size_t fp8_linear_partials(int max_rows, int n, int kb, bool gated, int num_sms)
 
 template <typename T, int BN, bool GATED> static cudaError_t linear_go(FlArgs& g, int num_sms, cudaStream_t st) {
   static unsigned long long allowed = 0;
-  constexpr size_t turn = 8 * 32 * 33 * sizeof(float), limit = 226 * 1024;
+  constexpr size_t turn = 4 * FL_PROMOTE * 2048, limit = 222 * 1024;
   const size_t stage = BN * FL_ROW + g.abox * FL_ROW, fixed = 1024 + (128 - g.abox) * FL_ROW;
   g.stages = (int)std::min<size_t>(FL_MAXST, (limit - fixed - turn) / stage);
   g.ring = (uint32_t)(fixed - 1024 + g.stages * stage);
