@@ -185,7 +185,7 @@ def lib():
         "medusa_fp8_get_status": (I, [P, P, C.POINTER(C.c_uint32)]),
         "medusa_fp8_round": (I, [P, P, I, I, C.c_longlong, P, P, I, P]),
         "medusa_fp8_read": (I, [P, P, P, I, I, P, I, C.c_longlong, P]),
-        "medusa_fp8_linear": (I, [P, C.POINTER(Fp8Product), P, SZ, P]),
+        "medusa_fp8_linear": (I, [P, C.c_char_p, P, SZ, P]),         # medusa_fp8_product as bytes
     }
     for name, (res, args) in sigs.items():
         f = getattr(L, name)
@@ -781,31 +781,34 @@ def _codes(what, h, t, s, rows, block, strides=False):
         _CODES, _FLOAT = (torch.float8_e4m3fn, torch.uint8), torch.float32
     if t.dtype not in _CODES or s.dtype is not _FLOAT:
         raise TypeError(f"{what}: float8_e4m3fn (or uint8) codes and float32 scales are needed, got {t.dtype}, {s.dtype}")
-    shape = (rows, h.k)
-    if t.shape != shape or not (t.is_contiguous() or (strides and t.stride(1) == 1)):
-        raise ValueError(f"{what}: codes [{rows}][{h.k}] in order are needed, got {tuple(t.shape)}, strides {t.stride()}")
+    k = h.k
+    if t.shape != (rows, k) or not (t.is_contiguous() or (strides and t.stride(1) == 1)):
+        raise ValueError(f"{what}: codes [{rows}][{k}] in order are needed, got {tuple(t.shape)}, strides {t.stride()}")
     if s.shape != (-(-rows // block), h.kb) or not s.is_contiguous():
         raise ValueError(f"{what}: contiguous scales [{-(-rows // block)}][{h.kb}] are needed, got {tuple(s.shape)}")
     if t.get_device() != h.device or s.get_device() != h.device:
         _elsewhere(h, t, s)
-    return t.stride(0)
+    return t.stride(0) if strides else k
 
 
-def _matrix(what, h, t, cols):
+def _matrix(what, h, t, rows, cols):
     """Checks t [rows][cols] with elements in order on the handle's device; its row stride."""
-    shape, strides = t.shape, t.stride()
-    if len(shape) != 2 or shape[1] != cols or (strides[1] != 1 and cols > 1):
-        raise ValueError(f"{what}: [rows][{cols}] with elements in order is needed, got {tuple(shape)}, strides {strides}")
+    strides = t.stride()
+    if t.shape != (rows, cols) or (strides[1] != 1 and cols > 1):
+        raise ValueError(f"{what}: [{rows}][{cols}] with elements in order is needed, got {tuple(t.shape)}, strides {strides}")
     if t.get_device() != h.device:
         _elsewhere(h, t)
     return strides[0]
 
 
+_PRODUCT = struct.Struct("PiPqiPPPPPqPiq")      # medusa_fp8_product as bytes
+
+
 def fp8_round(h, x, codes, scales, block=1, stream=None):
     """medusa_fp8_round: x [rows][k] (any row stride) to contiguous codes [rows][k] and scales
     [ceil(rows / block)][ceil(k / 128)]; block 1 (rows) or 128 (weights)."""
-    row = _matrix("x", h, x, h.k)
     rows = x.shape[0]
+    row = _matrix("x", h, x, rows, h.k)
     _codes("codes", h, codes, scales, rows, block)
     _check("medusa_fp8_round",
            lib().medusa_fp8_round(h.handle, x.data_ptr(), _dtype(x), rows, row, codes.data_ptr(), scales.data_ptr(),
@@ -814,8 +817,8 @@ def fp8_round(h, x, codes, scales, block=1, stream=None):
 
 def fp8_read(h, codes, scales, y, block=1, stream=None):
     """medusa_fp8_read: codes and scales, as fp8_round leaves them, to y [rows][k] (any row stride)."""
-    row = _matrix("y", h, y, h.k)
     rows = y.shape[0]
+    row = _matrix("y", h, y, rows, h.k)
     _codes("codes", h, codes, scales, rows, block)
     _check("medusa_fp8_read",
            lib().medusa_fp8_read(h.handle, codes.data_ptr(), scales.data_ptr(), rows, block, y.data_ptr(), _dtype(y),
@@ -825,27 +828,27 @@ def fp8_read(h, codes, scales, y, block=1, stream=None):
 def fp8_linear(h, x, w, w_scales, y, ws, x_scales=None, up=None, up_scales=None, add=None, stream=None):
     """medusa_fp8_linear: y = x w^T (+ add), or with `up` silu(x w^T) * (x up^T).  x [rows][k] is float32,
     bfloat16, or codes with x_scales; w, up contiguous codes [n][k]; y, add [rows][n] of one dtype."""
-    rows = x.shape[0]
+    rows, n = x.shape[0], h.n
     if x_scales is None:
-        x_dtype, x_row = _dtype(x), _matrix("x", h, x, h.k)
+        x_dtype, x_row, xs = _dtype(x), _matrix("x", h, x, rows, h.k), 0
     else:
-        x_dtype, x_row = E4M3, _codes("x", h, x, x_scales, rows, 1, strides=True)
-    _codes("w", h, w, w_scales, h.n, 128)
-    if (up is None) != (up_scales is None):
+        x_dtype, x_row, xs = E4M3, _codes("x", h, x, x_scales, rows, 1, strides=True), x_scales.data_ptr()
+    _codes("w", h, w, w_scales, n, 128)
+    upw = ups = addp = add_row = 0
+    if up is not None and up_scales is not None:
+        _codes("up", h, up, up_scales, n, 128)
+        upw, ups = up.data_ptr(), up_scales.data_ptr()
+    elif up is not None or up_scales is not None:
         raise ValueError("up and up_scales go together")
-    if up is not None:
-        _codes("up", h, up, up_scales, h.n, 128)
-    y_row, add_row = _matrix("y", h, y, h.n), 0
-    if y.shape[0] != rows:
-        raise ValueError(f"y: {rows} rows are needed, got {y.shape[0]}")
+    y_row = _matrix("y", h, y, rows, n)
     if add is not None:
         _same(y, add)
-        add_row = _matrix("add", h, add, h.n)
-        if add.shape[0] != rows:
-            raise ValueError(f"add: {rows} rows are needed, got {add.shape[0]}")
+        addp, add_row = add.data_ptr(), _matrix("add", h, add, rows, n)
     if ws.get_device() != h.device or not ws.is_contiguous():
         raise ValueError("ws: a contiguous tensor on the handle's device is needed")
-    p = Fp8Product(x.data_ptr(), x_dtype, ptr(x_scales), x_row, rows, w.data_ptr(), w_scales.data_ptr(), ptr(up),
-                   ptr(up_scales), ptr(add), add_row, y.data_ptr(), _dtype(y), y_row)
-    _check("medusa_fp8_linear",
-           lib().medusa_fp8_linear(h.handle, p, ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)))
+    code = lib().medusa_fp8_linear(
+        h.handle, _PRODUCT.pack(x.data_ptr(), x_dtype, xs, x_row, rows, w.data_ptr(), w_scales.data_ptr(), upw, ups,
+                                addp, add_row, y.data_ptr(), _dtype(y), y_row),
+        ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream))
+    if code:
+        raise MedusaError("medusa_fp8_linear", code)

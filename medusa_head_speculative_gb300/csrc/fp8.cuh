@@ -4,6 +4,7 @@
 
 #include "common.cuh"
 #include "fp8.h"
+#include "units.cuh"
 
 namespace medusa {
 
@@ -33,52 +34,6 @@ __device__ __forceinline__ void fp8_values(uint32_t codes, float (&x)[4]) {
   x[1] = lo.y;
   x[2] = hi.x;
   x[3] = hi.y;
-}
-
-// Four consecutive elements; vec: one aligned load or store.
-__device__ __forceinline__ void load4(const float* p, bool vec, float (&x)[4]) {
-  if (vec) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    x[0] = v.x;
-    x[1] = v.y;
-    x[2] = v.z;
-    x[3] = v.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = p[i];
-  }
-}
-__device__ __forceinline__ void load4(const bf16* p, bool vec, float (&x)[4]) {
-  if (vec) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    x[0] = __uint_as_float(v.x << 16);
-    x[1] = __uint_as_float(v.x & 0xffff0000u);
-    x[2] = __uint_as_float(v.y << 16);
-    x[3] = __uint_as_float(v.y & 0xffff0000u);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = to_f32(p[i]);
-  }
-}
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&p);
-}
-__device__ __forceinline__ void save4(float* p, bool vec, const float (&x)[4]) {
-  if (vec) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = x[i];
-  }
-}
-__device__ __forceinline__ void save4(bf16* p, bool vec, const float (&x)[4]) {
-  if (vec) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = __float2bfloat16_rn(x[i]);
-  }
 }
 
 }  // namespace medusa

@@ -10,6 +10,7 @@
 
 #include "launch.cuh"
 #include "prefix.cuh"
+#include "units.cuh"
 #include "tc_ptx.cuh"
 
 namespace medusa {
@@ -20,7 +21,8 @@ __device__ __forceinline__ bool nonfinite(float x) { return (__float_as_uint(x) 
 
 template <typename T, int DH>
 __global__ void __launch_bounds__(256) prefix_simt_kernel(PxWork w) {
-  constexpr int P = DH + 4, C = DH / 16;
+  constexpr int P = DH + 4, C = DH / 16, UNITS = PS_KEYS * DH / 4 / 256;
+  static_assert(PS_ROWS == PS_KEYS, "queries and keys are loaded alike");
   extern __shared__ float sm[];
   float* Qs = sm;                                 // [64][DH + 4]
   float* Ks = Qs + PS_ROWS * P;                   // [64][DH + 4]
@@ -39,9 +41,13 @@ __global__ void __launch_bounds__(256) prefix_simt_kernel(PxWork w) {
   while (px_next(w, walk, s)) {
     const int b = shared ? 0 : s.b, len = clamp_len(c, c.len[b]), prefix_chunks = (len + PX_KEYS - 1) / PX_KEYS;
     __syncthreads();
-    for (int e = tid; e < PS_ROWS * DH; e += 256) {
-      const PxRow x = px_row(w, shared, s, e / DH);
-      Qs[e / DH * P + e % DH] = x.ok ? to_f32(static_cast<const T*>(a.q)[x.node_row * a.q_row + x.head * a.q_head + e % DH]) : 0.f;
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {             // four elements a thread at a time
+      const int e = tid + u * 256, r = e / (DH / 4), i = e % (DH / 4) * 4;
+      const PxRow x = px_row(w, shared, s, r);
+      float v[4] = {};
+      if (x.ok) load4(static_cast<const T*>(a.q) + x.node_row * a.q_row + x.head * a.q_head + i, true, v);
+      *reinterpret_cast<float4*>(Qs + r * P + i) = make_float4(v[0], v[1], v[2], v[3]);
     }
     float o[4][C] = {}, m[4], l[4] = {};
     PxRow row[4];
@@ -57,32 +63,43 @@ __global__ void __launch_bounds__(256) prefix_simt_kernel(PxWork w) {
       __syncthreads();
       if (tid < 2) s_bad[tid] = 0;
       __syncthreads();
-      for (int e = tid; e < PS_KEYS * DH; e += 256) {
-        const int j = e / DH, i = e - j * DH, t = t0 + j;
-        float kx = 0.f, vx = 0.f;
-        if (t < end) {
-          if (tree) {
-            const long at = (((long)b * a.n1 + t) * c.Hkv + s.g) * DH + i;
-            kx = to_f32(static_cast<const T*>(a.tk)[at]);
-            vx = to_f32(static_cast<const T*>(a.tv)[at]);
-            if (nonfinite(vx)) {                  // not every row sees it: 0, and a NaN sum for those that do
-              vx = 0.f;
-              atomicOr(&s_bad[j >> 5], 1u << (j & 31));
-            }
-          } else {
-            long unit;
-            int in;
-            if (!unit_of(c, b, t, unit, in)) {
-              set_flag(c.status, MEDUSA_FLAG_PAGE_RANGE);
-              unit = 0;
-            }
-            const long at = plain_offset(c, unit, in, s.g) + i;
-            kx = to_f32(static_cast<const T*>(c.k)[at]);
-            vx = to_f32(static_cast<const T*>(c.v)[at]);
+      float kx[UNITS][4], vx[UNITS][4];           // all asked for before the first is used
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) {
+        const int e = tid + u * 256, t = t0 + e / (DH / 4), i = e % (DH / 4) * 4;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) kx[u][q] = vx[u][q] = 0.f;
+        if (t >= end) continue;
+        const T *ks, *vs;
+        if (tree) {
+          const long at = (((long)b * a.n1 + t) * c.Hkv + s.g) * DH + i;
+          ks = static_cast<const T*>(a.tk) + at;
+          vs = static_cast<const T*>(a.tv) + at;
+        } else {
+          long unit;
+          int in;
+          if (!unit_of(c, b, t, unit, in)) {
+            set_flag(c.status, MEDUSA_FLAG_PAGE_RANGE);
+            unit = 0;
           }
+          const long at = plain_offset(c, unit, in, s.g) + i;
+          ks = static_cast<const T*>(c.k) + at;
+          vs = static_cast<const T*>(c.v) + at;
         }
-        Ks[j * P + i] = kx;
-        Vs[j * DH + i] = vx;
+        load4(ks, true, kx[u]);
+        load4(vs, true, vx[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) {
+        const int e = tid + u * 256, j = e / (DH / 4), i = e % (DH / 4) * 4;
+        if (tree && (nonfinite(vx[u][0]) || nonfinite(vx[u][1]) || nonfinite(vx[u][2]) || nonfinite(vx[u][3]))) {
+          // not every row sees it: 0, and a NaN sum for those that do
+#pragma unroll
+          for (int q = 0; q < 4; ++q) vx[u][q] = 0.f;
+          atomicOr(&s_bad[j >> 5], 1u << (j & 31));
+        }
+        *reinterpret_cast<float4*>(Ks + j * P + i) = make_float4(kx[u][0], kx[u][1], kx[u][2], kx[u][3]);
+        *reinterpret_cast<float4*>(Vs + j * DH + i) = make_float4(vx[u][0], vx[u][1], vx[u][2], vx[u][3]);
       }
       __syncthreads();
       float p[4][4] = {};
@@ -323,8 +340,8 @@ cudaError_t launch_prefix_attention(const PrefixArgs& a, int dtype, void* ws, in
   row_blocks(tc, w.rows, &w.rbs, &w.nrbs);
   row_blocks(tc, w.R, &w.rbo, &w.nrbo);
   // a chunk against two tiles of rows takes longer than against one
-  w.cost_s = tc && w.rbs > 128 ? 2 : 1;
-  w.cost_o = tc && w.rbo > 128 ? 2 : 1;
+  w.cost_s = tc && w.rbs > 128 ? 3 : 2;
+  w.cost_o = tc && w.rbo > 128 ? 3 : 2;
   w.tree = a.tk ? (a.n1 + PX_KEYS - 1) / PX_KEYS : 0;
   w.ctas = max_ctas(num_sms);
   char* p = static_cast<char*>(ws);

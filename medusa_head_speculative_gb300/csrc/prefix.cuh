@@ -20,7 +20,7 @@
 namespace medusa {
 
 constexpr int PX_KEYS = 128;                      // keys of a chunk
-constexpr int PX_ITEM = 2;
+constexpr int PX_ITEM = 3;
 
 // Counted by the main kernel for the joining one.
 struct PxPlan {

@@ -49,7 +49,8 @@ def test_calls_without_a_handle_are_refused():
     assert L.medusa_fp8_get_status(None, None, None) == -1
     assert L.medusa_fp8_round(None, None, 0, 0, 0, None, None, 1, None) == -1
     assert L.medusa_fp8_read(None, None, None, 0, 1, None, 0, 0, None) == -1
-    assert L.medusa_fp8_linear(None, Bnd.Fp8Product(), None, 0, None) == -1
+    assert C.sizeof(Bnd.Fp8Product) == Bnd._PRODUCT.size
+    assert L.medusa_fp8_linear(None, bytes(Bnd._PRODUCT.size), None, 0, None) == -1
     assert L.medusa_prefix_attention(None, Bnd.KV(), None, Bnd.KV(), Bnd.KV4Query(), None, 0, None) == -1
     L.medusa_fp8_destroy(None)
 
