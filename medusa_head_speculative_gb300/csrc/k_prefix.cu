@@ -49,11 +49,14 @@ __global__ void __launch_bounds__(256) prefix_simt_kernel(PxWork w) {
       if (x.ok) load4(static_cast<const T*>(a.q) + x.node_row * a.q_row + x.head * a.q_head + i, true, v);
       *reinterpret_cast<float4*>(Qs + r * P + i) = make_float4(v[0], v[1], v[2], v[3]);
     }
-    float o[4][C] = {}, m[4], l[4] = {};
+    F2 o[4][C / 2];
+    float m[4], l[4] = {};
     PxRow row[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       m[i] = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < C / 2; ++e) o[i][e] = f2(0.f, 0.f);
       row[i] = px_row(w, shared, s, ty + 16 * i);
     }
     for (int jj = 2 * s.j; jj < 2 * (s.j + s.n); ++jj) {
@@ -102,21 +105,34 @@ __global__ void __launch_bounds__(256) prefix_simt_kernel(PxWork w) {
         *reinterpret_cast<float4*>(Vs + j * DH + i) = make_float4(vx[u][0], vx[u][1], vx[u][2], vx[u][3]);
       }
       __syncthreads();
-      float p[4][4] = {};
+      F2 p2[4][4];                                // even and odd elements' sums
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) p2[u][v] = f2(0.f, 0.f);
 #pragma unroll 4
       for (int i = 0; i < DH; i += 4) {
-        float4 q[4], k[4];
+        ulonglong2 q[4], k[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          q[u] = *reinterpret_cast<const float4*>(Qs + (ty + 16 * u) * P + i);
-          k[u] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * u) * P + i);
+          q[u] = *reinterpret_cast<const ulonglong2*>(Qs + (ty + 16 * u) * P + i);
+          k[u] = *reinterpret_cast<const ulonglong2*>(Ks + (tx + 16 * u) * P + i);
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u)
 #pragma unroll
           for (int v = 0; v < 4; ++v)
-            p[u][v] = fmaf(q[u].x, k[v].x, fmaf(q[u].y, k[v].y, fmaf(q[u].z, k[v].z, fmaf(q[u].w, k[v].w, p[u][v]))));
+            p2[u][v] = fma2(F2{q[u].y}, F2{k[v].y}, fma2(F2{q[u].x}, F2{k[v].x}, p2[u][v]));
       }
+      float p[4][4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          float a0, a1;
+          unf2(p2[u][v], a0, a1);
+          p[u][v] = a0 + a1;
+        }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         uint32_t see[2] = {0xffffffffu, 0xffffffffu};
@@ -148,7 +164,7 @@ __global__ void __launch_bounds__(256) prefix_simt_kernel(PxWork w) {
         l[u] = l[u] * f + sum;
         m[u] = top;
 #pragma unroll
-        for (int i = 0; i < C; ++i) o[u][i] *= f;
+        for (int i = 0; i < C / 2; ++i) o[u][i] = mul2(o[u][i], f2(f, f));
       }
       __syncwarp();                               // a row's probabilities are read by its own 16 lanes
       for (int j = 0; j < PS_KEYS; j += 4) {
@@ -163,17 +179,14 @@ __global__ void __launch_bounds__(256) prefix_simt_kernel(PxWork w) {
         }
 #pragma unroll
         for (int jj2 = 0; jj2 < 4; ++jj2) {
-          float v[C];
+          F2 v[C / 2];
 #pragma unroll
-          for (int i = 0; i < C; i += 2) {
-            const float2 x = *reinterpret_cast<const float2*>(Vs + (j + jj2) * DH + tx * 2 + 16 * i);
-            v[i] = x.x;
-            v[i + 1] = x.y;
-          }
+          for (int i = 0; i < C / 2; ++i)
+            v[i].v = *reinterpret_cast<const unsigned long long*>(Vs + (j + jj2) * DH + tx * 2 + 32 * i);
 #pragma unroll
           for (int u = 0; u < 4; ++u)
 #pragma unroll
-            for (int i = 0; i < C; ++i) o[u][i] = fmaf(pr[u][jj2], v[i], o[u][i]);
+            for (int i = 0; i < C / 2; ++i) o[u][i] = fma2(f2(pr[u][jj2], pr[u][jj2]), v[i], o[u][i]);
         }
       }
     }
@@ -186,8 +199,8 @@ __global__ void __launch_bounds__(256) prefix_simt_kernel(PxWork w) {
       if (!row[u].ok) continue;
       const long at = s.slot * rb + r;
 #pragma unroll
-      for (int i = 0; i < C; i += 2)
-        *reinterpret_cast<float2*>(po + at * DH + tx * 2 + 16 * i) = make_float2(o[u][i], o[u][i + 1]);
+      for (int i = 0; i < C / 2; ++i)
+        *reinterpret_cast<unsigned long long*>(po + at * DH + tx * 2 + 32 * i) = o[u][i].v;
       if (tx == 0) pml[at] = make_float2(l[u] != l[u] && m[u] == -INFINITY ? 0.f : m[u], l[u]);
     }
   }
@@ -220,7 +233,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(PxWork w) {
     if (kind == 0) {
       if (p.ns == 0) continue;
       const int rbi = gr / w.rbs, item = g * w.nrbs + rbi;
-      const long x = (long)item * px_units(p.ns) + PX_ITEM, c0 = cta(x, p.cs, p.ws);
+      const long x = (long)item * px_units(w, p.ns) + w.item, c0 = cta(x, p.cs, p.ws);
       n = (int)(cta(x + p.ns - 1, p.cs, p.ws) - c0) + 1;
       slot = c0 + item;
       rb = w.rbs;
@@ -228,7 +241,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(PxWork w) {
     } else {
       if (nb == 0) continue;
       const int rbi = r / w.rbo, per = a.own.Hkv * w.nrbo, item = g * w.nrbo + rbi;
-      const long x = first * per + (long)item * px_units(nb) + PX_ITEM, c0 = cta(x, p.co, p.wo);
+      const long x = first * per + (long)item * px_units(w, nb) + w.item, c0 = cta(x, p.co, p.wo);
       n = (int)(cta(x + nb - 1, p.co, p.wo) - c0) + 1;
       slot = c0 + (long)b * per + item;
       rb = w.rbo;
@@ -340,6 +353,7 @@ cudaError_t launch_prefix_attention(const PrefixArgs& a, int dtype, void* ws, in
   row_blocks(tc, w.rows, &w.rbs, &w.nrbs);
   row_blocks(tc, w.R, &w.rbo, &w.nrbo);
   // a chunk against two tiles of rows takes longer than against one
+  w.item = tc ? 3 : 0;
   w.cost_s = tc && w.rbs > 128 ? 3 : 2;
   w.cost_o = tc && w.rbo > 128 ? 3 : 2;
   w.tree = a.tk ? (a.n1 + PX_KEYS - 1) / PX_KEYS : 0;

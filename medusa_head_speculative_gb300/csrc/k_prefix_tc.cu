@@ -51,6 +51,7 @@ struct PtArgs {
   int tma[2];                                       // whole chunks come by them
   PxWork w;
   int nt[2], sk[2], sv[2];                          // shared, own: tiles of a block, stages of the rings
+  int qb[2];                                        // blocks of queries there is room for
 };
 
 // QF / QE: query tiles (with one tile: two in turn) written / no longer read.  KF and VF: stages full.  Per slot
@@ -117,10 +118,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
   }
   PxWalk walk = px_start(w, plan, blockIdx.x);
   const bool shared = uni(walk.shared);
-  const int kind = shared ? 0 : 1, nt = g.nt[kind], SK = g.sk[kind], SV = g.sv[kind];
+  const int kind = shared ? 0 : 1, nt = g.nt[kind], SK = g.sk[kind], SV = g.sv[kind], QB = g.qb[kind];
   const CacheView& c = shared ? a.shared : a.own;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t qs = base, k0s = base + 2 * CHUNK, v0s = k0s + SK * CHUNK;
+  const uint32_t qs = base, k0s = base + nt * QB * CHUNK, v0s = k0s + SK * CHUNK;
   const uint32_t bar0 = smem_u32(bars);
   auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   if (tid == 0) {
@@ -309,8 +310,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
         const int i0 = nt == 2 ? 0 : (slot - gc) & 1;    // this slot's first chunk
         len = uni(clamp_len(c, c.len[shared ? 0 : s.b]));
         pc = (len + PX_KEYS - 1) / PX_KEYS;
-        const int qb = nt == 2 ? 0 : qn & 1;
-        if (!kt_warp_wait(bar(XB_QF + qb), (nt == 2 ? qn : qn >> 1) & 1)) { dead = true; break; }
+        const int qb = QB == 1 ? 0 : qn & 1;
+        if (!kt_warp_wait(bar(XB_QF + qb), (QB == 1 ? qn : qn >> 1) & 1)) { dead = true; break; }
         fence_proxy_async();
         tc_fence_after();
         q = dq + qb * (CHUNK >> 4);
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
       const int unit = lane % UPR, sub = lane / UPR;
       const bf16* src = static_cast<const bf16*>(a.q);
       for (int qn = 0; px_next(w, walk, s); ++qn) {
-        const int qb = nt == 2 ? 0 : qn & 1, turn = nt == 2 ? qn : qn >> 1;
+        const int qb = QB == 1 ? 0 : qn & 1, turn = QB == 1 ? qn : qn >> 1;
         const uint32_t to = qs + qb * CHUNK + (unit >> 3) * TILE;
         for (int r0 = 32 * (warp - PT_QUERY_WARP); r0 < nt * PT_ROWS; r0 += 64) {
           const PxRow row = px_row(w, shared, s, r0 + lane);
@@ -632,7 +633,9 @@ template <int DH> static cudaError_t tc_go(PtArgs& g, cudaStream_t st) {
   constexpr size_t CHUNK = DH / 64 * 128 * 128, limit = 225 * 1024;
   static unsigned long long done = 0;
   for (int kind = 0; kind < 2; ++kind) {
-    const int stages = (int)((limit - 1024) / CHUNK) - 2;   // (two tiles of queries)
+    // with one tile a block's queries are copied a block ahead where blocks are short, of a few chunks
+    g.qb[kind] = g.nt[kind] == 1 && kind == 1 ? 2 : 1;
+    const int stages = (int)((limit - 1024) / CHUNK) - g.nt[kind] * g.qb[kind];
     if (g.nt[kind] == 1) {                           // even depths: see above
       g.sk[kind] = stages >= 6 ? 4 : 2;
       g.sv[kind] = stages - g.sk[kind] >= 4 ? 4 : 2;

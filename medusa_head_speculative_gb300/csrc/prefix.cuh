@@ -7,8 +7,8 @@
 //                 so that a chunk of the prefix is read once for a block of up to 256 rows of any sequences
 //   own items     (sequence b, head g, row block): b's slots, then the call's rows of b
 // Each CTA works on one of the two kinds (the kinds differ in their row blocks) and takes an even share of
-// that kind's units in one line, item after item.  An item's units are PX_ITEM for its queries and its partial,
-// which take about as long as so many chunks, and then its chunks; for every item of which a CTA has chunks
+// that kind's units in one line, item after item.  An item's units are PxWork::item for its queries and its
+// partial, which take about as long as so many chunks, and then its chunks; for every item of which a CTA has chunks
 // it writes a partial (o, reference, sum) to a slot of its own, and the joining kernel adds an item's
 // partials up in order.
 // Lengths are read on the device, so all of this is counted there, the same way by every warp.
@@ -20,7 +20,6 @@
 namespace medusa {
 
 constexpr int PX_KEYS = 128;                      // keys of a chunk
-constexpr int PX_ITEM = 3;
 
 // Counted by the main kernel for the joining one.
 struct PxPlan {
@@ -33,6 +32,7 @@ struct PxWork {
   int R, rows;                                    // rows of a head: a sequence's, all
   int rbs, nrbs, rbo, nrbo;                       // rows of a block and blocks of a head: shared, own
   int cost_s, cost_o;                             // of a chunk
+  int item;                                       // what an item costs besides, in chunks
   int tree;                                       // chunks of the call's own rows
   int ctas;
   float* o_s; float2* ml_s;                       // partials of shared items [slot][rbs][dh], [slot][rbs]
@@ -44,13 +44,13 @@ struct PxWork {
 __device__ __forceinline__ int px_chunks(const PxWork& w, int b) {
   return (clamp_len(w.a.own, w.a.own.len[b]) + PX_KEYS - 1) / PX_KEYS + w.tree;
 }
-__device__ __forceinline__ int px_units(int chunks) { return chunks > 0 ? chunks + PX_ITEM : 0; }
+__device__ __forceinline__ int px_units(const PxWork& w, int chunks) { return chunks > 0 ? chunks + w.item : 0; }
 // All lanes of a warp; writes the plan and `first` when asked to.
 __device__ __forceinline__ PxPlan px_plan(const PxWork& w, bool write) {
   const int lane = threadIdx.x & 31, B = w.a.own.B;
   long sum = 0;
   for (int b0 = 0; b0 < B; b0 += 32) {
-    const int mine = b0 + lane < B ? px_units(px_chunks(w, b0 + lane)) : 0;
+    const int mine = b0 + lane < B ? px_units(w, px_chunks(w, b0 + lane)) : 0;
     long upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -62,7 +62,7 @@ __device__ __forceinline__ PxPlan px_plan(const PxWork& w, bool write) {
   }
   PxPlan p;
   p.ns = (clamp_len(w.a.shared, w.a.shared.len[0]) + PX_KEYS - 1) / PX_KEYS;
-  p.ws = (long)px_units(p.ns) * w.a.own.Hkv * w.nrbs;
+  p.ws = (long)px_units(w, p.ns) * w.a.own.Hkv * w.nrbs;
   p.wo = sum * w.a.own.Hkv * w.nrbo;
   const float s = (float)p.ws * w.cost_s, t = (float)(sum * w.a.own.Hkv * w.nrbo) * w.cost_o;
   p.cs = p.ws == 0 ? 0 : p.wo == 0 ? w.ctas : min(max((int)(w.ctas * (s / (s + t)) + 0.5f), 1), w.ctas - 1);
@@ -92,7 +92,7 @@ __device__ __forceinline__ PxWalk px_start(const PxWork& w, const PxPlan& p, int
   k.left = 0;
   k.b = 0;
   k.item = k.j = 0;
-  k.nb = max(px_units(p.ns), 1);
+  k.nb = max(px_units(w, p.ns), 1);
   k.per = w.a.own.Hkv * (k.shared ? w.nrbs : w.nrbo);
   if (k.c >= n) return k;
   const long total = k.shared ? p.ws : p.wo;
@@ -106,7 +106,7 @@ __device__ __forceinline__ PxWalk px_start(const PxWork& w, const PxPlan& p, int
   const int lane = threadIdx.x & 31, B = w.a.own.B;
   long before = 0;
   for (int b0 = 0;; b0 += 32) {
-    const int mine = b0 + lane < B ? px_units(px_chunks(w, b0 + lane)) : 0;
+    const int mine = b0 + lane < B ? px_units(w, px_chunks(w, b0 + lane)) : 0;
     long upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -133,9 +133,9 @@ __device__ __forceinline__ bool px_next(const PxWork& w, PxWalk& k, PxSeg& s) {
     s.b = k.b;
     s.g = k.item / nrb;
     s.rb = k.item - s.g * nrb;
-    s.j = max(k.j - PX_ITEM, 0);
+    s.j = max(k.j - w.item, 0);
     const int n = (int)min((long)(k.nb - k.j), k.left);
-    s.n = max(k.j + n - PX_ITEM, 0) - s.j;        // (0: the share ends before the item's chunks)
+    s.n = max(k.j + n - w.item, 0) - s.j;        // (0: the share ends before the item's chunks)
     s.slot = (long)k.c + (k.shared ? (long)k.item : (long)k.b * k.per + k.item);
     k.left -= n;
     k.j = 0;
@@ -143,7 +143,7 @@ __device__ __forceinline__ bool px_next(const PxWork& w, PxWalk& k, PxSeg& s) {
       k.item = 0;
       do {
         ++k.b;
-        k.nb = px_units(px_chunks(w, k.b));       // (what is left lies in a later sequence)
+        k.nb = px_units(w, px_chunks(w, k.b));       // (what is left lies in a later sequence)
       } while (k.nb == 0);
     }
   } while (s.n == 0);
