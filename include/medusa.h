@@ -612,7 +612,8 @@ medusa_status medusa_kv4_attention(const medusa_cache* cache, const medusa_kv* k
  *   q, o, tree_k, tree_v: as in medusa_kv4_query, of the caches' dtype (k_scale and v_scale are not read)
  * A length outside 0..capacity is taken as the nearer end.  A page outside the pool is read as page 0 and
  * sets MEDUSA_FLAG_PAGE_RANGE in its cache's status; an expired wait sets MEDUSA_FLAG_TIMEOUT in own's.  A
- * row that sees nothing gives zeros, one that sees an infinity or a NaN gives infinities or NaN.  Slots from
+ * row that sees nothing gives zeros, one that sees a NaN gives NaN (in the elements it reaches or in all), and
+ * infinities that a row sees may give any result of that row.  Slots from
  * the lengths on and rows that are not seen may hold anything.  Calls that may run at the same time need
  * workspaces of their own.
  * Scores, softmax statistics and sums are 32 bits wide; with MEDUSA_BF16 probabilities keep 8 bits. */
@@ -659,7 +660,7 @@ enum { MEDUSA_E4M3 = 3 };
  *   w, up: codes [n][k], 16-byte aligned; w_scales, up_scales: any finite scales whose products with a
  *      row's are finite
  *   add: NULL or [rows][n] of y's dtype, row stride add_row; y itself with equal strides, or apart from it
- *   y: [rows][n], MEDUSA_F32 or MEDUSA_BF16, row stride y_row >= n
+ *   y: [rows][n], MEDUSA_F32 or MEDUSA_BF16, row stride y_row >= n, apart from everything but add
  * The products of 128 elements are summed in float on the tensor cores, scaled, and added up in float;
  * the result is rounded once.  rows = 0 does nothing.  Calls that may run at the same time need
  * workspaces of their own. */

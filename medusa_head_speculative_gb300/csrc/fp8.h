@@ -34,7 +34,7 @@ struct Fp8LinearArgs {
   uint32_t* status;
 };
 // Bytes of partials (`part`) a call may need.
-size_t fp8_linear_partials(int max_rows, int n, int kb, bool gated, int num_sms);
+size_t fp8_linear_partials(int max_rows, int n, int kb, int num_sms);
 cudaError_t launch_fp8_linear(const Fp8LinearArgs& a, int dtype, void* part, int num_sms, cudaStream_t st);
 
 }  // namespace medusa

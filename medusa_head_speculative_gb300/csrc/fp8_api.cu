@@ -64,7 +64,7 @@ medusa_status medusa_fp8_create(const medusa_fp8_dims* dims, medusa_fp8** out) {
   h->codes_bytes = round_up((size_t)dims->max_rows * dims->k, 256);
   h->scales_bytes = round_up((size_t)dims->max_rows * h->kb * sizeof(float), 256);
   h->ws_bytes = h->codes_bytes + h->scales_bytes +
-                fp8_linear_partials(dims->max_rows, dims->n, h->kb, dims->gated, h->num_sms);
+                fp8_linear_partials(dims->max_rows, dims->n, h->kb, h->num_sms);
   *out = h;
   return MEDUSA_OK;
 }

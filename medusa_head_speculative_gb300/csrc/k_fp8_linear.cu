@@ -529,9 +529,10 @@ static FlPlan fl_plan(int rows, int n, int kb, bool gated, int num_sms) {
   return p;
 }
 
-size_t fp8_linear_partials(int max_rows, int n, int kb, bool gated, int num_sms) {
-  // tiles that are left are fewer than CTAs, so that a call has at most twice the CTAs' slots
-  return (size_t)2 * num_sms * 128 * 256 * sizeof(float);
+size_t fp8_linear_partials(int max_rows, int n, int kb, int num_sms) {
+  // tiles that are left are fewer than CTAs, and a tile has no more shares than groups
+  const size_t tiles = (size_t)((max_rows + 127) / 128) * ((n + 127) / 128);
+  return std::min<size_t>(2 * (size_t)num_sms, tiles * (1 + (size_t)kb)) * 128 * 256 * sizeof(float);
 }
 
 template <typename T, int BN, bool GATED> static cudaError_t linear_go(FlArgs& g, int num_sms, cudaStream_t st) {
