@@ -170,25 +170,28 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
     auto abandon = [&](bool got) { timed_out = !got; return !got; };
     while (!timed_out && px_next(w, walk, s)) {
       const int b = shared ? 0 : s.b, len = clamp_len(c, c.len[b]), pc = (len + PX_KEYS - 1) / PX_KEYS;
-      // first element of the warp's row `lane` of chunk j (< 0: none)
-      auto offset = [&](int j) -> long {
+      // The page of the warp's row `lane` of chunk j, asked for a chunk ahead and not looked at before (a warp
+      // that needs it at once waits for memory); and the row's first element (< 0: none).
+      auto page_of = [&](int j) {
+        const int t = j * PX_KEYS + 32 * pw + lane;
+        return c.page_table && j < pc && t < len ? c.page_table[(long)b * c.pages_per_seq + t / c.page_size] : b;
+      };
+      auto offset = [&](int j, int page) -> long {
         const int t = (j < pc ? j : j - pc) * PX_KEYS + 32 * pw + lane;
         if (j >= pc) return t < a.n1 ? (((long)b * a.n1 + t) * c.Hkv + s.g) * DH : -1;
         if (t >= len) return -1;
-        long u;
-        int in;
-        if (!unit_of(c, b, t, u, in)) {
+        if (c.page_table && (page < 0 || page >= c.num_pages)) {
           set_flag(c.status, MEDUSA_FLAG_PAGE_RANGE);
-          u = 0;
+          page = 0;
         }
-        return plain_offset(c, u, in, s.g);
+        return plain_offset(c, page, c.page_table ? t % c.page_size : t, s.g);
       };
-      long next = offset(s.j);
+      int page = page_of(s.j);
       for (int i = 0; i < s.n; ++i, ++x) {
         const int j = s.j + i;
         const bool tree = j >= pc, engine = pt_engine(g, kind, j, len);
-        const long at = next;
-        if (i + 1 < s.n) next = offset(j + 1);
+        const long at = offset(j, page);
+        if (i + 1 < s.n) page = page_of(j + 1);
 #pragma unroll 1
         for (int part = 0; part < 2; ++part) {
           const int n = part ? SV : SK, st = part ? ring[1].st : ring[0].st;
