@@ -104,6 +104,14 @@ struct FlWalk {
   int tile;                                         // of the whole ones
   long w, w1;                                       // groups of the others
 };
+// Tile row and column of tile t.  Tiles that run at a time are neighbours: up to FL_GROUP rows of tiles by as many
+// columns as there are CTAs for, so that they share rows and weights in the L2 (all rows of a column first: rows of
+// 8192 x 13824 came from memory five times).
+constexpr int FL_GROUP = 16;
+__device__ __forceinline__ int2 fl_tile(const FlArgs& g, int t) {
+  const int first = t / (FL_GROUP * g.nt) * FL_GROUP, rows = min(FL_GROUP, g.mt - first), in = t - first * g.nt;
+  return make_int2(first + in % rows, in / rows);
+}
 template <int OC> __device__ __forceinline__ FlWalk fl_start(const FlArgs& g) {
   const long total = (long)(g.mt * g.nt - g.whole) * g.a.kb;
   if ((int)blockIdx.x >= g.shares) return {(int)blockIdx.x, 0, 0};
@@ -126,8 +134,9 @@ template <int OC> __device__ __forceinline__ bool fl_next(const FlArgs& g, FlWal
     s.slot = s.n == g.a.kb ? -1 : (long)blockIdx.x + i;
     k.w += s.n;
   }
-  s.m = t % g.mt;                                   // neighbours share weights
-  s.n0 = t / g.mt * OC;
+  const int2 at = fl_tile(g, t);
+  s.m = at.x;
+  s.n0 = at.y * OC;
   return true;
 }
 
@@ -447,7 +456,9 @@ __global__ void __launch_bounds__(256) fp8_join_kernel(const __grid_constant__ F
   constexpr int OC = GATED ? BN / 2 : BN, Q = OC / 4, SB = 4;
   pdl_trigger();
   const Fp8LinearArgs& a = g.a;
-  const int i = blockIdx.x, t = g.whole + i, m = t % g.mt, n0 = t / g.mt * OC;
+  const int i = blockIdx.x, t = g.whole + i;
+  const int2 tile = fl_tile(g, t);
+  const int m = tile.x, n0 = tile.y * OC;
   const long total = (long)(g.mt * g.nt - g.whole) * a.kb, x = (long)i * a.kb;
   auto cta = [&](long w) { return ((w + 1) * g.shares + total - 1) / total - 1; };
   const long c0 = cta(x), c1 = cta(x + a.kb - 1);
