@@ -210,13 +210,14 @@ __global__ void __launch_bounds__(256) prefix_simt_kernel(PxWork w) {
 // a row (dh/8 columns each), so that four rows' loads are in flight a warp: a row's time is a chain of loads (its
 // length, its references, its sums).  A row's partials are those of the CTAs that its item's chunks lie in:
 // with W units over C CTAs unit x is CTA ceil((x + 1) C / W) - 1's.
+constexpr int PJ_THREADS = 64;                    // few: small calls have a block an SM, and each round of loads counts
 template <typename T, int DH>
-__global__ void __launch_bounds__(256) prefix_join_kernel(PxWork w) {
-  constexpr int SB = 2, U = DH / 32;              // partials a round, 16-byte units a lane
+__global__ void __launch_bounds__(PJ_THREADS) prefix_join_kernel(PxWork w) {
+  constexpr int SB = 4, U = DH / 32;              // partials a round, 16-byte units a lane
   pdl_trigger();
   pdl_wait();
   const PrefixArgs& a = w.a;
-  const long i = (long)blockIdx.x * 32 + (threadIdx.x >> 3);
+  const long i = (long)blockIdx.x * (PJ_THREADS / 8) + (threadIdx.x >> 3);
   if (i >= (long)w.rows * a.own.Hkv) return;
   const int lane = threadIdx.x & 7;
   const int g = (int)(i / w.rows), gr = (int)(i - (long)g * w.rows);       // row of head g over all sequences
@@ -225,68 +226,61 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(PxWork w) {
   const int nb = px_chunks(w, b);
   const long first = w.first[b];
   auto cta = [](long x, long n, long total) { return (((x + 1) * n + total - 1) / total) - 1; };
+  // the row's first partial, how far the next one is and how many there are: of the shared item, of the own one
+  long at[2] = {0, 0};
+  int n[2] = {0, 0};
+  if (p.ns > 0) {
+    const int rbi = gr / w.rbs, item = g * w.nrbs + rbi;
+    const long x = (long)item * px_units(w, p.ns) + w.item, c0 = cta(x, p.cs, p.ws);
+    n[0] = (int)(cta(x + p.ns - 1, p.cs, p.ws) - c0) + 1;
+    at[0] = (c0 + item) * w.rbs + gr - rbi * w.rbs;
+  }
+  if (nb > 0) {
+    const int rbi = r / w.rbo, per = a.own.Hkv * w.nrbo, item = g * w.nrbo + rbi;
+    const long x = first * per + (long)item * px_units(w, nb) + w.item, c0 = cta(x, p.co, p.wo);
+    n[1] = (int)(cta(x + nb - 1, p.co, p.wo) - c0) + 1;
+    at[1] = (c0 + (long)b * per + item) * w.rbo + r - rbi * w.rbo;
+  }
   float M = -INFINITY, L = 0.f, acc[U][4] = {};
 #pragma unroll 1
-  for (int kind = 0; kind < 2; ++kind) {
-    long slot, rb, row;
-    int n;
-    if (kind == 0) {
-      if (p.ns == 0) continue;
-      const int rbi = gr / w.rbs, item = g * w.nrbs + rbi;
-      const long x = (long)item * px_units(w, p.ns) + w.item, c0 = cta(x, p.cs, p.ws);
-      n = (int)(cta(x + p.ns - 1, p.cs, p.ws) - c0) + 1;
-      slot = c0 + item;
-      rb = w.rbs;
-      row = gr - rbi * w.rbs;
-    } else {
-      if (nb == 0) continue;
-      const int rbi = r / w.rbo, per = a.own.Hkv * w.nrbo, item = g * w.nrbo + rbi;
-      const long x = first * per + (long)item * px_units(w, nb) + w.item, c0 = cta(x, p.co, p.wo);
-      n = (int)(cta(x + nb - 1, p.co, p.wo) - c0) + 1;
-      slot = c0 + (long)b * per + item;
-      rb = w.rbo;
-      row = r - rbi * w.rbo;
+  for (int s0 = 0; s0 < n[0] + n[1]; s0 += SB) {
+    float2 ml[SB];
+    float4 v[SB][U];
+#pragma unroll
+    for (int u = 0; u < SB; ++u) {
+      ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int e = 0; e < U; ++e) v[u][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int i = s0 + u, own = i - n[0];
+      if (own >= n[1]) continue;
+      const long row = own < 0 ? at[0] + (long)i * w.rbs : at[1] + (long)own * w.rbo;
+      ml[u] = (own < 0 ? w.ml_s : w.ml_o)[row];
+      const float* po = (own < 0 ? w.o_s : w.o_o) + row * DH + lane * 4;
+#pragma unroll
+      for (int e = 0; e < U; ++e) v[u][e] = *reinterpret_cast<const float4*>(po + e * 32);
     }
-    const float* po = kind == 0 ? w.o_s : w.o_o;
-    const float2* pml = kind == 0 ? w.ml_s : w.ml_o;
-    for (int s0 = 0; s0 < n; s0 += SB) {
-      float2 ml[SB];
-      float4 v[SB][U];
+    float top = M;
 #pragma unroll
-      for (int u = 0; u < SB; ++u) {
-        ml[u] = make_float2(-INFINITY, 0.f);
+    for (int u = 0; u < SB; ++u) top = fmaxf(top, ml[u].x);
+    if (top == -INFINITY) continue;               // nothing seen so far
+    const float f = M == -INFINITY ? 0.f : exp2f(M - top);
+    L *= f;
 #pragma unroll
-        for (int e = 0; e < U; ++e) v[u][e] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (s0 + u < n) {
-          const long at = (slot + s0 + u) * rb + row;
-          ml[u] = pml[at];
+    for (int e = 0; e < U; ++e)
 #pragma unroll
-          for (int e = 0; e < U; ++e) v[u][e] = *reinterpret_cast<const float4*>(po + at * DH + e * 32 + lane * 4);
-        }
-      }
-      float top = M;
+      for (int q = 0; q < 4; ++q) acc[e][q] *= f;
+    M = top;
 #pragma unroll
-      for (int u = 0; u < SB; ++u) top = fmaxf(top, ml[u].x);
-      if (top == -INFINITY) continue;             // nothing seen so far
-      const float f = M == -INFINITY ? 0.f : exp2f(M - top);
-      L *= f;
+    for (int u = 0; u < SB; ++u) {
+      if (ml[u].x == -INFINITY) continue;
+      const float x = exp2f(ml[u].x - M);
+      L += x * ml[u].y;
 #pragma unroll
-      for (int e = 0; e < U; ++e)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[e][q] *= f;
-      M = top;
-#pragma unroll
-      for (int u = 0; u < SB; ++u) {
-        if (ml[u].x == -INFINITY) continue;
-        const float x = exp2f(ml[u].x - M);
-        L += x * ml[u].y;
-#pragma unroll
-        for (int e = 0; e < U; ++e) {
-          acc[e][0] += x * v[u][e].x;
-          acc[e][1] += x * v[u][e].y;
-          acc[e][2] += x * v[u][e].z;
-          acc[e][3] += x * v[u][e].w;
-        }
+      for (int e = 0; e < U; ++e) {
+        acc[e][0] += x * v[u][e].x;
+        acc[e][1] += x * v[u][e].y;
+        acc[e][2] += x * v[u][e].z;
+        acc[e][3] += x * v[u][e].w;
       }
     }
   }
@@ -338,10 +332,10 @@ template <typename T> static cudaError_t prefix_go(const PxWork& w, bool tc, int
   else if (dh == 64) e = simt_go<T, 64>(w, st);
   else e = simt_go<T, 128>(w, st);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)(((long)w.rows * w.a.own.Hkv + 31) / 32));
-  if (dh == 32) return launch_kernel(prefix_join_kernel<T, 32>, grid, dim3(256), 0, st, 1, w);
-  if (dh == 64) return launch_kernel(prefix_join_kernel<T, 64>, grid, dim3(256), 0, st, 1, w);
-  return launch_kernel(prefix_join_kernel<T, 128>, grid, dim3(256), 0, st, 1, w);
+  const dim3 grid((unsigned)(((long)w.rows * w.a.own.Hkv + PJ_THREADS / 8 - 1) / (PJ_THREADS / 8)));
+  if (dh == 32) return launch_kernel(prefix_join_kernel<T, 32>, grid, dim3(PJ_THREADS), 0, st, 1, w);
+  if (dh == 64) return launch_kernel(prefix_join_kernel<T, 64>, grid, dim3(PJ_THREADS), 0, st, 1, w);
+  return launch_kernel(prefix_join_kernel<T, 128>, grid, dim3(PJ_THREADS), 0, st, 1, w);
 }
 
 cudaError_t launch_prefix_attention(const PrefixArgs& a, int dtype, void* ws, int num_sms, cudaStream_t st) {
