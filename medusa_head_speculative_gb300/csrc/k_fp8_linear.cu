@@ -20,6 +20,12 @@
 // evenly over the SMs; a CTA that has a part of a tile's groups writes a partial of its own, and a second
 // kernel adds a tile's partials up in order and finishes it.
 //
+// Measured (one GB300): 8192 x 5120 x 13824 with a residual 567 us (2.05 PFLOP/s), 520 x 15360 x 5120 52 us (1.57),
+// gated 688 x 14336 x 4096 100 us (1.61), gated 8 x 13824 x 5120 32 us (4.4 TB/s of weights, 6.6 while they stream),
+// 1 x 4096 x 4096 10.8 us with the rounding before and the joining behind it.  What bounds the large ones: a group takes
+// 700 to 950 cycles, its MMAs 460 and their commit 75; the accumulator's way to the promoting warps and back is seen in
+// between (510 cycles to promote), and residuals of 8192 rows wait for memory at a tile's end.
+//
 // Every wait is bounded; on expiry MEDUSA_FLAG_TIMEOUT is set, the CTA stops taking work, drains the copies
 // it issued and frees its tensor memory.
 #include <algorithm>

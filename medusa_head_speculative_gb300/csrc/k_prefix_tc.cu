@@ -25,6 +25,13 @@
 // alternate chunks, and the first warpgroup merges the second's (O, reference, sum) before it writes the
 // partial (of an item's only chunk its slot writes it).
 //
+// Measured (one GB300), joining included: 16 x 8 heads x 172 rows over a prefix of 8192 and 64-512 slots 119 us (800
+// TFLOP/s), 8 x 40 heads x 65 rows over 2048 + 0-1024 78 us, 32 x 8 heads x 4 rows over 16384 + 100-1000 slots in pages
+// of 16 51 us (2.7 TB/s).  What bounds them: with two tiles a chunk takes 5000 cycles, its MMAs 2050 and the softmax of a
+// slot 2900 (instructions a warp at a time; exponentials alone 2050 for both slots); pages of 16 slots come by
+// 16-byte copies, 4000 cycles a chunk; items of few chunks have their start and end besides.  Code size counts here:
+// more unrolling of the copies or the softmax makes every warp slower (64 keys at a time 112 -> 129 us).
+//
 // A wait names a phase by its parity: a waiter has to have seen the phase before.  With one tile a slot
 // sees every other chunk of the CTA, odd or even ones over all its items, and the rings are of two or four
 // stages, so that a stage is always the same slot's.
@@ -249,11 +256,22 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
             fence_proxy_async();
             mbar_arrive(full);
           } else {
+            if (__all_sync(0xffffffffu, at >= 0)) {
+              const char* from = reinterpret_cast<const char*>(src + unit * 8);
+              const uint32_t key = 32 * pw + sub;
 #pragma unroll 4
-            for (int y = 0; y < UPR; ++y) {
-              const int row = y * RPI + sub, r = 32 * pw + row;
-              const long o = __shfl_sync(0xffffffffu, at, row);
-              cp_async16(to + r * 128 + (((unit & 7) ^ (r & 7)) << 4), o >= 0 ? src + o + unit * 8 : src, o >= 0 ? 16 : 0);
+              for (int y = 0; y < UPR; ++y) {
+                const uint32_t r = key + y * RPI;
+                const long o = __shfl_sync(0xffffffffu, at, y * RPI + sub);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + r * 128 + (((unit & 7) ^ (r & 7)) << 4)), "l"(from + 2 * o));
+              }
+            } else {
+#pragma unroll 4
+              for (int y = 0; y < UPR; ++y) {
+                const int row = y * RPI + sub, r = 32 * pw + row;
+                const long o = __shfl_sync(0xffffffffu, at, row);
+                cp_async16(to + r * 128 + (((unit & 7) ^ (r & 7)) << 4), o >= 0 ? src + o + unit * 8 : src, o >= 0 ? 16 : 0);
+              }
             }
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
           }
