@@ -57,12 +57,11 @@ __device__ __forceinline__ bool mbar_try_for(uint32_t bar, uint32_t parity, uint
 // Wait for the phase of `parity` to complete; false after the time limit.  A waiting thread sleeps: one that
 // tries and reads the timer (500 cycles) in turn takes issue slots and notices late.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-  uint64_t t0 = 0;
-  while (!mbar_try_for(bar, parity, 100000)) {
-    const uint64_t t = gtimer();
-    if (t0 == 0) t0 = t;
-    if (t - t0 > limit_ns) return false;
-  }
+  if (mbar_try_for(bar, parity, 100000)) return true;
+  const uint64_t t0 = gtimer();
+#pragma unroll 1
+  while (!mbar_try_for(bar, parity, 100000))
+    if (gtimer() - t0 > limit_ns) return false;
   return true;
 }
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y,
