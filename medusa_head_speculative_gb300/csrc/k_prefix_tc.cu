@@ -552,7 +552,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
       const int first_tree = max(s.j, pc), n_trees = max(s.j + n - first_tree, 0);
       auto noted = [&]() {
         bool bad = false;
+#pragma unroll 1
         for (int q = 0; q < n_trees; ++q)
+#pragma unroll 1
           for (int u = 0; u < 4; ++u)
             bad |= row.ok && (px_sees(a, row.n, (first_tree - pc + q) * 4 + u) & *(volatile uint32_t*)&s_bad[(trees + q) & 7][u]) != 0u;
         return bad;
