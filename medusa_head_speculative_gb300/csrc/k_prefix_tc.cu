@@ -25,9 +25,9 @@
 // alternate chunks, and the first warpgroup merges the second's (O, reference, sum) before it writes the
 // partial (of an item's only chunk its slot writes it).
 //
-// Measured (one GB300), joining included: 16 x 8 heads x 172 rows over a prefix of 8192 and 64-512 slots 119 us (800
-// TFLOP/s), 8 x 40 heads x 65 rows over 2048 + 0-1024 78 us, 32 x 8 heads x 4 rows over 16384 + 100-1000 slots in pages
-// of 16 51 us (2.7 TB/s).  What bounds them: with two tiles a chunk takes 5000 cycles, its MMAs 2050 and the softmax of a
+// Measured (one GB300), joining included: 16 x 8 heads x 172 rows over a prefix of 8192 and 64-512 slots 115 us (830
+// TFLOP/s), 8 x 40 heads x 65 rows over 2048 + 0-1024 76 us, 32 x 8 heads x 4 rows over 16384 + 100-1000 slots in pages
+// of 16 50 us (2.8 TB/s).  What bounds them: with two tiles a chunk takes 5000 cycles, its MMAs 2050 and the softmax of a
 // slot 2900 (instructions a warp at a time; exponentials alone 2050 for both slots); pages of 16 slots come by
 // 16-byte copies, 4000 cycles a chunk; items of few chunks have their start and end besides.  Code size counts here:
 // more unrolling of the copies or the softmax makes every warp slower (64 keys at a time 112 -> 129 us).
