@@ -347,7 +347,9 @@ cudaError_t launch_prefix_attention(const PrefixArgs& a, int dtype, void* ws, in
   w.rows = a.own.B * w.R;
   row_blocks(tc, w.rows, &w.rbs, &w.nrbs);
   row_blocks(tc, w.R, &w.rbo, &w.nrbo);
-  // a chunk against two tiles of rows takes longer than against one
+  // In units of half a chunk against one tile.  A chunk against two tiles takes 3 (2: 8 x 65 nodes 84 us for 77), and an item
+  // besides as long as 3 chunks (1: 102; 2 and 4: 32 single rows 52 and 53 us for 50).  On the CUDA cores calls are small, and
+  // a share without chunks would be an idle CTA (3: 3 x 31 nodes 30 us for 20).
   w.item = tc ? 3 : 0;
   w.cost_s = tc && w.rbs > 128 ? 3 : 2;
   w.cost_o = tc && w.rbo > 128 ? 3 : 2;

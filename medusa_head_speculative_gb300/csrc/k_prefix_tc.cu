@@ -640,6 +640,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------------ host side
+// (The CUDA cores' kernel in place of this one: 16 x 43 nodes of 4 x 8 heads over 8192 slots 7.6 ms for 115 us; float rows
+// and heads of 32 it takes alone.)
 bool prefix_tc_takes(int dtype, int dh) { return dtype == MEDUSA_BF16 && (dh == 64 || dh == 128); }
 
 static bool make_map(CUtensorMap* map, const void* p, const CacheView& c) {
@@ -656,7 +658,8 @@ template <int DH> static cudaError_t tc_go(PtArgs& g, cudaStream_t st) {
   constexpr size_t CHUNK = DH / 64 * 128 * 128, limit = 225 * 1024;
   static unsigned long long done = 0;
   for (int kind = 0; kind < 2; ++kind) {
-    // with one tile a block's queries are copied a block ahead where blocks are short, of a few chunks
+    // with one tile a block's queries are copied a block ahead where blocks are short, of a few chunks (8 x 65 nodes
+    // 78.0 -> 76.5 us; with long ones, the shared kind's, it is the same either way)
     g.qb[kind] = g.nt[kind] == 1 && kind == 1 ? 2 : 1;
     const int stages = (int)((limit - 1024) / CHUNK) - g.nt[kind] * g.qb[kind];
     if (g.nt[kind] == 1) {                           // even depths: see above
