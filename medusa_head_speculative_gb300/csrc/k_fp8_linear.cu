@@ -29,6 +29,7 @@
 // Every wait is bounded; on expiry MEDUSA_FLAG_TIMEOUT is set, the CTA stops taking work, drains the copies
 // it issued and frees its tensor memory.
 #include <algorithm>
+#include <cfloat>
 
 #include "fp8.cuh"
 #include "launch.cuh"
@@ -153,6 +154,19 @@ __device__ __forceinline__ float2 fma2(float2 v, float2 s, float2 c) {
   return *reinterpret_cast<float2*>(&r);
 }
 
+// A group's sums reach 448^2 128 = 2^24.6, so where the product of a row's and a weight scale is no normal float it has lost
+// bits that the result needs.  The sum takes one after the other then, the larger one first: it is below
+// 2^-126 / 2^-149 = 2^23 and cannot make the sum overflow.
+struct FlScale {
+  float first, then;
+};
+__device__ __forceinline__ FlScale fl_apart(float x, float w) {
+  if (fabsf(x * w) >= FLT_MIN || x == 0.f || w == 0.f) return {1.f, x * w};
+  return fabsf(x) > fabsf(w) ? FlScale{x, w} : FlScale{w, x};
+}
+// Whether a scale may bring that about (of two without a small one the product is 2^-126 at least).
+__device__ __forceinline__ bool fl_small(float s) { return fabsf(s) < 0x1p-63f && s != 0.f; }
+
 // silu(x) u.  (__fdividef gives 0 where 1 + e^-x passes 2^126; the quotient is below 10^-35 there.)
 __device__ __forceinline__ float gate(float x, float u) { return __fdividef(x, 1.f + expf(-x)) * u; }
 
@@ -210,6 +224,7 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_linear_kernel(const __grid_
   __shared__ uint64_t bars[FB_COUNT];
   __shared__ uint32_t tmem_slot;
   __shared__ float s_x[FL_SC][128], s_w[FL_SC][2];   // scales
+  __shared__ int2 s_small[FL_SC];                    // whether there is a small one among them (of either warp's)
   __shared__ int s_issued, s_waited, s_abort;
   const Fp8LinearArgs& a = g.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, ST = g.stages;
@@ -341,6 +356,8 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_linear_kernel(const __grid_
             s_x[at][t] = f[0][e];
             s_x[at][t + 64] = f[1][e];
             if (t < 2) s_w[at][t] = u[e];
+            const int small = __any_sync(0xffffffffu, fl_small(f[0][e]) || fl_small(f[1][e]) || fl_small(u[e]));
+            if (lane == 0) (warp == 2 ? s_small[at].x : s_small[at].y) = small;
             mbar_arrive(bar(FB_SF + at));
             ++c;
           }
@@ -363,7 +380,11 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_linear_kernel(const __grid_
       for (int i = 0; i < HC / 2; ++i) acc[i] = make_float2(0.f, 0.f);
       for (int i = 0; i < s.n; ++i, ++c) {
         const int buf = c & 1, at = c % FL_SC;
-        const bool got = mbar_wait(bar(FB_SF + at), (c / FL_SC) & 1, TC_TIMEOUT_NS) && mbar_wait(bar(FB_DONE + k.st), k.ph, TC_TIMEOUT_NS);
+        bool got = mbar_wait(bar(FB_SF + at), (c / FL_SC) & 1, TC_TIMEOUT_NS);
+        const float x = s_x[at][wl * 32 + lane], w0 = s_w[at][GATED || BN == 128 ? 0 : part], w1 = GATED ? s_w[at][1] : w0;
+        float s0 = x * w0, s1 = x * w1;
+        const int2 small = s_small[at];
+        got = got && mbar_wait(bar(FB_DONE + k.st), k.ph, TC_TIMEOUT_NS);
         if (!__all_sync(0xffffffffu, got)) {
           timed_out = true;
           break;
@@ -371,9 +392,23 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_linear_kernel(const __grid_
         k.next(ST);
         tc_fence_after();
         if (live) {
-          const float x = s_x[at][wl * 32 + lane], s0 = x * s_w[at][GATED || BN == 128 ? 0 : part], s1 = GATED ? x * s_w[at][1] : s0;
           // 16 columns on their way while 16 are added up (gated: of the first matrix, then of the second)
           auto col = [&](int q) { return lanes + buf * BN + (GATED ? (q / GQ) * 128 + part * (HC / 2) + (q % GQ) * 16 : part * HC + q * 16); };
+          if (small.x | small.y) {                     // (in tensor memory: a second copy of the loop below is slower by more, also where none is small)
+            const FlScale f0 = fl_apart(x, w0), f1 = fl_apart(x, w1);
+#pragma unroll 1
+            for (int q = 0; q < HC / 16; ++q) {
+              uint32_t v[16];
+              float y[16];
+              fl_ld16(col(q), v);
+              fl_ld_wait(v);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) y[e] = __uint_as_float(v[e]) * (GATED && q >= GQ ? f1.first : f0.first);
+              tmem_st16(col(q), y);
+            }
+            s0 = f0.then;
+            s1 = f1.then;
+          }
           uint32_t v[2][16];
           fl_ld16(col(0), v[0]);
 #pragma unroll

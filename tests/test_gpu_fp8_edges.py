@@ -1,0 +1,103 @@
+"""8-bit products where a factor leaves the range of normal floats, against fp8_ref.py in 64 bits, through the public binding.
+The bounds are those that test_gpu_fp8.py derives, with what each test adds to them beside it."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_ref as F
+from harness import ensure_built
+from medusa_head_speculative_gb300 import binding as Bnd
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+MOST = float(np.finfo(np.float32).max)
+TINY = 2.0 ** -149                                # a step of floats below 2^-126
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    ensure_built()
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def codes_of(r, rows, k):
+    return F.round8(r.standard_normal((rows, k)), 128)[0]
+
+
+def dev(codes):
+    return torch.from_numpy(codes).view(torch.float8_e4m3fn).cuda()
+
+
+def scales(r, shape, of):
+    return np.float32(r.choice(np.float32(of), shape))
+
+
+def run(rows, n, k, x, xs, w, ws, up=None, us=None):
+    h = Bnd.Fp8(n=n, k=k, max_rows=rows, gated=up is not None)
+    y = torch.zeros(rows, n, device="cuda")
+    g = lambda s: None if s is None else torch.from_numpy(s).cuda()  # noqa: E731
+    Bnd.fp8_linear(h, x, dev(w), g(ws), y, torch.empty(h.workspace_size, dtype=torch.uint8, device="cuda"), x_scales=g(xs),
+                   up=None if up is None else dev(up), up_scales=g(us))
+    assert h.status() == 0
+    return f64(y)
+
+
+def product(x, w, ws, kb):
+    """x (64 bits) times weights: the value, and the bound of the library's sums.  Of its 2u (128 + kb + 4) the last 4 are for
+    the scales, one rounding each; where a result is below 2^-126 each group's addition is off by up to half a TINY."""
+    wv = F.values(w, ws.astype(float), 128)
+    return x @ wv.T, 2 * U * (128 + kb + 4) * (np.abs(x) @ np.abs(wv).T) + kb * TINY
+
+
+ROW_SCALES = [2.0 ** -126, 2.0 ** -122, 1.3 * 2.0 ** -118, 1.0, 0.0, -2.0 ** -120, 2.0 ** 20]
+WEIGHT_SCALES = [2.0 ** -24, 1.3 * 2.0 ** -24, 7.3e-4, 1.3e-6, -1e-3, 3 * 2.0 ** -149]
+
+
+@pytest.mark.parametrize("rows,n,k,gated", [(5, 700, 272, 0), (200, 770, 400, 0), (37, 641, 5120, 0), (33, 700, 400, 1), (150, 670, 144, 1)])
+def test_scales_whose_product_is_no_normal_float(rows, n, k, gated):
+    """Row scales as rounding tiny rows gives them times small weight scales: their product has lost bits, or is 0, where the
+    result is a normal float.  A row and a block of weights have one scale each; rows of other scales lie between them, so that
+    a warp has both kinds."""
+    r = np.random.default_rng(rows + n)
+    kb, nb = -(-k // 128), -(-n // 128)
+    x, w = codes_of(r, rows, k), codes_of(r, n, k)
+    xs = np.float32(np.repeat(np.float32(ROW_SCALES)[np.arange(rows) % 7, None], kb, 1))
+    ws = np.float32(np.repeat(np.float32(WEIGHT_SCALES)[np.arange(nb) % 6, None], kb, 1))
+    xv = F.values(x, xs.astype(float), 1)
+    a, da = product(xv, w, ws, kb)
+    assert ((np.abs(a) < 1e-30) & (np.abs(a) > 1e-37)).mean() > 0.1
+    if not gated:
+        want, tol = a, da
+        got = run(rows, n, k, dev(x), xs, w, ws)
+    else:                                         # large factors beside tiny ones
+        up, us = codes_of(r, n, k), scales(r, (nb, kb), [1e24, -3e23])
+        b, db = product(xv, up, us, kb)
+        s = F.silu(a)
+        want, tol = s * b, 1.1 * da * np.abs(b) + (np.abs(s) + 1.1 * da) * db + 8 * U * np.abs(s * b) + TINY * np.abs(b)
+        got = run(rows, n, k, dev(x), xs, w, ws, up, us)
+    tol = tol + U * np.abs(want) + TINY
+    far = np.abs(want) - tol > MOST               # a gated result past the range of floats is an infinity
+    assert (got[far] == np.copysign(np.inf, want[far])).all()
+    near = ~far & (np.abs(want) + tol <= MOST)
+    assert (near | far).mean() > 0.95             # (where a sum is large its bound may pass the range, whatever the result is)
+    err = np.abs(got - want)[near]
+    assert (err <= tol[near]).all(), (err / tol[near]).max()
+
+
+@pytest.mark.parametrize("size", [1e-37, 3e-36])
+def test_tiny_rows_times_small_weights(size):
+    """The same through the rounding of the call itself."""
+    rows, n, k = 9, 260, 656
+    r = np.random.default_rng(4)
+    x = torch.from_numpy(r.standard_normal((rows, k)) * size).float()
+    c, s = F.round8(f64(x), 1)
+    assert s.max() <= 2.0 ** -120
+    w, ws = codes_of(r, n, k), scales(r, (3, 6), [7.3e-4, 1.3e-6])
+    want, tol = product(F.values(c, s, 1), w, ws, 6)
+    err = np.abs(run(rows, n, k, x.cuda(), None, w, ws) - want)
+    tol = tol + U * np.abs(want) + TINY
+    assert (err <= tol).all(), (err / tol).max()
