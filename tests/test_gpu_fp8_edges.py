@@ -101,3 +101,20 @@ def test_tiny_rows_times_small_weights(size):
     err = np.abs(run(rows, n, k, x.cuda(), None, w, ws) - want)
     tol = tol + U * np.abs(want) + TINY
     assert (err <= tol).all(), (err / tol).max()
+
+
+def test_a_gate_far_below_zero():
+    """silu(a) b with a down to -300 and b up to 3e38.  Rows hold one 1 for each matrix, so that sums are exact: a = -scale, b = scale
+    * up's scale * code, one rounding.  silu(a) b: four exponentials (a unit in the last place each, 2u), five products, or one, a sum
+    and a quotient (two units): 16u of it with b's and the last rounding."""
+    a = -np.float32([0.5, 20, 63, 63.9, 64, 64.1, 70, 80, 87, 87.3, 87.4, 88, 88.7, 88.8, 95, 103, 110, 120, 150, 170, 180, 200, 300])
+    rows, n, k = len(a), 24, 16
+    x, w, up = (np.zeros((m, k), np.uint8) for m in (rows, n, n))
+    x[:, :2], w[:, 0] = 0x38, 0xb8                # 1, -1
+    up[:, 1] = F.encode(np.r_[1.0:13.0, -1.0, -3.5, 448, 0.5, 0, 0, 2.0 ** -9, 7, 9, 16, 20, 24])
+    for us in (1e-30, 1.0, 1e30, 2e33, 3e38 / 448 / 300):
+        b = np.float32(-a * np.float32(us)).astype(float)[:, None] * F.decode(up[:, 1])[None]
+        want = F.silu(a.astype(float))[:, None] * b
+        got = run(rows, n, k, dev(x), -a[:, None], w, np.ones((1, 1), np.float32), up, np.full((1, 1), us, np.float32))
+        err, tol = np.abs(got - want), 16 * U * np.abs(want) + TINY
+        assert (err <= tol).all(), (err / tol).max()
