@@ -623,6 +623,10 @@ medusa_status medusa_prefix_attention(const medusa_cache* own, const medusa_kv* 
                                       const medusa_cache* shared, const medusa_kv* shared_kv,
                                       const medusa_kv4_query* query, void* workspace, size_t ws_bytes,
                                       void* stream);
+/* Failure-path testing, as medusa_cache_expire_wait_once: for the next medusa_prefix_attention call with this
+ * cache as `own`.  MEDUSA_ERR_INVALID for ns = 0 or above 10 s, MEDUSA_ERR_UNSUPPORTED for caches whose kernel has no
+ * such waits (formats other than MEDUSA_BF16, heads of 32). */
+medusa_status medusa_prefix_expire_wait_once(medusa_cache* own, unsigned long long ns);
 
 /* ------------------------------------------------------------------ projections in 8 bits */
 /* Matrix products of rows and weights held in 8 bits, for the projections of a layer and for

@@ -178,6 +178,7 @@ def lib():
         "medusa_kv_read": (I, [P, C.POINTER(KV), C.POINTER(KVPlaces), C.c_float, C.c_float, P]),
         "medusa_kv4_attention": (I, [P, C.POINTER(KV), C.POINTER(KV4Query), P, SZ, P]),
         "medusa_prefix_workspace_size": (SZ, [P, P]),
+        "medusa_prefix_expire_wait_once": (I, [P, C.c_ulonglong]),
         "medusa_prefix_attention": (I, [P, C.POINTER(KV), P, C.POINTER(KV), C.POINTER(KV4Query), P, SZ, P]),
         "medusa_fp8_create": (I, [C.POINTER(Fp8Dims), C.POINTER(P)]),
         "medusa_fp8_destroy": (None, [P]),
@@ -624,6 +625,10 @@ class Cache:
     def expire_wait_once(self, ns):
         """Failure-path testing: see medusa_cache_expire_wait_once."""
         _check("medusa_cache_expire_wait_once", lib().medusa_cache_expire_wait_once(self.handle, int(ns)))
+
+    def prefix_expire_wait_once(self, ns):
+        """Failure-path testing: see medusa_prefix_expire_wait_once."""
+        _check("medusa_prefix_expire_wait_once", lib().medusa_prefix_expire_wait_once(self.handle, int(ns)))
 
     def close(self):
         if getattr(self, "handle", None):

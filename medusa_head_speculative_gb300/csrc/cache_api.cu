@@ -293,6 +293,13 @@ medusa_status medusa_cache_expire_wait_once(medusa_cache* c, unsigned long long 
   return MEDUSA_OK;
 }
 
+medusa_status medusa_prefix_expire_wait_once(medusa_cache* own, unsigned long long ns) {
+  if (!own || ns == 0 || ns > 10000000000ull) return MEDUSA_ERR_INVALID;
+  if (!prefix_tc_takes(own->d.format, own->d.dh)) return MEDUSA_ERR_UNSUPPORTED;
+  own->test_wait_ns.store(ns);
+  return MEDUSA_OK;
+}
+
 medusa_status medusa_kv_append(const medusa_cache* c, const medusa_kv* kv, const medusa_kv_rows* rows,
                                const medusa_rope* rope, float k_scale, float v_scale, void* stream) {
   EntryScope scope("medusa_kv_append");
@@ -425,6 +432,7 @@ medusa_status medusa_prefix_attention(const medusa_cache* own, const medusa_kv* 
   a.scale2 = (q->scale > 0 ? q->scale : 1.0f / std::sqrt((float)own->d.dh)) * 1.4426950408889634f;
   if (!(a.scale2 >= 1.2e-38f)) a.scale2 = 1.2e-38f;       // not 0: a masked score's -infinity stays one
   a.status = own->status;
+  if (own->test_wait_ns.load(std::memory_order_relaxed)) a.test_wait_ns = own->test_wait_ns.exchange(0);
   return done(launch_prefix_attention(a, q->dtype, ws, own->num_sms, S(stream)));
 }
 

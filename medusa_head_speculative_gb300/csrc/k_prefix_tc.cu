@@ -36,7 +36,7 @@
 // sees every other chunk of the CTA, odd or even ones over all its items, and the rings are of two or four
 // stages, so that a stage is always the same slot's.
 // Every wait is bounded; on expiry MEDUSA_FLAG_TIMEOUT is set, the CTA stops taking work, lets its MMAs and
-// copies end and frees its tensor memory.
+// copies end, also those that nobody came to wait for, and frees its tensor memory.
 #include <algorithm>
 
 #include "attn_mma.cuh"
@@ -66,11 +66,11 @@ struct PtArgs {
 // stage).  Per slot: P1 and P2 (P of the first 64 keys, of all written), O1 (P V of the first done).  One barrier for
 // both who wait: each commit costs the tensor cores 50 to 75 cycles (QK and PV of a chunk take 1025 cycles
 // without, 1390 with four).  MRG / MFR: the second slot's (reference, sum) are in shared
-// memory / consumed.  END: every MMA issued has completed.
+// memory / consumed.  END: every MMA issued has completed.  NEVER: nothing arrives (tests).
 enum {
   XB_QF = 0, XB_QE = 2, XB_KF = 4, XB_VF = XB_KF + PT_MAXST, XB_SF = XB_VF + PT_MAXST, XB_OF = XB_SF + 2 * PT_MAXST,
   XB_P1 = XB_OF + 2 * PT_MAXST, XB_P2 = XB_P1 + 2, XB_O1 = XB_P2 + 2, XB_MRG = XB_O1 + 2, XB_MFR = XB_MRG + 1,
-  XB_END = XB_MFR + 1, XB_COUNT = XB_END + 1
+  XB_END = XB_MFR + 1, XB_NEVER = XB_END + 1, XB_COUNT = XB_NEVER + 1
 };
 
 // Of chunk j (pc: chunks of cached slots, len of them): whether it is of the call's own rows, its keys, and
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t bars[XB_COUNT];
   __shared__ uint32_t tmem_slot, s_bad[8][4];        // keys of the call's own rows whose values are not finite
-  __shared__ int s_abort;
+  __shared__ int s_abort, s_copied;                  // s_copied: chunks whose copies have begun
   __shared__ float2 s_ml[PT_ROWS];                   // second slot's (reference, sum) per row
   const PxWork& w = g.w;
   const PrefixArgs& a = w.a;
@@ -152,7 +152,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
     mbar_init(bar(XB_MRG), PT_ROWS);
     mbar_init(bar(XB_MFR), PT_ROWS);
     mbar_init(bar(XB_END), 2);
-    s_abort = 0;
+    mbar_init(bar(XB_NEVER), 1);
+    s_abort = s_copied = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == PT_MMA_WARP) tmem_alloc(smem_u32(&tmem_slot), 2 * PT_SLOT_COLS);
@@ -284,12 +285,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
       if (aborted()) break;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    // the last copies of each ring: if the block gives up nobody else waits for them (bounded)
-    if (boss && (timed_out || aborted()))
-      for (int part = 0; part < 2; ++part) {
-        const int n = part ? SV : SK;
-        for (int y = max(0, x - n); y < x; ++y) mbar_wait(bar((part ? XB_VF : XB_KF) + y % n), (y / n) & 1, TC_TIMEOUT_NS / 16);
-      }
+    if (boss) s_copied = x + timed_out;              // (given up between a chunk's keys and its values: the keys count)
   } else if (warp >= PT_MMA_WARP) {
     // ------------------------------------------------------------ MMAs of one slot
     reg_fewer<PT_REG_REST>();
@@ -304,7 +300,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
       const int step = nt == 2 ? 1 : 2;                  // two tiles: every chunk; one: alternate ones
       int gc = 0, qn = 0, mc = 0;         // chunks, blocks and merged blocks so far
       int done = 0, halves = 0;           // this slot's chunks with rows so far, and those of more than 64 keys
-      bool dead = false;
+      bool dead = a.test_wait_ns && slot == 0 && !__all_sync(0xffffffffu, mbar_wait(bar(XB_NEVER), 0, a.test_wait_ns));
       int pc = 0, len = 0;                // of the item's cache
       PtRing kr = {nt == 2 ? 0 : slot, 0}, vr = kr;  // (rings have two stages at least)
       // a stage written by 16-byte copies (the generic proxy) is made visible to the MMAs
@@ -629,12 +625,25 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
     }
   }
   if (timed_out) {
+    kt_st_wait();                                    // (a softmax warp may have left in the middle of a chunk)
     set_flag(a.status, MEDUSA_FLAG_TIMEOUT);
     *(volatile int*)&s_abort = 1;
   }
   tc_fence_before();
   __syncthreads();
-  if (tid == 0) mbar_wait(bar(XB_END), 0, TC_TIMEOUT_NS);      // every MMA done
+  if (tid == 0) {
+    mbar_wait(bar(XB_END), 0, TC_TIMEOUT_NS);        // every MMA done
+    // and, where the block gave up, each ring's last copies: a stage that a consumer did not come to may still be written
+    // (without all arrivals its phase does not end, and the limit is far beyond the time of a copy)
+    if (aborted())
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part) {
+        const int n = part ? SV : SK;
+#pragma unroll 1
+        for (int y = max(0, s_copied - n); y < s_copied; ++y)
+          mbar_wait(bar((part ? XB_VF : XB_KF) + y % n), (y / n) & 1, TC_TIMEOUT_NS / 16);
+      }
+  }
   __syncthreads();
   if (warp == PT_MMA_WARP) tmem_dealloc(tmem, 2 * PT_SLOT_COLS);
 }

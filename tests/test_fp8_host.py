@@ -137,3 +137,7 @@ def test_reference_attention_is_a_mean():
     a, _ = A.attention(q, [(k, v)], None, 0.3, 0)
     b, _ = A.attention(q, [(k[2:], v[2:]), (k[:2], v[:2])], np.ones((2, 2), bool), 0.3, 0)
     assert np.abs(a - b).max() < 1e-12
+
+
+def test_prefix_expire_wait_needs_a_cache():
+    assert Bnd.lib().medusa_prefix_expire_wait_once(None, 1000) == Bnd.MEDUSA_ERR_INVALID
