@@ -624,8 +624,8 @@ medusa_status medusa_prefix_attention(const medusa_cache* own, const medusa_kv* 
                                       const medusa_kv4_query* query, void* workspace, size_t ws_bytes,
                                       void* stream);
 /* Failure-path testing, as medusa_cache_expire_wait_once: for the next medusa_prefix_attention call with this
- * cache as `own`.  MEDUSA_ERR_INVALID for ns = 0 or above 10 s, MEDUSA_ERR_UNSUPPORTED for caches whose kernel has no
- * such waits (formats other than MEDUSA_BF16, heads of 32). */
+ * cache as `own` (a captured one: in every replay).  MEDUSA_ERR_INVALID for ns = 0 or above 10 s,
+ * MEDUSA_ERR_UNSUPPORTED for caches whose kernel has no such waits (formats other than MEDUSA_BF16, heads of 32). */
 medusa_status medusa_prefix_expire_wait_once(medusa_cache* own, unsigned long long ns);
 
 /* ------------------------------------------------------------------ projections in 8 bits */
@@ -650,6 +650,9 @@ void medusa_fp8_destroy(medusa_fp8* h);
 size_t medusa_fp8_workspace_size(const medusa_fp8* h);
 /* As medusa_get_status, for the handle's own status word. */
 medusa_status medusa_fp8_get_status(const medusa_fp8* h, void* stream, uint32_t* flags);
+/* Failure-path testing, as medusa_plan_expire_wait_once: for the next medusa_fp8_linear call of at least one row with
+ * this handle (a captured one: in every replay).  MEDUSA_ERR_INVALID for ns = 0 or above 10 s. */
+medusa_status medusa_fp8_expire_wait_once(medusa_fp8* h, unsigned long long ns);
 /* Rounds x [rows][k] (element e of row r at x[r * x_row + e], dtype MEDUSA_F32 or MEDUSA_BF16) to
  * codes [rows][k] (4-byte aligned) and scales.  block = 1: rows, 0 <= rows <= max_rows; block = 128: weights, rows = n. */
 medusa_status medusa_fp8_round(const medusa_fp8* h, const void* x, int dtype, int rows, long long x_row,
@@ -666,8 +669,8 @@ enum { MEDUSA_E4M3 = 3 };
  *   add: NULL or [rows][n] of y's dtype, row stride add_row; y itself with equal strides, or apart from it
  *   y: [rows][n], MEDUSA_F32 or MEDUSA_BF16, row stride y_row >= n, apart from everything but add
  * The products of 128 elements are summed in float on the tensor cores, scaled, and added up in float;
- * the result is rounded once.  rows = 0 does nothing.  Calls that may run at the same time need
- * workspaces of their own. */
+ * the result is rounded once.  rows = 0 does nothing.  An expired wait sets MEDUSA_FLAG_TIMEOUT in the handle's
+ * status.  Calls that may run at the same time need workspaces of their own. */
 typedef struct {
   const void* x;
   int x_dtype;

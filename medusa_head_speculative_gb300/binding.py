@@ -184,6 +184,7 @@ def lib():
         "medusa_fp8_destroy": (None, [P]),
         "medusa_fp8_workspace_size": (SZ, [P]),
         "medusa_fp8_get_status": (I, [P, P, C.POINTER(C.c_uint32)]),
+        "medusa_fp8_expire_wait_once": (I, [P, C.c_ulonglong]),
         "medusa_fp8_round": (I, [P, P, I, I, C.c_longlong, P, P, I, P]),
         "medusa_fp8_read": (I, [P, P, P, I, I, P, I, C.c_longlong, P]),
         "medusa_fp8_linear": (I, [P, C.c_char_p, P, SZ, P]),         # medusa_fp8_product as bytes
@@ -762,6 +763,10 @@ class Fp8:
 
     def status(self, stream=None):
         return _status("medusa_fp8_get_status", self.handle, stream)
+
+    def expire_wait_once(self, ns):
+        """Failure-path testing: see medusa_fp8_expire_wait_once."""
+        _check("medusa_fp8_expire_wait_once", lib().medusa_fp8_expire_wait_once(self.handle, int(ns)))
 
     def close(self):
         if getattr(self, "handle", None):

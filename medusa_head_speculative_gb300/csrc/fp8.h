@@ -32,6 +32,7 @@ struct Fp8LinearArgs {
   void* y; long y_row;
   int rows, n, k, kb;
   uint32_t* status;
+  unsigned long long test_wait_ns;                // failure-path tests only (0 otherwise): a wait that runs out
 };
 // Bytes of partials (`part`) a call may need.
 size_t fp8_linear_partials(int max_rows, int n, int kb, int num_sms);

@@ -2,7 +2,7 @@
 // include/medusa.h.
 #include <cuda_runtime.h>
 
-#include <cmath>
+#include <atomic>
 #include <new>
 
 #include "api.h"
@@ -17,6 +17,7 @@ struct medusa_fp8 {
   uint32_t* status = nullptr;
   int device = 0, num_sms = 152, kb = 0;
   size_t codes_bytes = 0, scales_bytes = 0, ws_bytes = 0;
+  mutable std::atomic<unsigned long long> test_wait_ns{0};
 };
 
 namespace {
@@ -80,6 +81,12 @@ size_t medusa_fp8_workspace_size(const medusa_fp8* h) { return h ? h->ws_bytes :
 medusa_status medusa_fp8_get_status(const medusa_fp8* h, void* stream, uint32_t* flags) {
   if (!h || !flags || !here(h->device)) return MEDUSA_ERR_INVALID;
   return read_status(h->status, stream, flags);
+}
+
+medusa_status medusa_fp8_expire_wait_once(medusa_fp8* h, unsigned long long ns) {
+  if (!h || ns == 0 || ns > 10000000000ull) return MEDUSA_ERR_INVALID;
+  h->test_wait_ns.store(ns);
+  return MEDUSA_OK;
 }
 
 medusa_status medusa_fp8_round(const medusa_fp8* h, const void* x, int dtype, int rows, long long x_row,
@@ -178,6 +185,7 @@ medusa_status medusa_fp8_linear(const medusa_fp8* h, const medusa_fp8_product* p
     a.xs = r.scales;
     a.x_row = h->d.k;
   }
+  if (h->test_wait_ns.load(std::memory_order_relaxed)) a.test_wait_ns = h->test_wait_ns.exchange(0);
   return done(launch_fp8_linear(a, p->y_dtype, base + h->codes_bytes + h->scales_bytes, h->num_sms, S(stream)));
 }
 

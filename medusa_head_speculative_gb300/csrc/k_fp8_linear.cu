@@ -59,8 +59,9 @@ struct FlArgs {
 
 // FULL: a stage has landed.  DONE: its products are in an accumulator, and the stage is free (one barrier for both: a
 // commit costs the tensor cores 50 to 75 cycles).  TE: an accumulator has been read.  SF, SE: scales have been written, read.  END: every MMA is done.
+// NEVER: nothing arrives (tests).
 enum { FB_FULL = 0, FB_DONE = FL_MAXST, FB_TE = 2 * FL_MAXST, FB_SF = FB_TE + 2, FB_SE = FB_SF + FL_SC,
-       FB_END = FB_SE + FL_SC, FB_COUNT = FB_END + 1 };
+       FB_END = FB_SE + FL_SC, FB_NEVER = FB_END + 1, FB_COUNT = FB_NEVER + 1 };
 // A place in the ring of stages (a division by its depth would take longer than what it is needed for).
 struct FlRing {
   int st, ph;
@@ -253,6 +254,7 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_linear_kernel(const __grid_
       mbar_init(bar(FB_SE + i), 4 * FL_PROMOTE);
     }
     mbar_init(bar(FB_END), 1);
+    mbar_init(bar(FB_NEVER), 1);
     s_issued = s_waited = s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -304,6 +306,7 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_linear_kernel(const __grid_
       // ------------------------------------------------------------ MMAs
       const uint32_t idesc = idesc_e4m3(128, BN);
       int c = 0;
+      if (a.test_wait_ns) timed_out = !mbar_wait(bar(FB_NEVER), 0, a.test_wait_ns);
       while (!timed_out && fl_next<OC>(g, walk, s)) {
         for (int i = 0; i < s.n; ++i, ++c) {
           const int buf = c & 1;

@@ -141,3 +141,7 @@ def test_reference_attention_is_a_mean():
 
 def test_prefix_expire_wait_needs_a_cache():
     assert Bnd.lib().medusa_prefix_expire_wait_once(None, 1000) == Bnd.MEDUSA_ERR_INVALID
+
+
+def test_fp8_expire_wait_needs_a_handle():
+    assert Bnd.lib().medusa_fp8_expire_wait_once(None, 1000) == Bnd.MEDUSA_ERR_INVALID

@@ -1,5 +1,8 @@
-"""8-bit products where a factor leaves the range of normal floats, against fp8_ref.py in 64 bits, through the public binding.
+"""8-bit products where a factor leaves the range of normal floats, against fp8_ref.py in 64 bits, and waits that run out.
+
 The bounds are those that test_gpu_fp8.py derives, with what each test adds to them beside it."""
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -118,3 +121,45 @@ def test_a_gate_far_below_zero():
         got = run(rows, n, k, dev(x), -a[:, None], w, np.ones((1, 1), np.float32), up, np.full((1, 1), us, np.float32))
         err, tol = np.abs(got - want), 16 * U * np.abs(want) + TINY
         assert (err <= tol).all(), (err / tol).max()
+
+
+# rows, n, k, gated: shares of a few columns, whole tiles, tiles of 256 columns in shares, a pair
+@pytest.mark.parametrize("rows,n,k,gated", [(1, 4096, 4096, 0), (5, 130, 16, 0), (300, 700, 8192, 0), (700, 5000, 640, 0), (40, 3000, 2048, 1)])
+@pytest.mark.parametrize("x", ["codes", "bf16"])
+def test_expired_wait_is_reported_and_nothing_else_is_lost(rows, n, k, gated, x):
+    """A bounded wait is made to run out: the call returns with MEDUSA_FLAG_TIMEOUT, whatever the workspace held, and the next one
+    on the same workspace is as before."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    codes = lambda m: torch.randint(0, 119, (m, k), dtype=torch.uint8, device="cuda", generator=g)  # noqa: E731
+    h = Bnd.Fp8(n=n, k=k, max_rows=rows, gated=bool(gated))
+    kb, nb = h.kb, h.nb
+    y, ws = torch.zeros(rows, n, device="cuda"), torch.empty(h.workspace_size, dtype=torch.uint8, device="cuda")
+    args = dict(x=codes(rows), x_scales=torch.rand(rows, kb, device="cuda", generator=g) * 1e-3) if x == "codes" else \
+        dict(x=torch.randn(rows, k, device="cuda", generator=g).bfloat16())
+    args.update(w=codes(n), w_scales=torch.rand(nb, kb, device="cuda", generator=g) * 1e-6)
+    if gated:
+        args.update(up=codes(n), up_scales=torch.rand(nb, kb, device="cuda", generator=g) * 1e-6)
+
+    def call():
+        ws.fill_(0x7f)
+        y.fill_(7.0)
+        t0 = time.perf_counter()
+        Bnd.fp8_linear(h, y=y, ws=ws, **args)
+        torch.cuda.synchronize()
+        return y.clone(), time.perf_counter() - t0
+
+    clean, _ = call()
+    assert h.status() == 0 and torch.isfinite(clean).all()
+    h.expire_wait_once(2_000_000)
+    assert call()[1] < 30.0
+    assert h.status() == Bnd.FLAG_TIMEOUT
+    again, _ = call()
+    assert h.status() == 0 and torch.equal(again, clean)
+
+
+def test_expire_wait_argument_checks():
+    h = Bnd.Fp8(n=16, k=16, max_rows=1)
+    for ns in (0, 10**10 + 1):
+        with pytest.raises(Bnd.MedusaError) as e:
+            h.expire_wait_once(ns)
+        assert e.value.code == Bnd.MEDUSA_ERR_INVALID
