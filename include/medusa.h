@@ -650,6 +650,9 @@ void medusa_fp8_destroy(medusa_fp8* h);
 size_t medusa_fp8_workspace_size(const medusa_fp8* h);
 /* As medusa_get_status, for the handle's own status word. */
 medusa_status medusa_fp8_get_status(const medusa_fp8* h, void* stream, uint32_t* flags);
+/* How medusa_fp8_linear cuts a call of `rows` rows up (gated = 1: with `up`), for tests and measurements: tiles of 128 rows
+ * by *columns results, of which *whole are each computed by one block, and *shared added up from several blocks' sums. */
+medusa_status medusa_fp8_tiles(const medusa_fp8* h, int rows, int gated, int* columns, int* whole, int* shared);
 /* Failure-path testing, as medusa_plan_expire_wait_once: for the next medusa_fp8_linear call of at least one row with
  * this handle (a captured one: in every replay).  MEDUSA_ERR_INVALID for ns = 0 or above 10 s. */
 medusa_status medusa_fp8_expire_wait_once(medusa_fp8* h, unsigned long long ns);

@@ -184,6 +184,7 @@ def lib():
         "medusa_fp8_destroy": (None, [P]),
         "medusa_fp8_workspace_size": (SZ, [P]),
         "medusa_fp8_get_status": (I, [P, P, C.POINTER(C.c_uint32)]),
+        "medusa_fp8_tiles": (I, [P, I, I, C.POINTER(I), C.POINTER(I), C.POINTER(I)]),
         "medusa_fp8_expire_wait_once": (I, [P, C.c_ulonglong]),
         "medusa_fp8_round": (I, [P, P, I, I, C.c_longlong, P, P, I, P]),
         "medusa_fp8_read": (I, [P, P, P, I, I, P, I, C.c_longlong, P]),
@@ -763,6 +764,12 @@ class Fp8:
 
     def status(self, stream=None):
         return _status("medusa_fp8_get_status", self.handle, stream)
+
+    def tiles(self, rows, gated=False):
+        """medusa_fp8_tiles: (columns of a tile, tiles of one block each, tiles that several blocks share)."""
+        out = [C.c_int() for _ in range(3)]
+        _check("medusa_fp8_tiles", lib().medusa_fp8_tiles(self.handle, rows, 1 if gated else 0, *map(C.byref, out)))
+        return tuple(x.value for x in out)
 
     def expire_wait_once(self, ns):
         """Failure-path testing: see medusa_fp8_expire_wait_once."""

@@ -34,6 +34,12 @@ struct Fp8LinearArgs {
   uint32_t* status;
   unsigned long long test_wait_ns;                // failure-path tests only (0 otherwise): a wait that runs out
 };
+// How a call of so many rows is cut up: tiles of 128 rows by `columns` results, `whole` of them each one CTA's, `shared` added
+// up from several CTAs' partials.
+struct Fp8Tiles {
+  int columns, whole, shared;
+};
+Fp8Tiles fp8_linear_tiles(int rows, int n, int kb, bool gated, int num_sms);
 // Bytes of partials (`part`) a call may need.
 size_t fp8_linear_partials(int max_rows, int n, int kb, int num_sms);
 cudaError_t launch_fp8_linear(const Fp8LinearArgs& a, int dtype, void* part, int num_sms, cudaStream_t st);

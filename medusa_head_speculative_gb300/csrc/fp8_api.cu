@@ -83,6 +83,16 @@ medusa_status medusa_fp8_get_status(const medusa_fp8* h, void* stream, uint32_t*
   return read_status(h->status, stream, flags);
 }
 
+medusa_status medusa_fp8_tiles(const medusa_fp8* h, int rows, int gated, int* columns, int* whole, int* shared) {
+  if (!h || !columns || !whole || !shared || rows < 1 || rows > h->d.max_rows || (gated != 0 && gated != h->d.gated))
+    return MEDUSA_ERR_INVALID;
+  const Fp8Tiles t = fp8_linear_tiles(rows, h->d.n, h->kb, gated != 0, h->num_sms);
+  *columns = gated ? t.columns / 2 : t.columns;
+  *whole = t.whole;
+  *shared = t.shared;
+  return MEDUSA_OK;
+}
+
 medusa_status medusa_fp8_expire_wait_once(medusa_fp8* h, unsigned long long ns) {
   if (!h || ns == 0 || ns > 10000000000ull) return MEDUSA_ERR_INVALID;
   h->test_wait_ns.store(ns);

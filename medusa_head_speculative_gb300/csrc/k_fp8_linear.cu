@@ -606,6 +606,12 @@ static FlPlan fl_plan(int rows, int n, int kb, bool gated, int num_sms) {
   return p;
 }
 
+Fp8Tiles fp8_linear_tiles(int rows, int n, int kb, bool gated, int num_sms) {
+  const FlPlan p = fl_plan(rows, n, kb, gated, num_sms);
+  const int left = p.mt * p.nt - p.whole, shared = p.shares == left ? 0 : left;       // (as many CTAs as tiles: one each)
+  return {p.bn, p.mt * p.nt - shared, shared};
+}
+
 size_t fp8_linear_partials(int max_rows, int n, int kb, int num_sms) {
   // tiles that are left are fewer than CTAs, and a tile has no more shares than groups
   const size_t tiles = (size_t)((max_rows + 127) / 128) * ((n + 127) / 128);

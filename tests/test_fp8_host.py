@@ -145,3 +145,8 @@ def test_prefix_expire_wait_needs_a_cache():
 
 def test_fp8_expire_wait_needs_a_handle():
     assert Bnd.lib().medusa_fp8_expire_wait_once(None, 1000) == Bnd.MEDUSA_ERR_INVALID
+
+
+def test_fp8_tiles_needs_a_handle():
+    out = C.c_int()
+    assert Bnd.lib().medusa_fp8_tiles(None, 1, 0, out, out, out) == Bnd.MEDUSA_ERR_INVALID
