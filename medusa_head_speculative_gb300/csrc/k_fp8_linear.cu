@@ -583,10 +583,13 @@ struct FlPlan {
 static FlPlan fl_plan(int rows, int n, int kb, bool gated, int num_sms) {
   FlPlan p;
   p.mt = (rows + 127) / 128;
-  // Columns of a tile, 128 / 256, in us: 1 x 4096 x 4096 10.2 / 10.6, 64 rows of these 13.7 / 14.6, 128 x 15360 x 5120 21.1 /
-  // 28.9 (shares are evener), 128 x 32000 x 4096 34.0 / 29.9; 200 x 15360 x 5120 37.5 / 27.5, 520 x 4096 x 4096 28.1 / 23.0, 520 x
-  // 15360 x 5120 70 / 51 (each row loaded half as often).
-  p.bn = gated || p.mt > 1 ? 256 : 128;
+  // Columns of a tile.  With one row of tiles 128 share the weights more evenly as long as tiles of 256 are for less than half
+  // of the CTAs, and are slower from there on; with more, 256 load each row half as often.  128 / 256, in us: 1 x 4096 x 4096
+  // 10.2 / 10.6; over 15360 x 5120 (60 tiles of 256) 1 row 22.5 / 21.3, 64 24.3 / 25.8, 128 23.6 / 32.8; over 20480 x 4096 (80)
+  // 25.6 / 21.7, 31.7 / 26.8, 32.8 / 24.9; over 32000 x 4096 (125) 31.0 / 28.2, 34.8 / 29.7, 34.8 / 30.2; over 48000 x 4096 (188)
+  // 41.7 / 41.4, 47.1 / 48.4, 49.1 / 53.4; over 64000 x 4096 (250) 53.3 / 48.9, 58.6 / 52.9, 61.2 / 54.9; 200 x 15360 x 5120
+  // 37.5 / 27.5, 520 x 4096 x 4096 28.1 / 23.0.
+  p.bn = gated || p.mt > 1 || 2 * ((n + 255) / 256) >= num_sms ? 256 : 128;
   const int oc = gated ? 128 : p.bn;
   p.nt = (n + oc - 1) / oc;
   const long tiles = (long)p.mt * p.nt;

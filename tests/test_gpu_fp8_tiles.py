@@ -73,3 +73,17 @@ def test_tiles_of_one_and_of_several_blocks(rows, n, k, y, add, gated, columns, 
     err = (out.double() - want).abs()
     assert (err <= tol).all(), (err / tol).max()
     assert (wide[:, :3] == 7).all() and (wide[rows] == 7).all() and h.status() == 0
+
+
+@pytest.mark.parametrize("rows", [1, 64, 128])
+def test_columns_of_a_tile_go_by_how_many_blocks_have_one(rows):
+    """One row of tiles: 128 columns while tiles of 256 are for less than half of the blocks."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for n, columns in ((16, 128), (256 * (-(-sms // 2) - 1), 128), (256 * (-(-sms // 2) - 1) + 1, 256), (64000, 256)):
+        assert Bnd.Fp8(n=n, k=256, max_rows=200).tiles(rows)[0] == columns, n
+        assert Bnd.Fp8(n=n, k=256, max_rows=200).tiles(129)[0] == 256
+
+
+@pytest.mark.parametrize("rows,n,k,y", [(1, 20480, 4096, "f32"), (128, 24000, 2048, "bf16"), (77, 19457, 400, "f32"), (9, 39000, 656, "bf16")])
+def test_wide_weights_for_one_row_of_tiles(rows, n, k, y):
+    test_tiles_of_one_and_of_several_blocks(rows, n, k, y, 1, 0, None, None, None)
