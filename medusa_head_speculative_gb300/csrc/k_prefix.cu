@@ -321,7 +321,8 @@ size_t prefix_workspace(int B, int Hq, int Hkv, int dh, int max_nodes, int num_s
 
 template <typename T, int DH> static cudaError_t simt_go(const PxWork& w, cudaStream_t st) {
   const size_t smem = (size_t)(2 * PS_ROWS * (DH + 4) + PS_KEYS * DH + PS_ROWS * 68) * sizeof(float);
-  const cudaError_t e = cudaFuncSetAttribute(prefix_simt_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static unsigned long long done = 0;
+  const cudaError_t e = allow_smem(prefix_simt_kernel<T, DH>, smem, &done);
   if (e != cudaSuccess) return e;
   return launch_kernel(prefix_simt_kernel<T, DH>, dim3(w.ctas), dim3(256), smem, st, 1, w);
 }
