@@ -17,6 +17,12 @@ template <typename T> __device__ __forceinline__ T from_f32(float x);
 template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
 template <> __device__ __forceinline__ bf16 from_f32<bf16>(float x) { return __float2bfloat16_rn(x); }
 
+// Two bf16 in 32 bits, the first in the lower half.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
 // Split an fp32 value into bf16 hi + bf16 lo with hi + lo = x to ~2^-16 relative: the
 // tensor-core GEMMs take fp32 activations as two bf16 operands.
 __device__ __forceinline__ void split_hi_lo(float x, bf16& hi, bf16& lo) {

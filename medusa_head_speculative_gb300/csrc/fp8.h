@@ -17,13 +17,13 @@ struct Fp8RoundArgs {
   int vec;                                        // 4 elements of x are one aligned load
   uint32_t* status;
 };
-cudaError_t launch_fp8_round(const Fp8RoundArgs& a, int dtype, int block, cudaStream_t st);
+cudaError_t launch_fp8_round(const Fp8RoundArgs& a, int dtype, int block, int num_sms, cudaStream_t st);
 struct Fp8ReadArgs {
   const uint8_t* codes; const float* scales;
   void* y; long y_row;
   int rows, k, kb, block, vec;
 };
-cudaError_t launch_fp8_read(const Fp8ReadArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_fp8_read(const Fp8ReadArgs& a, int dtype, int num_sms, cudaStream_t st);
 
 struct Fp8LinearArgs {
   const uint8_t* x; const float* xs; long x_row;  // codes and scales [rows][kb]

@@ -116,7 +116,7 @@ medusa_status medusa_fp8_round(const medusa_fp8* h, const void* x, int dtype, in
   a.kb = h->kb;
   a.vec = aligned(x, 4 * elem(dtype)) && x_row % 4 == 0;
   a.status = h->status;
-  return done(launch_fp8_round(a, dtype, block, S(stream)));
+  return done(launch_fp8_round(a, dtype, block, h->num_sms, S(stream)));
 }
 
 medusa_status medusa_fp8_read(const medusa_fp8* h, const void* codes, const float* scales, int rows, int block,
@@ -137,7 +137,7 @@ medusa_status medusa_fp8_read(const medusa_fp8* h, const void* codes, const floa
   a.kb = h->kb;
   a.block = block;
   a.vec = aligned(y, 4 * elem(dtype)) && y_row % 4 == 0;
-  return done(launch_fp8_read(a, dtype, S(stream)));
+  return done(launch_fp8_read(a, dtype, h->num_sms, S(stream)));
 }
 
 medusa_status medusa_fp8_linear(const medusa_fp8* h, const medusa_fp8_product* p, void* ws, size_t ws_bytes,
@@ -189,7 +189,7 @@ medusa_status medusa_fp8_linear(const medusa_fp8* h, const medusa_fp8_product* p
     r.kb = h->kb;
     r.vec = aligned(p->x, 4 * elem(p->x_dtype)) && p->x_row % 4 == 0;
     r.status = h->status;
-    const cudaError_t e = launch_fp8_round(r, p->x_dtype, 1, S(stream));
+    const cudaError_t e = launch_fp8_round(r, p->x_dtype, 1, h->num_sms, S(stream));
     if (e != cudaSuccess) return MEDUSA_ERR_CUDA;
     a.x = base;
     a.xs = r.scales;

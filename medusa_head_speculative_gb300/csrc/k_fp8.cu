@@ -130,23 +130,24 @@ __global__ void __launch_bounds__(256) fp8_read_kernel(Fp8ReadArgs a) {
   }
 }
 
-static int group_blocks(int rows, int kb) {
-  const long per = 8 * FP8_ILP, groups = (long)rows * kb, blocks = (groups + per - 1) / per;
-  return (int)(blocks < 152 * 8 ? blocks : 152 * 8);
+// Blocks of 8 warps: all that an SM holds, at most.
+static int group_blocks(int rows, int kb, int num_sms) {
+  const long per = 8 * FP8_ILP, groups = (long)rows * kb, blocks = (groups + per - 1) / per, most = 8L * num_sms;
+  return (int)(blocks < most ? blocks : most);
 }
 
-cudaError_t launch_fp8_round(const Fp8RoundArgs& a, int dtype, int block, cudaStream_t st) {
+cudaError_t launch_fp8_round(const Fp8RoundArgs& a, int dtype, int block, int num_sms, cudaStream_t st) {
   const bool f32 = dtype == MEDUSA_F32;
   if (block == 1)
-    return launch_kernel(f32 ? fp8_round_rows_kernel<float> : fp8_round_rows_kernel<bf16>, dim3(group_blocks(a.rows, a.kb)),
+    return launch_kernel(f32 ? fp8_round_rows_kernel<float> : fp8_round_rows_kernel<bf16>, dim3(group_blocks(a.rows, a.kb, num_sms)),
                          dim3(256), 0, st, 1, a);
   const int nb = (a.rows + kFp8Group - 1) / kFp8Group;
   return launch_kernel(f32 ? fp8_round_blocks_kernel<float> : fp8_round_blocks_kernel<bf16>, dim3((unsigned)nb * a.kb),
                        dim3(256), 0, st, 1, a);
 }
-cudaError_t launch_fp8_read(const Fp8ReadArgs& a, int dtype, cudaStream_t st) {
+cudaError_t launch_fp8_read(const Fp8ReadArgs& a, int dtype, int num_sms, cudaStream_t st) {
   return launch_kernel(dtype == MEDUSA_F32 ? fp8_read_kernel<float> : fp8_read_kernel<bf16>,
-                       dim3(group_blocks(a.rows, a.kb)), dim3(256), 0, st, 1, a);
+                       dim3(group_blocks(a.rows, a.kb, num_sms)), dim3(256), 0, st, 1, a);
 }
 
 }  // namespace medusa

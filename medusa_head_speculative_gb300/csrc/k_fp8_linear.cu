@@ -31,6 +31,7 @@
 #include <algorithm>
 #include <cfloat>
 
+#include "f32x2.cuh"
 #include "fp8.cuh"
 #include "launch.cuh"
 #include "tc_ptx.cuh"
@@ -120,7 +121,7 @@ __device__ __forceinline__ int2 fl_tile(const FlArgs& g, int t) {
   const int first = t / (FL_GROUP * g.nt) * FL_GROUP, rows = min(FL_GROUP, g.mt - first), in = t - first * g.nt;
   return make_int2(first + in % rows, in / rows);
 }
-template <int OC> __device__ __forceinline__ FlWalk fl_start(const FlArgs& g) {
+__device__ __forceinline__ FlWalk fl_start(const FlArgs& g) {
   const long total = (long)(g.mt * g.nt - g.whole) * g.a.kb;
   if ((int)blockIdx.x >= g.shares) return {(int)blockIdx.x, 0, 0};
   return {(int)blockIdx.x, total * blockIdx.x / g.shares, total * (blockIdx.x + 1) / g.shares};
@@ -146,13 +147,6 @@ template <int OC> __device__ __forceinline__ bool fl_next(const FlArgs& g, FlWal
   s.m = at.x;
   s.n0 = at.y * OC;
   return true;
-}
-
-__device__ __forceinline__ float2 fma2(float2 v, float2 s, float2 c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r)
-      : "l"(*reinterpret_cast<uint64_t*>(&v)), "l"(*reinterpret_cast<uint64_t*>(&s)), "l"(*reinterpret_cast<uint64_t*>(&c)));
-  return *reinterpret_cast<float2*>(&r);
 }
 
 // A group's sums reach 448^2 128 = 2^24.6, so where the product of a row's and a weight scale is no normal float it has lost
@@ -266,7 +260,7 @@ __global__ void __launch_bounds__(FL_THREADS, 1) fp8_linear_kernel(const __grid_
   const uint32_t tmem = tmem_slot;
   bool timed_out = false;
   auto aborted = [&]() { return *(volatile int*)&s_abort != 0; };
-  FlWalk walk = fl_start<OC>(g);
+  FlWalk walk = fl_start(g);
   FlSeg s;
   FlRing k = {0, 0};
   if (warp < 4) {
@@ -621,7 +615,7 @@ size_t fp8_linear_partials(int max_rows, int n, int kb, int num_sms) {
   return std::min<size_t>(2 * (size_t)num_sms, tiles * (1 + (size_t)kb)) * 128 * 256 * sizeof(float);
 }
 
-template <typename T, int BN, bool GATED> static cudaError_t linear_go(FlArgs& g, int num_sms, cudaStream_t st) {
+template <typename T, int BN, bool GATED> static cudaError_t linear_go(FlArgs& g, cudaStream_t st) {
   static unsigned long long allowed = 0;
   constexpr size_t turn = 4 * FL_PROMOTE * 2048, limit = 222 * 1024;
   const size_t stage = BN * FL_ROW + g.abox * FL_ROW, fixed = 1024 + (128 - g.abox) * FL_ROW;
@@ -636,9 +630,9 @@ template <typename T, int BN, bool GATED> static cudaError_t linear_go(FlArgs& g
   return launch_kernel(fp8_join_kernel<T, BN, GATED>, dim3(left, (rows * (GATED ? BN / 8 : BN / 4) + 255) / 256), dim3(256), 0, st, 1, g);
 }
 
-template <typename T> static cudaError_t linear_type(FlArgs& g, int bn, int num_sms, cudaStream_t st) {
-  if (g.a.w[1]) return linear_go<T, 256, true>(g, num_sms, st);
-  return bn == 128 ? linear_go<T, 128, false>(g, num_sms, st) : linear_go<T, 256, false>(g, num_sms, st);
+template <typename T> static cudaError_t linear_type(FlArgs& g, int bn, cudaStream_t st) {
+  if (g.a.w[1]) return linear_go<T, 256, true>(g, st);
+  return bn == 128 ? linear_go<T, 128, false>(g, st) : linear_go<T, 256, false>(g, st);
 }
 
 cudaError_t launch_fp8_linear(const Fp8LinearArgs& a, int dtype, void* part, int num_sms, cudaStream_t st) {
@@ -657,7 +651,7 @@ cudaError_t launch_fp8_linear(const Fp8LinearArgs& a, int dtype, void* part, int
   if (!make_map(&g.tx, a.x, a.k, a.rows, a.x_row, g.abox) || !make_map(&g.tw[0], a.w[0], a.k, a.n, a.k, 128) ||
       (gated && !make_map(&g.tw[1], a.w[1], a.k, a.n, a.k, 128)))
     return cudaErrorInvalidValue;
-  return dtype == MEDUSA_F32 ? linear_type<float>(g, p.bn, num_sms, st) : linear_type<bf16>(g, p.bn, num_sms, st);
+  return dtype == MEDUSA_F32 ? linear_type<float>(g, p.bn, st) : linear_type<bf16>(g, p.bn, st);
 }
 
 }  // namespace medusa

@@ -294,8 +294,7 @@ __global__ void __launch_bounds__(PJ_THREADS) prefix_join_kernel(PxWork w) {
     if constexpr (sizeof(T) == 4) {
       *reinterpret_cast<float4*>(dst + e * 32) = make_float4(acc[e][0], acc[e][1], acc[e][2], acc[e][3]);
     } else {
-      __nv_bfloat162 lo = __floats2bfloat162_rn(acc[e][0], acc[e][1]), hi = __floats2bfloat162_rn(acc[e][2], acc[e][3]);
-      *reinterpret_cast<uint2*>(dst + e * 32) = make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+      *reinterpret_cast<uint2*>(dst + e * 32) = make_uint2(pack2(acc[e][0], acc[e][1]), pack2(acc[e][2], acc[e][3]));
     }
   }
 }
@@ -326,10 +325,10 @@ template <typename T, int DH> static cudaError_t simt_go(const PxWork& w, cudaSt
   if (e != cudaSuccess) return e;
   return launch_kernel(prefix_simt_kernel<T, DH>, dim3(w.ctas), dim3(256), smem, st, 1, w);
 }
-template <typename T> static cudaError_t prefix_go(const PxWork& w, bool tc, int num_sms, cudaStream_t st) {
+template <typename T> static cudaError_t prefix_go(const PxWork& w, bool tc, cudaStream_t st) {
   cudaError_t e;
   const int dh = w.a.own.dh;
-  if (tc) e = launch_prefix_tc(w, num_sms, st);
+  if (tc) e = launch_prefix_tc(w, st);
   else if (dh == 32) e = simt_go<T, 32>(w, st);
   else if (dh == 64) e = simt_go<T, 64>(w, st);
   else e = simt_go<T, 128>(w, st);
@@ -370,7 +369,7 @@ cudaError_t launch_prefix_attention(const PrefixArgs& a, int dtype, void* ws, in
   w.ml_o = reinterpret_cast<float2*>(take(so * 8));
   w.o_s = reinterpret_cast<float*>(take(ss * a.own.dh * 4));
   w.ml_s = reinterpret_cast<float2*>(take(ss * 8));
-  return dtype == MEDUSA_F32 ? prefix_go<float>(w, tc, num_sms, st) : prefix_go<bf16>(w, tc, num_sms, st);
+  return dtype == MEDUSA_F32 ? prefix_go<float>(w, tc, st) : prefix_go<bf16>(w, tc, st);
 }
 
 }  // namespace medusa

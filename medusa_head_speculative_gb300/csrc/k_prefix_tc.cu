@@ -99,11 +99,6 @@ struct PtRing {
 // an operand there costs as much as half an MMA (16 MMAs of a job 1800 cycles to issue, 1025 to run).
 __device__ __forceinline__ int uni(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&p);
-}
-
 template <int DH>
 __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_constant__ PtArgs g) {
   constexpr int H = DH / 64;                         // 64-element halves of a head
@@ -478,8 +473,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
                 p3 = ex2_approx(p3);
                 l0 = add2(l0, f2(p0, p1));
                 l1 = add2(l1, f2(p2, p3));
-                pk[e / 2] = bf16x2(p0, p1);
-                pk[e / 2 + 1] = bf16x2(p2, p3);
+                pk[e / 2] = pack2(p0, p1);
+                pk[e / 2 + 1] = pack2(p2, p3);
                 x0 = max3(x0, v[e], v[e + 1]);
                 x1 = max3(x1, v[e + 2], v[e + 3]);
               }
@@ -513,7 +508,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
                 kt_ld16(scol + 16 * e, u);
 #pragma unroll
                 for (int y = 0; y < 16; ++y)
-                  scaled[y] = bf16x2(__uint_as_float(__float_as_uint(u[y]) << 16) * f,
+                  scaled[y] = pack2(__uint_as_float(__float_as_uint(u[y]) << 16) * f,
                                      __uint_as_float(__float_as_uint(u[y]) & 0xffff0000u) * f);
                 kt_st16(scol + 16 * e, scaled);
               }
@@ -684,7 +679,7 @@ template <int DH> static cudaError_t tc_go(PtArgs& g, cudaStream_t st) {
   return launch_kernel(prefix_tc_kernel<DH>, dim3(g.w.ctas), dim3(PT_THREADS), limit, st, 1, g);
 }
 
-cudaError_t launch_prefix_tc(const PxWork& w, int num_sms, cudaStream_t st) {
+cudaError_t launch_prefix_tc(const PxWork& w, cudaStream_t st) {
   PtArgs g{};
   g.w = w;
   g.nt[0] = w.rbs > PT_ROWS ? 2 : 1;

@@ -7,6 +7,7 @@
 
 #include "cache.h"
 #include "common.cuh"
+#include "f32x2.cuh"
 
 namespace medusa {
 
@@ -100,10 +101,6 @@ template <int N> __device__ __forceinline__ void load_n(const float* p, bool vec
     for (int e = 0; e < N; ++e) f[e] = p[e];
   }
 }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&p);
-}
 template <int N> __device__ __forceinline__ void store_n(bf16* p, bool vec, const float (&f)[N]) {
   if (vec) {
 #pragma unroll
@@ -124,32 +121,6 @@ template <int N> __device__ __forceinline__ void store_n(float* p, bool vec, con
 #pragma unroll
     for (int e = 0; e < N; ++e) p[e] = f[e];
   }
-}
-
-// Two floats in one register pair: each half is one IEEE operation, as by itself.
-struct F2 {
-  unsigned long long v;
-};
-__device__ __forceinline__ F2 f2(float x, float y) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ void unf2(F2 a, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v)); }
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
 }
 
 // Eight floats to a word of e2m1 codes (nearest, ties to even, 6 at most).

@@ -177,6 +177,6 @@ __device__ __forceinline__ uint32_t px_sees(const PrefixArgs& a, int n, int i) {
 }
 
 // bf16 rows on the tensor cores (k_prefix_tc.cu): dh 64 or 128.
-cudaError_t launch_prefix_tc(const PxWork& w, int num_sms, cudaStream_t st);
+cudaError_t launch_prefix_tc(const PxWork& w, cudaStream_t st);
 
 }  // namespace medusa

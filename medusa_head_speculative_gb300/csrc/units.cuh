@@ -29,10 +29,6 @@ __device__ __forceinline__ void load4(const bf16* p, bool vec, float (&x)[4]) {
     for (int i = 0; i < 4; ++i) x[i] = to_f32(p[i]);
   }
 }
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&p);
-}
 __device__ __forceinline__ void save4(float* p, bool vec, const float (&x)[4]) {
   if (vec) {
     *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
@@ -43,7 +39,7 @@ __device__ __forceinline__ void save4(float* p, bool vec, const float (&x)[4]) {
 }
 __device__ __forceinline__ void save4(bf16* p, bool vec, const float (&x)[4]) {
   if (vec) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]));
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) p[i] = __float2bfloat16_rn(x[i]);
