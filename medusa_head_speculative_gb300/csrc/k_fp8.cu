@@ -5,8 +5,8 @@
 // reduction over the warp and loads and stores are whole 128- to 512-byte lines; FP8_ILP groups are in
 // flight a warp.  Weights: a CTA has one 128 x 128 block in registers, 16 rows a warp.
 //
-// Measured (one GB300): 13824 x 5120 float weights rounded and read back 123 us, 5.7 TB/s of 708 MB (copy: 6.8); 520 x
-// 5120 bf16 rows 7.7 us for the two launches, of which 2.4 are their bytes.
+// Measured (one GB300): 13824 x 5120 float weights rounded and read back 121 us, 5.8 TB/s of 708 MB (copy: 6.8); 520 x
+// 5120 bf16 rows 7.3 us for the two launches, of which 2.4 are their bytes.
 #include "fp8.cuh"
 #include "launch.cuh"
 

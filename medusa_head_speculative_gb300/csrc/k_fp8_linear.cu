@@ -20,11 +20,12 @@
 // evenly over the SMs; a CTA that has a part of a tile's groups writes a partial of its own, and a second
 // kernel adds a tile's partials up in order and finishes it.
 //
-// Measured (one GB300): 8192 x 5120 x 13824 with a residual 567 us (2.05 PFLOP/s), 520 x 15360 x 5120 52 us (1.57),
-// gated 688 x 14336 x 4096 100 us (1.61), gated 8 x 13824 x 5120 32 us (4.4 TB/s of weights, 6.6 while they stream),
-// 1 x 4096 x 4096 10.8 us with the rounding before and the joining behind it.  What bounds the large ones: a group takes
-// 700 to 950 cycles, its MMAs 460 and their commit 75; the accumulator's way to the promoting warps and back is seen in
-// between (510 cycles to promote), and residuals of 8192 rows wait for memory at a tile's end.
+// Measured (one GB300, calls in a graph): 8192 x 5120 x 13824 with a residual 581 us (2.0 PFLOP/s), 520 x 15360 x 5120 51 us
+// (1.59), gated 688 x 14336 x 4096 99 us (1.63), gated 8 x 13824 x 5120 33 us (4.3 TB/s of weights, 6.6 while they stream),
+// 1 x 4096 x 4096 11 us with the rounding before and the joining behind it.  What bounds the large ones: a group takes
+// 700 to 950 cycles, its MMAs 512 (8192 multiply-adds a cycle: 256 groups in line, with a commit each or with one); the
+// accumulator's way to the promoting warps and back is seen in between (510 cycles to promote), and residuals of 8192 rows
+// wait for memory at a tile's end.
 //
 // Every wait is bounded; on expiry MEDUSA_FLAG_TIMEOUT is set, the CTA stops taking work, drains the copies
 // it issued and frees its tensor memory.
@@ -58,9 +59,9 @@ struct FlArgs {
   int rows_last;                                    // weights are read once (mt == 1)
 };
 
-// FULL: a stage has landed.  DONE: its products are in an accumulator, and the stage is free (one barrier for both: a
-// commit costs the tensor cores 50 to 75 cycles).  TE: an accumulator has been read.  SF, SE: scales have been written, read.  END: every MMA is done.
-// NEVER: nothing arrives (tests).
+// FULL: a stage has landed.  DONE: its products are in an accumulator, and the stage is free (one barrier and one commit
+// for both).  TE: an accumulator has been read.  SF, SE: scales have been written, read.  END: every MMA is done.  NEVER:
+// nothing arrives (tests).
 enum { FB_FULL = 0, FB_DONE = FL_MAXST, FB_TE = 2 * FL_MAXST, FB_SF = FB_TE + 2, FB_SE = FB_SF + FL_SC,
        FB_END = FB_SE + FL_SC, FB_NEVER = FB_END + 1, FB_COUNT = FB_NEVER + 1 };
 // A place in the ring of stages (a division by its depth would take longer than what it is needed for).
@@ -114,8 +115,8 @@ struct FlWalk {
   long w, w1;                                       // groups of the others
 };
 // Tile row and column of tile t.  Tiles that run at a time are neighbours: up to FL_GROUP rows of tiles by as many
-// columns as there are CTAs for, so that they share rows and weights in the L2 (all rows of a column first: rows of
-// 8192 x 13824 came from memory five times).
+// columns as there are CTAs for, so that they share rows and weights in the L2 (8192 x 5120 x 13824: 651 MB from memory of
+// 268, with all rows of a column first 1204).
 constexpr int FL_GROUP = 16;
 __device__ __forceinline__ int2 fl_tile(const FlArgs& g, int t) {
   const int first = t / (FL_GROUP * g.nt) * FL_GROUP, rows = min(FL_GROUP, g.mt - first), in = t - first * g.nt;

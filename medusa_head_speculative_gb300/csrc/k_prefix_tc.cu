@@ -26,8 +26,8 @@
 // partial (of an item's only chunk its slot writes it).
 //
 // Measured (one GB300), joining included: 16 x 8 heads x 172 rows over a prefix of 8192 and 64-512 slots 115 us (830
-// TFLOP/s), 8 x 40 heads x 65 rows over 2048 + 0-1024 76 us, 32 x 8 heads x 4 rows over 16384 + 100-1000 slots in pages
-// of 16 50 us (2.8 TB/s).  What bounds them: with two tiles a chunk takes 5000 cycles, its MMAs 2050 and the softmax of a
+// TFLOP/s; heads of 64 99 us, 490), 8 x 40 heads x 65 rows over 2048 + 0-1024 76 us, 32 x 8 heads x 4 rows over 16384 +
+// 100-1000 slots in pages of 16 49 us (2.8 TB/s).  What bounds them: with two tiles a chunk takes 5000 cycles, its MMAs 2050 and the softmax of a
 // slot 2900 (instructions a warp at a time; exponentials alone 2050 for both slots); pages of 16 slots come by
 // 16-byte copies, 4000 cycles a chunk; items of few chunks have their start and end besides.  Code size counts here:
 // more unrolling of the copies or the softmax makes every warp slower (64 keys at a time 112 -> 129 us).
@@ -64,8 +64,8 @@ struct PtArgs {
 // QF / QE: query tiles (with one tile: two in turn) written / no longer read.  KF and VF: stages full.  Per slot
 // and stage: SF (S written, so that the keys' stage is free as far as the slot goes), OF (P V done, the values'
 // stage).  Per slot: P1 and P2 (P of the first 64 keys, of all written), O1 (P V of the first done).  One barrier for
-// both who wait: each commit costs the tensor cores 50 to 75 cycles (QK and PV of a chunk take 1025 cycles
-// without, 1390 with four).  MRG / MFR: the second slot's (reference, sum) are in shared
+// both who wait (with four commits a chunk's QK and PV took 1390 cycles in this kernel; such MMAs by themselves take 1024, also
+// with four commits among them).  MRG / MFR: the second slot's (reference, sum) are in shared
 // memory / consumed.  END: every MMA issued has completed.  NEVER: nothing arrives (tests).
 enum {
   XB_QF = 0, XB_QE = 2, XB_KF = 4, XB_VF = XB_KF + PT_MAXST, XB_SF = XB_VF + PT_MAXST, XB_OF = XB_SF + 2 * PT_MAXST,
@@ -644,8 +644,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefix_tc_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------------ host side
-// (The CUDA cores' kernel in place of this one: 16 x 43 nodes of 4 x 8 heads over 8192 slots 7.6 ms for 115 us; float rows
-// and heads of 32 it takes alone.)
+// (The CUDA cores' kernel in place of this one: 16 x 43 nodes of 4 x 8 heads of 128 over 8192 slots 3.66 ms for 115 us, 32 single
+// rows over 16384 687 us for 49.  Float rows it takes alone, and heads of 32, for which this one has not been built: the
+// same nodes take 1.25 ms with heads of 32 and 99 us with heads of 64.)
 bool prefix_tc_takes(int dtype, int dh) { return dtype == MEDUSA_BF16 && (dh == 64 || dh == 128); }
 
 static bool make_map(CUtensorMap* map, const void* p, const CacheView& c) {
