@@ -4,7 +4,10 @@
 //
 // For each row r, with s_j = scale q_r . k_j over the keys j it sees: o_r = sum_j 2^(s'_j - m_r) v_j and
 // l_r = sum_j 2^(s'_j - m_r), s' in base-2 units, m_r a running reference that is raised (and o rescaled)
-// only once a score passes it by PT_LAZY, o and l in float, probabilities rounded to bf16 for the product.
+// only once a score passes it by PT_LAZY, o and l in float, probabilities rounded to bf16 for the product: the MMA takes
+// both operands in one type, and values are bf16.  Results are then 0.0023 off the 64-bit ones (relative, over listed cases), of
+// which 0.0017 are their own rounding.  Probabilities as two summands of bf16, multiplied one after the other, keep 16 bits and
+// give 0.0017, but the cases below take 58, 96 and 152 us for 52, 81 and 118 (calls from Python): not worth it.
 //
 // One CTA per SM walks through its chunks of 128 keys, an item at a time.  A block of rows is one tile of 128
 // or two.  In the CTA
