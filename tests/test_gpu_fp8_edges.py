@@ -163,3 +163,29 @@ def test_expire_wait_argument_checks():
         with pytest.raises(Bnd.MedusaError) as e:
             h.expire_wait_once(ns)
         assert e.value.code == Bnd.MEDUSA_ERR_INVALID
+
+
+@pytest.mark.parametrize("rows", [5, 200])
+def test_rows_and_residuals_that_are_one_row(rows):
+    """Row strides of 0: one row of inputs for all, one row of residuals (a bias) for all."""
+    n, k = 300, 656
+    r = np.random.default_rng(rows)
+    w, ws = codes_of(r, n, k), scales(r, (3, 6), [0.5, 3.0])
+    x = torch.from_numpy(r.standard_normal((rows, k))).float().cuda()
+    bias = torch.from_numpy(r.standard_normal(n)).float().cuda()
+    h = Bnd.Fp8(n=n, k=k, max_rows=rows)
+    work, s = torch.empty(h.workspace_size, dtype=torch.uint8, device="cuda"), torch.from_numpy(ws).cuda()
+    for one in (False, True):
+        xin = x[:1].expand(rows, k) if one else x
+        y = torch.zeros(rows, n, device="cuda")
+        Bnd.fp8_linear(h, xin, dev(w), s, y, work, add=bias.expand(rows, n))
+        want, tol = product(F.values(*F.round8(f64(xin), 1), 1), w, ws, 6)
+        want = want + f64(bias)
+        tol = tol + 2 * U * (np.abs(want) + tol)
+        assert (np.abs(f64(y) - want) <= tol).all()
+        if one:
+            codes = torch.zeros(rows, k, dtype=torch.uint8, device="cuda")
+            sc = torch.zeros(rows, 6, device="cuda")
+            Bnd.fp8_round(h, xin, codes, sc)
+            assert (codes == codes[0]).all() and (sc == sc[0]).all()
+    assert h.status() == 0

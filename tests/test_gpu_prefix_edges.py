@@ -1,4 +1,4 @@
-"""Attention over a shared prefix: waits that run out."""
+"""Attention over a shared prefix: waits that run out, and operands that are one row or one cache."""
 import time
 
 import pytest
@@ -57,3 +57,22 @@ def test_expire_wait_argument_checks():
         with pytest.raises(Bnd.MedusaError) as e:
             cache(**kw).prefix_expire_wait_once(1000)
         assert e.value.code == Bnd.MEDUSA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_queries_that_are_one_row_and_caches_that_are_one(dtype):
+    """Row and head strides of 0 for the queries; and a sequence whose own cache is the shared one too (each key twice)."""
+    c = T.Case(12, 1, 6, 2, 64, 5, 200, [200], 0, 0, dtype, None)
+    q = c.q[:, :1, :1].expand_as(c.q)
+    o = c.run(q=q)
+    assert torch.equal(o[:, 1:].contiguous(), o[:, :1].expand(1, 4, 6, 64).contiguous())     # rows alike; heads of a key head too
+    assert torch.equal(o[:, :, 0], o[:, :, 2]) and not torch.equal(o[:, :, 0], o[:, :, 3])
+    (own, okv), _ = c.handles
+    ws = torch.empty(Bnd.prefix_workspace_size(own, own), dtype=torch.uint8, device="cuda")
+    twice, once = torch.empty_like(c.q), torch.empty_like(c.q)
+    c.shared_pool["len"].zero_()
+    c.shared_pool["lens"] = [0]
+    c.run(o=once)
+    Bnd.prefix_attention(own, okv, own, okv, c.q, twice, ws)
+    want, tol = c.want()                          # doubled weights of equal keys: the same mean, over twice as many terms
+    assert (abs(T.f64(once) - want) <= tol).all() and (abs(T.f64(twice) - want) <= 2 * tol).all() and own.status() == 0
